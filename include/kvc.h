@@ -72,6 +72,9 @@ typedef enum kvc_status {
 
 typedef enum kvc_dtype { KVC_F32 = 0, KVC_F16 = 1, KVC_BF16 = 2 } kvc_dtype;
 
+/* Codes of the one-byte caches with one scale per (block, kv head). */
+typedef enum kvc_code { KVC_E4M3 = 0, KVC_INT8 = 1 } kvc_code;
+
 /* Bits of the device error word. */
 #define KVC_FLAG_BAD_BLOCK 0x1u   /* block table entry outside [0, num_blocks) */
 #define KVC_FLAG_BAD_LEN 0x2u     /* context_len < 1 (multi-token: < n_tokens) or > max_blocks_per_seq*block_size */
@@ -205,6 +208,44 @@ kvc_status kvc_append_fp8(const void* k, const void* v, const int64_t* slot_mapp
 kvc_status kvc_append_int8(const void* k, const void* v, const int64_t* slot_mapping, int64_t num_tokens,
                            void* k_cache, void* v_cache, float* v_scale, const float* k_scale, int64_t num_blocks,
                            int block_size, int n_kv_heads, int head_dim, kvc_dtype dtype, kvc_stream stream);
+
+/* Append into a one-byte cache that keeps one scale for each (block, kv head):
+ * a cached row stands for code * scale[block, head]. k_cache, v_cache: codes
+ * [num_blocks, n_kv_heads, block_size, head_dim], uint8 e4m3 (code KVC_E4M3) or
+ * int8 (KVC_INT8); k_scale, v_scale: fp32 [num_blocks, n_kv_heads], 4 bytes per
+ * head and block against 4 per row (V) of kvc_append_fp8, and no calibrated
+ * K scales. k, v: [num_tokens, n_kv_heads, head_dim] in `dtype` (F32, F16, BF16).
+ *
+ * The tokens of the call that fall into one block form a run. For each kv
+ * head, with first = the run's lowest row in the block, A = the largest |x| of
+ * the run and Q = 448 (e4m3) or 127 (int8):
+ *   s = max(s_old, A * (1 / Q)), s_old = scale[block, head], or 0 if first == 0
+ *   rows below `first`: code = q(code * (s_old / s)) if s differs from s_old
+ *   the run's rows:     code = q(x * (1 / s)); then scale[block, head] = s
+ * Every operation is fp32, rounded once; q rounds to the nearest code, ties to
+ * even, saturating at +-Q. So the scale of a block grows with its loudest
+ * token, and earlier rows are rounded once more each time it does (a block
+ * written by one call never is); writing row 0 starts the block afresh,
+ * whatever it held. Rows behind the run that the call does not write keep
+ * their codes and must not be attended any more if the scale changed. A scale
+ * below the smallest normal number becomes 0, with codes 0. Entries that are
+ * not finite do not count for A: infinities saturate, NaN becomes the e4m3 NaN
+ * or int8 0.
+ *
+ * slot_mapping: as kvc_append (negative: skipped; >= num_blocks*block_size:
+ * skipped and KVC_FLAG_BAD_SLOT). The tokens of one block must be adjacent in
+ * it, as kvc_seq_reserve and kvc_seq_reserve_batch give them, with no skipped
+ * one between them; two runs of one block in one call race (the block's codes
+ * and scale are then a mixture of the two), as two tokens of one slot do.
+ * num_tokens == 0 is a no-op. head_dim 64, 128 or 256; block_size a multiple
+ * of 16 up to 128; k, v and the caches 16-byte aligned. A block's scales move
+ * with it: a copied block (kvc_copy_blocks) needs its scales copied too.
+ * Source: "KV-Cache——为什么AI回复越来越快" section 08 (KV-Cache quantisation);
+ * the scale per block and head is this library's. */
+kvc_status kvc_append_block8(const void* k, const void* v, const int64_t* slot_mapping, int64_t num_tokens,
+                             void* k_cache, void* v_cache, float* k_scale, float* v_scale, kvc_code code,
+                             int64_t num_blocks, int block_size, int n_kv_heads, int head_dim, kvc_dtype dtype,
+                             kvc_stream stream);
 
 /* Copy-on-write block copy inside one pool: for i < n_pairs, block
  * pairs[2i + 1] becomes a byte copy of block pairs[2i]. cache: device pool of
@@ -362,6 +403,110 @@ kvc_status kvc_decode_attention_int8(const void* q, const void* k_cache, const v
                                      kvc_dtype out_dtype, void* workspace, size_t workspace_bytes,
                                      kvc_stream stream);
 
+/* Scratch bytes for kvc_decode_attention_scored and kvc_decode_attention_block8
+ * (either cache element size) on the current device; scored != 0: for calls
+ * with a scores buffer, which adds 4 bytes per query and row that the tables
+ * can hold (batch x n_tokens x n_q_heads x max_blocks_per_seq x block_size).
+ * Same shape errors as the calls. */
+kvc_status kvc_decode_scored_workspace_size(int batch, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim,
+                                            int block_size, int max_blocks_per_seq, int scored, size_t* bytes);
+
+/* Decode attention that also adds up the attention weight every cached row
+ * receives: the record that kvc_evict_rows goes by.
+ *   out    as kvc_decode_attention_multi: q, out [batch, n_tokens, n_q_heads,
+ *          head_dim], token t of sequence i attends rows 0 .. n_i - n_tokens + t
+ *          (n_i = context_lens[i] counts the new rows; append them first)
+ *   scores fp32 [batch, n_kv_heads, max_blocks_per_seq * block_size], in table
+ *          order: entry (i, h, r) belongs to logical row r of sequence i. With
+ *          w = the sum of row r's softmax weights over the n_tokens *
+ *          (n_q_heads / n_kv_heads) queries of kv head h,
+ *            scores += w for r < n_i - n_tokens, scores = w for the new rows;
+ *          entries at and behind n_i are left as they are.
+ * So the entry of a row starts with the call that appended it; rows that were
+ * appended before without such a call need their entries cleared. A caller
+ * that changes the batch moves the rows of scores with those of block_tables.
+ * Sequences may share blocks: their scores are separate. Each entry is added
+ * up in a fixed order: the same inputs give the same bits.
+ * A sequence with n_i < n_tokens or n_i > max_blocks_per_seq * block_size sets
+ * KVC_FLAG_BAD_LEN; its outputs are zeros and its scores are left as they are.
+ * Rows in blocks outside the pool set KVC_FLAG_BAD_BLOCK and get no weight.
+ * dtype F16 or BF16; head_dim 64, 128 or 256; block_size a multiple of 16 up to
+ * 128; batch <= 4096; n_tokens <= 256; n_tokens * n_q_heads / n_kv_heads <=
+ * 4096; q and the caches 16-byte aligned. workspace: at least
+ * kvc_decode_scored_workspace_size() bytes, 256-byte aligned; it need not be
+ * cleared and holds nothing between calls; calls that may run concurrently
+ * must not share one. Two kernels on `stream`; may be captured.
+ * Sources: "KV缓存原理与显存估算" knowledge point 2 (the decode) and closing
+ * section (state that leaves the cache); the accumulated weights are this
+ * library's. */
+kvc_status kvc_decode_attention_scored(const void* q, const void* k_cache, const void* v_cache,
+                                       const int32_t* block_tables, int max_blocks_per_seq,
+                                       const int32_t* context_lens, int batch, int n_tokens, float scale,
+                                       int n_q_heads, int n_kv_heads, int head_dim, int block_size,
+                                       int64_t num_blocks, kvc_dtype dtype, void* out, kvc_dtype out_dtype,
+                                       float* scores, void* workspace, size_t workspace_bytes, kvc_stream stream);
+
+/* The same decode over the caches written by kvc_append_block8: k = code *
+ * k_scale[block, head], v = code * v_scale[block, head] (the scales enter the
+ * scores and the weights, so one byte per element is read). q F16 or BF16 in
+ * q_dtype. scores may be NULL (plain decode, no weights accumulated; the
+ * workspace query with scored = 0). Otherwise as kvc_decode_attention_scored.
+ * Source: "KV-Cache——为什么AI回复越来越快" section 08 (KV-Cache quantisation). */
+kvc_status kvc_decode_attention_block8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                       const float* v_scale, kvc_code code, const int32_t* block_tables,
+                                       int max_blocks_per_seq, const int32_t* context_lens, int batch, int n_tokens,
+                                       float scale, int n_q_heads, int n_kv_heads, int head_dim, int block_size,
+                                       int64_t num_blocks, kvc_dtype q_dtype, void* out, kvc_dtype out_dtype,
+                                       float* scores, void* workspace, size_t workspace_bytes, kvc_stream stream);
+
+/* --------------------------------------------------------------- eviction */
+
+/* Eviction by accumulated attention weight. Of sequence i's n = context_lens[i]
+ * rows, each kv head keeps m = min(n, budget): the newest min(recent, m) rows
+ * and, of the others, those with the largest scores[i, h, r] (ties: the lower
+ * row; NaN counts as the lowest score). The kept rows move, in their order,
+ * from the blocks of block_tables[i] to those of new_block_tables[i], the same
+ * pools' blocks, row j of the result at logical row j. Rows keep what position
+ * encoding they were cached with; the heads of one logical row may then hold
+ * different tokens.
+ *   scores      fp32 [batch, n_kv_heads, max_blocks_per_seq * block_size]
+ *   kept        int32 [batch, n_kv_heads, budget], written: the old row of
+ *               every new row, -1 at and behind m
+ *   new_lens    int32 [batch], written: m
+ *   new_scores  fp32 [batch, n_kv_heads, new_max_blocks_per_seq * block_size]:
+ *               entries below m written, the others left as they are
+ * The old blocks, lens and scores are only read, so blocks shared with forks
+ * are safe; the new blocks must not be among them (kvc_seq_evict hands out
+ * free ones), and no two sequences may share a new block. new_scores, new_lens
+ * and new_block_tables must not overlap the old ones.
+ * 1 <= budget <= new_max_blocks_per_seq * block_size, 0 <= recent <= budget.
+ * n = 0 keeps nothing; n < 0 or n > max_blocks_per_seq * block_size sets
+ * KVC_FLAG_BAD_LEN and counts as 0. A row whose old or new block lies outside
+ * the pool is not moved and sets KVC_FLAG_BAD_BLOCK. F32, F16 and BF16; head_dim
+ * times element size a multiple of 16 bytes; any block_size. No workspace; two
+ * kernels on `stream`; may be captured.
+ * Source: the closing section of "KV缓存原理与显存估算" (state that leaves the
+ * cache) and "KV-Cache——为什么AI回复越来越快" section 08 (keeping part of the
+ * rows); the choice by accumulated weight is this library's. */
+kvc_status kvc_evict_rows(const float* scores, void* k_cache, void* v_cache, const int32_t* block_tables,
+                          int max_blocks_per_seq, const int32_t* context_lens, int batch, int budget, int recent,
+                          const int32_t* new_block_tables, int new_max_blocks_per_seq, int64_t num_blocks,
+                          int block_size, int n_kv_heads, int head_dim, kvc_dtype dtype, int32_t* kept,
+                          int32_t* new_lens, float* new_scores, kvc_stream stream);
+
+/* The same for the caches of kvc_append_block8. The scale of a new block is the
+ * largest scale s' that its rows had; rows from blocks of a smaller scale s
+ * are rounded again, code = q(code * (s / s')) in fp32, the others keep their
+ * codes. head_dim a multiple of 16. */
+kvc_status kvc_evict_rows_block8(const float* scores, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                 kvc_code code, const int32_t* block_tables, int max_blocks_per_seq,
+                                 const int32_t* context_lens, int batch, int budget, int recent,
+                                 const int32_t* new_block_tables, int new_max_blocks_per_seq, int64_t num_blocks,
+                                 int block_size, int n_kv_heads, int head_dim, int32_t* kept, int32_t* new_lens,
+                                 float* new_scores, kvc_stream stream);
+
+/* --------------------------------------- decode without caller's scratch */
+
 /* kvc_decode_attention for callers that cannot allocate device memory.
  *
  * There is no counterpart of this call on the source pages: it exists for
@@ -470,6 +615,17 @@ kvc_status kvc_seq_reserve_batch(kvc_pool* pool, const int64_t* seqs, int n, int
  * Source: llm-compass 2.3 (blocks shared by reference count are copied
  * before a holder writes into them: parallel sampling, beam search). */
 kvc_status kvc_seq_reserve_cow(kvc_pool* pool, int64_t seq, int64_t n_new, int64_t* slots_out, int64_t* copy_pair);
+/* The host side of kvc_evict_rows: `seq` gets ceil(new_length / block_size)
+ * fresh blocks (the lowest free ids) in place of its present ones and the
+ * length new_length; each old block loses one reference. Build the old table
+ * (kvc_build_block_tables) before and the new one after this call. The old
+ * blocks count as free at once, although the rows are still to be copied out
+ * of them: launch kvc_evict_rows before anything that writes to blocks reserved
+ * later, on the same stream. KVC_ERR_INVALID_ARG for an unknown sequence or a
+ * new_length outside 0 .. length; KVC_ERR_NO_BLOCKS if the fresh blocks are not
+ * all free while the old ones are still held (nothing changes).
+ * Source: "KV Cache（键值缓存）" 2.3 (blocks counted by reference). */
+kvc_status kvc_seq_evict(kvc_pool* pool, int64_t seq, int64_t new_length);
 /* Drops the sequence; each of its blocks loses one reference and returns to
  * the free list at zero. KVC_ERR_INVALID_ARG for an unknown sequence.
  * Source: "KV Cache（键值缓存）" 2.3. */

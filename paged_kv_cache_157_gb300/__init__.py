@@ -21,9 +21,11 @@ __all__ = [
     "append", "append_latent", "decode_workspace_size", "decode_attention", "decode_attention_static",
     "decode_attention_window", "copy_blocks", "append_fp8", "decode_attention_fp8",
     "append_int8", "decode_attention_int8",
+    "append_block8", "decode_attention_block8", "decode_attention_scored", "scored_workspace_size",
+    "new_scored_workspace", "evict_rows",
     "decode_mla_workspace_size", "decode_attention_mla", "set_option", "get_option",
     "get_error_flags", "BlockPool", "slots_from_tables",
-    "F32", "F16", "BF16", "FLAG_BAD_BLOCK", "FLAG_BAD_LEN", "FLAG_BAD_SLOT", "FLAG_TIMEOUT", "FLAG_WORKSPACE",
+    "F32", "F16", "BF16", "E4M3", "INT8", "FLAG_BAD_BLOCK", "FLAG_BAD_LEN", "FLAG_BAD_SLOT", "FLAG_TIMEOUT", "FLAG_WORKSPACE",
     "new_decode_workspace",
     "OPT_CHECKED", "OPT_BLOCKS_PER_CTA", "OPT_MAX_CTAS", "OPT_GQA_ENGINE", "OPT_DYNAMIC_SHARE", "OPT_DYNAMIC_CHUNK",
     "OPT_WAIT_POLLS",
@@ -33,6 +35,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libkvc.so")
 
 F32, F16, BF16 = 0, 1, 2
+E4M3, INT8 = 0, 1  # code formats of the block-scaled one-byte caches
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_NO_BLOCKS, ERR_CUDA, ERR_OUT_OF_RANGE, ERR_WORKSPACE = range(7)
 FLAG_BAD_BLOCK, FLAG_BAD_LEN, FLAG_BAD_SLOT, FLAG_TIMEOUT, FLAG_WORKSPACE = 0x1, 0x2, 0x4, 0x8, 0x10
 OPT_CHECKED, OPT_BLOCKS_PER_CTA, OPT_MAX_CTAS, OPT_GQA_ENGINE, OPT_DYNAMIC_SHARE, OPT_DYNAMIC_CHUNK, OPT_WAIT_POLLS = \
@@ -89,6 +92,17 @@ SIGNATURES = {
     "kvc_append_int8": (_i32, [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp]),
     "kvc_decode_attention_int8": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _f32, _i32, _i32, _i32, _i32,
                                          _i64, _vp, _i32, _vp, _sz, _vp]),
+    "kvc_append_block8": (_i32, [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _i32, _i32, _vp]),
+    "kvc_decode_scored_workspace_size": (_i32, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _szp]),
+    "kvc_decode_attention_scored": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _f32, _i32, _i32, _i32, _i32,
+                                           _i64, _i32, _vp, _i32, _vp, _vp, _sz, _vp]),
+    "kvc_decode_attention_block8": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _f32, _i32,
+                                           _i32, _i32, _i32, _i64, _i32, _vp, _i32, _vp, _vp, _sz, _vp]),
+    "kvc_evict_rows": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _i32, _i64, _i32, _i32, _i32,
+                              _i32, _vp, _vp, _vp, _vp]),
+    "kvc_evict_rows_block8": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _i32, _i64,
+                                     _i32, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "kvc_seq_evict": (_i32, [_vp, _i64, _i64]),
     "kvc_seq_free": (_i32, [_vp, _i64]),
     "kvc_seq_length": (_i32, [_vp, _i64, _i64p]),
     "kvc_block_refcount": (_i32, [_vp, _i64, _i32p]),
@@ -444,6 +458,12 @@ class BlockPool:
         copy = None if pair[0] < 0 else (int(pair[0]), int(pair[1]))
         return [int(buf[i]) for i in range(n_new)], copy
 
+    def evict(self, seq: int, new_length: int):
+        """kvc_seq_evict: fresh blocks for ``new_length`` rows in place of the sequence's present ones. Build the
+        old table before and the new one after it, then call evict_rows before anything that writes to blocks
+        reserved later."""
+        _check(self._lib.kvc_seq_evict(self._h, seq, new_length), "kvc_seq_evict")
+
     def free(self, seq: int):
         _check(self._lib.kvc_seq_free(self._h, seq), "kvc_seq_free")
 
@@ -570,3 +590,179 @@ def decode_attention_int8(q, k_cache, v_cache, k_scale, v_scale, block_tables, c
     """kvc_decode_attention_int8: q bf16 [B, Hq, D] over INT8 caches written by append_int8."""
     _decode_q8("kvc_decode_attention_int8", _torch().int8, q, k_cache, v_cache, k_scale, v_scale, block_tables,
                context_lens, scale, out, workspace, stream)
+
+
+# ------------------------------------- block-scaled codes, scores, eviction
+
+def _code_format(codes, name) -> int:
+    """Code format of a block-scaled pool: uint8 holds e4m3 codes, int8 holds int8 codes."""
+    torch = _torch()
+    if codes.dtype == torch.uint8:
+        return E4M3
+    if codes.dtype == torch.int8:
+        return INT8
+    raise TypeError(f"{name} must hold uint8 (e4m3) or int8 codes, got {codes.dtype}")
+
+
+def _same_device(first, others):
+    """Refuses tensors of several devices, and of a device that is not current: the stream and the library's
+    launches belong to the current one."""
+    torch = _torch()
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    if first.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {first.device}, current device cuda:{torch.cuda.current_device()}")
+
+
+def _pools(k_cache, v_cache):
+    """Checks a pair of pools [num_blocks, Hkv, bs, D] and returns their shape."""
+    _require(k_cache, "k_cache")
+    _require(v_cache, "v_cache", k_cache.dtype)
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must both be [num_blocks, n_kv_heads, block_size, head_dim]")
+    return k_cache.shape
+
+
+def _block_scales(k_scale, v_scale, nb, hkv):
+    torch = _torch()
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _require(t, n, torch.float32)
+        if tuple(t.shape) != (nb, hkv):
+            raise ValueError(f"{n} must be [num_blocks, n_kv_heads]")
+
+
+def append_block8(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, stream=None):
+    """kvc_append_block8: k, v [T, Hkv, D] (f32/f16/bf16); slot_mapping int64 [T], the tokens of one block adjacent;
+    k_cache, v_cache codes [num_blocks, Hkv, bs, D], uint8 (e4m3) or int8; k_scale, v_scale fp32 [num_blocks, Hkv].
+    The blocks' scales grow with what is appended; a block's row 0 starts it afresh."""
+    torch = _torch()
+    nb, hkv, bs, d = _pools(k_cache, v_cache)
+    code = _code_format(k_cache, "k_cache")
+    _require(k, "k")
+    _require(v, "v", k.dtype)
+    _require(slot_mapping, "slot_mapping", torch.int64)
+    _block_scales(k_scale, v_scale, nb, hkv)
+    T = slot_mapping.numel()
+    if tuple(k.shape) != (T, hkv, d) or v.shape != k.shape:
+        raise ValueError("k and v must be [num_tokens, n_kv_heads, head_dim]")
+    _same_device(k_cache, (v_cache, k, v, slot_mapping, k_scale, v_scale))
+    _check(raw().kvc_append_block8(_ptr(k), _ptr(v), _ptr(slot_mapping), T, _ptr(k_cache), _ptr(v_cache),
+                                   _ptr(k_scale), _ptr(v_scale), code, nb, bs, hkv, d, _dtype_code(k),
+                                   _stream(stream)), "kvc_append_block8")
+
+
+def scored_workspace_size(batch, n_tokens, n_q_heads, n_kv_heads, head_dim, block_size, max_blocks_per_seq,
+                          scored=True) -> int:
+    n = ctypes.c_size_t()
+    _check(raw().kvc_decode_scored_workspace_size(batch, n_tokens, n_q_heads, n_kv_heads, head_dim, block_size,
+                                                  max_blocks_per_seq, int(bool(scored)), ctypes.byref(n)),
+           "kvc_decode_scored_workspace_size")
+    return n.value
+
+
+def new_scored_workspace(batch, n_tokens, n_q_heads, n_kv_heads, head_dim, block_size, max_blocks_per_seq,
+                         scored=True, device="cuda"):
+    """uint8 workspace for decode_attention_scored and decode_attention_block8 (``scored=False``: for the latter
+    without scores). It need not be cleared; calls that may overlap need one each."""
+    torch = _torch()
+    n = scored_workspace_size(batch, n_tokens, n_q_heads, n_kv_heads, head_dim, block_size, max_blocks_per_seq, scored)
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+
+
+def _decode_scored_args(q, k_cache, v_cache, block_tables, context_lens, out, scores, workspace, more=()):
+    """Checks what the two scored decodes share; returns (B, T, Hq, D, num_blocks, Hkv, bs, max_blocks)."""
+    torch = _torch()
+    nb, hkv, bs, d = _pools(k_cache, v_cache)
+    for t, n in ((q, "q"), (out, "out"), (workspace, "workspace")):
+        _require(t, n)
+    _require(block_tables, "block_tables", torch.int32)
+    _require(context_lens, "context_lens", torch.int32)
+    if q.dim() not in (3, 4) or q.shape[-1] != d or out.shape != q.shape:
+        raise ValueError("q and out must be [batch, n_q_heads, head_dim] or [batch, n_tokens, n_q_heads, head_dim]")
+    B, hq = q.shape[0], q.shape[-2]
+    T = q.shape[1] if q.dim() == 4 else 1
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.numel() != B:
+        raise ValueError("block_tables must be [batch, max_blocks] and context_lens [batch]")
+    mb = block_tables.shape[1]
+    if scores is not None:
+        _require(scores, "scores", torch.float32)
+        if tuple(scores.shape) != (B, hkv, mb * bs):
+            raise ValueError("scores must be [batch, n_kv_heads, max_blocks * block_size]")
+    _same_device(k_cache, (v_cache, q, out, block_tables, context_lens, scores, workspace, *more))
+    return B, T, hq, d, nb, hkv, bs, mb
+
+
+def decode_attention_scored(q, k_cache, v_cache, block_tables, context_lens, scale, out, scores, workspace,
+                            stream=None):
+    """kvc_decode_attention_scored: decode over a 16-bit cache that adds the attention weight of every cached row to
+    ``scores`` fp32 [B, Hkv, max_blocks * bs]. q/out [B, Hq, D], or [B, T, Hq, D] for the T newest rows of every
+    sequence; workspace from new_scored_workspace."""
+    B, T, hq, d, nb, hkv, bs, mb = _decode_scored_args(q, k_cache, v_cache, block_tables, context_lens, out, scores,
+                                                       workspace)
+    if scores is None:
+        raise TypeError("scores must be a tensor")
+    if q.dtype != k_cache.dtype:
+        raise TypeError(f"q must be {k_cache.dtype}, got {q.dtype}")
+    _check(raw().kvc_decode_attention_scored(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), mb,
+                                             _ptr(context_lens), B, T, float(scale), hq, hkv, d, bs, nb,
+                                             _dtype_code(k_cache), _ptr(out), _dtype_code(out), _ptr(scores),
+                                             _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                             _stream(stream)), "kvc_decode_attention_scored")
+
+
+def decode_attention_block8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale, out, workspace,
+                            scores=None, stream=None):
+    """kvc_decode_attention_block8: decode over the block-scaled codes of append_block8. q (f16/bf16) and out
+    [B, Hq, D], or [B, T, Hq, D] for the T newest rows of every sequence; scores as in decode_attention_scored, or
+    None; workspace from new_scored_workspace."""
+    B, T, hq, d, nb, hkv, bs, mb = _decode_scored_args(q, k_cache, v_cache, block_tables, context_lens, out, scores,
+                                                       workspace, (k_scale, v_scale))
+    code = _code_format(k_cache, "k_cache")
+    _block_scales(k_scale, v_scale, nb, hkv)
+    _check(raw().kvc_decode_attention_block8(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), code,
+                                             _ptr(block_tables), mb, _ptr(context_lens), B, T, float(scale), hq, hkv,
+                                             d, bs, nb, _dtype_code(q), _ptr(out), _dtype_code(out), _ptr(scores),
+                                             _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                             _stream(stream)), "kvc_decode_attention_block8")
+
+
+def evict_rows(scores, k_cache, v_cache, block_tables, context_lens, budget, recent, new_block_tables, kept, new_lens,
+               new_scores, k_scale=None, v_scale=None, stream=None):
+    """kvc_evict_rows, or kvc_evict_rows_block8 when the scales of a block-scaled cache are given. Every kv head keeps
+    the newest ``recent`` rows and those with the largest scores, ``budget`` in all, and they move from the blocks of
+    block_tables to those of new_block_tables. scores fp32 [B, Hkv, max_blocks * bs]; written: kept int32
+    [B, Hkv, budget] (old rows, -1 past the end), new_lens int32 [B], new_scores fp32 [B, Hkv, new_max_blocks * bs]."""
+    torch = _torch()
+    nb, hkv, bs, d = _pools(k_cache, v_cache)
+    for t, n in ((block_tables, "block_tables"), (context_lens, "context_lens"),
+                 (new_block_tables, "new_block_tables"), (kept, "kept"), (new_lens, "new_lens")):
+        _require(t, n, torch.int32)
+    _require(scores, "scores", torch.float32)
+    _require(new_scores, "new_scores", torch.float32)
+    if block_tables.dim() != 2 or new_block_tables.dim() != 2:
+        raise ValueError("block_tables and new_block_tables must be [batch, max_blocks]")
+    B, mb = block_tables.shape
+    new_mb = new_block_tables.shape[1]
+    if new_block_tables.shape[0] != B or context_lens.numel() != B or new_lens.numel() != B:
+        raise ValueError("new_block_tables, context_lens and new_lens must have one entry per sequence")
+    if tuple(scores.shape) != (B, hkv, mb * bs) or tuple(new_scores.shape) != (B, hkv, new_mb * bs):
+        raise ValueError("scores and new_scores must be [batch, n_kv_heads, max_blocks * block_size]")
+    if tuple(kept.shape) != (B, hkv, int(budget)):
+        raise ValueError("kept must be [batch, n_kv_heads, budget]")
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale go together")
+    _same_device(k_cache, (v_cache, scores, block_tables, context_lens, new_block_tables, kept, new_lens, new_scores,
+                           k_scale, v_scale))
+    if k_scale is None:
+        _check(raw().kvc_evict_rows(_ptr(scores), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), mb,
+                                    _ptr(context_lens), B, int(budget), int(recent), _ptr(new_block_tables), new_mb, nb,
+                                    bs, hkv, d, _dtype_code(k_cache), _ptr(kept), _ptr(new_lens), _ptr(new_scores),
+                                    _stream(stream)), "kvc_evict_rows")
+        return
+    code = _code_format(k_cache, "k_cache")
+    _block_scales(k_scale, v_scale, nb, hkv)
+    _check(raw().kvc_evict_rows_block8(_ptr(scores), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), code,
+                                       _ptr(block_tables), mb, _ptr(context_lens), B, int(budget), int(recent),
+                                       _ptr(new_block_tables), new_mb, nb, bs, hkv, d, _ptr(kept), _ptr(new_lens),
+                                       _ptr(new_scores), _stream(stream)), "kvc_evict_rows_block8")

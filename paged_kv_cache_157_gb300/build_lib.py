@@ -36,6 +36,13 @@ SOURCES = [
     "decode_gqa_mma_f16.cu",
     "decode_gqa_mma_fp8.cu",
     "decode_gqa_mma_int8.cu",
+    "decode_scored_bf16.cu",
+    "decode_scored_f16.cu",
+    "decode_scored_fp8.cu",
+    "decode_scored_int8.cu",
+    "decode_scored.cu",
+    "append_block.cu",
+    "evict.cu",
     "decode_wide.cu",
     "decode_mla.cu",
     "pool.cpp",

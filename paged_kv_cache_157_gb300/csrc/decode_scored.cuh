@@ -1,0 +1,1026 @@
+// Paged decode attention that also adds up the attention weight each cached
+// row receives, over 16-bit caches and over one-byte caches with one scale per
+// (block, kv head).
+//
+// Mathematics. Query v of a kv head (v = t * group + j: new token t, query
+// head j of the group) attends rows r <= n - n_tok + t:
+//   x_vr = scale * q_v . k_r,  p_vr = exp(x_vr) / sum_r exp(x_vr),
+//   o_v = sum_r p_vr v_r,      score_r += sum_v p_vr
+// with k_r = code * k_scale[block], v_r = code * v_scale[block] for one-byte
+// caches. One pass over the rows with the running maximum and sum of the
+// softmax; the weights of a row are only known once the denominator is, so the
+// pass leaves the scaled scores x (fp32, 4 bytes per query and row against 2 D
+// cache elements) in the workspace, and the finishing kernel, which merges the
+// partial outputs anyway, turns them into weights and adds them up. Reading K
+// a second time instead would cost D elements per row.
+//
+// What bounds it: HBM, for up to about 64 queries per kv head. Every cached
+// row is read once, by TMA, into a ring in shared memory.
+//
+// Work split. The 16-row tiles of all (sequence, kv head, column group) units
+// are laid end to end and cut into equal ranges, one per WARP. A warp is a
+// worker of its own: it issues its copies, waits for them and runs the
+// products, with no barrier between warps, so a unit may have any number of
+// kv heads, any length and any group, and eight workers per SM keep 128 to
+// 192 KB of copies in flight. A worker holds at most two parts of units
+// that other workers share; each leaves one record (maximum, sum, output).
+//
+// Products on m16n8k16 MMAs, rows (or dims) x queries:
+//   S^T [16 rows x 8 queries] = K [16 x D] . Q^T,
+//   O^T [D x 8 queries] += V^T [D x 16 rows] . P^T
+// fp32 accumulation. The weights enter as a sum of 16-bit parts: two f16 parts
+// (22 bits; a weight is at most 2^8, the second part reaches 2^-25) or, for bf16
+// caches, three bf16 parts (24 bits), because fp32 outputs are to be as good
+// as an fp32 softmax; the extra products are hidden behind HBM. One-byte codes
+// are exact f16 values and are converted in registers; queries become f16
+// after a scaling by a power of two that is exact, per query.
+#pragma once
+
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "decode_gqa_mma.cuh"
+#include "decode_scored.h"
+
+namespace kvc {
+
+namespace scored {
+
+// Byte offset of 16-byte chunk q of row r in a box of kBoxBytes-wide rows as
+// TMA leaves it: 128-byte swizzle (q ^ (r & 7)), or 64-byte swizzle
+// (q ^ ((r >> 1) & 3)).
+template <int BOXB>
+__device__ __forceinline__ uint32_t chunk_at(int r, int q) {
+  if constexpr (BOXB == 128) return static_cast<uint32_t>(r * 128 + ((q ^ (r & 7)) << 4));
+  return static_cast<uint32_t>(r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float fast_log2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// State of a segment (one unit's tiles in one worker's range). Lane 4g + c
+// holds queries 2c and 2c + 1 of every group of 8 (index e & 1).
+template <int D, int NT, bool ONE>
+struct State {
+  uint32_t q[NT][D / 16][2];  // Q^T B fragments
+  float o[NT][D / 16][4];     // O^T C fragments
+  float m[NT][2];             // reference maxima (log2 units), equal over g
+  float l[NT][2];             // this lane's sums of weights
+  float mo[ONE ? NT : 1][2];  // one-byte caches: the outputs' reference, max of x + log2(v_scale)
+  float fq[ONE ? NT : 1][2];  // one-byte caches: qscale / the query's power of two
+  int dt[NT][2];              // newest rows the query may not see: n_tok - 1 - t
+};
+
+// Sets x to -inf where the row is not visible. rem: the sequence's rows from
+// the tile's first on.
+template <int D, int NT, bool ONE>
+__device__ __forceinline__ void mask_edge(float (&x)[NT][4], const State<D, NT, ONE>& st, int rem, int g) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int v0 = rem - st.dt[n][0], v1 = rem - st.dt[n][1];
+    if (g >= v0) x[n][0] = kNegInf;
+    if (g >= v1) x[n][1] = kNegInf;
+    if (g + 8 >= v0) x[n][2] = kNegInf;
+    if (g + 8 >= v1) x[n][3] = kNegInf;
+  }
+}
+
+// Moves the references up (all lanes of the warp together) and rescales sums
+// and outputs. lvs: log2 of the tile's V scale (one-byte caches).
+template <int D, int NT, bool ONE>
+__device__ __forceinline__ void raise_references(const float (&x)[NT][4], State<D, NT, ONE>& st, float lvs) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float t[2] = {fmaxf(x[n][0], x[n][2]), fmaxf(x[n][1], x[n][3])};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int msk = 4; msk < 32; msk <<= 1) t[e] = fmaxf(t[e], __shfl_xor_sync(0xffffffffu, t[e], msk));
+    }
+    float a[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float m = fmaxf(st.m[n][e], t[e]);
+      a[e] = fast_exp2(st.m[n][e] - m);
+      st.l[n][e] *= a[e];
+      st.m[n][e] = m;
+      if constexpr (ONE) {
+        const float mo = fmaxf(st.mo[n][e], t[e] + lvs);
+        a[e] = fast_exp2(st.mo[n][e] - mo);
+        st.mo[n][e] = mo;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      st.o[n][i][0] *= a[0];
+      st.o[n][i][1] *= a[1];
+      st.o[n][i][2] *= a[0];
+      st.o[n][i][3] *= a[1];
+    }
+  }
+}
+
+// The weights' B fragments: parts of the 16-bit type whose sum is the fp32
+// weight, transposed from the C fragment [rows][queries] to [rows = k][queries = n].
+template <bool BF, int NT, int NP>
+__device__ __forceinline__ void weight_parts(const float (&w)[NT][4], uint32_t (&b)[NT][NP][2]) {
+  using namespace wmma16;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float r0 = w[n][0], r1 = w[n][1], r2 = w[n][2], r3 = w[n][3];
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const uint32_t h01 = pack2<BF>(r0, r1), h23 = pack2<BF>(r2, r3);
+      b[n][k][0] = movm_t(h01);
+      b[n][k][1] = movm_t(h23);
+      if (k + 1 < NP) {
+        const float2 f01 = unpack2<BF>(h01), f23 = unpack2<BF>(h23);
+        r0 -= f01.x;
+        r1 -= f01.y;
+        r2 -= f23.x;
+        r3 -= f23.y;
+      }
+    }
+  }
+}
+
+// Masks that clear the V rows at and behind rem (they may hold anything, and
+// 0 x NaN is NaN): rows 2c, 2c + 1 and 2c + 8, 2c + 9 of the lane's A fragments.
+__device__ __forceinline__ void keep_masks(int rem, int c, uint32_t& k01, uint32_t& k89) {
+  k01 = (2 * c < rem ? 0x0000ffffu : 0u) | (2 * c + 1 < rem ? 0xffff0000u : 0u);
+  k89 = (2 * c + 8 < rem ? 0x0000ffffu : 0u) | (2 * c + 9 < rem ? 0xffff0000u : 0u);
+}
+
+// Running softmax over one tile: x becomes the weights relative to the
+// references (of the outputs), sums take the weights relative to m.
+template <int D, int NT, bool ONE>
+__device__ __forceinline__ void softmax_step(float (&x)[NT][4], State<D, NT, ONE>& st, float lvs) {
+  bool need = false;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      need |= x[n][e] > st.m[n][e & 1] + 8.0f;
+      if constexpr (ONE) need |= x[n][e] + lvs > st.mo[n][e & 1] + 8.0f;
+    }
+  }
+  // lazy: a reference only moves when a score exceeds it by a factor 2^8
+  if (__any_sync(0xffffffffu, need)) raise_references<D, NT, ONE>(x, st, lvs);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float p = fast_exp2(x[n][e] - st.m[n][e & 1]);
+      st.l[n][e & 1] += p;
+      // one-byte caches: p * v_scale / 2^(mo - m), from its own exponent so
+      // that neither factor can leave the range of fp32
+      x[n][e] = ONE ? fast_exp2(x[n][e] + lvs - st.mo[ONE ? n : 0][e & 1]) : p;
+    }
+  }
+}
+
+// One 16-row tile of a 16-bit cache. k, v: the tile's boxes.
+template <bool BF, int D, int NT, bool EDGE>
+__device__ __forceinline__ void tile16(uint32_t k, uint32_t v, int rem, float qscale, float* lg, int qns, int col0,
+                                       int qn, State<D, NT, false>& st, int lane) {
+  using namespace wmma16;
+  constexpr int NP = BF ? 3 : 2;
+  constexpr int CH = NT == 1 ? 4 : 2;  // independent accumulator chains
+  constexpr uint32_t BOX = kTileRows * 128;
+  const int g = lane >> 2, c = lane & 3;
+  const int sw = lane & 7, s2 = sw >> 1;
+  float x[NT][4];
+  {
+    float sc[NT][CH][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[n][j][e] = 0.f;
+    // lane l addresses row (l & 7) + 8 ((l >> 3) & 1), dims chunk 2 ks + (l >> 4)
+    const uint32_t row = k + static_cast<uint32_t>(((lane & 7) + ((lane >> 3) & 1) * 8) * 128) +
+                         static_cast<uint32_t>((((lane >> 4) ^ sw) & 1) << 4);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint32_t a[4];
+      ldsm_x4(row + (ks >> 2) * BOX + static_cast<uint32_t>(((ks & 3) ^ s2) << 5), a);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma<BF>(sc[n][ks % CH], a, st.q[n][ks][0], st.q[n][ks][1]);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float s = sc[n][0][e] + sc[n][1][e];
+        if constexpr (CH == 4) s += sc[n][2][e] + sc[n][3][e];
+        x[n][e] = s * qscale;
+      }
+    }
+  }
+  if constexpr (EDGE) mask_edge<D, NT, false>(x, st, rem, g);
+  if (lg != nullptr) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int col = col0 + 8 * n + 2 * c;
+      if (col < qn) {
+        float* at = lg + static_cast<int64_t>(g) * qns + col;
+        if (!EDGE || g < rem) *reinterpret_cast<float2*>(at) = make_float2(x[n][0], x[n][1]);
+        if (!EDGE || g + 8 < rem) *reinterpret_cast<float2*>(at + 8 * qns) = make_float2(x[n][2], x[n][3]);
+      }
+    }
+  }
+  softmax_step<D, NT, false>(x, st, 0.f);
+  uint32_t b[NT][NP][2];
+  weight_parts<BF, NT, NP>(x, b);
+  uint32_t k01 = 0, k89 = 0;
+  if constexpr (EDGE) keep_masks(rem, c, k01, k89);
+  // lane l addresses row (l & 7) + 8 (l >> 4), dims chunk 2 i + ((l >> 3) & 1)
+  const uint32_t row = v + static_cast<uint32_t>(((lane & 7) + (lane >> 4) * 8) * 128) +
+                       static_cast<uint32_t>(((((lane >> 3) & 1) ^ sw) & 1) << 4);
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    uint32_t a[4];
+    ldsm_x4_t(row + (i >> 2) * BOX + static_cast<uint32_t>(((i & 3) ^ s2) << 5), a);
+    if constexpr (EDGE) {
+      a[0] &= k01;
+      a[1] &= k01;
+      a[2] &= k89;
+      a[3] &= k89;
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < NP; ++j) mma<BF>(st.o[n][i], a, b[n][j][0], b[n][j][1]);
+  }
+}
+
+// One 16-row tile of a one-byte cache (Q8 1: e4m3, 2: int8) whose block has
+// the scales ks and vs.
+//
+// The order of the dims inside a product is free, so a lane takes whole
+// 16-byte chunks: for S, lane 4g + c takes dims [D/4 of each 128] of rows g and
+// g + 8 (k-step s uses 4 bytes: the MMA's k-columns 2c, 2c + 1, 2c + 8, 2c + 9);
+// for PV, dims 16g .. 16g + 15 of every 128 (8g .. 8g + 7 of 64) of rows
+// 2c, 2c + 1, 2c + 8, 2c + 9, and a byte permute pairs two rows of one dim. Output
+// tile i of a span then holds its dims 16g + 2i and 16g + 2i + 1 (8g + 2i).
+template <int Q8, int D, int NT, bool EDGE>
+__device__ __forceinline__ void tile8(uint32_t k, uint32_t v, int rem, float ks, float vs, float* lg, int qns,
+                                      int col0, int qn, State<D, NT, true>& st, int lane) {
+  using namespace wmma16;
+  constexpr int NP = 2;
+  constexpr int CH = NT == 1 ? 4 : 2;
+  constexpr int BOXB = D < 128 ? D : 128;
+  constexpr int SPANS = D / BOXB;
+  constexpr int KS = BOXB / 16;  // k-steps (and output tiles) per span
+  constexpr uint32_t BOX = kTileRows * BOXB;
+  const int g = lane >> 2, c = lane & 3;
+  float x[NT][4];
+  {
+    float sc[NT][CH][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[n][j][e] = 0.f;
+#pragma unroll
+    for (int sp = 0; sp < SPANS; ++sp) {
+      uint32_t kw[2][KS];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < KS / 4; ++j) {
+          const uint4 u = lds128(k + sp * BOX + chunk_at<BOXB>(g + 8 * h, (KS / 4) * c + j));
+          kw[h][4 * j] = u.x;
+          kw[h][4 * j + 1] = u.y;
+          kw[h][4 * j + 2] = u.z;
+          kw[h][4 * j + 3] = u.w;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        uint32_t a[4];
+        codes_to_f16x2<Q8>(kw[0][s], a[0], a[2]);
+        codes_to_f16x2<Q8>(kw[1][s], a[1], a[3]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma<false>(sc[n][s % CH], a, st.q[n][sp * KS + s][0], st.q[n][sp * KS + s][1]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float s = sc[n][0][e] + sc[n][1][e];
+        if constexpr (CH == 4) s += sc[n][2][e] + sc[n][3][e];
+        x[n][e] = s * (st.fq[n][e & 1] * ks);
+      }
+    }
+  }
+  if constexpr (EDGE) mask_edge<D, NT, true>(x, st, rem, g);
+  if (lg != nullptr) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int col = col0 + 8 * n + 2 * c;
+      if (col < qn) {
+        float* at = lg + static_cast<int64_t>(g) * qns + col;
+        if (!EDGE || g < rem) *reinterpret_cast<float2*>(at) = make_float2(x[n][0], x[n][1]);
+        if (!EDGE || g + 8 < rem) *reinterpret_cast<float2*>(at + 8 * qns) = make_float2(x[n][2], x[n][3]);
+      }
+    }
+  }
+  softmax_step<D, NT, true>(x, st, fast_log2(vs));
+  uint32_t b[NT][NP][2];
+  weight_parts<false, NT, NP>(x, b);
+  uint32_t k01 = 0, k89 = 0;
+  if constexpr (EDGE) keep_masks(rem, c, k01, k89);
+#pragma unroll
+  for (int sp = 0; sp < SPANS; ++sp) {
+    uint32_t vw[4][KS / 2];  // rows 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = 2 * c + (j & 1) + 8 * (j >> 1);
+      if constexpr (BOXB == 128) {
+        const uint4 u = lds128(v + sp * BOX + chunk_at<BOXB>(r, g));
+        vw[j][0] = u.x;
+        vw[j][1] = u.y;
+        vw[j][2] = u.z;
+        vw[j][3] = u.w;
+      } else {
+        const uint2 u = lds64(v + chunk_at<BOXB>(r, g >> 1) + 8 * (g & 1));
+        vw[j][0] = u.x;
+        vw[j][1] = u.y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      // bytes 2 (i & 1) and + 1 of word i >> 1 of two rows, interleaved
+      const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
+      uint32_t a[4];
+      codes_to_f16x2<Q8>(__byte_perm(vw[0][i >> 1], vw[1][i >> 1], sel), a[0], a[1]);
+      codes_to_f16x2<Q8>(__byte_perm(vw[2][i >> 1], vw[3][i >> 1], sel), a[2], a[3]);
+      if constexpr (EDGE) {
+        a[0] &= k01;
+        a[1] &= k01;
+        a[2] &= k89;
+        a[3] &= k89;
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < NP; ++j) mma<false>(st.o[n][sp * KS + i], a, b[n][j][0], b[n][j][1]);
+    }
+  }
+}
+
+// The MMA column (query) g of column group n: its row of q and whether it exists.
+__device__ __forceinline__ int64_t query_row(const ScoredParams& p, int seq, int kvh, int v) {
+  const int t = v / p.group;
+  return (static_cast<int64_t>(seq) * p.n_tok + t) * p.n_q_heads + kvh * p.group + (v - t * p.group);
+}
+
+// Rows of a sequence that are cached, 0 if its length is invalid.
+__device__ __forceinline__ int valid_rows(const ScoredParams& p, int b) {
+  const int n = __ldg(p.context_lens + b);
+  return (n < p.n_tok || n > p.rows) ? 0 : n;
+}
+
+__device__ __forceinline__ int tiles_of(int rows) { return (rows + kTileRows - 1) / kTileRows; }
+
+// Exclusive prefix sums of the sequences' tiles into s_scan[0 .. batch]; the
+// whole CTA takes part. s_scan has batch + 33 entries.
+__device__ inline void scan_tiles(const ScoredParams& p, int* s_scan) {
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wid = tid >> 5, B = p.batch;
+  const int per = (B + nt - 1) / nt;
+  const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  int local = 0;
+  for (int b = b0; b < b1; ++b) local += tiles_of(valid_rows(p, b));
+  int v = local;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  int* wsum = s_scan + B + 1;
+  if (lane == 31) wsum[wid] = v;
+  __syncthreads();
+  int run = v - local;
+  for (int i = 0; i < wid; ++i) run += wsum[i];
+  for (int b = b0; b < b1; ++b) {
+    s_scan[b] = run;
+    run += tiles_of(valid_rows(p, b));
+    if (b == B - 1) s_scan[B] = run;
+  }
+  __syncthreads();
+}
+
+// The unit of global tile `pos`.
+struct Unit {
+  int64_t u0;  // its first tile
+  int seq, kvh, hsub, tiles;
+};
+
+__device__ __forceinline__ Unit locate(int64_t pos, const ScoredParams& p, const int* s_scan) {
+  const int64_t HN = static_cast<int64_t>(p.n_kv_heads) * p.n_hsub;
+  int a = 0, hi = p.batch - 1;  // the last sequence whose first tile is <= pos (skips empty ones)
+  while (a < hi) {
+    const int mid = (a + hi + 1) >> 1;
+    if (HN * s_scan[mid] <= pos) a = mid; else hi = mid - 1;
+  }
+  Unit u;
+  u.seq = a;
+  u.tiles = s_scan[a + 1] - s_scan[a];
+  const int64_t first = HN * s_scan[a];
+  const int idx = static_cast<int>((pos - first) / u.tiles);
+  u.kvh = idx / p.n_hsub;
+  u.hsub = idx - u.kvh * p.n_hsub;
+  u.u0 = first + static_cast<int64_t>(idx) * u.tiles;
+  return u;
+}
+
+}  // namespace scored
+
+template <typename CT, int D, int NT>
+__global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D>::kThreads, 1)
+    scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const ScoredParams p) {
+  using namespace scored;
+  constexpr bool ONE = sizeof(CT) == 1;
+  constexpr bool BF = std::is_same<CT, __nv_bfloat16>::value;
+  constexpr int Q8 = std::is_same<CT, fp8e4m3>::value ? 1 : 2;
+  using G = ScoredGeo<sizeof(CT), D>;
+  constexpr int TS = G::kStageTiles, S = G::kStages, W = G::kWarps, NC = 8 * NT;
+  constexpr uint32_t full = 0xffffffffu;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char* smem = smem_raw + (base - raw);
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + G::kRingBytes) + w * S;
+  float* s_scale = reinterpret_cast<float*>(smem + G::kRingBytes + W * S * 8) + w * S * TS * 2;
+  int* s_scan = reinterpret_cast<int*>(smem + G::kRingBytes + W * S * 8 + W * S * TS * 2 * 4);
+  const uint32_t ring = base + static_cast<uint32_t>(w * S * G::kStageBytes);
+
+  if (lane < S) mbar_init(bars + lane, 1);
+  fence_barrier_init();
+  if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
+  }
+  // The kernel may start while the stream's previous one runs; nothing of the
+  // caller's is read or written before that one has ended.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  scan_tiles(p, s_scan);  // ends with a CTA barrier
+
+  // Sequences of invalid length: flagged, their units marked for zero outputs.
+  for (int b = blockIdx.x * blockDim.x + tid; b < p.batch; b += gridDim.x * blockDim.x) {
+    if (s_scan[b + 1] == s_scan[b]) {
+      set_flag(p.err, KVC_FLAG_BAD_LEN);
+      const int HN = p.n_kv_heads * p.n_hsub;
+      for (int i = 0; i < HN; ++i) p.units[static_cast<int64_t>(b) * HN + i] = make_int4(kUnitEmpty, 0, 0, 0);
+    }
+  }
+
+  const int64_t N = static_cast<int64_t>(p.n_kv_heads) * p.n_hsub * s_scan[p.batch];
+  const int64_t most = (N + p.min_tiles - 1) / p.min_tiles;
+  const int64_t We = most < p.workers ? most : p.workers;
+  // consecutive workers sit on different SMs, so that few workers spread out
+  const int64_t wk = static_cast<int64_t>(w) * gridDim.x + blockIdx.x;
+  if (wk >= We) return;
+  const int64_t lo = wk * N / We, hi = (wk + 1) * N / We;
+  const int tpb = p.block_size / kTileRows;  // tiles per cache block
+  const uint64_t pol = policy_evict_first();
+
+  // ---- copies: the next tiles of the range into the next stage
+  int64_t ipos = lo, iend = lo;
+  int ij = 0, iseq = 0, ikvh = 0, wb = 0, tw = -1;
+  uint32_t islot = 0, ivalid = 0;  // ivalid: bit slot * TS + t: the tile's block is inside the pool
+  int issued = 0;
+  auto issue = [&]() {
+    if (ipos < hi) {
+      if (ipos >= iend) {
+        const Unit u = locate(ipos, p, s_scan);
+        iseq = u.seq;
+        ikvh = u.kvh;
+        ij = static_cast<int>(ipos - u.u0);
+        iend = u.u0 + u.tiles < hi ? u.u0 + u.tiles : hi;
+        wb = -64;  // no entries yet
+      }
+      const int cnt = iend - ipos < TS ? static_cast<int>(iend - ipos) : TS;
+      const int b_last = (ij + cnt - 1) / tpb;
+      if (b_last >= wb + 32) {  // lane i holds the table's entry wb + i
+        wb = ij / tpb;
+        tw = wb + lane < p.max_blocks ? __ldg(p.block_tables + static_cast<int64_t>(iseq) * p.max_blocks + wb + lane)
+                                      : -1;
+      }
+      // lane i copies box i: [tile][K or V][half]
+      constexpr int PER = 2 * G::kHalves;
+      const int t = lane / PER < cnt ? lane / PER : 0;
+      const int jt = ij + t, blk = jt / tpb;
+      const int phys = __shfl_sync(full, tw, blk - wb);
+      const bool ok = phys >= 0 && phys < p.num_blocks;
+      uint32_t mask = 0;
+#pragma unroll
+      for (int i = 0; i < TS; ++i)
+        if (i < cnt) mask |= (__shfl_sync(full, ok ? 1u : 0u, i * PER)) << i;
+      ivalid = (ivalid & ~(((1u << TS) - 1u) << (islot * TS))) | (mask << (islot * TS));
+      uint64_t* bar = bars + islot;
+      if (lane == 0) {
+        if (mask == 0)
+          mbar_arrive(bar);
+        else
+          mbar_arrive_expect_tx(bar, __popc(mask) * 2 * G::kTileBytes);
+        if (__popc(mask) != cnt) set_flag(p.err, KVC_FLAG_BAD_BLOCK);
+      }
+      __syncwarp();
+      if (lane < PER * cnt && ok) {
+        const int kv = (lane % PER) / G::kHalves, half = lane % G::kHalves;
+        const int y = (phys * p.n_kv_heads + ikvh) * p.block_size + (jt - blk * tpb) * kTileRows;
+        const uint32_t dst = ring + islot * G::kStageBytes + (t * 2 + kv) * G::kTileBytes +
+                             half * (kTileRows * G::kBoxBytes);
+        wmma16::tma2d(dst, kv == 0 ? &tm_k : &tm_v, half * (G::kBoxBytes / static_cast<int>(sizeof(CT))), y,
+                      smem_addr(bar), pol);
+      }
+      if constexpr (ONE) {
+        // lane i copies scale i: [tile][K or V]
+        const int t2 = (lane >> 1) < cnt ? lane >> 1 : 0;
+        const int phys2 = __shfl_sync(full, tw, (ij + t2) / tpb - wb);
+        if (lane < 2 * cnt && phys2 >= 0 && phys2 < p.num_blocks)
+          cp_async4(smem_addr(s_scale + (islot * TS + t2) * 2 + (lane & 1)),
+                    ((lane & 1) ? p.v_scale : p.k_scale) + static_cast<int64_t>(phys2) * p.n_kv_heads + ikvh);
+      }
+      ipos += cnt;
+      ij += cnt;
+      ++issued;
+      islot = islot + 1 == S ? 0 : islot + 1;
+    }
+    if constexpr (ONE) cp_async_commit();  // one group per call, whether or not it copied
+  };
+  for (int i = 0; i < S; ++i) issue();
+
+  // ---- products
+  uint32_t slot = 0, ph = 0;
+  int used = 0;
+  bool ok = true;
+  const int lanes_g = lane >> 2, c = lane & 3;
+  for (int64_t pos = lo; ok && pos < hi;) {
+    const Unit u = locate(pos, p, s_scan);
+    const int64_t end = u.u0 + u.tiles < hi ? u.u0 + u.tiles : hi;
+    const int n_rows = valid_rows(p, u.seq);
+    const int col0 = u.hsub * NC;
+    State<D, NT, ONE> st;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      // ---- Q^T fragments of query g (columns past the last query: zeros)
+      const int v = col0 + 8 * n + lanes_g;
+      const bool have = v < p.qn;
+      const unsigned short* qr =
+          static_cast<const unsigned short*>(p.q) + (have ? query_row(p, u.seq, u.kvh, v) * D : 0);
+      if constexpr (!ONE) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            st.q[n][ks][h] = have ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * ks + 8 * h + 2 * c)) : 0u;
+        }
+      } else {
+        // dims of lane c, k-step s of a span: 4 s .. 4 s + 3 of its part; scaled
+        // by 2^t so that the query's largest entry lies in [2^14, 2^15): exact
+        // in f16 but for entries below 2^-39 of the largest
+        constexpr int BOXB = D < 128 ? D : 128;
+        constexpr int KS = BOXB / 16;
+        float y[D / 16][4];
+        float amax = 0.f;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const int d = (s / KS) * BOXB + (BOXB / 4) * c + 4 * (s % KS);
+          uint2 u2 = make_uint2(0u, 0u);
+          if (have) u2 = __ldg(reinterpret_cast<const uint2*>(qr + d));
+          float2 a, b;
+          if (p.q_f16) {
+            a = wmma16::unpack2<false>(u2.x);
+            b = wmma16::unpack2<false>(u2.y);
+          } else {
+            a = wmma16::unpack2<true>(u2.x);
+            b = wmma16::unpack2<true>(u2.y);
+          }
+          y[s][0] = a.x;
+          y[s][1] = a.y;
+          y[s][2] = b.x;
+          y[s][3] = b.y;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(y[s][e]));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(full, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(full, amax, 2));
+        const int field = min(253, max(1, 268 - static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu)));
+        const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
+        const float down = p.qscale * __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          st.q[n][s][0] = wmma16::pack2<false>(y[s][0] * up, y[s][1] * up);
+          st.q[n][s][1] = wmma16::pack2<false>(y[s][2] * up, y[s][3] * up);
+        }
+        st.fq[n][0] = __shfl_sync(full, down, 8 * c);      // of query 2c, held by the lanes with g = 2c
+        st.fq[n][1] = __shfl_sync(full, down, 8 * c + 4);  // of query 2c + 1
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        st.m[n][e] = -1e30f;  // finite: a query that meets only masked rows keeps weight 0
+        st.l[n][e] = 0.f;
+        if constexpr (ONE) st.mo[n][e] = -1e30f;
+        const int t = (col0 + 8 * n + 2 * c + e) / p.group;
+        st.dt[n][e] = t < p.n_tok ? p.n_tok - 1 - t : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.o[n][i][e] = 0.f;
+      }
+    }
+    float* lg0 = p.scores == nullptr
+                     ? nullptr
+                     : p.logits + (static_cast<int64_t>(u.seq) * p.n_kv_heads + u.kvh) * p.rows * p.qns;
+    int j = static_cast<int>(pos - u.u0);
+    while (pos < end) {
+      const int cnt = end - pos < TS ? static_cast<int>(end - pos) : TS;
+      ok = mbar_wait_data(bars + slot, ph, p.wait_polls);
+      ok = __all_sync(full, ok);
+      if (!ok) break;
+      if constexpr (ONE) {
+        cp_async_wait<S - 1>();
+        __syncwarp();
+      }
+#pragma unroll 1
+      for (int t = 0; t < cnt; ++t) {
+        const int r0 = (j + t) * kTileRows;
+        const int rem = n_rows - r0;
+        float* lg = lg0 == nullptr ? nullptr : lg0 + static_cast<int64_t>(r0) * p.qns;
+        const uint32_t kt = ring + slot * G::kStageBytes + t * 2 * G::kTileBytes, vt = kt + G::kTileBytes;
+        if ((ivalid >> (slot * TS + t)) & 1u) {
+          const bool edge = rem < kTileRows + p.n_tok - 1;
+          if constexpr (ONE) {
+            const float ks = s_scale[(slot * TS + t) * 2], vs = s_scale[(slot * TS + t) * 2 + 1];
+            if (edge)
+              tile8<Q8, D, NT, true>(kt, vt, rem, ks, vs, lg, p.qns, col0, p.qn, st, lane);
+            else
+              tile8<Q8, D, NT, false>(kt, vt, rem, ks, vs, lg, p.qns, col0, p.qn, st, lane);
+          } else {
+            if (edge)
+              tile16<BF, D, NT, true>(kt, vt, rem, p.qscale, lg, p.qns, col0, p.qn, st, lane);
+            else
+              tile16<BF, D, NT, false>(kt, vt, rem, p.qscale, lg, p.qns, col0, p.qn, st, lane);
+          }
+        } else if (lg != nullptr) {  // a block outside the pool: its rows get no weight
+          const int cols = min(NC, p.qns - col0);
+          for (int i = lane; i < min(rem, kTileRows) * cols; i += 32)
+            lg[static_cast<int64_t>(i / cols) * p.qns + col0 + i % cols] = kNegInf;
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      slot = slot + 1 == S ? 0 : slot + 1;
+      if (slot == 0) ph ^= 1u;
+      ++used;
+      pos += cnt;
+      j += cnt;
+      issue();
+    }
+    if (!ok) break;
+
+    // ---- close the segment
+    const int64_t begin = u.u0 > lo ? u.u0 : lo;
+    const bool whole = begin == u.u0 && pos == u.u0 + u.tiles;
+    const int64_t unit = (static_cast<int64_t>(u.seq) * p.n_kv_heads + u.kvh) * p.n_hsub + u.hsub;
+    const int64_t rec = 2 * wk + (begin == lo ? 0 : 1);
+    if (lane == 0 && begin == u.u0) {
+      const int64_t c1 = whole ? wk : ((u.u0 + u.tiles) * We - 1) / N;  // the worker that holds the last tile
+      p.units[unit] = make_int4(whole ? kUnitWhole : static_cast<int>(rec), static_cast<int>(wk + 1),
+                                static_cast<int>(c1), 0);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = st.l[n][e];
+#pragma unroll
+        for (int msk = 4; msk < 32; msk <<= 1) l += __shfl_xor_sync(full, l, msk);
+        const int col = 8 * n + 2 * c + e, v = col0 + col;
+        if (v >= p.qn) continue;
+        float f = 1.f;
+        if constexpr (ONE) f = fast_exp2(st.mo[n][e] - st.m[n][e]);
+        // dims of the lane's values: 16-bit caches 16 i + g (+ 8), one-byte
+        // caches [span] + (span / 8) g + 2 i (+ 1)
+        constexpr int BOXB = D < 128 ? D : 128;
+        constexpr int KS = BOXB / 16;
+        auto dim = [&](int i) {
+          return ONE ? (i / KS) * BOXB + (BOXB / 8) * lanes_g + 2 * (i % KS) : 16 * i + lanes_g;
+        };
+        constexpr int SECOND = ONE ? 1 : 8;
+        if (whole) {
+          const int64_t row = query_row(p, u.seq, u.kvh, v);
+          const float inv = l == 0.f ? 0.f : f / l;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            store_out(p.out, row * D + dim(i), st.o[n][i][e] * inv, p.out_dtype);
+            store_out(p.out, row * D + dim(i) + SECOND, st.o[n][i][e + 2] * inv, p.out_dtype);
+          }
+          if (p.scores != nullptr && lanes_g == 0) p.lse[row] = st.m[n][e] + fast_log2(l);
+        } else {
+          float* ro = p.rec_o + (rec * NC + col) * D;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            ro[dim(i)] = st.o[n][i][e] * f;
+            ro[dim(i) + SECOND] = st.o[n][i][e + 2] * f;
+          }
+          if (lanes_g == 0)
+            *reinterpret_cast<float2*>(p.rec_ml + (rec * NC + col) * 2) = make_float2(st.m[n][e], l);
+        }
+      }
+    }
+  }
+  if (!ok) {
+    // Gave up: report it and wait (bounded) for this warp's own copies still in
+    // flight, so that shared memory is not reused under them.
+    if (lane == 0) set_flag(p.err, KVC_FLAG_TIMEOUT);
+    for (; used < issued; ++used) {
+      (void)mbar_wait_bounded(bars + slot, ph);
+      slot = slot + 1 == S ? 0 : slot + 1;
+      if (slot == 0) ph ^= 1u;
+    }
+  }
+  if constexpr (ONE) cp_async_wait<0>();
+}
+
+// ------------------------------------------------------------------ finish
+//
+// One grid column (blockIdx.x) per unit of (sequence, kv head), gridDim.y CTAs
+// each. They share the unit's queries: o_v = sum_r 2^(m_r - M) O_r / sum_r
+// 2^(m_r - M) l_r over the records r of v, one warp per query while there are
+// few records and the whole CTA otherwise; and its rows: score += sum_v
+// 2^(x - lse_v), lanes over the queries of a row, in a fixed order. Bound by
+// the scores' and logits' bytes (which mostly sit in L2) and, for small calls,
+// by three dependent loads.
+constexpr int kFinishThreads = 256;
+constexpr int kFinishRows = 512;  // cached rows per step of a CTA
+constexpr int kFewRecords = 8;
+
+// Records of a query's unit: first slot, then 2 a, 2 (a + 1), ... (n in all).
+struct RecList {
+  int first, a, n;
+};
+__device__ __forceinline__ RecList record_list(const int4 u, int workers) {
+  RecList r;
+  r.first = u.x;
+  r.a = u.y;
+  r.n = 0;
+  // entries outside the workspace (left by a call that gave up) are not followed
+  if (u.x >= 0 && u.x < 2 * workers && u.y >= 0 && u.z >= u.y - 1 && u.z < workers) r.n = u.z - u.y + 2;
+  return r;
+}
+__device__ __forceinline__ int64_t record_slot(const RecList& r, int i) {
+  return i == 0 ? r.first : 2 * static_cast<int64_t>(r.a + i - 1);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kFinishThreads) scored_finish_kernel(const ScoredParams p, int NC) {
+  using namespace scored;
+  constexpr int V = D / 32;  // output dims per lane
+  extern __shared__ float s_lse[];  // [qn]
+  __shared__ float s_m[8], s_l[8], s_o[8][D];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int64_t pair = blockIdx.x;
+  const int seq = static_cast<int>(pair / p.n_kv_heads), kvh = static_cast<int>(pair % p.n_kv_heads);
+  const int4* units = p.units + pair * p.n_hsub;
+  auto store = [&](int v, const float (&o)[V], float inv) {
+    float val[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) val[i] = o[i] * inv;
+    store_out_vec<V>(p.out, query_row(p, seq, kvh, v) * D + V * lane, val, p.out_dtype);
+  };
+
+  // ---- outputs, one warp per query
+  for (int v = blockIdx.y * 8 + w; v < p.qn; v += gridDim.y * 8) {
+    const int4 u = units[v / NC];
+    const int col = v % NC;
+    float o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = 0.f;
+    if (u.x == kUnitEmpty) {
+      store(v, o, 0.f);
+      continue;
+    }
+    const RecList r = record_list(u, p.workers);
+    if (r.n == 0 || r.n > kFewRecords) continue;
+    float m = kNegInf, l = 0.f;
+    if (lane < r.n) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.rec_ml + (record_slot(r, lane) * NC + col) * 2);
+      m = ml.x;
+      l = ml.y;
+    }
+    const float M = warp_max(m);
+    const float f = lane < r.n ? fast_exp2(m - M) : 0.f;
+    const float L = warp_sum(f * l);
+    for (int i = 0; i < r.n; ++i) {
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      const float* ro = p.rec_o + (record_slot(r, i) * NC + col) * D + V * lane;
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] += fi * ro[k];
+    }
+    store(v, o, L == 0.f ? 0.f : 1.0f / L);
+  }
+  // ---- outputs of units with many records, the whole CTA per query
+  for (int v = blockIdx.y; v < p.qn; v += gridDim.y) {
+    const RecList r = record_list(units[v / NC], p.workers);
+    if (r.n <= kFewRecords) continue;
+    const int col = v % NC;
+    float m = kNegInf, l = 0.f;  // online over this warp's records, lanes over the dims
+    float o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = 0.f;
+    for (int i = w; i < r.n; i += 8) {
+      const int64_t at = record_slot(r, i) * NC + col;
+      const float2 ml = *reinterpret_cast<const float2*>(p.rec_ml + at * 2);
+      const float M = fmaxf(m, ml.x);
+      const float a = fast_exp2(m - M), b = fast_exp2(ml.x - M);
+      m = M;
+      l = l * a + ml.y * b;
+      const float* ro = p.rec_o + at * D + V * lane;
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] = o[k] * a + ro[k] * b;
+    }
+    __syncthreads();
+    if (lane == 0) {
+      s_m[w] = m;
+      s_l[w] = l;
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) s_o[w][V * lane + k] = o[k];
+    __syncthreads();
+    if (w == 0) {
+      float M = kNegInf, L = 0.f;
+      for (int i = 0; i < 8; ++i) M = fmaxf(M, s_m[i]);
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] = 0.f;
+      for (int i = 0; i < 8; ++i) {
+        const float b = fast_exp2(s_m[i] - M);  // r.n > 8: every warp had a record
+        L += s_l[i] * b;
+#pragma unroll
+        for (int k = 0; k < V; ++k) o[k] += s_o[i][V * lane + k] * b;
+      }
+      store(v, o, L == 0.f ? 0.f : 1.0f / L);
+    }
+  }
+  if (p.scores == nullptr) return;
+  const int n = valid_rows(p, seq);
+  if (static_cast<int>(blockIdx.y) * kFinishRows >= n) return;
+
+  // ---- log2 of the queries' softmax denominators: a thread per query with
+  // few records, a warp per query with many
+  for (int v = tid; v < p.qn; v += kFinishThreads) {
+    const int4 u = units[v / NC];
+    float lse = kNegInf;
+    if (u.x == kUnitWhole) {
+      lse = p.lse[query_row(p, seq, kvh, v)];
+    } else {
+      const RecList r = record_list(u, p.workers);
+      if (r.n > kFewRecords) continue;
+      float m = kNegInf, l = 0.f;
+      for (int i = 0; i < r.n; ++i) {
+        const float2 ml = *reinterpret_cast<const float2*>(p.rec_ml + (record_slot(r, i) * NC + v % NC) * 2);
+        const float M = fmaxf(m, ml.x);
+        l = l * fast_exp2(m - M) + ml.y * fast_exp2(ml.x - M);
+        m = M;
+      }
+      if (r.n > 0) lse = m + fast_log2(l);
+    }
+    s_lse[v] = lse == kNegInf ? -kNegInf : lse;  // no weight at all: 2^(x - inf) = 0
+  }
+  for (int v = w; v < p.qn; v += 8) {
+    const RecList r = record_list(units[v / NC], p.workers);
+    if (r.n <= kFewRecords) continue;
+    float m = kNegInf, l = 0.f;
+    for (int i = lane; i < r.n; i += 32) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.rec_ml + (record_slot(r, i) * NC + v % NC) * 2);
+      const float M = fmaxf(m, ml.x);
+      l = l * fast_exp2(m - M) + ml.y * fast_exp2(ml.x - M);
+      m = M;
+    }
+    const float M = warp_max(m);
+    const float L = warp_sum(m == kNegInf ? 0.f : l * fast_exp2(m - M));
+    const float lse = M + fast_log2(L);
+    if (lane == 0) s_lse[v] = lse == kNegInf ? -kNegInf : lse;
+  }
+  __syncthreads();
+
+  // ---- rows: sub lanes per row, each over pairs of queries
+  const int pairs = p.qns / 2;
+  int sub = 1;
+  while (sub < 32 && sub < pairs) sub *= 2;
+  const int per = kFinishThreads / sub;  // rows per pass
+  const int sl = tid % sub;
+  const float* lg = p.logits + pair * p.rows * p.qns;
+  float* sc = p.scores + pair * p.rows;
+  for (int r0 = blockIdx.y * kFinishRows; r0 < n; r0 += gridDim.y * kFinishRows) {
+    const int r1 = min(n, r0 + kFinishRows);
+    for (int rb = r0; rb < r1; rb += per) {
+      const int r = rb + tid / sub;
+      float s = 0.f;
+      if (r < r1) {
+        const float2* row = reinterpret_cast<const float2*>(lg + static_cast<int64_t>(r) * p.qns);
+        for (int k = sl; k < pairs; k += sub) {
+          const float2 x = __ldcg(row + k);
+          s += fast_exp2(x.x - s_lse[2 * k]);
+          if (2 * k + 1 < p.qn) s += fast_exp2(x.y - s_lse[2 * k + 1]);
+        }
+      }
+      for (int o = sub / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+      // the call's own rows are new: their weight starts here
+      if (r < r1 && sl == 0) sc[r] = r < n - p.n_tok ? sc[r] + s : s;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ launch
+
+namespace scored {
+
+template <typename CT, int D, int NT>
+kvc_status run(const ScoredParams& p, int grid, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
+  using G = ScoredGeo<sizeof(CT), D>;
+  auto* k = scored_decode_kernel<CT, D, NT>;
+  // The opt-in to large shared memory holds per device: made at the first call on each.
+  static std::atomic<uint64_t> opted{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if ((opted.load() & bit) == 0) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(scored_smem_bytes<sizeof(CT), D>(kScoredMaxBatch)));
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(scored decode)");
+    opted.fetch_or(bit);
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(G::kThreads);
+  cfg.dynamicSmemBytes = scored_smem_bytes<sizeof(CT), D>(p.batch);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, k, tk, tv, p);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx(scored decode)");
+  // CTAs per (sequence, kv head): enough to fill the GPU, no more than there is work for
+  const int64_t pairs = static_cast<int64_t>(p.batch) * p.n_kv_heads;
+  const int64_t want = (8 * 152 + pairs - 1) / pairs;
+  int64_t most = (p.qn + 7) / 8;
+  if (grid > 1 && p.qn > most) most = p.qn;
+  if (p.scores != nullptr) most = std::max<int64_t>(most, (p.rows + kFinishRows - 1) / kFinishRows);
+  cudaLaunchConfig_t fin = {};
+  fin.gridDim = dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(std::max<int64_t>(1, std::min(want, most))));
+  fin.blockDim = dim3(kFinishThreads);
+  fin.dynamicSmemBytes = p.scores != nullptr ? static_cast<size_t>(p.qn) * 4 : 0;
+  fin.stream = stream;
+  fin.attrs = attr;
+  fin.numAttrs = 1;
+  e = cudaLaunchKernelEx(&fin, scored_finish_kernel<D>, p, 8 * NT);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx(scored finish)");
+  return KVC_OK;
+}
+
+}  // namespace scored
+
+template <typename CT>
+kvc_status scored_launch(const ScoredParams& p, int D, int nt, int grid, const CUtensorMap& tk, const CUtensorMap& tv,
+                         cudaStream_t stream) {
+  if (D == 64 && nt == 1) return scored::run<CT, 64, 1>(p, grid, tk, tv, stream);
+  if (D == 64) return scored::run<CT, 64, 2>(p, grid, tk, tv, stream);
+  if (D == 128 && nt == 1) return scored::run<CT, 128, 1>(p, grid, tk, tv, stream);
+  if (D == 128) return scored::run<CT, 128, 2>(p, grid, tk, tv, stream);
+  return scored::run<CT, 256, 1>(p, grid, tk, tv, stream);
+}
+
+}  // namespace kvc

@@ -16,6 +16,7 @@
 #include <new>
 #include <queue>
 #include <unordered_map>
+#include <utility>
 #include <vector>
 
 #include "kvc_internal.h"
@@ -191,6 +192,36 @@ kvc_status kvc_seq_reserve_cow(kvc_pool* pool, int64_t seq, int64_t n_new, int64
     copy_pair[1] = fresh;
   }
   return kvc_seq_reserve(pool, seq, n_new, slots_out);
+}
+
+kvc_status kvc_seq_evict(kvc_pool* pool, int64_t seq, int64_t new_length) {
+  kvc::clear_error();
+  kvc_pool::Seq* sq = nullptr;
+  kvc_status s = find_seq(pool, seq, &sq);
+  if (s != KVC_OK) return s;
+  if (new_length < 0 || new_length > sq->length)
+    return kvc::fail(KVC_ERR_INVALID_ARG, "new_length %lld outside 0 .. %lld", static_cast<long long>(new_length),
+                     static_cast<long long>(sq->length));
+  const int64_t bs = pool->block_size;
+  const int64_t need = (new_length + bs - 1) / bs;
+  // the rows are copied out of the present blocks, so none of them is reused here
+  if (need > static_cast<int64_t>(pool->free_heap.size()))
+    return kvc::fail(KVC_ERR_NO_BLOCKS, "need %lld blocks, %zu free", static_cast<long long>(need),
+                     pool->free_heap.size());
+  std::vector<int64_t> fresh(static_cast<size_t>(need));
+  for (int64_t& b : fresh) {
+    b = pool->free_heap.top();
+    pool->free_heap.pop();
+    pool->ref[static_cast<size_t>(b)] = 1;
+  }
+  for (int64_t b : sq->blocks) {
+    int32_t& r = pool->ref[static_cast<size_t>(b)];
+    r -= 1;
+    if (r == 0) pool->free_heap.push(b);
+  }
+  sq->blocks = std::move(fresh);
+  sq->length = new_length;
+  return KVC_OK;
 }
 
 kvc_status kvc_seq_free(kvc_pool* pool, int64_t seq) {
