@@ -593,43 +593,74 @@ def decode_attention_int8(q, k_cache, v_cache, k_scale, v_scale, block_tables, c
 
 
 # ------------------------------------- block-scaled codes, scores, eviction
+#
+# These calls are short on the device, so their host side is kept cheap: one
+# pass over the tensors, pointers as plain integers.
 
-def _code_format(codes, name) -> int:
+_codes = {}  # dtype -> kvc_dtype, filled at the first call
+
+
+def _code_of(t) -> int:
+    if not _codes:
+        torch = _torch()
+        _codes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
+
+
+def _stream_of(stream, t):
+    """Address of ``stream``, or of the current stream of ``t``'s device."""
+    if stream is not None:
+        return int(getattr(stream, "cuda_stream", stream))
+    torch = _torch()
+    raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # what current_stream() wraps in an object
+    return raw_stream(t.get_device()) if raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _checked(first, name, tensors):
+    """Checks ``first`` and ``tensors`` [(tensor, name, dtype or None)]: contiguous CUDA tensors of one device, the
+    current one (the stream and the library's launches belong to it)."""
+    torch = _torch()
+    for t, n, dtype in ((first, name, None), *tensors):
+        try:
+            device = t.device
+            if dtype is not None and t.dtype is not dtype:
+                raise TypeError(f"{n} must be {dtype}, got {t.dtype}")
+            contiguous = t.is_contiguous()
+        except AttributeError:
+            raise TypeError(f"{n} must be a tensor") from None
+        if not t.is_cuda:
+            raise ValueError(f"{n} must be a CUDA tensor")
+        if not contiguous:
+            raise ValueError(f"{n} must be contiguous")
+        if device != first.device:
+            raise ValueError(f"{name} is on {first.device}, {n} on {device}")
+    if first.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {first.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _pool_shape(k_cache, v_cache):
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must both be [num_blocks, n_kv_heads, block_size, head_dim]")
+    return shape
+
+
+def _code_format(codes) -> int:
     """Code format of a block-scaled pool: uint8 holds e4m3 codes, int8 holds int8 codes."""
     torch = _torch()
-    if codes.dtype == torch.uint8:
+    if codes.dtype is torch.uint8:
         return E4M3
-    if codes.dtype == torch.int8:
+    if codes.dtype is torch.int8:
         return INT8
-    raise TypeError(f"{name} must hold uint8 (e4m3) or int8 codes, got {codes.dtype}")
+    raise TypeError(f"block-scaled caches must hold uint8 (e4m3) or int8 codes, got {codes.dtype}")
 
 
-def _same_device(first, others):
-    """Refuses tensors of several devices, and of a device that is not current: the stream and the library's
-    launches belong to the current one."""
-    torch = _torch()
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
-    if first.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {first.device}, current device cuda:{torch.cuda.current_device()}")
-
-
-def _pools(k_cache, v_cache):
-    """Checks a pair of pools [num_blocks, Hkv, bs, D] and returns their shape."""
-    _require(k_cache, "k_cache")
-    _require(v_cache, "v_cache", k_cache.dtype)
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must both be [num_blocks, n_kv_heads, block_size, head_dim]")
-    return k_cache.shape
-
-
-def _block_scales(k_scale, v_scale, nb, hkv):
-    torch = _torch()
-    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _require(t, n, torch.float32)
-        if tuple(t.shape) != (nb, hkv):
-            raise ValueError(f"{n} must be [num_blocks, n_kv_heads]")
+def _check_block_scales(k_scale, v_scale, nb, hkv):
+    if k_scale.shape != (nb, hkv) or v_scale.shape != (nb, hkv):
+        raise ValueError("k_scale and v_scale must be [num_blocks, n_kv_heads]")
 
 
 def append_block8(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, stream=None):
@@ -637,19 +668,19 @@ def append_block8(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, stream
     k_cache, v_cache codes [num_blocks, Hkv, bs, D], uint8 (e4m3) or int8; k_scale, v_scale fp32 [num_blocks, Hkv].
     The blocks' scales grow with what is appended; a block's row 0 starts it afresh."""
     torch = _torch()
-    nb, hkv, bs, d = _pools(k_cache, v_cache)
-    code = _code_format(k_cache, "k_cache")
-    _require(k, "k")
-    _require(v, "v", k.dtype)
-    _require(slot_mapping, "slot_mapping", torch.int64)
-    _block_scales(k_scale, v_scale, nb, hkv)
+    f32 = torch.float32
+    _checked(k_cache, "k_cache", ((v_cache, "v_cache", getattr(k_cache, "dtype", None)), (k, "k", None),
+                                  (v, "v", getattr(k, "dtype", None)), (slot_mapping, "slot_mapping", torch.int64),
+                                  (k_scale, "k_scale", f32), (v_scale, "v_scale", f32)))
+    nb, hkv, bs, d = _pool_shape(k_cache, v_cache)
+    code = _code_format(k_cache)
+    _check_block_scales(k_scale, v_scale, nb, hkv)
     T = slot_mapping.numel()
-    if tuple(k.shape) != (T, hkv, d) or v.shape != k.shape:
+    if k.shape != (T, hkv, d) or v.shape != k.shape:
         raise ValueError("k and v must be [num_tokens, n_kv_heads, head_dim]")
-    _same_device(k_cache, (v_cache, k, v, slot_mapping, k_scale, v_scale))
-    _check(raw().kvc_append_block8(_ptr(k), _ptr(v), _ptr(slot_mapping), T, _ptr(k_cache), _ptr(v_cache),
-                                   _ptr(k_scale), _ptr(v_scale), code, nb, bs, hkv, d, _dtype_code(k),
-                                   _stream(stream)), "kvc_append_block8")
+    _check(raw().kvc_append_block8(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T, k_cache.data_ptr(),
+                                   v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), code, nb, bs, hkv, d,
+                                   _code_of(k), _stream_of(stream, k_cache)), "kvc_append_block8")
 
 
 def scored_workspace_size(batch, n_tokens, n_q_heads, n_kv_heads, head_dim, block_size, max_blocks_per_seq,
@@ -670,27 +701,20 @@ def new_scored_workspace(batch, n_tokens, n_q_heads, n_kv_heads, head_dim, block
     return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
 
 
-def _decode_scored_args(q, k_cache, v_cache, block_tables, context_lens, out, scores, workspace, more=()):
-    """Checks what the two scored decodes share; returns (B, T, Hq, D, num_blocks, Hkv, bs, max_blocks)."""
-    torch = _torch()
-    nb, hkv, bs, d = _pools(k_cache, v_cache)
-    for t, n in ((q, "q"), (out, "out"), (workspace, "workspace")):
-        _require(t, n)
-    _require(block_tables, "block_tables", torch.int32)
-    _require(context_lens, "context_lens", torch.int32)
-    if q.dim() not in (3, 4) or q.shape[-1] != d or out.shape != q.shape:
+def _decode_shape(q, out, k_cache, v_cache, block_tables, context_lens, scores):
+    """Shapes the two scored decodes share: (B, T, Hq, D, num_blocks, Hkv, bs, max_blocks)."""
+    nb, hkv, bs, d = _pool_shape(k_cache, v_cache)
+    shape = q.shape
+    if len(shape) not in (3, 4) or shape[-1] != d or out.shape != shape:
         raise ValueError("q and out must be [batch, n_q_heads, head_dim] or [batch, n_tokens, n_q_heads, head_dim]")
-    B, hq = q.shape[0], q.shape[-2]
-    T = q.shape[1] if q.dim() == 4 else 1
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.numel() != B:
+    B, hq = shape[0], shape[-2]
+    T = shape[1] if len(shape) == 4 else 1
+    table = block_tables.shape
+    if len(table) != 2 or table[0] != B or context_lens.numel() != B:
         raise ValueError("block_tables must be [batch, max_blocks] and context_lens [batch]")
-    mb = block_tables.shape[1]
-    if scores is not None:
-        _require(scores, "scores", torch.float32)
-        if tuple(scores.shape) != (B, hkv, mb * bs):
-            raise ValueError("scores must be [batch, n_kv_heads, max_blocks * block_size]")
-    _same_device(k_cache, (v_cache, q, out, block_tables, context_lens, scores, workspace, *more))
-    return B, T, hq, d, nb, hkv, bs, mb
+    if scores is not None and scores.shape != (B, hkv, table[1] * bs):
+        raise ValueError("scores must be [batch, n_kv_heads, max_blocks * block_size]")
+    return B, T, hq, d, nb, hkv, bs, table[1]
 
 
 def decode_attention_scored(q, k_cache, v_cache, block_tables, context_lens, scale, out, scores, workspace,
@@ -698,17 +722,17 @@ def decode_attention_scored(q, k_cache, v_cache, block_tables, context_lens, sca
     """kvc_decode_attention_scored: decode over a 16-bit cache that adds the attention weight of every cached row to
     ``scores`` fp32 [B, Hkv, max_blocks * bs]. q/out [B, Hq, D], or [B, T, Hq, D] for the T newest rows of every
     sequence; workspace from new_scored_workspace."""
-    B, T, hq, d, nb, hkv, bs, mb = _decode_scored_args(q, k_cache, v_cache, block_tables, context_lens, out, scores,
-                                                       workspace)
-    if scores is None:
-        raise TypeError("scores must be a tensor")
-    if q.dtype != k_cache.dtype:
-        raise TypeError(f"q must be {k_cache.dtype}, got {q.dtype}")
-    _check(raw().kvc_decode_attention_scored(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), mb,
-                                             _ptr(context_lens), B, T, float(scale), hq, hkv, d, bs, nb,
-                                             _dtype_code(k_cache), _ptr(out), _dtype_code(out), _ptr(scores),
-                                             _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                             _stream(stream)), "kvc_decode_attention_scored")
+    torch = _torch()
+    i32, dtype = torch.int32, getattr(k_cache, "dtype", None)
+    _checked(k_cache, "k_cache", ((v_cache, "v_cache", dtype), (q, "q", dtype), (block_tables, "block_tables", i32),
+                                  (context_lens, "context_lens", i32), (out, "out", None),
+                                  (scores, "scores", torch.float32), (workspace, "workspace", None)))
+    B, T, hq, d, nb, hkv, bs, mb = _decode_shape(q, out, k_cache, v_cache, block_tables, context_lens, scores)
+    _check(raw().kvc_decode_attention_scored(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                             block_tables.data_ptr(), mb, context_lens.data_ptr(), B, T, scale, hq, hkv,
+                                             d, bs, nb, _code_of(k_cache), out.data_ptr(), _code_of(out),
+                                             scores.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                                             _stream_of(stream, k_cache)), "kvc_decode_attention_scored")
 
 
 def decode_attention_block8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale, out, workspace,
@@ -716,15 +740,21 @@ def decode_attention_block8(q, k_cache, v_cache, k_scale, v_scale, block_tables,
     """kvc_decode_attention_block8: decode over the block-scaled codes of append_block8. q (f16/bf16) and out
     [B, Hq, D], or [B, T, Hq, D] for the T newest rows of every sequence; scores as in decode_attention_scored, or
     None; workspace from new_scored_workspace."""
-    B, T, hq, d, nb, hkv, bs, mb = _decode_scored_args(q, k_cache, v_cache, block_tables, context_lens, out, scores,
-                                                       workspace, (k_scale, v_scale))
-    code = _code_format(k_cache, "k_cache")
-    _block_scales(k_scale, v_scale, nb, hkv)
-    _check(raw().kvc_decode_attention_block8(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), code,
-                                             _ptr(block_tables), mb, _ptr(context_lens), B, T, float(scale), hq, hkv,
-                                             d, bs, nb, _dtype_code(q), _ptr(out), _dtype_code(out), _ptr(scores),
-                                             _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                             _stream(stream)), "kvc_decode_attention_block8")
+    torch = _torch()
+    i32, f32 = torch.int32, torch.float32
+    tensors = ((v_cache, "v_cache", getattr(k_cache, "dtype", None)), (q, "q", None), (k_scale, "k_scale", f32),
+               (v_scale, "v_scale", f32), (block_tables, "block_tables", i32), (context_lens, "context_lens", i32),
+               (out, "out", None), (workspace, "workspace", None))
+    _checked(k_cache, "k_cache", tensors if scores is None else (*tensors, (scores, "scores", f32)))
+    code = _code_format(k_cache)
+    B, T, hq, d, nb, hkv, bs, mb = _decode_shape(q, out, k_cache, v_cache, block_tables, context_lens, scores)
+    _check_block_scales(k_scale, v_scale, nb, hkv)
+    _check(raw().kvc_decode_attention_block8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                             v_scale.data_ptr(), code, block_tables.data_ptr(), mb,
+                                             context_lens.data_ptr(), B, T, scale, hq, hkv, d, bs, nb, _code_of(q),
+                                             out.data_ptr(), _code_of(out),
+                                             None if scores is None else scores.data_ptr(), workspace.data_ptr(),
+                                             workspace.nbytes, _stream_of(stream, k_cache)), "kvc_decode_attention_block8")
 
 
 def evict_rows(scores, k_cache, v_cache, block_tables, context_lens, budget, recent, new_block_tables, kept, new_lens,
@@ -734,35 +764,37 @@ def evict_rows(scores, k_cache, v_cache, block_tables, context_lens, budget, rec
     block_tables to those of new_block_tables. scores fp32 [B, Hkv, max_blocks * bs]; written: kept int32
     [B, Hkv, budget] (old rows, -1 past the end), new_lens int32 [B], new_scores fp32 [B, Hkv, new_max_blocks * bs]."""
     torch = _torch()
-    nb, hkv, bs, d = _pools(k_cache, v_cache)
-    for t, n in ((block_tables, "block_tables"), (context_lens, "context_lens"),
-                 (new_block_tables, "new_block_tables"), (kept, "kept"), (new_lens, "new_lens")):
-        _require(t, n, torch.int32)
-    _require(scores, "scores", torch.float32)
-    _require(new_scores, "new_scores", torch.float32)
+    i32, f32 = torch.int32, torch.float32
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale go together")
+    tensors = ((v_cache, "v_cache", getattr(k_cache, "dtype", None)), (scores, "scores", f32),
+               (block_tables, "block_tables", i32), (context_lens, "context_lens", i32),
+               (new_block_tables, "new_block_tables", i32), (kept, "kept", i32), (new_lens, "new_lens", i32),
+               (new_scores, "new_scores", f32))
+    if k_scale is not None:
+        tensors = (*tensors, (k_scale, "k_scale", f32), (v_scale, "v_scale", f32))
+    _checked(k_cache, "k_cache", tensors)
+    nb, hkv, bs, d = _pool_shape(k_cache, v_cache)
     if block_tables.dim() != 2 or new_block_tables.dim() != 2:
         raise ValueError("block_tables and new_block_tables must be [batch, max_blocks]")
     B, mb = block_tables.shape
-    new_mb = new_block_tables.shape[1]
-    if new_block_tables.shape[0] != B or context_lens.numel() != B or new_lens.numel() != B:
+    new_b, new_mb = new_block_tables.shape
+    if new_b != B or context_lens.numel() != B or new_lens.numel() != B:
         raise ValueError("new_block_tables, context_lens and new_lens must have one entry per sequence")
-    if tuple(scores.shape) != (B, hkv, mb * bs) or tuple(new_scores.shape) != (B, hkv, new_mb * bs):
+    if scores.shape != (B, hkv, mb * bs) or new_scores.shape != (B, hkv, new_mb * bs):
         raise ValueError("scores and new_scores must be [batch, n_kv_heads, max_blocks * block_size]")
-    if tuple(kept.shape) != (B, hkv, int(budget)):
+    if kept.shape != (B, hkv, budget):
         raise ValueError("kept must be [batch, n_kv_heads, budget]")
-    if (k_scale is None) != (v_scale is None):
-        raise ValueError("k_scale and v_scale go together")
-    _same_device(k_cache, (v_cache, scores, block_tables, context_lens, new_block_tables, kept, new_lens, new_scores,
-                           k_scale, v_scale))
     if k_scale is None:
-        _check(raw().kvc_evict_rows(_ptr(scores), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), mb,
-                                    _ptr(context_lens), B, int(budget), int(recent), _ptr(new_block_tables), new_mb, nb,
-                                    bs, hkv, d, _dtype_code(k_cache), _ptr(kept), _ptr(new_lens), _ptr(new_scores),
-                                    _stream(stream)), "kvc_evict_rows")
+        _check(raw().kvc_evict_rows(scores.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+                                    mb, context_lens.data_ptr(), B, budget, recent, new_block_tables.data_ptr(), new_mb,
+                                    nb, bs, hkv, d, _code_of(k_cache), kept.data_ptr(), new_lens.data_ptr(),
+                                    new_scores.data_ptr(), _stream_of(stream, k_cache)), "kvc_evict_rows")
         return
-    code = _code_format(k_cache, "k_cache")
-    _block_scales(k_scale, v_scale, nb, hkv)
-    _check(raw().kvc_evict_rows_block8(_ptr(scores), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), code,
-                                       _ptr(block_tables), mb, _ptr(context_lens), B, int(budget), int(recent),
-                                       _ptr(new_block_tables), new_mb, nb, bs, hkv, d, _ptr(kept), _ptr(new_lens),
-                                       _ptr(new_scores), _stream(stream)), "kvc_evict_rows_block8")
+    code = _code_format(k_cache)
+    _check_block_scales(k_scale, v_scale, nb, hkv)
+    _check(raw().kvc_evict_rows_block8(scores.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                       v_scale.data_ptr(), code, block_tables.data_ptr(), mb, context_lens.data_ptr(),
+                                       B, budget, recent, new_block_tables.data_ptr(), new_mb, nb, bs, hkv, d,
+                                       kept.data_ptr(), new_lens.data_ptr(), new_scores.data_ptr(), _stream_of(stream, k_cache)),
+           "kvc_evict_rows_block8")

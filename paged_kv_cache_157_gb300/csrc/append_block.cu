@@ -10,12 +10,14 @@
 // saturating). The scale of a block never shrinks while the block fills, so
 // earlier rows are rounded again only when a louder token arrives.
 //
-// One warp per (run, kv head, K or V). A warp looks at a stretch of tokens,
-// finds the runs that begin in it and takes them one by one: two sweeps over
-// the rows in 16-byte loads, the second (the codes) out of L1/L2. Bound by
-// HBM for prompts; by the chain slot -> scale -> row -> code of four dependent
-// accesses for a decode step, which is why a step's warps get one token each.
+// A CTA finds the runs that begin in a stretch of tokens and takes them one by
+// one for some of the heads, a short run by one warp, a long one by all. A run's rows are read once, in 16-byte loads that are all
+// in flight together, and stay in registers between the maximum and the codes
+// (runs beyond 16 KB are read again, out of L2). Bound by HBM for prompts; by
+// the chain slots -> rows and scale -> codes of dependent accesses for a decode step,
+// whose tokens get a warp each.
 #include <algorithm>
+#include <type_traits>
 
 #include "code8.cuh"
 
@@ -23,9 +25,20 @@ namespace kvc {
 
 namespace {
 
+// Largest |x| of m and the values of one 16-byte chunk of T; NaN if any is.
+template <typename T>
+__device__ __forceinline__ float chunk_max(float m, const uint4& u) {
+#pragma unroll
+  for (int i = 0; i < 16 / static_cast<int>(sizeof(T)) / 2; ++i) {
+    const float2 x = Elem<T>::pair(u, i);
+    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(x.x), "f"(x.y));
+  }
+  return m;
+}
+
 // Largest finite |x| among the values of one 16-byte chunk of T.
 template <typename T>
-__device__ __forceinline__ float chunk_max(const uint4& u) {
+__device__ __forceinline__ float finite_max(const uint4& u) {
   float m = 0.f;
 #pragma unroll
   for (int i = 0; i < 16 / static_cast<int>(sizeof(T)) / 2; ++i) {
@@ -44,7 +57,8 @@ struct AppendBlockParams {
   float *k_scale, *v_scale;          // [num_blocks, n_heads]
   int64_t num_tokens, num_slots;
   int n_heads, block_size;
-  int stretch;  // tokens a warp looks at (1 .. 32)
+  int stretch;     // tokens a CTA looks at at a time
+  unsigned items;  // stretches x heads x 2
   unsigned int* err;
 };
 
@@ -56,117 +70,267 @@ __device__ __forceinline__ int64_t block_of(int64_t slot, const AppendBlockParam
 }
 
 constexpr int kAppendWarps = 4;
+constexpr int kAppendThreads = 32 * kAppendWarps;
+constexpr int kWindows = 8;       // of 32 tokens, that a CTA looks at: its stretch (at most 4) and what its last run may reach
+constexpr int kInFlight = 8;      // 16-byte chunks a lane holds
+constexpr int kAppendCtasPerSm = 4;
 
-template <typename T, bool INT8, int D>
-__global__ void __launch_bounds__(32 * kAppendWarps) append_block_kernel(const AppendBlockParams p) {
+// A run: `rows` tokens from the one x and slots point at.
+struct Run {
+  const uint4* x;        // head h of the run's first token
+  const int64_t* slots;  // of the run's first token
+  int64_t first_slot;    // of the block
+  float* scale;
+  unsigned char* dst;    // the block's codes of head h
+  int rows;
+  int first;             // its lowest row in the block
+};
+
+// One run by a group of NW warps (thread g of it); token_chunks: 16-byte
+// chunks from a token to the next. ASC: the tokens fill ascending rows, from
+// run.first on; otherwise each token's slot is looked up.
+template <typename T, bool INT8, int D, int NW, bool ASC>
+__device__ __noinline__ void append_run(const Run run, uint32_t token_chunks, int g, uint32_t* s_red) {
   constexpr int VEC = 16 / sizeof(T);  // values per 16-byte chunk
   constexpr int CPR = D / VEC;         // chunks per row
-  constexpr int U = 8;                 // chunks in flight per lane
+  constexpr int STEP = 32 * NW;
+  constexpr int RPS = STEP >= CPR ? STEP / CPR : 1;  // rows per step (a row may take two steps)
+  constexpr int SPR = STEP >= CPR ? 1 : CPR / STEP;  // steps per row
+  const int lane = g & 31;
+  // the lane's chunk of step i: row (i / SPR) * RPS + r0 of the run, chunk c0 + (i % SPR) * STEP of it
+  const int r0 = g / CPR, c0 = g % CPR;
+  const int steps = (run.rows + RPS - 1) / RPS * SPR;
+  auto row_of = [&](int i) { return (i / SPR) * RPS + r0; };
+  // rows past the end: the last one, whose values count already
+  const uint4* x0 = run.x + c0;
+  auto chunk_of = [&](int i) {
+    const int r = min(row_of(i), run.rows - 1);
+    // ascending rows: at most a block of them, 32-bit offsets
+    if constexpr (ASC) return x0 + (static_cast<uint32_t>(r) * token_chunks + (i % SPR) * STEP);
+    return x0 + (static_cast<int64_t>(r) * token_chunks + (i % SPR) * STEP);
+  };
+  auto block_row = [&](int i) {
+    return ASC ? run.first + row_of(i) : static_cast<int>(__ldg(run.slots + row_of(i)) - run.first_slot);
+  };
+  const float held = *run.scale;
+  uint4 u[kInFlight];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int j = 0; j < kInFlight; ++j)
+      if (j == 0 || i0 + j < steps) u[j] = *chunk_of(i0 + j);
+  };
+  float m = 0.f;
+  for (int i0 = 0; i0 < steps; i0 += kInFlight) {
+    load(i0);
+#pragma unroll
+    for (int j = 0; j < kInFlight; ++j)
+      if (j == 0 || i0 + j < steps) m = chunk_max<T>(m, u[j]);
+  }
+  // as integers the magnitudes keep their order, with infinity and NaN on top
+  uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(m) & 0x7fffffffu);
+  if constexpr (NW > 1) {  // (also: every warp has read the old scale)
+    if (lane == 0) s_red[g >> 5] = mb;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NW; ++i) mb = max(mb, s_red[i]);
+    __syncthreads();  // s_red may be used again
+  }
+  const bool odd = mb >= 0x7f800000u;  // the run has a value that is not finite (the same in every thread)
+  m = __uint_as_float(mb);
+  if (odd) {
+    m = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < steps; ++i) m = fmaxf(m, finite_max<T>(*chunk_of(i)));
+    m = warp_max(m);
+    if constexpr (NW > 1) {
+      if (lane == 0) s_red[g >> 5] = __float_as_uint(m);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < NW; ++i) m = fmaxf(m, __uint_as_float(s_red[i]));
+      __syncthreads();
+    }
+  }
+  const float old = run.first == 0 ? 0.f : held;
+  float s = fmaxf(old, m * Code8<INT8>::kInvMax);
+  if (!(s >= kTinyScale)) s = 0.f;
+  const float inv = s > 0.f ? __fdiv_rn(1.0f, s) : 0.f;
+  if (run.first > 0 && s != old) {
+    const float f = s > 0.f ? __fdiv_rn(old, s) : 0.f;
+    uint4* rows16 = reinterpret_cast<uint4*>(run.dst);
+#pragma unroll 1
+    for (int i = g; i < run.first * (D / 16); i += STEP) rows16[i] = rescale16<INT8>(rows16[i], f);
+  }
+  // Codes of a chunk to its row of the block. Products and codes are rounded
+  // separately: no fused multiply-add.
+  unsigned char* dst0 = run.dst + c0 * VEC;
+  auto put = [&](int i, const uint4& x, const auto& in_range) {
+    unsigned char* to = dst0 + static_cast<uint32_t>(block_row(i) * D + (i % SPR) * STEP * VEC);
+    uint32_t code[VEC / 4];
+#pragma unroll
+    for (int k = 0; k < VEC / 4; ++k) {
+      float2 a = Elem<T>::pair(x, 2 * k), b = Elem<T>::pair(x, 2 * k + 1);
+      a = make_float2(__fmul_rn(a.x, inv), __fmul_rn(a.y, inv));
+      b = make_float2(__fmul_rn(b.x, inv), __fmul_rn(b.y, inv));
+      if constexpr (std::decay_t<decltype(in_range)>::value)
+        code[k] = encode4_in_range<INT8>(a, b);
+      else
+        code[k] = s > 0.f ? encode4<INT8>(a.x, a.y, b.x, b.y) : 0u;
+    }
+    if constexpr (VEC == 8)
+      *reinterpret_cast<uint2*>(to) = make_uint2(code[0], code[1]);
+    else
+      *reinterpret_cast<uint32_t*>(to) = code[0];
+  };
+  if (odd || s == 0.f) {
+    // values that are not finite saturate; with scale 0 every finite entry counts as 0
+#pragma unroll 1
+    for (int i = 0; i < steps; ++i)
+      if (row_of(i) < run.rows) put(i, *chunk_of(i), std::false_type{});
+  } else {
+    // with finite values and s >= A / Q, |x / s| rounds to at most Q
+    for (int i0 = 0; i0 < steps; i0 += kInFlight) {
+      if (steps > kInFlight) load(i0);
+#pragma unroll
+      for (int j = 0; j < kInFlight; ++j)
+        if (row_of(i0 + j) < run.rows) put(i0 + j, u[j], std::true_type{});
+    }
+  }
+  if (g == 0) *run.scale = s;
+}
+
+// Work: items (stretch, head, K or V), stretch-major; every CTA takes an equal
+// range of them, so that it finds a stretch's runs once for several heads (a
+// CTA per item spent 15 of 36 us of a 16384-token prompt on finding them).
+template <typename T, bool INT8, int D>
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtasPerSm) append_block_kernel(const AppendBlockParams p) {
+  constexpr int CPR = D * static_cast<int>(sizeof(T)) / 16;
   constexpr uint32_t full = 0xffffffffu;
+  __shared__ uint32_t s_red[2 * kAppendWarps];
+  __shared__ int64_t s_slot[1 + 32 * kWindows];  // of the token before the stretch, and of the windows' tokens
+  __shared__ uint32_t s_ends[kWindows];          // bit masks: a token that is not written, or begins a run
+  __shared__ int s_first[kAppendThreads], s_end[kAppendThreads];  // the runs: first token, and the one behind
+  __shared__ int64_t s_block[kAppendThreads];
+  __shared__ int s_runs[kAppendWarps];           // per window
   // a decode launched behind this kernel may set itself up meanwhile; it waits
   // for this grid to end before it reads any cached row
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const int64_t wi = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
-  const int kv = static_cast<int>(wi % 2);
-  const int h = static_cast<int>((wi / 2) % p.n_heads);
-  const int64_t t0 = wi / 2 / p.n_heads * p.stretch;
-  if (t0 >= p.num_tokens) return;
-  const T* x = static_cast<const T*>(kv ? p.v : p.k);
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int bs = p.block_size;
-
-  int64_t mine = -1;  // this lane's token's block
-  bool leads = false;
-  if (lane < p.stretch && t0 + lane < p.num_tokens) {
-    const int64_t slot = __ldg(p.slots + t0 + lane);
-    mine = block_of(slot, p);
-    if (slot >= p.num_slots && h == 0 && kv == 0) set_flag(p.err, KVC_FLAG_BAD_SLOT);
-    leads = mine >= 0 && (t0 + lane == 0 || block_of(__ldg(p.slots + t0 + lane - 1), p) != mine);
-  }
-  for (uint32_t todo = __ballot_sync(full, leads); todo != 0; todo &= todo - 1) {
-    const int at = __ffs(todo) - 1;
-    const int64_t blk = __shfl_sync(full, mine, at);
-    const int64_t a = t0 + at;  // the run's first token
-    // its end, and the lowest row it writes
-    int64_t e = a;
-    int first = bs;
-    for (;;) {
-      bool in = false;
-      int row = bs;
-      if (e + lane < p.num_tokens) {
-        const int64_t slot = __ldg(p.slots + e + lane);
-        in = block_of(slot, p) == blk;
-        if (in) row = static_cast<int>(slot - blk * bs);
+  const int per_stretch = 2 * p.n_heads;
+  const uint32_t token_chunks = static_cast<uint32_t>(p.n_heads) * CPR;
+  unsigned item = static_cast<unsigned>(static_cast<uint64_t>(p.items) * blockIdx.x / gridDim.x);
+  const unsigned item_end = static_cast<unsigned>(static_cast<uint64_t>(p.items) * (blockIdx.x + 1) / gridDim.x);
+#pragma unroll 1
+  while (item < item_end) {
+    const unsigned st = item / per_stretch;
+    const int r0 = static_cast<int>(item - st * per_stretch);
+    const int r1 = min(per_stretch, r0 + static_cast<int>(item_end - item));  // (head, K or V) of this stretch
+    item += r1 - r0;
+    const int64_t t0 = static_cast<int64_t>(st) * p.stretch, left = p.num_tokens - t0;
+    const int len = left < p.stretch ? static_cast<int>(left) : p.stretch;
+    const int windows = (len + 31) / 32, seen = windows + (bs + 31) / 32;  // with runs of this stretch, and looked at
+    __syncthreads();  // the last stretch's tables have been read
+#pragma unroll
+    for (int i = 0; i < 32 * kWindows; i += kAppendThreads) {
+      int64_t slot = -1;
+      if (i + tid < 32 * seen && i + tid < left) slot = __ldg(p.slots + t0 + i + tid);
+      s_slot[1 + i + tid] = slot;
+      if (i + tid < len && slot >= p.num_slots) set_flag(p.err, KVC_FLAG_BAD_SLOT);
+    }
+    if (tid == 0) s_slot[0] = t0 > 0 ? __ldg(p.slots + t0 - 1) : -1;
+    __syncthreads();
+    // a run begins at a token that is written and does not share its block
+    // with the one before, and ends at the next token that begins one or is not written
+    uint32_t leads = 0;
+    int64_t blk = -1;
+#pragma unroll
+    for (int i = kWindows - kAppendWarps; i >= 0; i -= kAppendWarps) {  // this warp's windows, the stretch's last
+      const int64_t slot = s_slot[1 + 32 * (i + w) + lane], prev = s_slot[32 * (i + w) + lane];
+      blk = block_of(slot, p);
+      const bool ends = blk < 0 || !(prev >= blk * bs && prev < blk * bs + bs);
+      const uint32_t be = __ballot_sync(full, ends);
+      leads = __ballot_sync(full, ends && blk >= 0 && 32 * w + lane < len);
+      if (lane == 0) s_ends[i + w] = be;
+    }
+    if (lane == 0) s_runs[w] = __popc(leads);
+    __syncthreads();
+    int n = 0, runs = 0;  // runs before this warp's, and all
+#pragma unroll
+    for (int i = 0; i < kAppendWarps; ++i) {
+      if (i < w) n += s_runs[i];
+      runs += s_runs[i];
+    }
+    if ((leads >> lane) & 1u) {
+      int end = 32 * kWindows;
+      uint32_t x = s_ends[w] & ~((2u << lane) - 1u);
+      for (int j = w;;) {
+        if (x != 0) {
+          end = 32 * j + __ffs(x) - 1;
+          break;
+        }
+        if (++j == kWindows) break;
+        x = s_ends[j];
       }
-      const uint32_t got = __ballot_sync(full, in);
-      const int len = got == full ? 32 : __ffs(~got) - 1;
-      first = min(first, static_cast<int>(__reduce_min_sync(full, lane < len ? row : bs)));
-      e += len;
-      if (len < 32) break;
+      n += __popc(leads & ((1u << lane) - 1u));
+      s_first[n] = 32 * w + lane;
+      s_end[n] = end;
+      s_block[n] = blk;
     }
-    float* scale = (kv ? p.v_scale : p.k_scale) + blk * p.n_heads + h;
-    const float old = first == 0 ? 0.f : *scale;
-    const int64_t chunks = (e - a) * CPR;
-    auto src = [&](int64_t i) {  // chunk i of the run
-      return reinterpret_cast<const uint4*>(x + ((a + i / CPR) * p.n_heads + h) * D) + i % CPR;
-    };
-    float m = 0.f;
-    for (int64_t i0 = lane; i0 < chunks; i0 += 32 * U) {
-      uint4 u[U];
-#pragma unroll
-      for (int j = 0; j < U; ++j) u[j] = i0 + 32 * j < chunks ? *src(i0 + 32 * j) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int j = 0; j < U; ++j) m = fmaxf(m, chunk_max<T>(u[j]));
-    }
-    m = warp_max(m);
-    float s = fmaxf(old, m * Code8<INT8>::kInvMax);
-    if (!(s >= kTinyScale)) s = 0.f;
-    const float inv = s > 0.f ? __fdiv_rn(1.0f, s) : 0.f;
-    unsigned char* dst = (kv ? p.v_codes : p.k_codes) + (blk * p.n_heads + h) * static_cast<int64_t>(bs) * D;
-    if (first > 0 && s != old) {
-      const float f = s > 0.f ? __fdiv_rn(old, s) : 0.f;
-      uint4* rows = reinterpret_cast<uint4*>(dst);
-      for (int i = lane; i < first * (D / 16); i += 32) rows[i] = rescale16<INT8>(rows[i], f);
-    }
-    for (int64_t i0 = lane; i0 < chunks; i0 += 32 * U) {
-      uint4 u[U];
-      int row[U];
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int64_t i = i0 + 32 * j;
-        row[j] = -1;
-        if (i < chunks) {
-          u[j] = *src(i);
-          row[j] = static_cast<int>(__ldg(p.slots + a + i / CPR) - blk * bs);
+    __syncthreads();
+    int nth = 0;
+#pragma unroll 1
+    for (int i = 0; i < runs; ++i) {
+      Run run;
+      const int a = s_first[i];
+      const int64_t b = s_block[i];
+      int end = s_end[i];
+      run.first_slot = b * bs;
+      if (end >= 32 * seen && end < left) {  // longer than a block: a slot is named more than once
+        for (int64_t e = t0 + 32 * seen;; e += 32) {
+          const int64_t sl = e + lane < p.num_tokens ? __ldg(p.slots + e + lane) : -1;
+          const uint32_t out = __ballot_sync(full, !(sl >= run.first_slot && sl < run.first_slot + bs));
+          end = static_cast<int>(e - t0) + (out != 0 ? __ffs(out) - 1 : 32);
+          if (out != 0) break;
         }
       }
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        if (row[j] < 0) continue;
-        unsigned char* to = dst + row[j] * D + static_cast<int>((i0 + 32 * j) % CPR) * VEC;
-        float2 v[VEC / 2];
-#pragma unroll
-        for (int k = 0; k < VEC / 2; ++k) {
-          v[k] = Elem<T>::pair(u[j], k);
-          // scale 0: every finite entry is 0 (or too small to count), and 0 x inf would not be
-          v[k].x = s > 0.f ? v[k].x * inv : 0.f;
-          v[k].y = s > 0.f ? v[k].y * inv : 0.f;
-        }
-        if constexpr (VEC == 8)
-          *reinterpret_cast<uint2*>(to) = make_uint2(encode4<INT8>(v[0].x, v[0].y, v[1].x, v[1].y),
-                                                     encode4<INT8>(v[2].x, v[2].y, v[3].x, v[3].y));
+      run.rows = end - a;
+      run.slots = p.slots + t0 + a;
+      // its lowest row, and whether the rows ascend by one: the same in every thread
+      int first = bs;
+      bool asc = true;
+      for (int t = lane; t < run.rows; t += 32) {
+        const int64_t sl = a + t < 32 * kWindows ? s_slot[1 + a + t] : __ldg(run.slots + t);
+        first = min(first, static_cast<int>(sl - run.first_slot));
+        asc = asc && sl - s_slot[1 + a] == t;
+      }
+      run.first = __reduce_min_sync(full, first);
+      asc = __all_sync(full, asc);
+      const bool all = run.rows * CPR > 32 * kInFlight;  // all warps take it together
+#pragma unroll 1
+      for (int r = r0; r < r1; ++r) {
+        if (!all && nth++ % kAppendWarps != w) continue;
+        const int h = r >> 1;
+        const bool v = r & 1;
+        const int64_t head = b * p.n_heads + h;
+        run.x = static_cast<const uint4*>(v ? p.v : p.k) + ((t0 + a) * p.n_heads + h) * CPR;
+        run.scale = (v ? p.v_scale : p.k_scale) + head;
+        run.dst = (v ? p.v_codes : p.k_codes) + head * bs * D;
+        if (all && asc)
+          append_run<T, INT8, D, kAppendWarps, true>(run, token_chunks, tid, s_red);
+        else if (all)
+          append_run<T, INT8, D, kAppendWarps, false>(run, token_chunks, tid, s_red);
+        else if (asc)
+          append_run<T, INT8, D, 1, true>(run, token_chunks, lane, s_red);
         else
-          *reinterpret_cast<uint32_t*>(to) = encode4<INT8>(v[0].x, v[0].y, v[1].x, v[1].y);
+          append_run<T, INT8, D, 1, false>(run, token_chunks, lane, s_red);
       }
     }
-    __syncwarp();
-    if (lane == 0) *scale = s;
   }
 }
 
 template <typename T, bool INT8>
 void launch(const AppendBlockParams& p, int D, int64_t grid, cudaStream_t s) {
-  const dim3 g(static_cast<unsigned>(grid)), b(32 * kAppendWarps);
+  const dim3 g(static_cast<unsigned>(grid)), b(kAppendThreads);
   if (D == 64) append_block_kernel<T, INT8, 64><<<g, b, 0, s>>>(p);
   else if (D == 128) append_block_kernel<T, INT8, 128><<<g, b, 0, s>>>(p);
   else append_block_kernel<T, INT8, 256><<<g, b, 0, s>>>(p);
@@ -218,13 +382,16 @@ extern "C" kvc_status kvc_append_block8(const void* k, const void* v, const int6
   p.n_heads = n_kv_heads;
   p.block_size = block_size;
   p.err = dev->error_word;
-  // one token per warp while the warps fit the GPU at once, longer stretches
-  // beyond: most warps of a prompt find no run that begins in theirs
-  const int64_t items = 2 * num_tokens * n_kv_heads, resident = 64LL * dev->num_sms;
-  p.stretch = static_cast<int>(std::min<int64_t>(32, (items + resident - 1) / resident));
-  const int64_t warps = (num_tokens + p.stretch - 1) / p.stretch * n_kv_heads * 2;
-  const int64_t grid = (warps + kAppendWarps - 1) / kAppendWarps;
-  if (grid >= (1ll << 31)) return fail(KVC_ERR_UNSUPPORTED, "num_tokens x n_kv_heads too large");
+  // Stretches of a block for prompts, so that a stretch has one run. With few
+  // tokens, shorter ones: the CTAs are to fill the GPU, with a run for each of
+  // a CTA's warps if every token is one (a decode step).
+  const int64_t resident = static_cast<int64_t>(kAppendCtasPerSm) * dev->num_sms;
+  const int64_t pairs = 2 * num_tokens * n_kv_heads;  // (token, head, K or V)
+  p.stretch = static_cast<int>(std::min<int64_t>(block_size, std::max<int64_t>(kAppendWarps, pairs / resident)));
+  const int64_t items = (num_tokens + p.stretch - 1) / p.stretch * n_kv_heads * 2;
+  if (items >= (1ll << 31)) return fail(KVC_ERR_UNSUPPORTED, "num_tokens x n_kv_heads too large");
+  p.items = static_cast<unsigned>(items);
+  const int64_t grid = std::min(items, resident);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (dtype) {
     case KVC_F32: launch<float>(p, head_dim, code, grid, s); break;

@@ -27,6 +27,21 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
   }
 }
 
+// encode4 for values known to be finite and, rounded, within the codes' range:
+// int8 codes come out of the low mantissa bits of 1.5 x 2^23 + x (the addition
+// rounds to the nearest integer, ties to even).
+template <bool INT8>
+__device__ __forceinline__ uint32_t encode4_in_range(float2 a, float2 b) {
+  if constexpr (INT8) {
+    constexpr float k = 12582912.0f;
+    const uint32_t lo = __byte_perm(__float_as_uint(__fadd_rn(a.x, k)), __float_as_uint(__fadd_rn(a.y, k)), 0x0040u);
+    const uint32_t hi = __byte_perm(__float_as_uint(__fadd_rn(b.x, k)), __float_as_uint(__fadd_rn(b.y, k)), 0x0040u);
+    return __byte_perm(lo, hi, 0x5410u);
+  } else {
+    return encode4<false>(a.x, a.y, b.x, b.y);
+  }
+}
+
 // The codes of one word times f, rounded to codes again.
 template <bool INT8>
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {

@@ -68,7 +68,7 @@ ScoredLayout layout(const ScoredShape& s, int elt, bool scored, int num_sms) {
   l.qns = (qn + 1) / 2 * 2;
   const int64_t units = static_cast<int64_t>(s.batch) * s.n_kv_heads * l.n_hsub;
   const int64_t tiles = units * ((s.rows() + kTileRows - 1) / kTileRows);
-  const int warps = scored_warps(elt, s.D);
+  const int warps = scored_warps(elt, s.D, l.nt);
   // few tiles spread over as many SMs as there are workers
   l.grid = static_cast<int>(std::min<int64_t>(num_sms, (tiles + kMinTiles - 1) / kMinTiles));
   l.workers = l.grid * warps;
@@ -185,7 +185,7 @@ kvc_status decode(Cache cache, const ScoredShape& s, const void* q, kvc_dtype q_
   p.wait_polls = static_cast<unsigned int>(option(KVC_OPT_WAIT_POLLS));
   const int64_t cap = option(KVC_OPT_MAX_CTAS), forced = option(KVC_OPT_BLOCKS_PER_CTA);
   const int grid = static_cast<int>(cap > 0 ? std::min<int64_t>(cap, l.grid) : l.grid);
-  p.workers = grid * scored_warps(elt, s.D);
+  p.workers = grid * scored_warps(elt, s.D, l.nt);
   // the work split's option counts cache blocks per worker, here a warp
   p.min_tiles = forced > 0 ? static_cast<int>(std::min<int64_t>(forced, 1 << 20)) * (s.block_size / kTileRows)
                            : kMinTiles;

@@ -21,9 +21,10 @@
 // are laid end to end and cut into equal ranges, one per WARP. A warp is a
 // worker of its own: it issues its copies, waits for them and runs the
 // products, with no barrier between warps, so a unit may have any number of
-// kv heads, any length and any group, and eight workers per SM keep 128 to
-// 192 KB of copies in flight. A worker holds at most two parts of units
-// that other workers share; each leaves one record (maximum, sum, output).
+// kv heads, any length and any group, and eight or twelve workers per SM keep
+// 128 to 192 KB of copies in flight. Neighbouring workers sit in one CTA: what
+// its warps hold at the ends of their ranges is merged in shared memory, so a
+// unit has about one record (maximum, sum, output) per CTA it spans.
 //
 // Products on m16n8k16 MMAs, rows (or dims) x queries:
 //   S^T [16 rows x 8 queries] = K [16 x D] . Q^T,
@@ -163,11 +164,21 @@ __device__ __forceinline__ void weight_parts(const float (&w)[NT][4], uint32_t (
   }
 }
 
-// Masks that clear the V rows at and behind rem (they may hold anything, and
-// 0 x NaN is NaN): rows 2c, 2c + 1 and 2c + 8, 2c + 9 of the lane's A fragments.
-__device__ __forceinline__ void keep_masks(int rem, int c, uint32_t& k01, uint32_t& k89) {
-  k01 = (2 * c < rem ? 0x0000ffffu : 0u) | (2 * c + 1 < rem ? 0xffff0000u : 0u);
-  k89 = (2 * c + 8 < rem ? 0x0000ffffu : 0u) | (2 * c + 9 < rem ? 0xffff0000u : 0u);
+// Clears the V rows at and behind rem (< 16) of a tile: they may hold anything,
+// and 0 x NaN is NaN. The fence orders these writes before the copy that
+// next fills the stage.
+template <int BOXB, int HALVES>
+__device__ __forceinline__ void clear_rows(uint32_t v, int rem, int lane) {
+  constexpr int CH = BOXB / 16;
+#pragma unroll 1
+  for (int i = rem * CH + lane; i < kTileRows * CH; i += 32) {
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + h * (kTileRows * BOXB) + i * 16), "r"(0u)
+                   : "memory");
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
 }
 
 // Running softmax over one tile: x becomes the weights relative to the
@@ -198,9 +209,12 @@ __device__ __forceinline__ void softmax_step(float (&x)[NT][4], State<D, NT, ONE
   }
 }
 
-// One 16-row tile of a 16-bit cache. k, v: the tile's boxes.
-template <bool BF, int D, int NT, bool EDGE>
-__device__ __forceinline__ void tile16(uint32_t k, uint32_t v, int rem, float qscale, float* lg, int qns, int col0,
+// One 16-row tile of a 16-bit cache. k, v: the tile's boxes; rem: the
+// sequence's rows from the tile's first on; edge: some query does not see all
+// 16. (One body for both: small calls run every line once, and what they wait
+// for then is instructions.)
+template <bool BF, int D, int NT>
+__device__ __forceinline__ void tile16(uint32_t k, uint32_t v, int rem, bool edge, float qscale, float* lg, int qns, int col0,
                                        int qn, State<D, NT, false>& st, int lane) {
   using namespace wmma16;
   constexpr int NP = BF ? 3 : 2;
@@ -237,23 +251,24 @@ __device__ __forceinline__ void tile16(uint32_t k, uint32_t v, int rem, float qs
       }
     }
   }
-  if constexpr (EDGE) mask_edge<D, NT, false>(x, st, rem, g);
+  if (edge) {
+    mask_edge<D, NT, false>(x, st, rem, g);
+    if (rem < kTileRows) clear_rows<128, D / 64>(v, rem, lane);
+  }
   if (lg != nullptr) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int col = col0 + 8 * n + 2 * c;
       if (col < qn) {
         float* at = lg + static_cast<int64_t>(g) * qns + col;
-        if (!EDGE || g < rem) *reinterpret_cast<float2*>(at) = make_float2(x[n][0], x[n][1]);
-        if (!EDGE || g + 8 < rem) *reinterpret_cast<float2*>(at + 8 * qns) = make_float2(x[n][2], x[n][3]);
+        if (g < rem) *reinterpret_cast<float2*>(at) = make_float2(x[n][0], x[n][1]);
+        if (g + 8 < rem) *reinterpret_cast<float2*>(at + 8 * qns) = make_float2(x[n][2], x[n][3]);
       }
     }
   }
   softmax_step<D, NT, false>(x, st, 0.f);
   uint32_t b[NT][NP][2];
   weight_parts<BF, NT, NP>(x, b);
-  uint32_t k01 = 0, k89 = 0;
-  if constexpr (EDGE) keep_masks(rem, c, k01, k89);
   // lane l addresses row (l & 7) + 8 (l >> 4), dims chunk 2 i + ((l >> 3) & 1)
   const uint32_t row = v + static_cast<uint32_t>(((lane & 7) + (lane >> 4) * 8) * 128) +
                        static_cast<uint32_t>(((((lane >> 3) & 1) ^ sw) & 1) << 4);
@@ -261,12 +276,6 @@ __device__ __forceinline__ void tile16(uint32_t k, uint32_t v, int rem, float qs
   for (int i = 0; i < D / 16; ++i) {
     uint32_t a[4];
     ldsm_x4_t(row + (i >> 2) * BOX + static_cast<uint32_t>(((i & 3) ^ s2) << 5), a);
-    if constexpr (EDGE) {
-      a[0] &= k01;
-      a[1] &= k01;
-      a[2] &= k89;
-      a[3] &= k89;
-    }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -283,8 +292,8 @@ __device__ __forceinline__ void tile16(uint32_t k, uint32_t v, int rem, float qs
 // for PV, dims 16g .. 16g + 15 of every 128 (8g .. 8g + 7 of 64) of rows
 // 2c, 2c + 1, 2c + 8, 2c + 9, and a byte permute pairs two rows of one dim. Output
 // tile i of a span then holds its dims 16g + 2i and 16g + 2i + 1 (8g + 2i).
-template <int Q8, int D, int NT, bool EDGE>
-__device__ __forceinline__ void tile8(uint32_t k, uint32_t v, int rem, float ks, float vs, float* lg, int qns,
+template <int Q8, int D, int NT>
+__device__ __forceinline__ void tile8(uint32_t k, uint32_t v, int rem, bool edge, float ks, float vs, float* lg, int qns,
                                       int col0, int qn, State<D, NT, true>& st, int lane) {
   using namespace wmma16;
   constexpr int NP = 2;
@@ -336,23 +345,24 @@ __device__ __forceinline__ void tile8(uint32_t k, uint32_t v, int rem, float ks,
       }
     }
   }
-  if constexpr (EDGE) mask_edge<D, NT, true>(x, st, rem, g);
+  if (edge) {
+    mask_edge<D, NT, true>(x, st, rem, g);
+    if (rem < kTileRows) clear_rows<BOXB, SPANS>(v, rem, lane);
+  }
   if (lg != nullptr) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int col = col0 + 8 * n + 2 * c;
       if (col < qn) {
         float* at = lg + static_cast<int64_t>(g) * qns + col;
-        if (!EDGE || g < rem) *reinterpret_cast<float2*>(at) = make_float2(x[n][0], x[n][1]);
-        if (!EDGE || g + 8 < rem) *reinterpret_cast<float2*>(at + 8 * qns) = make_float2(x[n][2], x[n][3]);
+        if (g < rem) *reinterpret_cast<float2*>(at) = make_float2(x[n][0], x[n][1]);
+        if (g + 8 < rem) *reinterpret_cast<float2*>(at + 8 * qns) = make_float2(x[n][2], x[n][3]);
       }
     }
   }
   softmax_step<D, NT, true>(x, st, fast_log2(vs));
   uint32_t b[NT][NP][2];
   weight_parts<false, NT, NP>(x, b);
-  uint32_t k01 = 0, k89 = 0;
-  if constexpr (EDGE) keep_masks(rem, c, k01, k89);
 #pragma unroll
   for (int sp = 0; sp < SPANS; ++sp) {
     uint32_t vw[4][KS / 2];  // rows 2c, 2c + 1, 2c + 8, 2c + 9
@@ -378,12 +388,6 @@ __device__ __forceinline__ void tile8(uint32_t k, uint32_t v, int rem, float ks,
       uint32_t a[4];
       codes_to_f16x2<Q8>(__byte_perm(vw[0][i >> 1], vw[1][i >> 1], sel), a[0], a[1]);
       codes_to_f16x2<Q8>(__byte_perm(vw[2][i >> 1], vw[3][i >> 1], sel), a[2], a[3]);
-      if constexpr (EDGE) {
-        a[0] &= k01;
-        a[1] &= k01;
-        a[2] &= k89;
-        a[3] &= k89;
-      }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -433,6 +437,13 @@ __device__ inline void scan_tiles(const ScoredParams& p, int* s_scan) {
   __syncthreads();
 }
 
+// a / b for a >= 0, b > 0, with a 32-bit division when both fit.
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+  return (static_cast<uint64_t>(a | b) >> 32) == 0
+             ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
+             : a / b;
+}
+
 // The unit of global tile `pos`.
 struct Unit {
   int64_t u0;  // its first tile
@@ -450,7 +461,7 @@ __device__ __forceinline__ Unit locate(int64_t pos, const ScoredParams& p, const
   u.seq = a;
   u.tiles = s_scan[a + 1] - s_scan[a];
   const int64_t first = HN * s_scan[a];
-  const int idx = static_cast<int>((pos - first) / u.tiles);
+  const int idx = static_cast<int>(quot(pos - first, u.tiles));
   u.kvh = idx / p.n_hsub;
   u.hsub = idx - u.kvh * p.n_hsub;
   u.u0 = first + static_cast<int64_t>(idx) * u.tiles;
@@ -460,16 +471,18 @@ __device__ __forceinline__ Unit locate(int64_t pos, const ScoredParams& p, const
 }  // namespace scored
 
 template <typename CT, int D, int NT>
-__global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D>::kThreads, 1)
+__global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
     scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const ScoredParams p) {
   using namespace scored;
   constexpr bool ONE = sizeof(CT) == 1;
   constexpr bool BF = std::is_same<CT, __nv_bfloat16>::value;
   constexpr int Q8 = std::is_same<CT, fp8e4m3>::value ? 1 : 2;
-  using G = ScoredGeo<sizeof(CT), D>;
+  using G = ScoredGeo<sizeof(CT), D, NT>;
   constexpr int TS = G::kStageTiles, S = G::kStages, W = G::kWarps, NC = 8 * NT;
   constexpr uint32_t full = 0xffffffffu;
+  static_assert(static_cast<size_t>(S) * G::kStageBytes >= (D + 2) * NC * 4, "a warp's part fits its ring");
+  __shared__ int s_held[W];
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -502,12 +515,19 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D>::kThreads, 1)
   }
 
   const int64_t N = static_cast<int64_t>(p.n_kv_heads) * p.n_hsub * s_scan[p.batch];
-  const int64_t most = (N + p.min_tiles - 1) / p.min_tiles;
+  const int64_t most = quot(N + p.min_tiles - 1, p.min_tiles);
   const int64_t We = most < p.workers ? most : p.workers;
-  // consecutive workers sit on different SMs, so that few workers spread out
-  const int64_t wk = static_cast<int64_t>(w) * gridDim.x + blockIdx.x;
-  if (wk >= We) return;
-  const int64_t lo = wk * N / We, hi = (wk + 1) * N / We;
+  // K workers per CTA, so that few workers spread over all SMs
+  const int K = static_cast<int>(quot(We + gridDim.x - 1, gridDim.x));
+  const int64_t wk = static_cast<int64_t>(blockIdx.x) * K + w;
+  const bool works = w < K && wk < We;
+  // Merging the CTA's parts costs every CTA a barrier and about 2 us at its
+  // end; it pays where a query would otherwise have many records to merge
+  // (e4m3, one sequence of 131071 rows: 77 -> 69 us; batch 32 x U[512, 4096],
+  // seven records each: 37 -> 39 us).
+  const int64_t n_units = static_cast<int64_t>(p.batch) * p.n_kv_heads * p.n_hsub;
+  const bool merge = K > 1 && We > 16 * n_units;
+  const int64_t lo = works ? quot(wk * N, We) : 0, hi = works ? quot((wk + 1) * N, We) : 0;
   const int tpb = p.block_size / kTileRows;  // tiles per cache block
   const uint64_t pol = policy_evict_first();
 
@@ -582,6 +602,7 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D>::kThreads, 1)
   uint32_t slot = 0, ph = 0;
   int used = 0;
   bool ok = true;
+  int held = -1;  // the unit of the part at the range's end
   const int lanes_g = lane >> 2, c = lane & 3;
   for (int64_t pos = lo; ok && pos < hi;) {
     const Unit u = locate(pos, p, s_scan);
@@ -680,16 +701,10 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D>::kThreads, 1)
         if ((ivalid >> (slot * TS + t)) & 1u) {
           const bool edge = rem < kTileRows + p.n_tok - 1;
           if constexpr (ONE) {
-            const float ks = s_scale[(slot * TS + t) * 2], vs = s_scale[(slot * TS + t) * 2 + 1];
-            if (edge)
-              tile8<Q8, D, NT, true>(kt, vt, rem, ks, vs, lg, p.qns, col0, p.qn, st, lane);
-            else
-              tile8<Q8, D, NT, false>(kt, vt, rem, ks, vs, lg, p.qns, col0, p.qn, st, lane);
+            const float* sc = s_scale + (slot * TS + t) * 2;
+            tile8<Q8, D, NT>(kt, vt, rem, edge, sc[0], sc[1], lg, p.qns, col0, p.qn, st, lane);
           } else {
-            if (edge)
-              tile16<BF, D, NT, true>(kt, vt, rem, p.qscale, lg, p.qns, col0, p.qn, st, lane);
-            else
-              tile16<BF, D, NT, false>(kt, vt, rem, p.qscale, lg, p.qns, col0, p.qn, st, lane);
+            tile16<BF, D, NT>(kt, vt, rem, edge, p.qscale, lg, p.qns, col0, p.qn, st, lane);
           }
         } else if (lg != nullptr) {  // a block outside the pool: its rows get no weight
           const int cols = min(NC, p.qns - col0);
@@ -707,16 +722,34 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D>::kThreads, 1)
     }
     if (!ok) break;
 
-    // ---- close the segment
+    // ---- close the segment. A whole unit: its outputs. A part that ends
+    // inside the range (the unit began in an earlier worker's): record 2 wk.
+    // The part at the range's end: merged with its neighbours' below.
     const int64_t begin = u.u0 > lo ? u.u0 : lo;
-    const bool whole = begin == u.u0 && pos == u.u0 + u.tiles;
     const int64_t unit = (static_cast<int64_t>(u.seq) * p.n_kv_heads + u.kvh) * p.n_hsub + u.hsub;
-    const int64_t rec = 2 * wk + (begin == lo ? 0 : 1);
+    const bool whole = begin == u.u0 && pos == u.u0 + u.tiles;
     if (lane == 0 && begin == u.u0) {
-      const int64_t c1 = whole ? wk : ((u.u0 + u.tiles) * We - 1) / N;  // the worker that holds the last tile
-      p.units[unit] = make_int4(whole ? kUnitWhole : static_cast<int>(rec), static_cast<int>(wk + 1),
-                                static_cast<int>(c1), 0);
+      int4 info = make_int4(kUnitWhole, 0, 0, 0);
+      if (!whole) {
+        const int64_t last = u.u0 + u.tiles;  // behind its last tile
+        const int64_t c1 = quot(last * We - 1, N);  // the worker that holds it
+        info = make_int4(static_cast<int>(wk), static_cast<int>(c1), last < quot((c1 + 1) * N, We) ? 1 : 0,
+                         merge ? K : 1);
+      }
+      p.units[unit] = info;
     }
+    // The part at the range's end goes to this warp's ring (all its copies have
+    // landed) if it is to be merged.
+    const bool last_part = !whole && pos == hi, keep = last_part && merge;
+    float* so = reinterpret_cast<float*>(smem + static_cast<size_t>(w) * S * G::kStageBytes);
+    const int64_t rec = 2 * wk + (last_part ? 1 : 0);
+    if (keep) __syncwarp();
+    // dims of the lane's values: 16-bit caches 16 i + g (+ 8), one-byte caches
+    // [span] + (span / 8) g + 2 i (+ 1)
+    constexpr int BOXB = D < 128 ? D : 128;
+    constexpr int KS = BOXB / 16;
+    auto dim = [&](int i) { return ONE ? (i / KS) * BOXB + (BOXB / 8) * lanes_g + 2 * (i % KS) : 16 * i + lanes_g; };
+    constexpr int SECOND = ONE ? 1 : 8;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -728,35 +761,41 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D>::kThreads, 1)
         if (v >= p.qn) continue;
         float f = 1.f;
         if constexpr (ONE) f = fast_exp2(st.mo[n][e] - st.m[n][e]);
-        // dims of the lane's values: 16-bit caches 16 i + g (+ 8), one-byte
-        // caches [span] + (span / 8) g + 2 i (+ 1)
-        constexpr int BOXB = D < 128 ? D : 128;
-        constexpr int KS = BOXB / 16;
-        auto dim = [&](int i) {
-          return ONE ? (i / KS) * BOXB + (BOXB / 8) * lanes_g + 2 * (i % KS) : 16 * i + lanes_g;
-        };
-        constexpr int SECOND = ONE ? 1 : 8;
-        if (whole) {
-          const int64_t row = query_row(p, u.seq, u.kvh, v);
-          const float inv = l == 0.f ? 0.f : f / l;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            store_out(p.out, row * D + dim(i), st.o[n][i][e] * inv, p.out_dtype);
-            store_out(p.out, row * D + dim(i) + SECOND, st.o[n][i][e + 2] * inv, p.out_dtype);
-          }
-          if (p.scores != nullptr && lanes_g == 0) p.lse[row] = st.m[n][e] + fast_log2(l);
-        } else {
-          float* ro = p.rec_o + (rec * NC + col) * D;
+        if (!whole) {
+          float* ro = keep ? so + col * D : p.rec_o + (rec * NC + col) * D;
+          float* ml = keep ? so + NC * D + 2 * col : p.rec_ml + (rec * NC + col) * 2;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             ro[dim(i)] = st.o[n][i][e] * f;
             ro[dim(i) + SECOND] = st.o[n][i][e + 2] * f;
           }
-          if (lanes_g == 0)
-            *reinterpret_cast<float2*>(p.rec_ml + (rec * NC + col) * 2) = make_float2(st.m[n][e], l);
+          if (lanes_g == 0) *reinterpret_cast<float2*>(ml) = make_float2(st.m[n][e], l);
+          continue;
         }
+        const int64_t row = query_row(p, u.seq, u.kvh, v);
+        const float inv = l == 0.f ? 0.f : f / l;
+        if (p.out_dtype == KVC_F32) {
+          float* to = static_cast<float*>(p.out) + row * D;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            to[dim(i)] = st.o[n][i][e] * inv;
+            to[dim(i) + SECOND] = st.o[n][i][e + 2] * inv;
+          }
+        } else {
+          unsigned short* to = static_cast<unsigned short*>(p.out) + row * D;
+          const bool f16 = p.out_dtype == KVC_F16;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const float a = st.o[n][i][e] * inv, b = st.o[n][i][e + 2] * inv;
+            const uint32_t x = f16 ? wmma16::pack2<false>(a, b) : wmma16::pack2<true>(a, b);
+            to[dim(i)] = static_cast<unsigned short>(x);
+            to[dim(i) + SECOND] = static_cast<unsigned short>(x >> 16);
+          }
+        }
+        if (p.scores != nullptr && lanes_g == 0) p.lse[row] = st.m[n][e] + fast_log2(l);
       }
     }
+    if (keep) held = static_cast<int>(unit);
   }
   if (!ok) {
     // Gave up: report it and wait (bounded) for this warp's own copies still in
@@ -769,48 +808,201 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D>::kThreads, 1)
     }
   }
   if constexpr (ONE) cp_async_wait<0>();
+
+  // ---- merge the parts at the ends of the CTA's ranges: neighbouring warps
+  // that hold the same unit leave one record, 2 (first warp's worker) + 1
+  if (!merge) return;  // the same in every warp of the grid
+  if (lane == 0) s_held[w] = held;
+  __syncthreads();
+  for (int a = 0; a < K;) {
+    const int unit = s_held[a];
+    int b = a + 1;
+    while (b < K && s_held[b] == unit) ++b;
+    if (unit >= 0) {
+      const int64_t rec = 2 * (static_cast<int64_t>(blockIdx.x) * K + a) + 1;
+      const int cols = min(NC, p.qn - (unit % p.n_hsub) * NC);
+      auto part = [&](int i) {
+        return reinterpret_cast<const float*>(smem + static_cast<size_t>(i) * S * G::kStageBytes);
+      };
+      for (int i = tid; i < cols * (D / 4); i += G::kThreads) {
+        const int col = i / (D / 4), d = 4 * (i % (D / 4));
+        float m = kNegInf;
+        for (int x = a; x < b; ++x) m = fmaxf(m, part(x)[NC * D + 2 * col]);
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x = a; x < b; ++x) {
+          const float f = fast_exp2(part(x)[NC * D + 2 * col] - m);
+          const float4 y = *reinterpret_cast<const float4*>(part(x) + col * D + d);
+          l += f * part(x)[NC * D + 2 * col + 1];
+          o.x += f * y.x;
+          o.y += f * y.y;
+          o.z += f * y.z;
+          o.w += f * y.w;
+        }
+        *reinterpret_cast<float4*>(p.rec_o + (rec * NC + col) * D + d) = o;
+        if (d == 0) *reinterpret_cast<float2*>(p.rec_ml + (rec * NC + col) * 2) = make_float2(m, l);
+      }
+    }
+    a = b;
+  }
 }
 
 // ------------------------------------------------------------------ finish
 //
-// One grid column (blockIdx.x) per unit of (sequence, kv head), gridDim.y CTAs
-// each. They share the unit's queries: o_v = sum_r 2^(m_r - M) O_r / sum_r
-// 2^(m_r - M) l_r over the records r of v, one warp per query while there are
-// few records and the whole CTA otherwise; and its rows: score += sum_v
-// 2^(x - lse_v), lanes over the queries of a row, in a fixed order. Bound by
-// the scores' and logits' bytes (which mostly sit in L2) and, for small calls,
-// by three dependent loads.
+// One grid column (blockIdx.x) per unit of (sequence, kv head). The first
+// out_ctas CTAs of a column share the unit's queries: o_v = sum_r 2^(m_r - M)
+// O_r / sum_r 2^(m_r - M) l_r over the records r of v, one warp per query while
+// a warp's lanes hold its records, the whole CTA beyond. The others share its
+// rows: score += sum_v 2^(x - lse_v), lanes over the queries of a row, in a
+// fixed order. Every step loads what it needs at once: bound by the scores' and
+// logits' bytes (which mostly sit in L2), for small calls by the chain unit ->
+// maxima -> outputs, or logits, of three loads.
 constexpr int kFinishThreads = 256;
-constexpr int kFinishRows = 512;  // cached rows per step of a CTA
-constexpr int kFewRecords = 8;
+constexpr int kFinishWarps = kFinishThreads / 32;
+// cached rows a CTA takes at least: about 4 KB of scores, 16 KB of wide rows
+__host__ __device__ inline int finish_rows(int qns) { return qns <= 8 ? 256 : qns <= 32 ? 128 : 64; }
+constexpr int kFewRecords = 16;
+constexpr int kFinishCtas = 4 * 152;  // what the GPU holds at once, about
 
-// Records of a query's unit: first slot, then 2 a, 2 (a + 1), ... (n in all).
+// Records of a query's unit: one per CTA from CTA `cta` on, left by the first
+// of its workers that held the unit's end of range, then perhaps the last worker's own.
 struct RecList {
-  int first, a, n;
+  int first, cta, K, merged, n, last;
 };
 __device__ __forceinline__ RecList record_list(const int4 u, int workers) {
   RecList r;
-  r.first = u.x;
-  r.a = u.y;
   r.n = 0;
   // entries outside the workspace (left by a call that gave up) are not followed
-  if (u.x >= 0 && u.x < 2 * workers && u.y >= 0 && u.z >= u.y - 1 && u.z < workers) r.n = u.z - u.y + 2;
+  if (u.x < 0 || u.y < u.x || u.y >= workers || u.w < 1 || u.w > 32) return r;
+  r.first = u.x;
+  r.last = u.y;
+  r.K = u.w;
+  r.cta = u.x / u.w;
+  const int end = u.y / u.w;
+  r.merged = end - r.cta + 1;
+  // the last worker's part is a record of its own: none from its CTA if it comes first there
+  if (u.z != 0 && max(u.x, end * u.w) == u.y) --r.merged;
+  r.n = r.merged + (u.z != 0 ? 1 : 0);
   return r;
 }
 __device__ __forceinline__ int64_t record_slot(const RecList& r, int i) {
-  return i == 0 ? r.first : 2 * static_cast<int64_t>(r.a + i - 1);
+  return i < r.merged ? 2 * static_cast<int64_t>(max(r.first, (r.cta + i) * r.K)) + 1 : 2 * static_cast<int64_t>(r.last);
+}
+
+// V consecutive floats (V 2, 4 or 8; aligned to 8 or 16 bytes).
+template <int V>
+__device__ __forceinline__ void load_floats(const float* p, float (&x)[V]) {
+  if constexpr (V == 2) {
+    const float2 t = __ldcg(reinterpret_cast<const float2*>(p));
+    x[0] = t.x;
+    x[1] = t.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 t = __ldcg(reinterpret_cast<const float4*>(p + i));
+      x[i] = t.x;
+      x[i + 1] = t.y;
+      x[i + 2] = t.z;
+      x[i + 3] = t.w;
+    }
+  }
+}
+
+// log2 of a softmax denominator as the rows use it: without any weight (an
+// empty sum) it is +inf, so that 2^(x - lse) is 0.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  const float lse = m + scored::fast_log2(l);
+  return lse == kNegInf ? -kNegInf : lse;
+}
+
+// Adds the weights of the rows [r0, r1) of one (sequence, kv head) to their
+// scores. SUB lanes share a row, W (2 or 4) of its queries at a time; ONCE: that
+// covers all of them. e: the queries' log2 denominators, +inf past the last.
+template <int W, int SUB, bool ONCE>
+__device__ __forceinline__ void add_weights(const float* lg, float* sc, const float* e, int r0, int r1, int n_old,
+                                            int qns) {
+  constexpr int U = 4;                       // rows in flight per lane
+  constexpr int PER = kFinishThreads / SUB;  // rows per pass
+  const int sl = threadIdx.x % SUB, tr = threadIdx.x / SUB;
+  float ee[W];
+  bool ready = false;  // e is complete
+  for (int rb = r0 + tr; rb - tr < r1; rb += PER * U) {
+    float s[U], old[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      s[u] = 0.f;
+      old[u] = rb + u * PER < r1 && rb + u * PER < n_old && sl == 0 ? sc[rb + u * PER] : 0.f;
+    }
+    for (int k = W * sl; ONCE || k - W * sl < qns; k += W * SUB) {
+      float x[U][W];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) x[u][i] = 0.f;
+        if (rb + u * PER < r1 && k < qns) {
+          const float* at = lg + static_cast<int64_t>(rb + u * PER) * qns + k;
+          if constexpr (W == 4) {
+            const float4 t = __ldcg(reinterpret_cast<const float4*>(at));
+            x[u][0] = t.x;
+            x[u][1] = t.y;
+            x[u][2] = t.z;
+            x[u][3] = t.w;
+          } else {
+            const float2 t = __ldcg(reinterpret_cast<const float2*>(at));
+            x[u][0] = t.x;
+            x[u][1] = t.y;
+          }
+        }
+      }
+      if (!ONCE || !ready) {
+        if (!ready) __syncthreads();
+        ready = true;
+#pragma unroll
+        for (int i = 0; i < W; ++i) ee[i] = k < qns ? e[k + i] : -kNegInf;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) s[u] += fast_exp2(x[u][i] - ee[i]);
+      }
+      if constexpr (ONCE) break;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int o = SUB / 2; o > 0; o /= 2) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+      // the call's own rows are new: their weight starts here (old is 0)
+      if (rb + u * PER < r1 && sl == 0) sc[rb + u * PER] = old[u] + s[u];
+    }
+  }
+}
+
+template <int W>
+__device__ __forceinline__ void add_weights(const float* lg, float* sc, const float* e, int r0, int r1, int n_old,
+                                            int qns) {
+  const int vecs = qns / W;
+  if (vecs <= 1) add_weights<W, 1, true>(lg, sc, e, r0, r1, n_old, qns);
+  else if (vecs <= 2) add_weights<W, 2, true>(lg, sc, e, r0, r1, n_old, qns);
+  else if (vecs <= 4) add_weights<W, 4, true>(lg, sc, e, r0, r1, n_old, qns);
+  else if (vecs <= 8) add_weights<W, 8, true>(lg, sc, e, r0, r1, n_old, qns);
+  else add_weights<W, 32, false>(lg, sc, e, r0, r1, n_old, qns);
 }
 
 template <int D>
-__global__ void __launch_bounds__(kFinishThreads) scored_finish_kernel(const ScoredParams p, int NC) {
+__global__ void __launch_bounds__(kFinishThreads) scored_finish_kernel(const ScoredParams p, int nc_log2,
+                                                                        int out_ctas) {
   using namespace scored;
+  const int NC = 1 << nc_log2;  // queries of a column group
   constexpr int V = D / 32;  // output dims per lane
-  extern __shared__ float s_lse[];  // [qn]
-  __shared__ float s_m[8], s_l[8], s_o[8][D];
+  constexpr int U = D > 128 ? 4 : 8;  // records' outputs in flight per warp
+  constexpr uint32_t full = 0xffffffffu;
+  extern __shared__ float s_dyn[];  // [max(qns, records of a unit)]
+  __shared__ float s_red[2][kFinishWarps], s_o[kFinishWarps][D];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int64_t pair = blockIdx.x;
-  const int seq = static_cast<int>(pair / p.n_kv_heads), kvh = static_cast<int>(pair % p.n_kv_heads);
+  const int seq = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.n_kv_heads));
+  const int kvh = static_cast<int>(blockIdx.x) - seq * p.n_kv_heads;
   const int4* units = p.units + pair * p.n_hsub;
   auto store = [&](int v, const float (&o)[V], float inv) {
     float val[V];
@@ -820,145 +1012,174 @@ __global__ void __launch_bounds__(kFinishThreads) scored_finish_kernel(const Sco
   };
 
   // ---- outputs, one warp per query
-  for (int v = blockIdx.y * 8 + w; v < p.qn; v += gridDim.y * 8) {
-    const int4 u = units[v / NC];
-    const int col = v % NC;
-    float o[V];
+  if (static_cast<int>(blockIdx.y) < out_ctas) {
+    for (int v = blockIdx.y * kFinishWarps + w; v < p.qn; v += out_ctas * kFinishWarps) {
+      const int4 u = __ldcg(units + (v >> nc_log2));
+      const int col = (v & (NC - 1));
+      float o[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = 0.f;
-    if (u.x == kUnitEmpty) {
-      store(v, o, 0.f);
-      continue;
-    }
-    const RecList r = record_list(u, p.workers);
-    if (r.n == 0 || r.n > kFewRecords) continue;
-    float m = kNegInf, l = 0.f;
-    if (lane < r.n) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.rec_ml + (record_slot(r, lane) * NC + col) * 2);
-      m = ml.x;
-      l = ml.y;
-    }
-    const float M = warp_max(m);
-    const float f = lane < r.n ? fast_exp2(m - M) : 0.f;
-    const float L = warp_sum(f * l);
-    for (int i = 0; i < r.n; ++i) {
-      const float fi = __shfl_sync(0xffffffffu, f, i);
-      const float* ro = p.rec_o + (record_slot(r, i) * NC + col) * D + V * lane;
+      for (int i = 0; i < V; ++i) o[i] = 0.f;
+      if (u.x == kUnitEmpty) {
+        store(v, o, 0.f);
+        continue;
+      }
+      const RecList r = record_list(u, p.workers);
+      if (r.n == 0 || r.n > 32) continue;
+      float m = kNegInf, l = 0.f;
+      if (lane < r.n) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.rec_ml + (record_slot(r, lane) * NC + col) * 2));
+        m = ml.x;
+        l = ml.y;
+      }
+      const float M = warp_max(m);
+      const float f = lane < r.n ? fast_exp2(m - M) : 0.f;
+      const float L = warp_sum(f * l);
+      for (int i0 = 0; i0 < r.n; i0 += U) {
+        float x[U][V];
 #pragma unroll
-      for (int k = 0; k < V; ++k) o[k] += fi * ro[k];
-    }
-    store(v, o, L == 0.f ? 0.f : 1.0f / L);
-  }
-  // ---- outputs of units with many records, the whole CTA per query
-  for (int v = blockIdx.y; v < p.qn; v += gridDim.y) {
-    const RecList r = record_list(units[v / NC], p.workers);
-    if (r.n <= kFewRecords) continue;
-    const int col = v % NC;
-    float m = kNegInf, l = 0.f;  // online over this warp's records, lanes over the dims
-    float o[V];
+        for (int i = 0; i < U; ++i)
+          if (i0 + i < r.n) load_floats<V>(p.rec_o + (record_slot(r, i0 + i) * NC + col) * D + V * lane, x[i]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = 0.f;
-    for (int i = w; i < r.n; i += 8) {
-      const int64_t at = record_slot(r, i) * NC + col;
-      const float2 ml = *reinterpret_cast<const float2*>(p.rec_ml + at * 2);
-      const float M = fmaxf(m, ml.x);
-      const float a = fast_exp2(m - M), b = fast_exp2(ml.x - M);
-      m = M;
-      l = l * a + ml.y * b;
-      const float* ro = p.rec_o + at * D + V * lane;
+        for (int i = 0; i < U; ++i) {
+          const float fi = __shfl_sync(full, f, min(i0 + i, 31));
+          if (i0 + i < r.n) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) o[k] = o[k] * a + ro[k] * b;
-    }
-    __syncthreads();
-    if (lane == 0) {
-      s_m[w] = m;
-      s_l[w] = l;
-    }
-#pragma unroll
-    for (int k = 0; k < V; ++k) s_o[w][V * lane + k] = o[k];
-    __syncthreads();
-    if (w == 0) {
-      float M = kNegInf, L = 0.f;
-      for (int i = 0; i < 8; ++i) M = fmaxf(M, s_m[i]);
-#pragma unroll
-      for (int k = 0; k < V; ++k) o[k] = 0.f;
-      for (int i = 0; i < 8; ++i) {
-        const float b = fast_exp2(s_m[i] - M);  // r.n > 8: every warp had a record
-        L += s_l[i] * b;
-#pragma unroll
-        for (int k = 0; k < V; ++k) o[k] += s_o[i][V * lane + k] * b;
+            for (int k = 0; k < V; ++k) o[k] += fi * x[i][k];
+          }
+        }
       }
       store(v, o, L == 0.f ? 0.f : 1.0f / L);
     }
+    // ---- outputs of units with many records, the whole CTA per query
+    for (int v = blockIdx.y; v < p.qn; v += out_ctas) {
+      const RecList r = record_list(__ldcg(units + (v >> nc_log2)), p.workers);
+      if (r.n <= 32) continue;
+      const int col = (v & (NC - 1));
+      float m = kNegInf;
+      __syncthreads();  // the previous query's shared values have been read
+      for (int i = tid; i < r.n; i += kFinishThreads) {
+        const float mi = __ldcg(p.rec_ml + (record_slot(r, i) * NC + col) * 2);
+        s_dyn[i] = mi;
+        m = fmaxf(m, mi);
+      }
+      m = warp_max(m);
+      if (lane == 0) s_red[0][w] = m;
+      __syncthreads();
+      m = s_red[0][0];
+      for (int i = 1; i < kFinishWarps; ++i) m = fmaxf(m, s_red[0][i]);
+      float l = 0.f;
+      for (int i = tid; i < r.n; i += kFinishThreads) {
+        const float f = fast_exp2(s_dyn[i] - m);
+        l += f * __ldcg(p.rec_ml + (record_slot(r, i) * NC + col) * 2 + 1);
+        s_dyn[i] = f;
+      }
+      l = warp_sum(l);
+      if (lane == 0) s_red[1][w] = l;
+      __syncthreads();
+      float o[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] = 0.f;
+      for (int i0 = w; i0 < r.n; i0 += kFinishWarps * U) {
+        float x[U][V];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int j = i0 + i * kFinishWarps;
+          if (j < r.n) load_floats<V>(p.rec_o + (record_slot(r, j) * NC + col) * D + V * lane, x[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int j = i0 + i * kFinishWarps;
+          if (j < r.n) {
+            const float f = s_dyn[j];
+#pragma unroll
+            for (int k = 0; k < V; ++k) o[k] += f * x[i][k];
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < V; ++k) s_o[w][V * lane + k] = o[k];
+      __syncthreads();
+      if (w == 0) {
+        float L = 0.f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) o[k] = 0.f;
+        for (int i = 0; i < kFinishWarps; ++i) {
+          L += s_red[1][i];
+#pragma unroll
+          for (int k = 0; k < V; ++k) o[k] += s_o[i][V * lane + k];
+        }
+        store(v, o, L == 0.f ? 0.f : 1.0f / L);
+      }
+    }
+    return;
   }
-  if (p.scores == nullptr) return;
+
+  // ---- rows
   const int n = valid_rows(p, seq);
-  if (static_cast<int>(blockIdx.y) * kFinishRows >= n) return;
+  const int row_ctas = gridDim.y - out_ctas, y = blockIdx.y - out_ctas;
+  const int stretch = max(finish_rows(p.qns), ((n + row_ctas - 1) / row_ctas + 31) / 32 * 32);
+  const int64_t first = static_cast<int64_t>(y) * stretch;
+  if (first >= n) return;
+  const int r0 = static_cast<int>(first), r1 = min(n, r0 + stretch);
 
   // ---- log2 of the queries' softmax denominators: a thread per query with
   // few records, a warp per query with many
+  bool many = false;
   for (int v = tid; v < p.qn; v += kFinishThreads) {
-    const int4 u = units[v / NC];
-    float lse = kNegInf;
+    const int4 u = __ldcg(units + (v >> nc_log2));
     if (u.x == kUnitWhole) {
-      lse = p.lse[query_row(p, seq, kvh, v)];
-    } else {
-      const RecList r = record_list(u, p.workers);
-      if (r.n > kFewRecords) continue;
+      s_dyn[v] = row_lse(__ldcg(p.lse + query_row(p, seq, kvh, v)), 1.f);
+      continue;
+    }
+    const RecList r = record_list(u, p.workers);
+    if (r.n > kFewRecords) {
+      many = true;
+      continue;
+    }
+    float m = kNegInf, l = 0.f;
+    for (int i0 = 0; i0 < r.n; i0 += 4) {
+      float2 ml[4];
+      float M = m;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ml[i] = make_float2(kNegInf, 0.f);
+        if (i0 + i < r.n)
+          ml[i] = __ldcg(reinterpret_cast<const float2*>(p.rec_ml + (record_slot(r, i0 + i) * NC + (v & (NC - 1))) * 2));
+        M = fmaxf(M, ml[i].x);
+      }
+      l *= fast_exp2(m - M);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i0 + i < r.n) l += ml[i].y * fast_exp2(ml[i].x - M);
+      m = M;
+    }
+    s_dyn[v] = row_lse(m, l);
+  }
+  if (__syncthreads_or(many)) {
+    for (int v = w; v < p.qn; v += kFinishWarps) {
+      const RecList r = record_list(__ldcg(units + (v >> nc_log2)), p.workers);
+      if (r.n <= kFewRecords) continue;
       float m = kNegInf, l = 0.f;
-      for (int i = 0; i < r.n; ++i) {
-        const float2 ml = *reinterpret_cast<const float2*>(p.rec_ml + (record_slot(r, i) * NC + v % NC) * 2);
+      for (int i = lane; i < r.n; i += 32) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.rec_ml + (record_slot(r, i) * NC + (v & (NC - 1))) * 2));
         const float M = fmaxf(m, ml.x);
         l = l * fast_exp2(m - M) + ml.y * fast_exp2(ml.x - M);
         m = M;
       }
-      if (r.n > 0) lse = m + fast_log2(l);
+      const float M = warp_max(m);
+      const float L = warp_sum(m == kNegInf ? 0.f : l * fast_exp2(m - M));
+      if (lane == 0) s_dyn[v] = row_lse(M, L);
     }
-    s_lse[v] = lse == kNegInf ? -kNegInf : lse;  // no weight at all: 2^(x - inf) = 0
   }
-  for (int v = w; v < p.qn; v += 8) {
-    const RecList r = record_list(units[v / NC], p.workers);
-    if (r.n <= kFewRecords) continue;
-    float m = kNegInf, l = 0.f;
-    for (int i = lane; i < r.n; i += 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.rec_ml + (record_slot(r, i) * NC + v % NC) * 2);
-      const float M = fmaxf(m, ml.x);
-      l = l * fast_exp2(m - M) + ml.y * fast_exp2(ml.x - M);
-      m = M;
-    }
-    const float M = warp_max(m);
-    const float L = warp_sum(m == kNegInf ? 0.f : l * fast_exp2(m - M));
-    const float lse = M + fast_log2(L);
-    if (lane == 0) s_lse[v] = lse == kNegInf ? -kNegInf : lse;
-  }
-  __syncthreads();
+  if (tid == 0 && p.qns > p.qn) s_dyn[p.qn] = -kNegInf;
+  // (add_weights waits for the CTA's denominators when it has its first scores)
 
-  // ---- rows: sub lanes per row, each over pairs of queries
-  const int pairs = p.qns / 2;
-  int sub = 1;
-  while (sub < 32 && sub < pairs) sub *= 2;
-  const int per = kFinishThreads / sub;  // rows per pass
-  const int sl = tid % sub;
   const float* lg = p.logits + pair * p.rows * p.qns;
   float* sc = p.scores + pair * p.rows;
-  for (int r0 = blockIdx.y * kFinishRows; r0 < n; r0 += gridDim.y * kFinishRows) {
-    const int r1 = min(n, r0 + kFinishRows);
-    for (int rb = r0; rb < r1; rb += per) {
-      const int r = rb + tid / sub;
-      float s = 0.f;
-      if (r < r1) {
-        const float2* row = reinterpret_cast<const float2*>(lg + static_cast<int64_t>(r) * p.qns);
-        for (int k = sl; k < pairs; k += sub) {
-          const float2 x = __ldcg(row + k);
-          s += fast_exp2(x.x - s_lse[2 * k]);
-          if (2 * k + 1 < p.qn) s += fast_exp2(x.y - s_lse[2 * k + 1]);
-        }
-      }
-      for (int o = sub / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-      // the call's own rows are new: their weight starts here
-      if (r < r1 && sl == 0) sc[r] = r < n - p.n_tok ? sc[r] + s : s;
-    }
-  }
+  if (p.qns % 4 == 0)
+    add_weights<4>(lg, sc, s_dyn, r0, r1, n - p.n_tok, p.qns);
+  else
+    add_weights<2>(lg, sc, s_dyn, r0, r1, n - p.n_tok, p.qns);
 }
 
 // ------------------------------------------------------------------ launch
@@ -967,7 +1188,7 @@ namespace scored {
 
 template <typename CT, int D, int NT>
 kvc_status run(const ScoredParams& p, int grid, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
-  using G = ScoredGeo<sizeof(CT), D>;
+  using G = ScoredGeo<sizeof(CT), D, NT>;
   auto* k = scored_decode_kernel<CT, D, NT>;
   // The opt-in to large shared memory holds per device: made at the first call on each.
   static std::atomic<uint64_t> opted{0};
@@ -977,7 +1198,7 @@ kvc_status run(const ScoredParams& p, int grid, const CUtensorMap& tk, const CUt
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if ((opted.load() & bit) == 0) {
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(scored_smem_bytes<sizeof(CT), D>(kScoredMaxBatch)));
+                             static_cast<int>(scored_smem_bytes<sizeof(CT), D, NT>(kScoredMaxBatch)));
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(scored decode)");
     opted.fetch_or(bit);
   }
@@ -987,26 +1208,35 @@ kvc_status run(const ScoredParams& p, int grid, const CUtensorMap& tk, const CUt
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(G::kThreads);
-  cfg.dynamicSmemBytes = scored_smem_bytes<sizeof(CT), D>(p.batch);
+  cfg.dynamicSmemBytes = scored_smem_bytes<sizeof(CT), D, NT>(p.batch);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, k, tk, tv, p);
   if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx(scored decode)");
-  // CTAs per (sequence, kv head): enough to fill the GPU, no more than there is work for
+  // CTAs per (sequence, kv head): one wave of them on the GPU, no more than
+  // there is work for. For the outputs a warp per query or a few of them in
+  // turn, or up to a CTA per query where few units share all workers and a
+  // query may have more than 32 records; the rest for the rows.
   const int64_t pairs = static_cast<int64_t>(p.batch) * p.n_kv_heads;
-  const int64_t want = (8 * 152 + pairs - 1) / pairs;
-  int64_t most = (p.qn + 7) / 8;
-  if (grid > 1 && p.qn > most) most = p.qn;
-  if (p.scores != nullptr) most = std::max<int64_t>(most, (p.rows + kFinishRows - 1) / kFinishRows);
+  const int64_t want = std::max<int64_t>(1, kFinishCtas / pairs);
+  int64_t out_ctas = (p.qn + kFinishWarps - 1) / kFinishWarps;
+  if (pairs * 32 < p.workers)
+    out_ctas = std::max(out_ctas, std::min<int64_t>(want, p.qn));
+  else if (p.scores != nullptr)
+    out_ctas = std::max<int64_t>(1, std::min(out_ctas, want / 4));
+  int64_t row_ctas = 0;
+  if (p.scores != nullptr)
+    row_ctas = std::max<int64_t>(1, std::min<int64_t>(want - std::min(want / 4, out_ctas),
+                                                      (p.rows + finish_rows(p.qns) - 1) / finish_rows(p.qns)));
   cudaLaunchConfig_t fin = {};
-  fin.gridDim = dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(std::max<int64_t>(1, std::min(want, most))));
+  fin.gridDim = dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(out_ctas + row_ctas));
   fin.blockDim = dim3(kFinishThreads);
-  fin.dynamicSmemBytes = p.scores != nullptr ? static_cast<size_t>(p.qn) * 4 : 0;
+  fin.dynamicSmemBytes = static_cast<size_t>(std::max(p.qns, p.workers + 1)) * 4;
   fin.stream = stream;
   fin.attrs = attr;
   fin.numAttrs = 1;
-  e = cudaLaunchKernelEx(&fin, scored_finish_kernel<D>, p, 8 * NT);
+  e = cudaLaunchKernelEx(&fin, scored_finish_kernel<D>, p, NT == 1 ? 3 : 4, static_cast<int>(out_ctas));
   if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx(scored finish)");
   return KVC_OK;
 }

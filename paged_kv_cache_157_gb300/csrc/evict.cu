@@ -7,12 +7,12 @@
 // the rows stays, so windows and causal masks keep their meaning.
 //
 // select: one cluster of CTAs per (sequence, kv head). The scores become
-// unsigned keys of the same order; three counting passes over 11, 11 and 10
-// bits find the key T of the last row that stays and how many rows with that
+// unsigned keys of the same order; counting passes over 11 (in a
+// cluster 8) bits find the key T of the last row that stays and how many rows with that
 // key stay; a prefix sum over the rows writes the kept rows in order. A CTA
-// holds its share of the keys in shared memory, so a score is read once.
-// Bound by the passes' shared-memory atomics and the barriers between them; a
-// cluster splits a long row over up to 8 SMs.
+// holds its share of the keys in registers, so a score is read once (shares
+// beyond 8192 rows are read again each pass). Bound by the chain of passes and
+// barriers; a cluster splits a long row over up to 8 SMs.
 //
 // move: one warp per 32 kept rows (one block of the new table for one-byte
 // codes). Lanes look up the rows' addresses together, then move 16-byte chunks
@@ -44,7 +44,7 @@ struct EvictParams {
   int batch, n_heads, block_size, max_blocks, new_max_blocks;
   int rows, new_rows;           // max_blocks * block_size, new_max_blocks * block_size
   int budget, recent;
-  int row_chunks;               // 16-byte chunks of a cached row
+  int row_chunks, row_shift;    // 16-byte chunks of a cached row, log2 of it if it is a power of two
   unsigned int* err;
 };
 
@@ -63,20 +63,40 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 }
 
 constexpr int kSelectThreads = 512;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kKeys = 16;                            // keys a thread holds
+constexpr int kSpan = kKeys * kSelectThreads;        // keys a CTA holds
 constexpr int kBins = 2048;
-constexpr int kHeldKeys = 16384;  // keys a CTA holds in shared memory (64 KB)
+constexpr int kMaxCluster = 8;
 
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParams p) {
+// Inclusive prefix sum over the lanes.
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+__global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictParams p) {
+  constexpr uint32_t full = 0xffffffffu;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks()), cr = static_cast<int>(cluster.block_rank());
-  extern __shared__ uint32_t s_keys[];       // [kHeldKeys]
-  __shared__ uint32_t s_hist[kBins];
-  __shared__ uint32_t s_warp[2][kSelectThreads / 32];
-  __shared__ uint32_t s_found[2];            // digit, rows above it in this pass
-  __shared__ uint32_t s_total[2];            // this CTA's rows above T, and at T
+  __shared__ __align__(16) uint32_t s_hist[3 * kBins];  // a pass's counts behind the last one's
+  __shared__ uint32_t s_warp[kSelectWarps];
+  __shared__ uint32_t s_found[3];                   // digit, rows above it and with it in this pass
+  __shared__ uint32_t s_total[2];                   // this CTA's rows above T, and at T
+  __shared__ uint32_t s_cnt[kKeys][kSelectWarps];   // rows above T (low half) and at T of a warp's 32 keys
+  __shared__ uint32_t s_row[kKeys];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int64_t unit = blockIdx.x / C;
-  const int b = static_cast<int>(unit / p.n_heads);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  auto sync_all = [&]() {
+    if (C == 1) __syncthreads(); else cluster.sync();
+  };
+  const uint32_t unit32 = blockIdx.x / C;
+  const int64_t unit = unit32;
+  const int b = static_cast<int>(unit32 / p.n_heads);
   bool bad;
   const int n = rows_of(p, b, &bad);
   const int m = min(n, p.budget), recent = min(p.recent, m);
@@ -87,7 +107,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
   const int gt = cr * kSelectThreads + tid, gn = C * kSelectThreads;
   if (gt == 0) {
     if (bad) set_flag(p.err, KVC_FLAG_BAD_LEN);
-    if (unit % p.n_heads == 0) p.new_lens[b] = m;
+    if (unit32 % p.n_heads == 0) p.new_lens[b] = m;
   }
   for (int i = gt; i < recent; i += gn) kept[k + i] = cand + i;
   for (int i = m + gt; i < p.budget; i += gn) kept[i] = -1;
@@ -96,109 +116,165 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
     return;
   }
 
-  // this CTA's rows: a stretch of the candidates
+  // this CTA's rows: a stretch of the candidates, in spans of kSpan keys; the
+  // keys of the only span stay in registers, several are read again each pass
   const int per = (cand + C - 1) / C;
-  const int lo = min(cand, cr * per), hi = min(cand, lo + per);
-  const int cnt = hi - lo;
-  const bool held = per <= kHeldKeys;
-  auto key = [&](int i) { return held ? s_keys[i] : key_of(__ldg(scores + lo + i)); };
-  if (held)
-    for (int i = tid; i < cnt; i += kSelectThreads) s_keys[i] = key_of(__ldg(scores + lo + i));
+  // (never empty: a CTA beyond the candidates takes none of the last row)
+  const int lo = min(cand - 1, cr * per), cnt = min(cand - lo, cr * per < cand ? per : 0);
+  const int spans = max(1, (cnt + kSpan - 1) / kSpan);
+  uint32_t key[kKeys];  // of row lo + span * kSpan + j * kSelectThreads + tid
+  auto load = [&](int span) {
+    float x[kKeys];  // all loads first (of the last row where there is none): no branch between them
+#pragma unroll
+    for (int j = 0; j < kKeys; ++j) x[j] = __ldg(scores + lo + min(span * kSpan + j * kSelectThreads + tid, max(cnt, 1) - 1));
+#pragma unroll
+    for (int j = 0; j < kKeys; ++j) key[j] = key_of(x[j]);
+  };
+  auto valid = [&](int span, int j) { return span * kSpan + j * kSelectThreads + tid < cnt; };
+  load(0);
+  for (int i = tid; i < (C == 1 ? 3 * kBins : 4 * 256); i += kSelectThreads) s_hist[i] = 0;
+  if (tid < 2) s_total[tid] = 0;
+  __syncthreads();
 
+  // digits of 11, 11 and 10 bits, or of 8 in a cluster, whose CTAs read each
+  // other's counts: 2048 bins of 8 CTAs took 4500 cycles a pass, mostly that
+  const int width = C == 1 ? 11 : 8, passes = C == 1 ? 3 : 4;
   uint32_t prefix = 0, need = static_cast<uint32_t>(k);  // T's leading bits, places left among rows that match them
+  uint32_t at_t = 0;                                     // rows that match them
   int shift = 32;
-  for (int pass = 0; pass < 3; ++pass) {
-    const int bits = pass < 2 ? 11 : 10;
+  for (int pass = 0; pass < passes; ++pass) {
+    const int bits = min(width, shift);
     shift -= bits;
-    for (int i = tid; i < kBins; i += kSelectThreads) s_hist[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < cnt; i += kSelectThreads) {
-      const uint32_t x = key(i);
-      if (pass == 0 || (x >> (shift + bits)) == prefix) atomicAdd(&s_hist[(x >> shift) & ((1u << bits) - 1u)], 1u);
+    uint32_t* hist = s_hist + (pass << width);
+    for (int span = 0; span < spans; ++span) {
+      if (spans > 1) load(span);
+#pragma unroll
+      for (int j = 0; j < kKeys; ++j) {
+        if (span * kSpan + j * kSelectThreads >= cnt) break;  // short rows: nothing to do for any thread
+        if (valid(span, j) && (pass == 0 || (key[j] >> (shift + bits)) == prefix))
+          atomicAdd(&hist[(key[j] >> shift) & ((1u << bits) - 1u)], 1u);
+      }
     }
-    cluster.sync();
-    // each CTA adds up the cluster's counts: thread t the digits of its four
+    sync_all();
+    // every CTA adds up the cluster's counts: thread t the digits of its four
     // bins from the top, so that a prefix sum over the threads counts the rows
     // with a larger digit
-    constexpr int B = kBins / kSelectThreads;
-    uint32_t c[B], sum = 0;
+    const int bin = (1 << width) - 4 - 4 * tid;
+    uint4 c = make_uint4(0u, 0u, 0u, 0u);
+    if (bin >= 0) {
+      c = *reinterpret_cast<const uint4*>(&hist[bin]);
+      if (C > 1) {
+        uint4 x[kMaxCluster];  // all reads in flight together
 #pragma unroll
-    for (int i = 0; i < B; ++i) {
-      const int bin = kBins - 1 - (tid * B + i);
-      c[i] = 0;
-      for (int r = 0; r < C; ++r) c[i] += *cluster.map_shared_rank(&s_hist[bin], r);
-      sum += c[i];
-    }
-    uint32_t v = sum;
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < C && r != cr) x[r] = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&hist[bin], r));
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    if (lane == 31) s_warp[0][w] = v;
-    __syncthreads();
-    uint32_t above = v - sum;
-    for (int i = 0; i < w; ++i) above += s_warp[0][i];
-#pragma unroll
-    for (int i = 0; i < B; ++i) {
-      if (above < need && above + c[i] >= need) {
-        s_found[0] = static_cast<uint32_t>(kBins - 1 - (tid * B + i));
-        s_found[1] = above;
+        for (int r = 0; r < kMaxCluster; ++r) {
+          if (r < C && r != cr) {
+            c.x += x[r].x;
+            c.y += x[r].y;
+            c.z += x[r].z;
+            c.w += x[r].w;
+          }
+        }
       }
-      above += c[i];
+    }
+    const uint32_t sum = c.x + c.y + c.z + c.w, v = warp_scan(sum, lane);
+    if (lane == 31) s_warp[w] = v;
+    __syncthreads();
+    const uint32_t ws = warp_scan(lane < kSelectWarps ? s_warp[lane] : 0u, lane);
+    const uint32_t before = __shfl_sync(full, ws, (w + 31) & 31);
+    uint32_t above = v - sum + (w > 0 ? before : 0u);  // rows above this thread's bins
+    if (above < need && above + sum >= need) {
+      const uint32_t cs[4] = {c.w, c.z, c.y, c.x};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (above < need && above + cs[i] >= need) {
+          s_found[0] = static_cast<uint32_t>(bin + 3 - i);
+          s_found[1] = above;
+          s_found[2] = cs[i];
+        }
+        above += cs[i];
+      }
     }
     __syncthreads();
     prefix = (prefix << bits) | s_found[0];
     need -= s_found[1];
-    cluster.sync();  // every CTA has read the counts before they are cleared
+    at_t = s_found[2];
   }
 
-  // prefix is the key T; of the rows at T the `need` lowest stay. Thread t takes
-  // the t-th stretch of the CTA's rows.
-  const int tper = (cnt + kSelectThreads - 1) / kSelectThreads;
-  const int a = min(cnt, tid * tper), e = min(cnt, a + tper);
-  uint32_t more = 0, same = 0;
-  for (int i = a; i < e; ++i) {
-    const uint32_t x = key(i);
-    more += x > prefix;
-    same += x == prefix;
-  }
-  uint32_t vm = more, vs = same;
+  // prefix is the key T; of the rows at T the `need` lowest stay (mostly all:
+  // then they count as above T). What the cluster's earlier CTAs hold comes first.
+  const bool ties = at_t != need;
+  auto is_more = [&](int span, int j) { return valid(span, j) && (ties ? key[j] > prefix : key[j] >= prefix); };
+  auto is_same = [&](int span, int j) { return valid(span, j) && key[j] == prefix; };
+  uint32_t before_more = 0, before_same = 0;
+  if (C > 1) {
+    uint32_t more = 0, same = 0;
+    for (int span = 0; span < spans; ++span) {
+      if (spans > 1) load(span);
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t um = __shfl_up_sync(0xffffffffu, vm, o), us = __shfl_up_sync(0xffffffffu, vs, o);
-    if (lane >= o) {
-      vm += um;
-      vs += us;
+      for (int j = 0; j < kKeys; ++j) {
+        if (span * kSpan + j * kSelectThreads >= cnt) break;
+        more += __popc(__ballot_sync(full, is_more(span, j)));
+        if (ties) same += __popc(__ballot_sync(full, is_same(span, j)));
+      }
+    }
+    if (lane == 0) {
+      atomicAdd(&s_total[0], more);
+      atomicAdd(&s_total[1], same);
+    }
+    cluster.sync();
+#pragma unroll
+    for (int r = 0; r < kMaxCluster - 1; ++r) {
+      if (r < cr) {
+        before_more += *cluster.map_shared_rank(&s_total[0], r);
+        before_same += *cluster.map_shared_rank(&s_total[1], r);
+      }
     }
   }
-  if (lane == 31) {
-    s_warp[0][w] = vm;
-    s_warp[1][w] = vs;
+  const uint32_t below = (1u << lane) - 1u;
+  for (int span = 0; span < spans; ++span) {
+    if (spans > 1) {
+      load(span);
+      __syncthreads();  // the last span's counts have been read
+    }
+#pragma unroll
+    for (int j = 0; j < kKeys; ++j) {
+      uint32_t x = 0;
+      if (span * kSpan + j * kSelectThreads < cnt) {
+        x = __popc(__ballot_sync(full, is_more(span, j)));
+        if (ties) x |= __popc(__ballot_sync(full, is_same(span, j))) << 16;
+      }
+      if (lane == 0) s_cnt[j][w] = x;
+    }
+    __syncthreads();
+    {  // prefix sums of both halves at once: a span has fewer than 2^16 keys
+      static_assert(kKeys == kSelectWarps, "one warp per row of counts");
+      const uint32_t x = lane < kSelectWarps ? s_cnt[w][lane] : 0u, v = warp_scan(x, lane);
+      if (lane < kSelectWarps) s_cnt[w][lane] = v - x;
+      if (lane == 31) s_row[w] = v;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kKeys; ++j) {
+      if (span * kSpan + j * kSelectThreads >= cnt) break;
+      const uint32_t x = s_cnt[j][w], total = s_row[j];
+      const int row = lo + span * kSpan + j * kSelectThreads + tid;
+      const bool m1 = is_more(span, j);
+      const uint32_t more = before_more + (x & 0xffffu) + __popc(__ballot_sync(full, m1) & below);
+      if (!ties) {
+        if (m1) kept[more] = row;
+      } else {
+        const bool s1 = is_same(span, j);
+        const uint32_t same = before_same + (x >> 16) + __popc(__ballot_sync(full, s1) & below);
+        if (m1 || (s1 && same < need)) kept[more + min(same, need)] = row;
+      }
+      before_more += total & 0xffffu;
+      before_same += total >> 16;
+    }
   }
-  __syncthreads();
-  uint32_t before_more = vm - more, before_same = vs - same;
-  for (int i = 0; i < w; ++i) {
-    before_more += s_warp[0][i];
-    before_same += s_warp[1][i];
-  }
-  if (tid == kSelectThreads - 1) {
-    s_total[0] = before_more + more;
-    s_total[1] = before_same + same;
-  }
-  cluster.sync();
-  for (int r = 0; r < cr; ++r) {
-    before_more += *cluster.map_shared_rank(&s_total[0], r);
-    before_same += *cluster.map_shared_rank(&s_total[1], r);
-  }
-  uint32_t at = before_more + min(before_same, need);
-  for (int i = a; i < e; ++i) {
-    const uint32_t x = key(i);
-    const bool stays = x > prefix || (x == prefix && before_same < need);
-    before_same += x == prefix;
-    if (stays) kept[at++] = lo + i;
-  }
-  cluster.sync();  // no CTA ends while another reads its totals
+  if (C > 1) cluster.sync();  // no CTA ends while another reads its totals
 }
 
 // ---------------------------------------------------------------------- move
@@ -222,16 +298,19 @@ __device__ __forceinline__ int64_t pool_row(const EvictParams& p, const int32_t*
 // (e4m3), 2 (int8): a warp fills one block of the new table; its scale is the
 // largest of its rows' old scales, and rows from blocks with a smaller scale
 // are rounded again.
-template <int Q8>
+// POW2: row_chunks is a power of two.
+template <int Q8, bool POW2>
 __global__ void __launch_bounds__(32 * kMoveWarps) move_kernel(const EvictParams p) {
   constexpr uint32_t full = 0xffffffffu;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while select runs
   const int lane = threadIdx.x & 31;
   const int group = Q8 == 0 ? 32 : p.block_size;  // rows per warp
   const int groups = (p.budget + group - 1) / group;
-  const int64_t wi = static_cast<int64_t>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
-  const int64_t unit = wi / groups;
-  if (unit >= static_cast<int64_t>(p.batch) * p.n_heads) return;
-  const int b = static_cast<int>(unit / p.n_heads), h = static_cast<int>(unit % p.n_heads);
+  const uint32_t wi = blockIdx.x * kMoveWarps + (threadIdx.x >> 5);  // below 2^31: checked on the host
+  const uint32_t unit32 = wi / groups;
+  const int64_t unit = unit32;
+  const int b = static_cast<int>(unit32 / p.n_heads), h = static_cast<int>(unit32 % p.n_heads);
+  if (b >= p.batch) return;
   const int j0 = static_cast<int>(wi % groups) * group;
   const int m = min(rows_of(p, b), p.budget);
   const int j1 = min(m, j0 + group);
@@ -284,7 +363,8 @@ __global__ void __launch_bounds__(32 * kMoveWarps) move_kernel(const EvictParams
 #pragma unroll
       for (int i = 0; i < kMoveUnroll; ++i) {
         const int c = c0 + 32 * i;
-        const int r = min(c / p.row_chunks, 31), part = c - r * p.row_chunks;
+        const int r = POW2 ? min(c >> p.row_shift, 31) : min(c / p.row_chunks, 31);
+        const int part = POW2 ? c & (p.row_chunks - 1) : c - r * p.row_chunks;
         const int64_t s = __shfl_sync(full, src, r);
         d[i] = __shfl_sync(full, dst, r);
         if constexpr (Q8 != 0) {
@@ -293,9 +373,10 @@ __global__ void __launch_bounds__(32 * kMoveWarps) move_kernel(const EvictParams
         }
         if (c >= chunks || s < 0) d[i] = -1;
         if (d[i] >= 0) {
-          d[i] = d[i] * p.row_chunks + part;
-          u[0][i] = __ldcs(reinterpret_cast<const uint4*>(p.pool[0]) + s * p.row_chunks + part);
-          u[1][i] = __ldcs(reinterpret_cast<const uint4*>(p.pool[1]) + s * p.row_chunks + part);
+          d[i] = (POW2 ? d[i] << p.row_shift : d[i] * p.row_chunks) + part;
+          const int64_t from = (POW2 ? s << p.row_shift : s * p.row_chunks) + part;
+          u[0][i] = __ldcs(reinterpret_cast<const uint4*>(p.pool[0]) + from);
+          u[1][i] = __ldcs(reinterpret_cast<const uint4*>(p.pool[1]) + from);
         }
       }
 #pragma unroll
@@ -338,7 +419,7 @@ kvc_status evict(const float* scores, void* k_cache, void* v_cache, float* k_sca
   const int64_t units = static_cast<int64_t>(batch) * n_heads;
   const int group = code < 0 ? 32 : block_size;
   const int64_t warps = units * ((budget + group - 1) / group);
-  if (units * 8 >= (1ll << 31) || warps / kMoveWarps >= (1ll << 31) - 1)
+  if (units * 8 >= (1ll << 31) || warps >= (1ll << 31) - kMoveWarps)
     return fail(KVC_ERR_UNSUPPORTED, "batch x heads x budget too large");
   if (scores == nullptr || k_cache == nullptr || v_cache == nullptr || tables == nullptr || lens == nullptr ||
       new_tables == nullptr || kept == nullptr || new_lens == nullptr || new_scores == nullptr)
@@ -375,14 +456,12 @@ kvc_status evict(const float* scores, void* k_cache, void* v_cache, float* k_sca
   p.budget = budget;
   p.recent = recent;
   p.row_chunks = static_cast<int>(row_bytes / 16);
+  while ((1 << p.row_shift) < p.row_chunks) ++p.row_shift;
   p.err = dev->error_word;
 
-  // CTAs per row of scores: one per 4096 rows the table can hold, up to 8, while the GPU has SMs for them
+  // CTAs per row of scores: as many as the table's rows fill with 4096 each, up to 8, while the GPU has SMs for them
   int C = 1;
-  while (C < 8 && C * 4096LL < rows && units * C * 2 <= dev->num_sms) C *= 2;
-  const size_t smem = static_cast<size_t>(std::min<int64_t>(kHeldKeys, (rows + C - 1) / C)) * 4;
-  cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldKeys * 4);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(evict select)");
+  while (C < kMaxCluster && C * 4096LL < rows && units * C * 2 <= dev->num_sms) C *= 2;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = C;
@@ -391,16 +470,21 @@ kvc_status evict(const float* scores, void* k_cache, void* v_cache, float* k_sca
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(units * C));
   cfg.blockDim = dim3(kSelectThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, select_kernel, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel, p);
   if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx(evict select)");
-  const dim3 grid(static_cast<unsigned>((warps + kMoveWarps - 1) / kMoveWarps)), block(32 * kMoveWarps);
-  if (code < 0) move_kernel<0><<<grid, block, 0, stream>>>(p);
-  else if (code == KVC_E4M3) move_kernel<1><<<grid, block, 0, stream>>>(p);
-  else move_kernel<2><<<grid, block, 0, stream>>>(p);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + kMoveWarps - 1) / kMoveWarps));
+  cfg.blockDim = dim3(32 * kMoveWarps);
+  const bool pow2 = (1 << p.row_shift) == p.row_chunks;
+  auto* move = code < 0              ? (pow2 ? move_kernel<0, true> : move_kernel<0, false>)
+               : code == KVC_E4M3 ? (pow2 ? move_kernel<1, true> : move_kernel<1, false>)
+                                  : (pow2 ? move_kernel<2, true> : move_kernel<2, false>);
+  e = cudaLaunchKernelEx(&cfg, move, p);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx(evict move)");
   return finish_call(stream);
 }
 
