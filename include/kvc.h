@@ -476,8 +476,9 @@ kvc_status kvc_decode_attention_block8(const void* q, const void* k_cache, const
  *   new_scores  fp32 [batch, n_kv_heads, new_max_blocks_per_seq * block_size]:
  *               entries below m written, the others left as they are
  * The old blocks, lens and scores are only read, so blocks shared with forks
- * are safe; the new blocks must not be among them (kvc_seq_evict hands out
- * free ones), and no two sequences may share a new block. new_scores, new_lens
+ * are safe; the new blocks must not be among any sequence's old ones
+ * (kvc_seq_evict_batch hands out free ones), and no two sequences may share a
+ * new block. new_scores, new_lens
  * and new_block_tables must not overlap the old ones.
  * 1 <= budget <= new_max_blocks_per_seq * block_size, 0 <= recent <= budget.
  * n = 0 keeps nothing; n < 0 or n > max_blocks_per_seq * block_size sets
@@ -615,17 +616,19 @@ kvc_status kvc_seq_reserve_batch(kvc_pool* pool, const int64_t* seqs, int n, int
  * Source: llm-compass 2.3 (blocks shared by reference count are copied
  * before a holder writes into them: parallel sampling, beam search). */
 kvc_status kvc_seq_reserve_cow(kvc_pool* pool, int64_t seq, int64_t n_new, int64_t* slots_out, int64_t* copy_pair);
-/* The host side of kvc_evict_rows: `seq` gets ceil(new_length / block_size)
- * fresh blocks (the lowest free ids) in place of its present ones and the
- * length new_length; each old block loses one reference. Build the old table
- * (kvc_build_block_tables) before and the new one after this call. The old
- * blocks count as free at once, although the rows are still to be copied out
- * of them: launch kvc_evict_rows before anything that writes to blocks reserved
- * later, on the same stream. KVC_ERR_INVALID_ARG for an unknown sequence or a
- * new_length outside 0 .. length; KVC_ERR_NO_BLOCKS if the fresh blocks are not
- * all free while the old ones are still held (nothing changes).
+/* The host side of kvc_evict_rows, for the sequences of one such call: each of
+ * the distinct seqs[0..n) gets ceil(new_lengths[i] / block_size) fresh blocks
+ * (the lowest free ids, in that order) in place of its present ones and the
+ * length new_lengths[i]; each old block loses one reference. No sequence gets
+ * an old block of another one. Build the old tables (kvc_build_block_tables)
+ * before and the new ones after this call. The old blocks count as free at
+ * once, although their rows are still to be copied: launch kvc_evict_rows before
+ * anything that writes to blocks handed out later, on the same stream. All or
+ * nothing: KVC_ERR_INVALID_ARG for an unknown or repeated id or a new length
+ * outside 0 .. length, KVC_ERR_NO_BLOCKS if the fresh blocks are not all free
+ * while the old ones are still held.
  * Source: "KV Cache（键值缓存）" 2.3 (blocks counted by reference). */
-kvc_status kvc_seq_evict(kvc_pool* pool, int64_t seq, int64_t new_length);
+kvc_status kvc_seq_evict_batch(kvc_pool* pool, const int64_t* seqs, int n, const int64_t* new_lengths);
 /* Drops the sequence; each of its blocks loses one reference and returns to
  * the free list at zero. KVC_ERR_INVALID_ARG for an unknown sequence.
  * Source: "KV Cache（键值缓存）" 2.3. */

@@ -102,7 +102,7 @@ SIGNATURES = {
                               _i32, _vp, _vp, _vp, _vp]),
     "kvc_evict_rows_block8": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _i32, _i64,
                                      _i32, _i32, _i32, _vp, _vp, _vp, _vp]),
-    "kvc_seq_evict": (_i32, [_vp, _i64, _i64]),
+    "kvc_seq_evict_batch": (_i32, [_vp, _vp, _i32, _vp]),
     "kvc_seq_free": (_i32, [_vp, _i64]),
     "kvc_seq_length": (_i32, [_vp, _i64, _i64p]),
     "kvc_block_refcount": (_i32, [_vp, _i64, _i32p]),
@@ -458,11 +458,16 @@ class BlockPool:
         copy = None if pair[0] < 0 else (int(pair[0]), int(pair[1]))
         return [int(buf[i]) for i in range(n_new)], copy
 
-    def evict(self, seq: int, new_length: int):
-        """kvc_seq_evict: fresh blocks for ``new_length`` rows in place of the sequence's present ones. Build the
-        old table before and the new one after it, then call evict_rows before anything that writes to blocks
-        reserved later."""
-        _check(self._lib.kvc_seq_evict(self._h, seq, new_length), "kvc_seq_evict")
+    def evict_batch(self, seqs, new_lengths):
+        """kvc_seq_evict_batch: fresh blocks for new_lengths[i] rows in place of the present ones of each of the
+        distinct sequences `seqs`, all or nothing. Build the old tables before and the new ones after it, then call
+        evict_rows for all of them at once, before anything that writes to blocks handed out later."""
+        n = len(seqs)
+        if len(new_lengths) != n:
+            raise ValueError("one new length per sequence")
+        ids = (ctypes.c_int64 * max(1, n))(*seqs)
+        lens = (ctypes.c_int64 * max(1, n))(*new_lengths)
+        _check(self._lib.kvc_seq_evict_batch(self._h, ids, n, lens), "kvc_seq_evict_batch")
 
     def free(self, seq: int):
         _check(self._lib.kvc_seq_free(self._h, seq), "kvc_seq_free")

@@ -83,6 +83,11 @@ ScoredLayout layout(const ScoredShape& s, int elt, bool scored, int num_sms) {
   return l;
 }
 
+// What the size query answers: one size for either kind of cache.
+size_t workspace_needed(const ScoredShape& s, bool scored, int num_sms) {
+  return std::max(layout(s, 1, scored, num_sms).total, layout(s, 2, scored, num_sms).total);
+}
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -142,9 +147,10 @@ kvc_status decode(Cache cache, const ScoredShape& s, const void* q, kvc_dtype q_
   if ((st = current_device(&dev)) != KVC_OK) return st;
   const int elt = cache == Cache::kBf16 || cache == Cache::kF16 ? 2 : 1;
   const ScoredLayout l = layout(s, elt, scores != nullptr, dev->num_sms);
-  if (workspace == nullptr || workspace_bytes < l.total)
+  const size_t needed = workspace_needed(s, scores != nullptr, dev->num_sms);
+  if (workspace == nullptr || workspace_bytes < needed)
     return fail(KVC_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace == nullptr ? 0 : workspace_bytes,
-                l.total);
+                needed);
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(KVC_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   CUtensorMap tk, tv;
@@ -214,8 +220,7 @@ kvc_status kvc_decode_scored_workspace_size(int batch, int n_tokens, int n_q_hea
   if (st != KVC_OK) return st;
   DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev)) != KVC_OK) return st;
-  // one size for either kind of cache
-  *bytes = std::max(layout(s, 1, scored != 0, dev->num_sms).total, layout(s, 2, scored != 0, dev->num_sms).total);
+  *bytes = workspace_needed(s, scored != 0, dev->num_sms);
   return KVC_OK;
 }
 

@@ -194,33 +194,54 @@ kvc_status kvc_seq_reserve_cow(kvc_pool* pool, int64_t seq, int64_t n_new, int64
   return kvc_seq_reserve(pool, seq, n_new, slots_out);
 }
 
-kvc_status kvc_seq_evict(kvc_pool* pool, int64_t seq, int64_t new_length) {
+kvc_status kvc_seq_evict_batch(kvc_pool* pool, const int64_t* seqs, int n, const int64_t* new_lengths) {
   kvc::clear_error();
-  kvc_pool::Seq* sq = nullptr;
-  kvc_status s = find_seq(pool, seq, &sq);
-  if (s != KVC_OK) return s;
-  if (new_length < 0 || new_length > sq->length)
-    return kvc::fail(KVC_ERR_INVALID_ARG, "new_length %lld outside 0 .. %lld", static_cast<long long>(new_length),
-                     static_cast<long long>(sq->length));
+  if (pool == nullptr) return kvc::fail(KVC_ERR_INVALID_ARG, "pool is NULL");
+  if (n < 0) return kvc::fail(KVC_ERR_INVALID_ARG, "n must be >= 0");
+  if (n == 0) return KVC_OK;
+  if (seqs == nullptr || new_lengths == nullptr) return kvc::fail(KVC_ERR_INVALID_ARG, "NULL argument");
+  // check everything first, so that a refused batch changes nothing
   const int64_t bs = pool->block_size;
-  const int64_t need = (new_length + bs - 1) / bs;
-  // the rows are copied out of the present blocks, so none of them is reused here
+  std::vector<kvc_pool::Seq*> ss(static_cast<size_t>(n));
+  std::unordered_map<int64_t, int> seen;
+  int64_t need = 0;
+  for (int i = 0; i < n; ++i) {
+    kvc_status s = find_seq(pool, seqs[i], &ss[static_cast<size_t>(i)]);
+    if (s != KVC_OK) return s;
+    if (!seen.emplace(seqs[i], i).second)
+      return kvc::fail(KVC_ERR_INVALID_ARG, "sequence %lld appears twice", static_cast<long long>(seqs[i]));
+    const int64_t len = ss[static_cast<size_t>(i)]->length;
+    if (new_lengths[i] < 0 || new_lengths[i] > len)
+      return kvc::fail(KVC_ERR_INVALID_ARG, "sequence %lld: new length %lld outside 0 .. %lld",
+                       static_cast<long long>(seqs[i]), static_cast<long long>(new_lengths[i]),
+                       static_cast<long long>(len));
+    need += (new_lengths[i] + bs - 1) / bs;
+  }
   if (need > static_cast<int64_t>(pool->free_heap.size()))
     return kvc::fail(KVC_ERR_NO_BLOCKS, "need %lld blocks, %zu free", static_cast<long long>(need),
                      pool->free_heap.size());
-  std::vector<int64_t> fresh(static_cast<size_t>(need));
-  for (int64_t& b : fresh) {
-    b = pool->free_heap.top();
-    pool->free_heap.pop();
-    pool->ref[static_cast<size_t>(b)] = 1;
+  // the rows are copied out of the present blocks of all of them: every fresh
+  // block is taken before any of those is given back
+  std::vector<std::vector<int64_t>> old(static_cast<size_t>(n));
+  for (int i = 0; i < n; ++i) {
+    kvc_pool::Seq* sq = ss[static_cast<size_t>(i)];
+    std::vector<int64_t> fresh(static_cast<size_t>((new_lengths[i] + bs - 1) / bs));
+    for (int64_t& b : fresh) {
+      b = pool->free_heap.top();
+      pool->free_heap.pop();
+      pool->ref[static_cast<size_t>(b)] = 1;
+    }
+    old[static_cast<size_t>(i)] = std::move(sq->blocks);
+    sq->blocks = std::move(fresh);
+    sq->length = new_lengths[i];
   }
-  for (int64_t b : sq->blocks) {
-    int32_t& r = pool->ref[static_cast<size_t>(b)];
-    r -= 1;
-    if (r == 0) pool->free_heap.push(b);
+  for (const std::vector<int64_t>& blocks : old) {
+    for (int64_t b : blocks) {
+      int32_t& r = pool->ref[static_cast<size_t>(b)];
+      r -= 1;
+      if (r == 0) pool->free_heap.push(b);
+    }
   }
-  sq->blocks = std::move(fresh);
-  sq->length = new_length;
   return KVC_OK;
 }
 

@@ -128,14 +128,13 @@ def test_pool_evict(kvc):
     pool.reserve(a, 70)  # blocks 0 .. 4
     pool.reserve(b, 16)  # block 5
     c = pool.fork(a)
-    old, lens = pool.tables([a], 5)
-    assert (old, lens) == ([[0, 1, 2, 3, 4]], [70])
-    pool.evict(a, 33)
+    assert pool.tables([a], 5) == ([[0, 1, 2, 3, 4]], [70])
+    pool.evict_batch([a], [33])
     assert pool.tables([a], 3) == ([[6, 7, 8]], [33])
     assert pool.tables([c], 5) == ([[0, 1, 2, 3, 4]], [70])  # the fork keeps the old blocks
     assert [pool.refcount(i) for i in range(9)] == [1] * 9
     with pytest.raises(kvc.KvcError):
-        pool.evict(c, 70)  # needs 5 of the 3 free blocks
+        pool.evict_batch([c], [70])  # needs 5 of the 3 free blocks
     pool.free(c)
     assert pool.stats()["free_blocks"] == 8
 
@@ -145,17 +144,39 @@ def test_pool_evict_needs_blocks(kvc):
     a = pool.add()
     pool.reserve(a, 80)
     with pytest.raises(kvc.KvcError) as e:
-        pool.evict(a, 64)  # 4 fresh blocks, 3 free: the old ones still hold the rows
+        pool.evict_batch([a], [64])  # 4 fresh blocks, 3 free: the old ones still hold the rows
     assert e.value.status == kvc.ERR_NO_BLOCKS
     assert pool.length(a) == 80 and pool.tables([a], 5)[0] == [[0, 1, 2, 3, 4]]
     for n in (-1, 81):
         with pytest.raises(kvc.KvcError) as e:
-            pool.evict(a, n)
+            pool.evict_batch([a], [n])
         assert e.value.status == kvc.ERR_INVALID_ARG
     with pytest.raises(kvc.KvcError):
-        pool.evict(99, 0)
-    pool.evict(a, 48)
+        pool.evict_batch([99], [0])
+    pool.evict_batch([a], [48])
     assert pool.tables([a], 3) == ([[5, 6, 7]], [48])
     assert pool.reserve(a, 1) == [0]  # the old blocks are free again
-    pool.evict(a, 0)
+    pool.evict_batch([a], [0])
     assert pool.length(a) == 0 and pool.stats()["free_blocks"] == 8
+    pool.evict_batch([], [])
+
+
+def test_pool_evict_batch_keeps_old_and_new_blocks_apart(kvc):
+    pool = kvc.BlockPool(20, 16)
+    seqs = [pool.add() for _ in range(3)]
+    pool.reserve_batch(seqs, 64)  # blocks 0 .. 11
+    old = {b for row in pool.tables(seqs, 4)[0] for b in row}
+    for bad in ([seqs[0], seqs[0]], [seqs[0], 77, seqs[1]]):
+        with pytest.raises(kvc.KvcError) as e:
+            pool.evict_batch(bad, [16] * len(bad))
+        assert e.value.status == kvc.ERR_INVALID_ARG
+    with pytest.raises(kvc.KvcError) as e:
+        pool.evict_batch(seqs, [48, 48, 48])  # 9 fresh blocks, 8 free: nothing changes
+    assert e.value.status == kvc.ERR_NO_BLOCKS
+    with pytest.raises(ValueError):
+        pool.evict_batch(seqs, [1, 2])
+    assert {b for row in pool.tables(seqs, 4)[0] for b in row} == old
+    pool.evict_batch(seqs, [33, 17, 0])
+    rows, lens = pool.tables(seqs, 3)
+    assert rows == [[12, 13, 14], [15, 16, 0], [0, 0, 0]] and lens == [33, 17, 0]
+    assert pool.stats()["free_blocks"] == 15
