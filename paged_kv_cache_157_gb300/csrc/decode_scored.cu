@@ -43,10 +43,12 @@ kvc_status check_shape(const ScoredShape& s) {
   if (static_cast<int64_t>(s.n_tok) * s.group() > kScoredMaxQueries)
     return fail(KVC_ERR_UNSUPPORTED, "n_tokens x query heads per kv head must be at most %d", kScoredMaxQueries);
   if (s.rows() > (1ll << 30)) return fail(KVC_ERR_UNSUPPORTED, "max_blocks_per_seq x block_size too large");
-  // the kernel's prefix sums of 16-row tiles and its unit numbers are 32-bit
-  if (s.batch * s.rows() / kTileRows >= (1ll << 31) ||
+  // the kernel's tile positions and unit numbers are 32-bit
+  const int nc = 8 * scored_nt(s.D, s.qn()), n_hsub = (s.qn() + nc - 1) / nc;
+  const int64_t units = static_cast<int64_t>(s.batch) * s.n_kv_heads * n_hsub;
+  if (units >= (1ll << 27) || units * ((s.rows() + kTileRows - 1) / kTileRows) >= (1ll << 31) ||
       static_cast<int64_t>(s.batch) * s.n_tok * s.n_q_heads >= (1ll << 31))
-    return fail(KVC_ERR_UNSUPPORTED, "batch x rows or batch x queries too large");
+    return fail(KVC_ERR_UNSUPPORTED, "batch x heads x queries x rows too large");
   return KVC_OK;
 }
 

@@ -437,36 +437,65 @@ __device__ inline void scan_tiles(const ScoredParams& p, int* s_scan) {
   __syncthreads();
 }
 
-// a / b for a >= 0, b > 0, with a 32-bit division when both fit.
-__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
-  return (static_cast<uint64_t>(a | b) >> 32) == 0
-             ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
-             : a / b;
+// n / d for d >= 1 from m = magic(d): exact while n * d < 2^32.
+__device__ __forceinline__ uint32_t magic(uint32_t d) { return d == 1 ? 0u : 0xffffffffu / d + 1u; }
+__device__ __forceinline__ int divided(int n, uint32_t m) {
+  return m == 0u ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), m));
 }
 
-// The unit of global tile `pos`.
-struct Unit {
-  int64_t u0;  // its first tile
-  int seq, kvh, hsub, tiles;
+// Tiles of the work: positions [0, N) in equal ranges, the first `rest` of
+// them one longer. All positions are below 2^31 (checked on the host).
+struct Split {
+  int per, rest;
+  __device__ __forceinline__ int start(int wk) const { return wk * per + min(wk, rest); }
+  __device__ __forceinline__ int holder(int pos) const {
+    const int longer = rest * (per + 1);
+    return pos < longer ? pos / (per + 1) : rest + (pos - longer) / per;
+  }
 };
 
-__device__ __forceinline__ Unit locate(int64_t pos, const ScoredParams& p, const int* s_scan) {
-  const int64_t HN = static_cast<int64_t>(p.n_kv_heads) * p.n_hsub;
-  int a = 0, hi = p.batch - 1;  // the last sequence whose first tile is <= pos (skips empty ones)
-  while (a < hi) {
-    const int mid = (a + hi + 1) >> 1;
-    if (HN * s_scan[mid] <= pos) a = mid; else hi = mid - 1;
+// A (sequence, kv head, column group) and its tiles [u0, u0 + tiles).
+struct Unit {
+  int u0, seq, kvh, hsub, tiles;
+};
+
+// Rows and tiles of the sequences and where their units lie. Up to 32
+// sequences sit in the lanes of every warp (no barrier, no search); more in
+// shared memory, as prefix sums.
+struct Batch {
+  int rows, tiles, before;  // of sequence `lane`; before: tiles of the sequences before it
+  int total;
+  const int* s_scan;  // NULL: in the lanes
+  __device__ __forceinline__ Unit locate(int pos, const ScoredParams& p) const {
+    const int HN = p.n_kv_heads * p.n_hsub;
+    Unit u;
+    int first;
+    if (s_scan == nullptr) {
+      // the last sequence whose first tile is <= pos (skips empty ones)
+      const bool below = static_cast<int>(threadIdx.x & 31) < p.batch && HN * before <= pos;
+      u.seq = 31 - __clz(__ballot_sync(0xffffffffu, below));
+      u.tiles = __shfl_sync(0xffffffffu, tiles, u.seq);
+      first = HN * __shfl_sync(0xffffffffu, before, u.seq);
+    } else {
+      int a = 0, hi = p.batch - 1;
+      while (a < hi) {
+        const int mid = (a + hi + 1) >> 1;
+        if (HN * s_scan[mid] <= pos) a = mid; else hi = mid - 1;
+      }
+      u.seq = a;
+      u.tiles = s_scan[a + 1] - s_scan[a];
+      first = HN * s_scan[a];
+    }
+    const int idx = static_cast<int>(static_cast<uint32_t>(pos - first) / static_cast<uint32_t>(u.tiles));
+    u.kvh = p.n_hsub == 1 ? idx : idx / p.n_hsub;
+    u.hsub = idx - u.kvh * p.n_hsub;
+    u.u0 = first + idx * u.tiles;
+    return u;
   }
-  Unit u;
-  u.seq = a;
-  u.tiles = s_scan[a + 1] - s_scan[a];
-  const int64_t first = HN * s_scan[a];
-  const int idx = static_cast<int>(quot(pos - first, u.tiles));
-  u.kvh = idx / p.n_hsub;
-  u.hsub = idx - u.kvh * p.n_hsub;
-  u.u0 = first + static_cast<int64_t>(idx) * u.tiles;
-  return u;
-}
+  __device__ __forceinline__ int rows_of(int seq, const ScoredParams& p) const {
+    return s_scan == nullptr ? __shfl_sync(0xffffffffu, rows, seq) : valid_rows(p, seq);
+  }
+};
 
 }  // namespace scored
 
@@ -499,64 +528,90 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
   }
+  __syncwarp();
   // The kernel may start while the stream's previous one runs; nothing of the
   // caller's is read or written before that one has ended.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  scan_tiles(p, s_scan);  // ends with a CTA barrier
+  // Small calls spend their time in this prologue (11000 cycles before it was
+  // cut down): no barrier for up to 32 sequences, 32-bit positions, one copy of
+  // each piece of code.
+  Batch bt;
+  if (p.batch <= 32) {
+    bt.s_scan = nullptr;
+    bt.rows = lane < p.batch ? valid_rows(p, lane) : 0;
+    bt.tiles = tiles_of(bt.rows);
+    int v = bt.tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(full, v, o);
+      if (lane >= o) v += x;
+    }
+    bt.before = v - bt.tiles;
+    bt.total = __shfl_sync(full, v, 31);
+  } else {
+    scan_tiles(p, s_scan);  // ends with a CTA barrier
+    bt.s_scan = s_scan;
+    bt.rows = bt.tiles = bt.before = 0;
+    bt.total = s_scan[p.batch];
+  }
 
   // Sequences of invalid length: flagged, their units marked for zero outputs.
+  const int HN = p.n_kv_heads * p.n_hsub;
   for (int b = blockIdx.x * blockDim.x + tid; b < p.batch; b += gridDim.x * blockDim.x) {
-    if (s_scan[b + 1] == s_scan[b]) {
+    if (valid_rows(p, b) == 0) {
       set_flag(p.err, KVC_FLAG_BAD_LEN);
-      const int HN = p.n_kv_heads * p.n_hsub;
       for (int i = 0; i < HN; ++i) p.units[static_cast<int64_t>(b) * HN + i] = make_int4(kUnitEmpty, 0, 0, 0);
     }
   }
 
-  const int64_t N = static_cast<int64_t>(p.n_kv_heads) * p.n_hsub * s_scan[p.batch];
-  const int64_t most = quot(N + p.min_tiles - 1, p.min_tiles);
-  const int64_t We = most < p.workers ? most : p.workers;
+  const int N = HN * bt.total;
+  if (N == 0) return;
+  const int We = min(static_cast<int>((static_cast<uint32_t>(N) + p.min_tiles - 1) / p.min_tiles), p.workers);
   // K workers per CTA, so that few workers spread over all SMs
-  const int K = static_cast<int>(quot(We + gridDim.x - 1, gridDim.x));
-  const int64_t wk = static_cast<int64_t>(blockIdx.x) * K + w;
+  const int K = static_cast<int>((We + gridDim.x - 1) / gridDim.x);
+  const int wk = static_cast<int>(blockIdx.x) * K + w;
   const bool works = w < K && wk < We;
   // Merging the CTA's parts costs every CTA a barrier and about 2 us at its
   // end; it pays where a query would otherwise have many records to merge
   // (e4m3, one sequence of 131071 rows: 77 -> 69 us; batch 32 x U[512, 4096],
   // seven records each: 37 -> 39 us).
-  const int64_t n_units = static_cast<int64_t>(p.batch) * p.n_kv_heads * p.n_hsub;
-  const bool merge = K > 1 && We > 16 * n_units;
-  const int64_t lo = works ? quot(wk * N, We) : 0, hi = works ? quot((wk + 1) * N, We) : 0;
-  const int tpb = p.block_size / kTileRows;  // tiles per cache block
+  const bool merge = K > 1 && We > 16 * p.batch * HN;
+  if (!works && !merge) return;
+  Split sp;
+  sp.per = N / We;
+  sp.rest = N - sp.per * We;
+  const int lo = works ? sp.start(wk) : 0, hi = works ? sp.start(wk + 1) : 0;
+  const uint32_t tpb = p.block_size / kTileRows;  // tiles per cache block
+  const uint32_t m_tpb = magic(tpb), m_group = magic(p.group);
   const uint64_t pol = policy_evict_first();
 
   // ---- copies: the next tiles of the range into the next stage
-  int64_t ipos = lo, iend = lo;
+  int ipos = lo, iend = lo;
   int ij = 0, iseq = 0, ikvh = 0, wb = 0, tw = -1;
   uint32_t islot = 0, ivalid = 0;  // ivalid: bit slot * TS + t: the tile's block is inside the pool
   int issued = 0;
   auto issue = [&]() {
     if (ipos < hi) {
       if (ipos >= iend) {
-        const Unit u = locate(ipos, p, s_scan);
+        const Unit u = bt.locate(ipos, p);
         iseq = u.seq;
         ikvh = u.kvh;
-        ij = static_cast<int>(ipos - u.u0);
-        iend = u.u0 + u.tiles < hi ? u.u0 + u.tiles : hi;
+        ij = ipos - u.u0;
+        iend = min(u.u0 + u.tiles, hi);
         wb = -64;  // no entries yet
       }
-      const int cnt = iend - ipos < TS ? static_cast<int>(iend - ipos) : TS;
-      const int b_last = (ij + cnt - 1) / tpb;
+      const int cnt = min(iend - ipos, TS);
+      const int b_last = divided(ij + cnt - 1, m_tpb);
       if (b_last >= wb + 32) {  // lane i holds the table's entry wb + i
-        wb = ij / tpb;
+        wb = divided(ij, m_tpb);
         tw = wb + lane < p.max_blocks ? __ldg(p.block_tables + static_cast<int64_t>(iseq) * p.max_blocks + wb + lane)
                                       : -1;
       }
       // lane i copies box i: [tile][K or V][half]
       constexpr int PER = 2 * G::kHalves;
       const int t = lane / PER < cnt ? lane / PER : 0;
-      const int jt = ij + t, blk = jt / tpb;
+      const int jt = ij + t, blk = divided(jt, m_tpb);
       const int phys = __shfl_sync(full, tw, blk - wb);
       const bool ok = phys >= 0 && phys < p.num_blocks;
       uint32_t mask = 0;
@@ -575,7 +630,7 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
       __syncwarp();
       if (lane < PER * cnt && ok) {
         const int kv = (lane % PER) / G::kHalves, half = lane % G::kHalves;
-        const int y = (phys * p.n_kv_heads + ikvh) * p.block_size + (jt - blk * tpb) * kTileRows;
+        const int y = (phys * p.n_kv_heads + ikvh) * p.block_size + (jt - blk * static_cast<int>(tpb)) * kTileRows;
         const uint32_t dst = ring + islot * G::kStageBytes + (t * 2 + kv) * G::kTileBytes +
                              half * (kTileRows * G::kBoxBytes);
         wmma16::tma2d(dst, kv == 0 ? &tm_k : &tm_v, half * (G::kBoxBytes / static_cast<int>(sizeof(CT))), y,
@@ -584,7 +639,7 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
       if constexpr (ONE) {
         // lane i copies scale i: [tile][K or V]
         const int t2 = (lane >> 1) < cnt ? lane >> 1 : 0;
-        const int phys2 = __shfl_sync(full, tw, (ij + t2) / tpb - wb);
+        const int phys2 = __shfl_sync(full, tw, divided(ij + t2, m_tpb) - wb);
         if (lane < 2 * cnt && phys2 >= 0 && phys2 < p.num_blocks)
           cp_async4(smem_addr(s_scale + (islot * TS + t2) * 2 + (lane & 1)),
                     ((lane & 1) ? p.v_scale : p.k_scale) + static_cast<int64_t>(phys2) * p.n_kv_heads + ikvh);
@@ -596,27 +651,38 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
     }
     if constexpr (ONE) cp_async_commit();  // one group per call, whether or not it copied
   };
-  for (int i = 0; i < S; ++i) issue();
 
-  // ---- products
+  // ---- products, stage by stage; a segment is one unit's tiles in the range
   uint32_t slot = 0, ph = 0;
-  int used = 0;
+  int used = 0, ahead = 0;  // stages released; issue() calls ahead of the next one to use
   bool ok = true;
   int held = -1;  // the unit of the part at the range's end
   const int lanes_g = lane >> 2, c = lane & 3;
-  for (int64_t pos = lo; ok && pos < hi;) {
-    const Unit u = locate(pos, p, s_scan);
-    const int64_t end = u.u0 + u.tiles < hi ? u.u0 + u.tiles : hi;
-    const int n_rows = valid_rows(p, u.seq);
-    const int col0 = u.hsub * NC;
-    State<D, NT, ONE> st;
+  State<D, NT, ONE> st;
+  Unit u{};
+  int end = lo, n_rows = 0, col0 = 0, j = 0;
+  float* lg0 = nullptr;
+#pragma unroll 1
+  for (int pos = lo; pos < hi;) {
+#pragma unroll 1
+    for (; ahead < S; ++ahead) issue();
+    if (pos == end) {  // a new segment
+      u = bt.locate(pos, p);
+      end = min(u.u0 + u.tiles, hi);
+      n_rows = bt.rows_of(u.seq, p);
+      col0 = u.hsub * NC;
+      j = pos - u.u0;
+      lg0 = p.scores == nullptr
+                ? nullptr
+                : p.logits + (static_cast<int64_t>(u.seq) * p.n_kv_heads + u.kvh) * p.rows * p.qns;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       // ---- Q^T fragments of query g (columns past the last query: zeros)
       const int v = col0 + 8 * n + lanes_g;
       const bool have = v < p.qn;
-      const unsigned short* qr =
-          static_cast<const unsigned short*>(p.q) + (have ? query_row(p, u.seq, u.kvh, v) * D : 0);
+      const int tq = divided(v, m_group);
+      const int64_t qrow = (static_cast<int64_t>(u.seq) * p.n_tok + tq) * p.n_q_heads + u.kvh * p.group + v - tq * p.group;
+      const unsigned short* qr = static_cast<const unsigned short*>(p.q) + (have ? qrow * D : 0);
       if constexpr (!ONE) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
@@ -670,7 +736,7 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
         st.m[n][e] = -1e30f;  // finite: a query that meets only masked rows keeps weight 0
         st.l[n][e] = 0.f;
         if constexpr (ONE) st.mo[n][e] = -1e30f;
-        const int t = (col0 + 8 * n + 2 * c + e) / p.group;
+        const int t = divided(col0 + 8 * n + 2 * c + e, m_group);
         st.dt[n][e] = t < p.n_tok ? p.n_tok - 1 - t : 0;
       }
 #pragma unroll
@@ -679,12 +745,9 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
         for (int e = 0; e < 4; ++e) st.o[n][i][e] = 0.f;
       }
     }
-    float* lg0 = p.scores == nullptr
-                     ? nullptr
-                     : p.logits + (static_cast<int64_t>(u.seq) * p.n_kv_heads + u.kvh) * p.rows * p.qns;
-    int j = static_cast<int>(pos - u.u0);
-    while (pos < end) {
-      const int cnt = end - pos < TS ? static_cast<int>(end - pos) : TS;
+    }
+    {
+      const int cnt = min(end - pos, TS);
       ok = mbar_wait_data(bars + slot, ph, p.wait_polls);
       ok = __all_sync(full, ok);
       if (!ok) break;
@@ -716,25 +779,24 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
       slot = slot + 1 == S ? 0 : slot + 1;
       if (slot == 0) ph ^= 1u;
       ++used;
+      --ahead;
       pos += cnt;
       j += cnt;
-      issue();
     }
-    if (!ok) break;
+    if (pos < end) continue;
 
     // ---- close the segment. A whole unit: its outputs. A part that ends
     // inside the range (the unit began in an earlier worker's): record 2 wk.
     // The part at the range's end: merged with its neighbours' below.
-    const int64_t begin = u.u0 > lo ? u.u0 : lo;
+    const int begin = max(u.u0, lo);
     const int64_t unit = (static_cast<int64_t>(u.seq) * p.n_kv_heads + u.kvh) * p.n_hsub + u.hsub;
     const bool whole = begin == u.u0 && pos == u.u0 + u.tiles;
     if (lane == 0 && begin == u.u0) {
       int4 info = make_int4(kUnitWhole, 0, 0, 0);
       if (!whole) {
-        const int64_t last = u.u0 + u.tiles;  // behind its last tile
-        const int64_t c1 = quot(last * We - 1, N);  // the worker that holds it
-        info = make_int4(static_cast<int>(wk), static_cast<int>(c1), last < quot((c1 + 1) * N, We) ? 1 : 0,
-                         merge ? K : 1);
+        const int last = u.u0 + u.tiles;  // behind its last tile
+        const int c1 = sp.holder(last - 1);
+        info = make_int4(wk, c1, last < sp.start(c1 + 1) ? 1 : 0, merge ? K : 1);
       }
       p.units[unit] = info;
     }
@@ -742,7 +804,7 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
     // landed) if it is to be merged.
     const bool last_part = !whole && pos == hi, keep = last_part && merge;
     float* so = reinterpret_cast<float*>(smem + static_cast<size_t>(w) * S * G::kStageBytes);
-    const int64_t rec = 2 * wk + (last_part ? 1 : 0);
+    const int64_t rec = 2ll * wk + (last_part ? 1 : 0);
     if (keep) __syncwarp();
     // dims of the lane's values: 16-bit caches 16 i + g (+ 8), one-byte caches
     // [span] + (span / 8) g + 2 i (+ 1)
