@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtasPerSm) append_block
       int first = bs;
       bool asc = true;
       for (int t = lane; t < run.rows; t += 32) {
-        const int64_t sl = a + t < 32 * kWindows ? s_slot[1 + a + t] : __ldg(run.slots + t);
+        const int64_t sl = a + t < 32 * seen ? s_slot[1 + a + t] : __ldg(run.slots + t);
         first = min(first, static_cast<int>(sl - run.first_slot));
         asc = asc && sl - s_slot[1 + a] == t;
       }

@@ -155,3 +155,32 @@ def test_unwritten_blocks_are_left_alone(kvc):
     p = Pools(5, 2, 32, 128, "e4m3")
     p.append(kvc, *rows(3, 2, 128, "bf16", 1), [64, 65, 66])
     p.same()  # compares every block
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("T", [40, 300, 700])
+def test_one_slot_named_many_times(kvc, code, T):
+    """Tokens of one slot race; with equal rows the result is theirs. The runs are longer than any block."""
+    H, D, bs = 2, 64, 16
+    p = Pools(6, H, bs, D, code, seed=T)
+    k, v = (x[:1].expand(T, H, D).contiguous() for x in rows(1, H, D, "bf16", 3))
+    p.append(kvc, k, v, [2 * bs + 5] * T)
+    p.same()
+    p.append(kvc, k, v, [3 * bs] * (T - 3) + [3 * bs + 1, 4 * bs + 7, -1])
+    p.same()
+
+
+def test_offsets_past_32_bits(kvc):
+    H, D, bs, nb = 8, 256, 128, 16500  # 4.3e9 codes per pool
+    assert nb * H * bs * D > 2 ** 32
+    codes = [torch.empty((nb, H, bs, D), dtype=torch.int8, device="cuda") for _ in range(2)]
+    scales = [torch.zeros((nb, H), device="cuda") for _ in range(2)]
+    slots = [(nb - 1) * bs + r for r in range(100)] + [(nb - 2) * bs + 3, 5]
+    k, v = rows(len(slots), H, D, "bf16", 1)
+    before = [c[torch.tensor([nb - 1, nb - 2, 0], device="cuda")].cpu().numpy() for c in codes]
+    kvc.append_block8(k.cuda(), v.cuda(), torch.tensor(slots, device="cuda"), *codes, *scales)
+    small = [r for r in range(100)] + [bs + 3, 2 * bs + 5]  # the same in a pool of the three blocks
+    for x, c, s, b in zip((k, v), codes, scales, before):
+        want, ws = O.append_block8(x.float().numpy(), small, b, np.zeros((3, H), dtype=np.float32), "int8")
+        at = torch.tensor([nb - 1, nb - 2, 0], device="cuda")
+        assert np.array_equal(c[at].cpu().numpy(), want) and np.array_equal(s[at].cpu().numpy(), ws)

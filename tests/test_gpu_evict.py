@@ -170,3 +170,24 @@ def test_on_a_stream_and_in_a_graph(kvc):
         torch.cuda.synchronize()
         ref, ref_lens = O.evict(sc2, lens2, budget, 9)
         assert np.array_equal(kept.cpu().numpy(), ref) and np.array_equal(new_lens.cpu().numpy(), ref_lens)
+
+
+def test_offsets_past_32_bits(kvc):
+    H, D, bs, nb = 8, 256, 128, 16500  # 4.3e9 elements per pool
+    assert nb * H * bs * D > 2 ** 32
+    lens, budget = [300], 140
+    tables, new_tables, pools, sc = setup("bf16", lens, H, D, bs, budget, 5)
+    used = pools[0][0].shape[0]
+    far = np.array([nb - 1 - i for i in range(used)])
+    at = torch.from_numpy(far).cuda()
+    big = []
+    for t, _, _ in pools:
+        b = torch.empty((nb, H, bs, D), dtype=t.dtype, device="cuda")
+        b[at] = t
+        big.append((b, None, None))
+    run(kvc, "bf16", tables, new_tables, pools, sc, lens, budget, 20)
+    run(kvc, "bf16", far[np.minimum(tables, used - 1)].astype(np.int32),
+        far[np.minimum(new_tables, used - 1)].astype(np.int32), big, sc, lens, budget, 20)
+    torch.cuda.synchronize()
+    for (t, _, _), (b, _, _) in zip(pools, big):
+        assert np.array_equal(bits(t), bits(b[at]))  # the small pool's result is checked by test_ragged_batches

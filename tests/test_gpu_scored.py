@@ -291,3 +291,66 @@ def test_non_finite_values_stay_in_their_sequence(kvc):
     bad = torch.isnan(out)
     assert bad[0, 0, :4, 5].all() and int(bad.sum()) == 4
     assert torch.isfinite(scores).all()
+
+
+def test_the_largest_batch(kvc):
+    rng = np.random.default_rng(2)
+    lens = rng.integers(1, 20, 4096).tolist()
+    lens[0], lens[100], lens[4095] = 150, 33, 64
+    check(kvc, "int8", lens, 1, 2, 1, 64, 16, seed=61)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_offsets_past_32_bits(kvc, kind):
+    H, D, bs, nb = 8, 256, 128, 16500  # 4.3e9 elements per pool, of which a few blocks at both ends are used
+    assert nb * H * bs * D > 2 ** 32
+    lens = [300, 129]
+    q, pools, tables, scores = make(kind, lens, 1, 16, H, D, bs, seed=62)
+    used = pools[0][0].shape[0]
+    far = np.array([nb - 1 - i if i % 2 else i for i in range(used)])  # where the small pool's blocks go
+    at = torch.from_numpy(far).cuda()
+    big = []
+    for t, s, _ in pools:
+        b = torch.empty((nb, H, bs, D), dtype=t.dtype, device="cuda")
+        b[at] = t
+        bs_ = None
+        if s is not None:
+            bs_ = torch.zeros((nb, H), device="cuda")
+            bs_[at] = s
+        big.append((b, bs_, None))
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    far_tables = np.where(tables < used, far[np.minimum(tables, used - 1)], tables).astype(np.int32)
+    other = scores.clone()
+    out, far_out = torch.empty(q.shape, device="cuda"), torch.empty(q.shape, device="cuda")
+    ws = workspace_for(kvc, q, pools[0][0], tables, True)
+    call_decode(kvc, kind, q, pools, torch.from_numpy(tables).cuda(), n, 0.1, out, scores, ws)
+    call_decode(kvc, kind, q, big, torch.from_numpy(far_tables).cuda(), n, 0.1, far_out, other, ws)
+    torch.cuda.synchronize()
+    assert kvc.get_error_flags() == 0
+    assert torch.equal(out, far_out) and torch.equal(scores, other)  # and out is what test_head_layouts checks
+
+
+def test_two_graphs_share_a_workspace(kvc):
+    lens = [800, 3]
+    q, pools, tables, scores = make("bf16", lens, 1, 8, 2, 128, 16, seed=63)
+    t, n = torch.from_numpy(tables).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = workspace_for(kvc, q, pools[0][0], tables, True)
+    qs = [q, -q]
+    want = []
+    for x in qs:
+        o, sc = torch.empty(q.shape, device="cuda"), scores.clone()
+        call_decode(kvc, "bf16", x, pools, t, n, 0.1, o, sc, workspace_for(kvc, q, pools[0][0], tables, True))
+        want.append((o, sc))
+    graphs, got = [], []
+    for x in qs:
+        o, sc = torch.empty(q.shape, device="cuda"), scores.clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call_decode(kvc, "bf16", x, pools, t, n, 0.1, o, sc, ws)
+        graphs.append(g)
+        got.append((o, sc))
+    for g in graphs:  # one after the other on one stream
+        g.replay()
+    torch.cuda.synchronize()
+    for (o, sc), (wo, wsc) in zip(got, want):
+        assert torch.equal(o, wo) and torch.equal(sc, wsc)
