@@ -627,23 +627,35 @@ def _stream_of(stream, t):
 def _checked(first, name, tensors):
     """Checks ``first`` and ``tensors`` [(tensor, name, dtype or None)]: contiguous CUDA tensors of one device, the
     current one (the stream and the library's launches belong to it)."""
-    torch = _torch()
+    n = name
+    try:
+        device = first.get_device()  # -1: not on a GPU
+        if device >= 0 and first.is_contiguous():
+            for t, n, dtype in tensors:
+                if t.get_device() != device or not t.is_contiguous() or (dtype is not None and t.dtype is not dtype):
+                    break
+            else:
+                if device == _torch().cuda.current_device():
+                    return
+    except AttributeError:
+        raise TypeError(f"{n} must be a tensor") from None
+    _refuse(first, name, tensors)
+
+
+def _refuse(first, name, tensors):
+    """Says what _checked found wrong."""
     for t, n, dtype in ((first, name, None), *tensors):
-        try:
-            device = t.device
-            if dtype is not None and t.dtype is not dtype:
-                raise TypeError(f"{n} must be {dtype}, got {t.dtype}")
-            contiguous = t.is_contiguous()
-        except AttributeError:
-            raise TypeError(f"{n} must be a tensor") from None
+        if not hasattr(t, "get_device"):
+            raise TypeError(f"{n} must be a tensor")
+        if dtype is not None and t.dtype is not dtype:
+            raise TypeError(f"{n} must be {dtype}, got {t.dtype}")
         if not t.is_cuda:
             raise ValueError(f"{n} must be a CUDA tensor")
-        if not contiguous:
+        if not t.is_contiguous():
             raise ValueError(f"{n} must be contiguous")
-        if device != first.device:
-            raise ValueError(f"{name} is on {first.device}, {n} on {device}")
-    if first.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {first.device}, the current device is cuda:{torch.cuda.current_device()}")
+        if t.device != first.device:
+            raise ValueError(f"{name} is on {first.device}, {n} on {t.device}")
+    raise ValueError(f"{name} is on {first.device}, the current device is cuda:{_torch().cuda.current_device()}")
 
 
 def _pool_shape(k_cache, v_cache):

@@ -1047,6 +1047,7 @@ __device__ __forceinline__ void add_weights(const float* lg, float* sc, const fl
   else if (vecs <= 2) add_weights<W, 2, true>(lg, sc, e, r0, r1, n_old, qns);
   else if (vecs <= 4) add_weights<W, 4, true>(lg, sc, e, r0, r1, n_old, qns);
   else if (vecs <= 8) add_weights<W, 8, true>(lg, sc, e, r0, r1, n_old, qns);
+  else if (vecs <= 32) add_weights<W, 32, true>(lg, sc, e, r0, r1, n_old, qns);
   else add_weights<W, 32, false>(lg, sc, e, r0, r1, n_old, qns);
 }
 
