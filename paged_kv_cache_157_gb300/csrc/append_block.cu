@@ -11,11 +11,14 @@
 // earlier rows are rounded again only when a louder token arrives.
 //
 // A CTA finds the runs that begin in a stretch of tokens and takes them one by
-// one for some of the heads, a short run by one warp, a long one by all. A run's rows are read once, in 16-byte loads that are all
-// in flight together, and stay in registers between the maximum and the codes
-// (runs beyond 16 KB are read again, out of L2). Bound by HBM for prompts; by
-// the chain slots -> rows and scale -> codes of dependent accesses for a decode step,
-// whose tokens get a warp each.
+// one for some of the heads, a short run by one warp, a long one by all. A
+// run's rows are read once, in 16-byte loads that are all in flight together,
+// and stay in registers between the maximum and the codes (runs beyond 16 KB
+// are read again, out of L2). Bound, for prompts, by the load, barrier and store
+// phases of four CTAs per SM rather than by HBM; for a decode step, whose tokens
+// get a warp each, by the chain slots -> rows and scale -> codes of dependent
+// accesses. Measured (8 heads, D 128, bf16): a prompt of 16384 tokens 29.5 us
+// (3.4 TB/s of its 101 MB, 41 % issue), a step of 64 tokens 6.4 us.
 #include <algorithm>
 #include <type_traits>
 

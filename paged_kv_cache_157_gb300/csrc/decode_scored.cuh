@@ -14,8 +14,12 @@
 // partial outputs anyway, turns them into weights and adds them up. Reading K
 // a second time instead would cost D elements per row.
 //
-// What bounds it: HBM, for up to about 64 queries per kv head. Every cached
-// row is read once, by TMA, into a ring in shared memory.
+// What bounds it: HBM, for up to about 16 queries per kv head. Every cached
+// row is read once, by TMA, into a ring in shared memory. Measured (32 query, 8
+// kv heads, D 128), decode and finish: bf16, batch 32 x 4096 rows 97.7 us (90 us
+// of them the decode, 6.05 TB/s); e4m3 blocks, batch 32 x U[512, 4096] 34.7 us, at
+// 7.0 TB/s for what a larger batch adds. More queries (32 tokens, 128 queries per
+// kv head over 2 x 4000 rows: 37 us) are bound by the products' latency.
 //
 // Work split. The 16-row tiles of all (sequence, kv head, column group) units
 // are laid end to end and cut into equal ranges, one per WARP. A warp is a
@@ -918,7 +922,8 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
 // rows: score += sum_v 2^(x - lse_v), lanes over the queries of a row, in a
 // fixed order. Every step loads what it needs at once: bound by the scores' and
 // logits' bytes (which mostly sit in L2), for small calls by the chain unit ->
-// maxima -> outputs, or logits, of three loads.
+// maxima -> outputs, or logits, of three loads: 5 us for a few short sequences,
+// 13 us for 32 x 4096 rows of 4 queries (25 MB), most of it under the end of the decode.
 constexpr int kFinishThreads = 256;
 constexpr int kFinishWarps = kFinishThreads / 32;
 // cached rows a CTA takes at least: about 4 KB of scores, 16 KB of wide rows
