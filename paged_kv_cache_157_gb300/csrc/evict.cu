@@ -9,10 +9,11 @@
 // select: one cluster of CTAs per (sequence, kv head). The scores become
 // unsigned keys of the same order; counting passes over digits of 11 bits (8
 // in a cluster) find the key T of the last row that stays and how many rows
-// with that key stay; a prefix sum over the rows writes the kept rows in order.
+// with that key stay (they end early when all that match so far stay); a prefix
+// sum over the rows writes the kept rows in order.
 // A CTA holds its share of the keys in registers, so a score is read once
 // (shares beyond 8192 rows are read again each pass). Bound by the chain of
-// passes and barriers (12 us for 256 rows of 4096 scores, 18 us for 8 rows of
+// passes and barriers (11 us for 256 rows of 4096 scores, 15 us for 8 rows of
 // 65537); a cluster splits a long row over up to 8 SMs.
 //
 // move: one warp per 32 kept rows (one block of the new table for one-byte
@@ -127,7 +128,8 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictPa
   auto load = [&](int span) {
     float x[kKeys];  // all loads first (of the last row where there is none): no branch between them
 #pragma unroll
-    for (int j = 0; j < kKeys; ++j) x[j] = __ldg(scores + lo + min(span * kSpan + j * kSelectThreads + tid, max(cnt, 1) - 1));
+    for (int j = 0; j < kKeys; ++j)
+      x[j] = __ldg(scores + lo + min(span * kSpan + j * kSelectThreads + tid, max(cnt, 1) - 1));
 #pragma unroll
     for (int j = 0; j < kKeys; ++j) key[j] = key_of(x[j]);
   };
@@ -202,12 +204,16 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictPa
     prefix = (prefix << bits) | s_found[0];
     need -= s_found[1];
     at_t = s_found[2];
+    if (at_t == need) break;  // all that match stay, whatever their lower digits (the same in every CTA)
   }
 
-  // prefix is the key T; of the rows at T the `need` lowest stay (mostly all:
-  // then they count as above T). What the cluster's earlier CTAs hold comes first.
+  // prefix is the key T, or the leading bits of the keys at it that all stay
+  // (mostly: then they count as above T); else the `need` lowest rows at T stay.
+  // What the cluster's earlier CTAs hold comes first.
   const bool ties = at_t != need;
-  auto is_more = [&](int span, int j) { return valid(span, j) && (ties ? key[j] > prefix : key[j] >= prefix); };
+  auto is_more = [&](int span, int j) {
+    return valid(span, j) && (ties ? key[j] > prefix : (key[j] >> shift) >= prefix);
+  };
   auto is_same = [&](int span, int j) { return valid(span, j) && key[j] == prefix; };
   uint32_t before_more = 0, before_same = 0;
   if (C > 1) {
