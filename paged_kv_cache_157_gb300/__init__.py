@@ -25,8 +25,8 @@ __all__ = [
     "new_scored_workspace", "evict_rows",
     "decode_mla_workspace_size", "decode_attention_mla", "set_option", "get_option",
     "get_error_flags", "BlockPool", "slots_from_tables",
-    "F32", "F16", "BF16", "E4M3", "INT8", "FLAG_BAD_BLOCK", "FLAG_BAD_LEN", "FLAG_BAD_SLOT", "FLAG_TIMEOUT", "FLAG_WORKSPACE",
-    "new_decode_workspace",
+    "F32", "F16", "BF16", "E4M3", "INT8", "FLAG_BAD_BLOCK", "FLAG_BAD_LEN", "FLAG_BAD_SLOT", "FLAG_TIMEOUT",
+    "FLAG_WORKSPACE", "new_decode_workspace",
     "OPT_CHECKED", "OPT_BLOCKS_PER_CTA", "OPT_MAX_CTAS", "OPT_GQA_ENGINE", "OPT_DYNAMIC_SHARE", "OPT_DYNAMIC_CHUNK",
     "OPT_WAIT_POLLS",
 ]
@@ -746,8 +746,8 @@ def decode_attention_scored(q, k_cache, v_cache, block_tables, context_lens, sca
                                   (scores, "scores", torch.float32), (workspace, "workspace", None)))
     B, T, hq, d, nb, hkv, bs, mb = _decode_shape(q, out, k_cache, v_cache, block_tables, context_lens, scores)
     _check(raw().kvc_decode_attention_scored(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                             block_tables.data_ptr(), mb, context_lens.data_ptr(), B, T, scale, hq, hkv,
-                                             d, bs, nb, _code_of(k_cache), out.data_ptr(), _code_of(out),
+                                             block_tables.data_ptr(), mb, context_lens.data_ptr(), B, T, float(scale),
+                                             hq, hkv, d, bs, nb, _code_of(k_cache), out.data_ptr(), _code_of(out),
                                              scores.data_ptr(), workspace.data_ptr(), workspace.nbytes,
                                              _stream_of(stream, k_cache)), "kvc_decode_attention_scored")
 
@@ -768,10 +768,11 @@ def decode_attention_block8(q, k_cache, v_cache, k_scale, v_scale, block_tables,
     _check_block_scales(k_scale, v_scale, nb, hkv)
     _check(raw().kvc_decode_attention_block8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                                              v_scale.data_ptr(), code, block_tables.data_ptr(), mb,
-                                             context_lens.data_ptr(), B, T, scale, hq, hkv, d, bs, nb, _code_of(q),
-                                             out.data_ptr(), _code_of(out),
+                                             context_lens.data_ptr(), B, T, float(scale), hq, hkv, d, bs, nb,
+                                             _code_of(q), out.data_ptr(), _code_of(out),
                                              None if scores is None else scores.data_ptr(), workspace.data_ptr(),
-                                             workspace.nbytes, _stream_of(stream, k_cache)), "kvc_decode_attention_block8")
+                                             workspace.nbytes, _stream_of(stream, k_cache)),
+           "kvc_decode_attention_block8")
 
 
 def evict_rows(scores, k_cache, v_cache, block_tables, context_lens, budget, recent, new_block_tables, kept, new_lens,
@@ -782,6 +783,7 @@ def evict_rows(scores, k_cache, v_cache, block_tables, context_lens, budget, rec
     [B, Hkv, budget] (old rows, -1 past the end), new_lens int32 [B], new_scores fp32 [B, Hkv, new_max_blocks * bs]."""
     torch = _torch()
     i32, f32 = torch.int32, torch.float32
+    budget, recent = int(budget), int(recent)
     if (k_scale is None) != (v_scale is None):
         raise ValueError("k_scale and v_scale go together")
     tensors = ((v_cache, "v_cache", getattr(k_cache, "dtype", None)), (scores, "scores", f32),
@@ -813,5 +815,5 @@ def evict_rows(scores, k_cache, v_cache, block_tables, context_lens, budget, rec
     _check(raw().kvc_evict_rows_block8(scores.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                                        v_scale.data_ptr(), code, block_tables.data_ptr(), mb, context_lens.data_ptr(),
                                        B, budget, recent, new_block_tables.data_ptr(), new_mb, nb, bs, hkv, d,
-                                       kept.data_ptr(), new_lens.data_ptr(), new_scores.data_ptr(), _stream_of(stream, k_cache)),
-           "kvc_evict_rows_block8")
+                                       kept.data_ptr(), new_lens.data_ptr(), new_scores.data_ptr(),
+                                       _stream_of(stream, k_cache)), "kvc_evict_rows_block8")

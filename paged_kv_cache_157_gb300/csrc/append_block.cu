@@ -74,7 +74,8 @@ __device__ __forceinline__ int64_t block_of(int64_t slot, const AppendBlockParam
 
 constexpr int kAppendWarps = 4;
 constexpr int kAppendThreads = 32 * kAppendWarps;
-constexpr int kWindows = 8;       // of 32 tokens, that a CTA looks at: its stretch (at most 4) and what its last run may reach
+// windows of 32 tokens that a CTA looks at: its stretch (at most 4) and what its last run may reach
+constexpr int kWindows = 8;
 constexpr int kInFlight = 8;      // 16-byte chunks a lane holds
 constexpr int kAppendCtasPerSm = 4;
 

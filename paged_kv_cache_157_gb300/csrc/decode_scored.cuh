@@ -218,8 +218,8 @@ __device__ __forceinline__ void softmax_step(float (&x)[NT][4], State<D, NT, ONE
 // 16. (One body for both: small calls run every line once, and what they wait
 // for then is instructions.)
 template <bool BF, int D, int NT>
-__device__ __forceinline__ void tile16(uint32_t k, uint32_t v, int rem, bool edge, float qscale, float* lg, int qns, int col0,
-                                       int qn, State<D, NT, false>& st, int lane) {
+__device__ __forceinline__ void tile16(uint32_t k, uint32_t v, int rem, bool edge, float qscale, float* lg, int qns,
+                                       int col0, int qn, State<D, NT, false>& st, int lane) {
   using namespace wmma16;
   constexpr int NP = BF ? 3 : 2;
   constexpr int CH = NT == 1 ? 4 : 2;  // independent accumulator chains
@@ -297,8 +297,8 @@ __device__ __forceinline__ void tile16(uint32_t k, uint32_t v, int rem, bool edg
 // 2c, 2c + 1, 2c + 8, 2c + 9, and a byte permute pairs two rows of one dim. Output
 // tile i of a span then holds its dims 16g + 2i and 16g + 2i + 1 (8g + 2i).
 template <int Q8, int D, int NT>
-__device__ __forceinline__ void tile8(uint32_t k, uint32_t v, int rem, bool edge, float ks, float vs, float* lg, int qns,
-                                      int col0, int qn, State<D, NT, true>& st, int lane) {
+__device__ __forceinline__ void tile8(uint32_t k, uint32_t v, int rem, bool edge, float ks, float vs, float* lg,
+                                      int qns, int col0, int qn, State<D, NT, true>& st, int lane) {
   using namespace wmma16;
   constexpr int NP = 2;
   constexpr int CH = NT == 1 ? 4 : 2;
@@ -680,113 +680,112 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
                 ? nullptr
                 : p.logits + (static_cast<int64_t>(u.seq) * p.n_kv_heads + u.kvh) * p.rows * p.qns;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      // ---- Q^T fragments of query g (columns past the last query: zeros)
-      const int v = col0 + 8 * n + lanes_g;
-      const bool have = v < p.qn;
-      const int tq = divided(v, m_group);
-      const int64_t qrow = (static_cast<int64_t>(u.seq) * p.n_tok + tq) * p.n_q_heads + u.kvh * p.group + v - tq * p.group;
-      const unsigned short* qr = static_cast<const unsigned short*>(p.q) + (have ? qrow * D : 0);
-      if constexpr (!ONE) {
+      for (int n = 0; n < NT; ++n) {
+        // ---- Q^T fragments of query g (columns past the last query: zeros)
+        const int v = col0 + 8 * n + lanes_g;
+        const bool have = v < p.qn;
+        const int tq = divided(v, m_group);
+        const int64_t qrow =
+            (static_cast<int64_t>(u.seq) * p.n_tok + tq) * p.n_q_heads + u.kvh * p.group + v - tq * p.group;
+        const unsigned short* qr = static_cast<const unsigned short*>(p.q) + (have ? qrow * D : 0);
+        if constexpr (!ONE) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
+          for (int ks = 0; ks < D / 16; ++ks) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            st.q[n][ks][h] = have ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * ks + 8 * h + 2 * c)) : 0u;
-        }
-      } else {
-        // dims of lane c, k-step s of a span: 4 s .. 4 s + 3 of its part; scaled
-        // by 2^t so that the query's largest entry lies in [2^14, 2^15): exact
-        // in f16 but for entries below 2^-39 of the largest
-        constexpr int BOXB = D < 128 ? D : 128;
-        constexpr int KS = BOXB / 16;
-        float y[D / 16][4];
-        float amax = 0.f;
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const int d = (s / KS) * BOXB + (BOXB / 4) * c + 4 * (s % KS);
-          uint2 u2 = make_uint2(0u, 0u);
-          if (have) u2 = __ldg(reinterpret_cast<const uint2*>(qr + d));
-          float2 a, b;
-          if (p.q_f16) {
-            a = wmma16::unpack2<false>(u2.x);
-            b = wmma16::unpack2<false>(u2.y);
-          } else {
-            a = wmma16::unpack2<true>(u2.x);
-            b = wmma16::unpack2<true>(u2.y);
+            for (int h = 0; h < 2; ++h)
+              st.q[n][ks][h] = have ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * ks + 8 * h + 2 * c)) : 0u;
           }
-          y[s][0] = a.x;
-          y[s][1] = a.y;
-          y[s][2] = b.x;
-          y[s][3] = b.y;
+        } else {
+          // dims of lane c, k-step s of a span: 4 s .. 4 s + 3 of its part; scaled
+          // by 2^t so that the query's largest entry lies in [2^14, 2^15): exact
+          // in f16 but for entries below 2^-39 of the largest
+          constexpr int BOXB = D < 128 ? D : 128;
+          constexpr int KS = BOXB / 16;
+          float y[D / 16][4];
+          float amax = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(y[s][e]));
+          for (int s = 0; s < D / 16; ++s) {
+            const int d = (s / KS) * BOXB + (BOXB / 4) * c + 4 * (s % KS);
+            uint2 u2 = make_uint2(0u, 0u);
+            if (have) u2 = __ldg(reinterpret_cast<const uint2*>(qr + d));
+            float2 a, b;
+            if (p.q_f16) {
+              a = wmma16::unpack2<false>(u2.x);
+              b = wmma16::unpack2<false>(u2.y);
+            } else {
+              a = wmma16::unpack2<true>(u2.x);
+              b = wmma16::unpack2<true>(u2.y);
+            }
+            y[s][0] = a.x;
+            y[s][1] = a.y;
+            y[s][2] = b.x;
+            y[s][3] = b.y;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(y[s][e]));
+          }
+          amax = fmaxf(amax, __shfl_xor_sync(full, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(full, amax, 2));
+          const int field = min(253, max(1, 268 - static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu)));
+          const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
+          const float down = p.qscale * __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            st.q[n][s][0] = wmma16::pack2<false>(y[s][0] * up, y[s][1] * up);
+            st.q[n][s][1] = wmma16::pack2<false>(y[s][2] * up, y[s][3] * up);
+          }
+          st.fq[n][0] = __shfl_sync(full, down, 8 * c);      // of query 2c, held by the lanes with g = 2c
+          st.fq[n][1] = __shfl_sync(full, down, 8 * c + 4);  // of query 2c + 1
         }
-        amax = fmaxf(amax, __shfl_xor_sync(full, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(full, amax, 2));
-        const int field = min(253, max(1, 268 - static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu)));
-        const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
-        const float down = p.qscale * __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          st.q[n][s][0] = wmma16::pack2<false>(y[s][0] * up, y[s][1] * up);
-          st.q[n][s][1] = wmma16::pack2<false>(y[s][2] * up, y[s][3] * up);
+        for (int e = 0; e < 2; ++e) {
+          st.m[n][e] = -1e30f;  // finite: a query that meets only masked rows keeps weight 0
+          st.l[n][e] = 0.f;
+          if constexpr (ONE) st.mo[n][e] = -1e30f;
+          const int t = divided(col0 + 8 * n + 2 * c + e, m_group);
+          st.dt[n][e] = t < p.n_tok ? p.n_tok - 1 - t : 0;
         }
-        st.fq[n][0] = __shfl_sync(full, down, 8 * c);      // of query 2c, held by the lanes with g = 2c
-        st.fq[n][1] = __shfl_sync(full, down, 8 * c + 4);  // of query 2c + 1
-      }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        st.m[n][e] = -1e30f;  // finite: a query that meets only masked rows keeps weight 0
-        st.l[n][e] = 0.f;
-        if constexpr (ONE) st.mo[n][e] = -1e30f;
-        const int t = divided(col0 + 8 * n + 2 * c + e, m_group);
-        st.dt[n][e] = t < p.n_tok ? p.n_tok - 1 - t : 0;
-      }
+        for (int i = 0; i < D / 16; ++i) {
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) st.o[n][i][e] = 0.f;
+          for (int e = 0; e < 4; ++e) st.o[n][i][e] = 0.f;
+        }
       }
     }
+    const int cnt = min(end - pos, TS);
+    ok = mbar_wait_data(bars + slot, ph, p.wait_polls);
+    ok = __all_sync(full, ok);
+    if (!ok) break;
+    if constexpr (ONE) {
+      cp_async_wait<S - 1>();
+      __syncwarp();
     }
-    {
-      const int cnt = min(end - pos, TS);
-      ok = mbar_wait_data(bars + slot, ph, p.wait_polls);
-      ok = __all_sync(full, ok);
-      if (!ok) break;
-      if constexpr (ONE) {
-        cp_async_wait<S - 1>();
-        __syncwarp();
-      }
 #pragma unroll 1
-      for (int t = 0; t < cnt; ++t) {
-        const int r0 = (j + t) * kTileRows;
-        const int rem = n_rows - r0;
-        float* lg = lg0 == nullptr ? nullptr : lg0 + static_cast<int64_t>(r0) * p.qns;
-        const uint32_t kt = ring + slot * G::kStageBytes + t * 2 * G::kTileBytes, vt = kt + G::kTileBytes;
-        if ((ivalid >> (slot * TS + t)) & 1u) {
-          const bool edge = rem < kTileRows + p.n_tok - 1;
-          if constexpr (ONE) {
-            const float* sc = s_scale + (slot * TS + t) * 2;
-            tile8<Q8, D, NT>(kt, vt, rem, edge, sc[0], sc[1], lg, p.qns, col0, p.qn, st, lane);
-          } else {
-            tile16<BF, D, NT>(kt, vt, rem, edge, p.qscale, lg, p.qns, col0, p.qn, st, lane);
-          }
-        } else if (lg != nullptr) {  // a block outside the pool: its rows get no weight
-          const int cols = min(NC, p.qns - col0);
-          for (int i = lane; i < min(rem, kTileRows) * cols; i += 32)
-            lg[static_cast<int64_t>(i / cols) * p.qns + col0 + i % cols] = kNegInf;
+    for (int t = 0; t < cnt; ++t) {
+      const int r0 = (j + t) * kTileRows;
+      const int rem = n_rows - r0;
+      float* lg = lg0 == nullptr ? nullptr : lg0 + static_cast<int64_t>(r0) * p.qns;
+      const uint32_t kt = ring + slot * G::kStageBytes + t * 2 * G::kTileBytes, vt = kt + G::kTileBytes;
+      if ((ivalid >> (slot * TS + t)) & 1u) {
+        const bool edge = rem < kTileRows + p.n_tok - 1;
+        if constexpr (ONE) {
+          const float* sc = s_scale + (slot * TS + t) * 2;
+          tile8<Q8, D, NT>(kt, vt, rem, edge, sc[0], sc[1], lg, p.qns, col0, p.qn, st, lane);
+        } else {
+          tile16<BF, D, NT>(kt, vt, rem, edge, p.qscale, lg, p.qns, col0, p.qn, st, lane);
         }
+      } else if (lg != nullptr) {  // a block outside the pool: its rows get no weight
+        const int cols = min(NC, p.qns - col0);
+        for (int i = lane; i < min(rem, kTileRows) * cols; i += 32)
+          lg[static_cast<int64_t>(i / cols) * p.qns + col0 + i % cols] = kNegInf;
       }
-      __syncwarp();  // every lane has read the stage
-      slot = slot + 1 == S ? 0 : slot + 1;
-      if (slot == 0) ph ^= 1u;
-      ++used;
-      --ahead;
-      pos += cnt;
-      j += cnt;
     }
+    __syncwarp();  // every lane has read the stage
+    slot = slot + 1 == S ? 0 : slot + 1;
+    if (slot == 0) ph ^= 1u;
+    ++used;
+    --ahead;
+    pos += cnt;
+    j += cnt;
     if (pos < end) continue;
 
     // ---- close the segment. A whole unit: its outputs. A part that ends
@@ -953,7 +952,7 @@ __device__ __forceinline__ RecList record_list(const int4 u, int workers) {
   return r;
 }
 __device__ __forceinline__ int64_t record_slot(const RecList& r, int i) {
-  return i < r.merged ? 2 * static_cast<int64_t>(max(r.first, (r.cta + i) * r.K)) + 1 : 2 * static_cast<int64_t>(r.last);
+  return i < r.merged ? 2ll * max(r.first, (r.cta + i) * r.K) + 1 : 2ll * r.last;
 }
 
 // V consecutive floats (V 2, 4 or 8; aligned to 8 or 16 bytes).
@@ -1060,8 +1059,8 @@ __device__ __forceinline__ void add_weights(const float* lg, float* sc, const fl
 // 32-token window 40.5 -> 37.1 us), without them the outputs' loads want the registers (decode of
 // e4m3 blocks, batch 32: 34.8 us against 36.1).
 template <int D, bool SCORED>
-__global__ void __launch_bounds__(kFinishThreads, SCORED ? 4 : 2) scored_finish_kernel(const ScoredParams p, int nc_log2,
-                                                                        int out_ctas) {
+__global__ void __launch_bounds__(kFinishThreads, SCORED ? 4 : 2)
+    scored_finish_kernel(const ScoredParams p, int nc_log2, int out_ctas) {
   using namespace scored;
   const int NC = 1 << nc_log2;  // queries of a column group
   constexpr int V = D / 32;  // output dims per lane
@@ -1216,7 +1215,7 @@ __global__ void __launch_bounds__(kFinishThreads, SCORED ? 4 : 2) scored_finish_
       for (int i = 0; i < 4; ++i) {
         ml[i] = make_float2(kNegInf, 0.f);
         if (i0 + i < r.n)
-          ml[i] = __ldcg(reinterpret_cast<const float2*>(p.rec_ml + (record_slot(r, i0 + i) * NC + (v & (NC - 1))) * 2));
+          ml[i] = __ldcg(reinterpret_cast<const float2*>(p.rec_ml) + record_slot(r, i0 + i) * NC + (v & (NC - 1)));
         M = fmaxf(M, ml[i].x);
       }
       l *= fast_exp2(m - M);
@@ -1233,7 +1232,7 @@ __global__ void __launch_bounds__(kFinishThreads, SCORED ? 4 : 2) scored_finish_
       if (r.n <= kFewRecords) continue;
       float m = kNegInf, l = 0.f;
       for (int i = lane; i < r.n; i += 32) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.rec_ml + (record_slot(r, i) * NC + (v & (NC - 1))) * 2));
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.rec_ml) + record_slot(r, i) * NC + (v & (NC - 1)));
         const float M = fmaxf(m, ml.x);
         l = l * fast_exp2(m - M) + ml.y * fast_exp2(ml.x - M);
         m = M;

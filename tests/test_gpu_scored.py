@@ -177,6 +177,7 @@ def test_rows_behind_the_end_may_hold_anything(kvc, kind):
 def test_invalid_lengths_and_blocks(kvc, kind):
     # lengths below the new tokens, negative, and beyond the table: zeros, flagged, scores left
     check(kvc, kind, [3, 0, 2, -5, 97, 64], 3, 8, 2, 64, 16, seed=31, width=6, flags=kvc.FLAG_BAD_LEN)
+    check(kvc, kind, [0, -1, 49], 1, 8, 2, 64, 16, seed=33, width=3, flags=kvc.FLAG_BAD_LEN)  # none is valid
     # entries outside the pool: their rows get no weight; a sequence with no other rows gives zeros
     lens, H, D, bs = [100, 16, 33], 2, 128, 16
     q, pools, tables, scores = make(kind, lens, 1, 8, H, D, bs, seed=32)
@@ -291,6 +292,15 @@ def test_non_finite_values_stay_in_their_sequence(kvc):
     bad = torch.isnan(out)
     assert bad[0, 0, :4, 5].all() and int(bad.sum()) == 4
     assert torch.isfinite(scores).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_more_sequences_than_lanes_with_several_tokens(kvc, kind):
+    rng = np.random.default_rng(3)
+    for B in (31, 32, 33, 50):
+        lens = rng.integers(3, 120, B).tolist()
+        lens[B // 2], lens[B - 1] = 0, 2  # invalid ones inside and at the end
+        check(kvc, kind, lens, 3, 6, 2, 64, 16, seed=B, width=9, flags=kvc.FLAG_BAD_LEN)
 
 
 def test_the_largest_batch(kvc):
