@@ -163,6 +163,7 @@ kvc_status decode(Cache cache, const ScoredShape& s, const void* q, kvc_dtype q_
   char* ws = static_cast<char*>(workspace);
   ScoredParams p{};
   p.q = q;
+  p.v_cache = v_cache;
   p.block_tables = block_tables;
   p.context_lens = context_lens;
   p.k_scale = k_scale;

@@ -19,7 +19,7 @@
 // kv heads, D 128), decode and finish: bf16, batch 32 x 4096 rows 97.7 us (90 us
 // of them the decode, 6.05 TB/s); e4m3 blocks, batch 32 x U[512, 4096] 34.7 us, at
 // 7.0 TB/s for what a larger batch adds. More queries (32 tokens, 128 queries per
-// kv head over 2 x 4000 rows: 37 us) are bound by the products' latency.
+// kv head over 2 x 4000 rows: 38 us) are bound by the products' latency.
 //
 // Work split. The 16-row tiles of all (sequence, kv head, column group) units
 // are laid end to end and cut into equal ranges, one per WARP. A warp is a
@@ -183,6 +183,39 @@ __device__ __forceinline__ void clear_rows(uint32_t v, int rem, int lane) {
   }
   fence_proxy_async_smem();
   __syncwarp();
+}
+
+// Rows [r0, r1) of a tile's V, which some of the new tokens see and others do
+// not: an infinity or NaN there would reach the latter too (0 x NaN), so it
+// becomes 0 (close_odd_rows gives it to the others). True if there was one.
+// FIELD: the elements' exponents (e4m3: all but the sign), LOW: their lowest
+// bits; a full field carries into its element's sign.
+template <int BOXB, int HALVES, uint32_t FIELD, uint32_t LOW>
+__device__ __forceinline__ bool clean_rows(uint32_t v, int r0, int r1, int lane) {
+  constexpr int CH = BOXB / 16;
+  constexpr uint32_t SIGN = FIELD + LOW, ELEM = SIGN == 0x80808080u ? 0xffu : 0xffffu;
+  bool any = false;
+#pragma unroll 2
+  for (int i = r0 * CH + lane; i < r1 * CH; i += 32) {
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h) {
+      const uint32_t at = v + h * (kTileRows * BOXB) + i * 16;
+      const uint4 u = wmma16::lds128(at);
+      auto odd = [](uint32_t x) { return (((x & FIELD) + LOW) & SIGN) / (ELEM / 2 + 1) * ELEM; };
+      const uint32_t a = odd(u.x), b = odd(u.y), c = odd(u.z), d = odd(u.w);
+      if ((a | b | c | d) == 0) continue;
+      any = true;
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(u.x & ~a), "r"(u.y & ~b), "r"(u.z & ~c),
+                   "r"(u.w & ~d)
+                   : "memory");
+    }
+  }
+  any = __any_sync(0xffffffffu, any);
+  if (any) {
+    fence_proxy_async_smem();
+    __syncwarp();
+  }
+  return any;
 }
 
 // Running softmax over one tile: x becomes the weights relative to the
@@ -501,9 +534,60 @@ struct Batch {
   }
 };
 
+// Dim of o[.][i][0 and 1] in the lanes with lane / 4 = g; that of [2 and 3] is
+// 8 behind it (16-bit caches) or 1 (one-byte caches).
+template <int D, bool ONE>
+__device__ __forceinline__ int out_dim(int i, int g) {
+  constexpr int BOXB = D < 128 ? D : 128;
+  constexpr int KS = BOXB / 16;
+  return ONE ? (i / KS) * BOXB + (BOXB / 8) * g + 2 * (i % KS) : 16 * i + g;
+}
+
+// Gives the infinities and NaN of the segment's rows that clean_rows cleared to
+// the queries that see them (their weights are positive: the value itself). Rare.
+template <typename CT, int D, int NT>
+__device__ __forceinline__ void close_odd_rows(const ScoredParams& p, const Unit& u, int n_rows, int tile0, int tile1,
+                                               State<D, NT, sizeof(CT) == 1>& st, int lane) {
+  constexpr bool ONE = sizeof(CT) == 1;
+  const int g = lane >> 2;
+  const int r1 = min(n_rows, tile1 * kTileRows);
+#pragma unroll 1
+  for (int r = max(n_rows - p.n_tok + 1, tile0 * kTileRows); r < r1; ++r) {
+    const int b = r / p.block_size;
+    const int phys = __ldg(p.block_tables + static_cast<int64_t>(u.seq) * p.max_blocks + b);
+    if (phys < 0 || phys >= p.num_blocks) continue;
+    const int64_t at = (static_cast<int64_t>(phys) * p.n_kv_heads + u.kvh) * p.block_size + (r - b * p.block_size);
+    const CT* row = static_cast<const CT*>(p.v_cache) + at * D;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const CT* x = row + out_dim<D, ONE>(i, g) + (ONE ? k : 8 * k);
+        float y = 0.f;
+        if constexpr (ONE) {
+          if ((__ldg(reinterpret_cast<const unsigned char*>(x)) & 0x7f) == 0x7f) y = __int_as_float(0x7fffffff);
+        } else {
+          y = wmma16::unpack2<std::is_same<CT, __nv_bfloat16>::value>(
+                  __ldg(reinterpret_cast<const unsigned short*>(x))).x;
+        }
+        if (fabsf(y) < __builtin_huge_valf()) continue;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (r < n_rows - st.dt[n][e]) st.o[n][i][2 * k + e] += y;
+        }
+      }
+    }
+  }
+}
+
 }  // namespace scored
 
-template <typename CT, int D, int NT>
+// SHUT: rows of the last tokens are searched for infinities and NaN, which
+// earlier tokens do not see (several new tokens; the code costs the others 1 us
+// of 35 where it is merely present).
+template <typename CT, int D, int NT, bool SHUT>
 __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
     scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const ScoredParams p) {
@@ -665,6 +749,8 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
   State<D, NT, ONE> st;
   Unit u{};
   int end = lo, n_rows = 0, col0 = 0, j = 0;
+  int shared_rows = 0;  // rows that all tokens see
+  bool odd = false;     // clean_rows found an infinity or NaN in this segment
   float* lg0 = nullptr;
 #pragma unroll 1
   for (int pos = lo; pos < hi;) {
@@ -674,6 +760,7 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
       u = bt.locate(pos, p);
       end = min(u.u0 + u.tiles, hi);
       n_rows = bt.rows_of(u.seq, p);
+      shared_rows = n_rows - p.n_tok + 1;
       col0 = u.hsub * NC;
       j = pos - u.u0;
       lg0 = p.scores == nullptr
@@ -759,6 +846,20 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
       cp_async_wait<S - 1>();
       __syncwarp();
     }
+    if constexpr (SHUT) {
+      if ((j + cnt) * kTileRows > shared_rows) {
+        constexpr uint32_t FIELD = ONE ? 0x7f7f7f7fu : BF ? 0x7f807f80u : 0x7c007c00u;
+        constexpr uint32_t LOW = ONE ? 0x01010101u : BF ? 0x00800080u : 0x04000400u;
+#pragma unroll 1
+        for (int t = 0; t < cnt; ++t) {
+          const int r0 = (j + t) * kTileRows;
+          if ((ivalid >> (slot * TS + t)) & 1u)
+            odd |= clean_rows<G::kBoxBytes, G::kHalves, FIELD, LOW>(
+                ring + slot * G::kStageBytes + (2 * t + 1) * G::kTileBytes, max(shared_rows - r0, 0),
+                min(n_rows - r0, kTileRows), lane);
+        }
+      }
+    }
 #pragma unroll 1
     for (int t = 0; t < cnt; ++t) {
       const int r0 = (j + t) * kTileRows;
@@ -788,6 +889,10 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
     j += cnt;
     if (pos < end) continue;
 
+    if constexpr (SHUT) {
+      if (odd) close_odd_rows<CT, D, NT>(p, u, n_rows, max(u.u0, lo) - u.u0, pos - u.u0, st, lane);
+      odd = false;
+    }
     // ---- close the segment. A whole unit: its outputs. A part that ends
     // inside the range (the unit began in an earlier worker's): record 2 wk.
     // The part at the range's end: merged with its neighbours' below.
@@ -809,11 +914,7 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
     float* so = reinterpret_cast<float*>(smem + static_cast<size_t>(w) * S * G::kStageBytes);
     const int64_t rec = 2ll * wk + (last_part ? 1 : 0);
     if (keep) __syncwarp();
-    // dims of the lane's values: 16-bit caches 16 i + g (+ 8), one-byte caches
-    // [span] + (span / 8) g + 2 i (+ 1)
-    constexpr int BOXB = D < 128 ? D : 128;
-    constexpr int KS = BOXB / 16;
-    auto dim = [&](int i) { return ONE ? (i / KS) * BOXB + (BOXB / 8) * lanes_g + 2 * (i % KS) : 16 * i + lanes_g; };
+    auto dim = [&](int i) { return out_dim<D, ONE>(i, lanes_g); };
     constexpr int SECOND = ONE ? 1 : 8;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -1257,10 +1358,10 @@ __global__ void __launch_bounds__(kFinishThreads, SCORED ? 4 : 2)
 
 namespace scored {
 
-template <typename CT, int D, int NT>
-kvc_status run(const ScoredParams& p, int grid, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
-  using G = ScoredGeo<sizeof(CT), D, NT>;
-  auto* k = scored_decode_kernel<CT, D, NT>;
+template <typename CT, int D, int NT, bool SHUT>
+kvc_status run_decode(const ScoredParams& p, int grid, const CUtensorMap& tk, const CUtensorMap& tv,
+                      cudaLaunchAttribute* attr, cudaStream_t stream) {
+  auto* k = scored_decode_kernel<CT, D, NT, SHUT>;
   // The opt-in to large shared memory holds per device: made at the first call on each.
   static std::atomic<uint64_t> opted{0};
   int dev = 0;
@@ -1273,18 +1374,26 @@ kvc_status run(const ScoredParams& p, int grid, const CUtensorMap& tk, const CUt
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(scored decode)");
     opted.fetch_or(bit);
   }
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(G::kThreads);
+  cfg.blockDim = dim3(ScoredGeo<sizeof(CT), D, NT>::kThreads);
   cfg.dynamicSmemBytes = scored_smem_bytes<sizeof(CT), D, NT>(p.batch);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, k, tk, tv, p);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx(scored decode)");
+  return e == cudaSuccess ? KVC_OK : cuda_fail(e, "cudaLaunchKernelEx(scored decode)");
+}
+
+template <typename CT, int D, int NT>
+kvc_status run(const ScoredParams& p, int grid, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  constexpr bool FINITE = std::is_same<CT, s8q>::value;  // every int8 code is
+  const kvc_status st = FINITE || p.n_tok == 1 ? run_decode<CT, D, NT, false>(p, grid, tk, tv, attr, stream)
+                                               : run_decode<CT, D, NT, !FINITE>(p, grid, tk, tv, attr, stream);
+  if (st != KVC_OK) return st;
   // CTAs per (sequence, kv head): one wave of them on the GPU, no more than
   // there is work for. For the outputs a warp per query or a few of them in
   // turn, or up to a CTA per query where few units share all workers and a
@@ -1307,8 +1416,8 @@ kvc_status run(const ScoredParams& p, int grid, const CUtensorMap& tk, const CUt
   fin.stream = stream;
   fin.attrs = attr;
   fin.numAttrs = 1;
-  e = cudaLaunchKernelEx(&fin, p.scores != nullptr ? scored_finish_kernel<D, true> : scored_finish_kernel<D, false>, p,
-                         NT == 1 ? 3 : 4, static_cast<int>(out_ctas));
+  auto* finish = p.scores != nullptr ? scored_finish_kernel<D, true> : scored_finish_kernel<D, false>;
+  const cudaError_t e = cudaLaunchKernelEx(&fin, finish, p, NT == 1 ? 3 : 4, static_cast<int>(out_ctas));
   if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx(scored finish)");
   return KVC_OK;
 }

@@ -17,6 +17,7 @@ struct ScoredParams {
   const void* q;                // [batch, n_tok, n_q_heads, D]
   const int32_t* block_tables;  // [batch, max_blocks]
   const int32_t* context_lens;  // [batch]
+  const void* v_cache;
   const float* k_scale;         // one-byte caches: [num_blocks, n_kv_heads]
   const float* v_scale;
   void* out;      // [batch, n_tok, n_q_heads, D]

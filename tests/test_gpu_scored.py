@@ -294,6 +294,41 @@ def test_non_finite_values_stay_in_their_sequence(kvc):
     assert torch.isfinite(scores).all()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kind", KINDS[:3])  # every int8 code is finite
+def test_tokens_do_not_see_non_finite_rows_behind_them(kvc, kind, D):
+    # the rows of the last tokens hold infinities and NaN: the tokens before give the same bits as without them, a
+    # token that sees one gives what fp64 gives, in the dims where it stands
+    lens, H, bs, T = [41, 16, 9, 64, 130], 2, 16, 7
+    q, pools, tables, scores = make(kind, lens, T, 6, H, D, bs, seed=61)
+    n, t = torch.tensor(lens, dtype=torch.int32, device="cuda"), torch.from_numpy(tables).cuda()
+    ws = workspace_for(kvc, q, pools[0][0], tables, True)
+    res = []
+    for odd in (False, True):
+        if odd:
+            for i, m in enumerate(lens):
+                for back, dim in ((1, D - 3), (3, 0), (3, D // 2 + 9)):  # rows n - 1 and n - 3
+                    b, r = int(tables[i, (m - back) // bs]), (m - back) % bs
+                    pools[1][0][b, 0, r, dim] = 0x7f if kind == "e4m3" else float("inf") if dim == 0 else float("nan")
+        out = torch.empty(q.shape, device="cuda")
+        call_decode(kvc, kind, q, pools, t, n, 0.1, out, scores.clone(), ws)
+        res.append(out.view(len(lens), T, H, 3, D))
+    clean, got = res
+    assert torch.isfinite(clean).all()
+    seen = torch.zeros_like(clean, dtype=torch.bool)  # token T - 1 sees row n - 1, T - 3 and later see n - 3
+    seen[:, T - 1:, 0, :, D - 3] = True
+    seen[:, T - 3:, 0, :, 0] = True
+    seen[:, T - 3:, 0, :, D // 2 + 9] = True
+    assert torch.equal(torch.isfinite(got), ~seen)
+    assert torch.equal(got[:, :T - 3], clean[:, :T - 3])
+    assert torch.equal(got[:, :, 1], clean[:, :, 1])
+    if kind != "e4m3":
+        assert (got[:, T - 3:, 0, :, 0] == float("inf")).all()
+    # the other dims of a row that is taken by itself: within a few roundings of the weights' parts and the sums
+    spread = (got - clean)[~seen].abs().max().item()
+    assert spread <= 130 * 2.0 ** -22 * max(1.0, float(np.abs(pools[1][2]).max()))
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_more_sequences_than_lanes_with_several_tokens(kvc, kind):
     rng = np.random.default_rng(3)
