@@ -485,8 +485,8 @@ kvc_status kvc_decode_attention_block8(const void* q, const void* k_cache, const
  * n = 0 keeps nothing; n < 0 or n > max_blocks_per_seq * block_size sets
  * KVC_FLAG_BAD_LEN and counts as 0. A row whose old or new block lies outside
  * the pool is not moved and sets KVC_FLAG_BAD_BLOCK. F32, F16 and BF16; head_dim
- * times element size a multiple of 16 bytes; any block_size. No workspace; two
- * kernels on `stream`; may be captured.
+ * times element size a multiple of 16 bytes, 1 MB at most; any block_size. No
+ * workspace; two kernels on `stream`; may be captured.
  * Source: the closing section of "KV缓存原理与显存估算" (state that leaves the
  * cache) and "KV-Cache——为什么AI回复越来越快" section 08 (keeping part of the
  * rows); the choice by accumulated weight is this library's. */

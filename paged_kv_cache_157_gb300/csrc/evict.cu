@@ -421,6 +421,7 @@ kvc_status evict(const float* scores, void* k_cache, void* v_cache, float* k_sca
                 static_cast<long long>(new_rows));
   if (row_bytes % 16 != 0)
     return fail(KVC_ERR_UNSUPPORTED, "head_dim x element size must be a multiple of 16 bytes");
+  if (row_bytes > (1 << 20)) return fail(KVC_ERR_UNSUPPORTED, "head_dim x element size above 1 MB");
   if (rows > (1ll << 30) || new_rows > (1ll << 30))
     return fail(KVC_ERR_UNSUPPORTED, "max_blocks_per_seq x block_size too large");
   const int64_t units = static_cast<int64_t>(batch) * n_heads;

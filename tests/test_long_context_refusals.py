@@ -89,7 +89,7 @@ def evict(kvc, **kw):
     (dict(B=0), "INVALID_ARG"), (dict(H=0), "INVALID_ARG"), (dict(bs=0), "INVALID_ARG"), (dict(nb=0), "INVALID_ARG"),
     (dict(budget=0), "INVALID_ARG"), (dict(recent=-1), "INVALID_ARG"), (dict(recent=33), "INVALID_ARG"),
     (dict(budget=33), "INVALID_ARG"), (dict(D=0), "INVALID_ARG"), (dict(D=4), "UNSUPPORTED"),
-    (dict(dtype=3), "INVALID_ARG"), (dict(mb=1 << 27), "UNSUPPORTED"), (dict(scores=Z), "INVALID_ARG"),
+    (dict(D=1 << 30), "UNSUPPORTED"), (dict(dtype=3), "INVALID_ARG"), (dict(mb=1 << 27), "UNSUPPORTED"), (dict(scores=Z), "INVALID_ARG"),
     (dict(kept=Z), "INVALID_ARG"), (dict(k=ODD), "INVALID_ARG"), (dict(ns=P), "INVALID_ARG"),
     (dict(nl=P), "INVALID_ARG"), (dict(new=P), "INVALID_ARG"),
 ])
