@@ -168,6 +168,25 @@ __device__ __forceinline__ void weight_parts(const float (&w)[NT][4], uint32_t (
   }
 }
 
+// Leaves a tile's scaled scores to the finishing kernel, two queries at a time.
+// The column that pads an odd number of queries gets weight 0 whatever its
+// product was (0 x infinity is NaN).
+template <int NT>
+__device__ __forceinline__ void store_scores(const float (&x)[NT][4], float* lg, int qns, int col0, int qn, int rem,
+                                             int lane) {
+  const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int col = col0 + 8 * n + 2 * c;
+    if (col < qn) {
+      const bool pad = col + 1 == qn;
+      float* at = lg + static_cast<int64_t>(g) * qns + col;
+      if (g < rem) *reinterpret_cast<float2*>(at) = make_float2(x[n][0], pad ? kNegInf : x[n][1]);
+      if (g + 8 < rem) *reinterpret_cast<float2*>(at + 8 * qns) = make_float2(x[n][2], pad ? kNegInf : x[n][3]);
+    }
+  }
+}
+
 // Clears the V rows at and behind rem (< 16) of a tile: they may hold anything,
 // and 0 x NaN is NaN. The fence orders these writes before the copy that
 // next fills the stage.
@@ -292,17 +311,7 @@ __device__ __forceinline__ void tile16(uint32_t k, uint32_t v, int rem, bool edg
     mask_edge<D, NT, false>(x, st, rem, g);
     if (rem < kTileRows) clear_rows<128, D / 64>(v, rem, lane);
   }
-  if (lg != nullptr) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int col = col0 + 8 * n + 2 * c;
-      if (col < qn) {
-        float* at = lg + static_cast<int64_t>(g) * qns + col;
-        if (g < rem) *reinterpret_cast<float2*>(at) = make_float2(x[n][0], x[n][1]);
-        if (g + 8 < rem) *reinterpret_cast<float2*>(at + 8 * qns) = make_float2(x[n][2], x[n][3]);
-      }
-    }
-  }
+  if (lg != nullptr) store_scores<NT>(x, lg, qns, col0, qn, rem, lane);
   softmax_step<D, NT, false>(x, st, 0.f);
   uint32_t b[NT][NP][2];
   weight_parts<BF, NT, NP>(x, b);
@@ -386,17 +395,7 @@ __device__ __forceinline__ void tile8(uint32_t k, uint32_t v, int rem, bool edge
     mask_edge<D, NT, true>(x, st, rem, g);
     if (rem < kTileRows) clear_rows<BOXB, SPANS>(v, rem, lane);
   }
-  if (lg != nullptr) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int col = col0 + 8 * n + 2 * c;
-      if (col < qn) {
-        float* at = lg + static_cast<int64_t>(g) * qns + col;
-        if (g < rem) *reinterpret_cast<float2*>(at) = make_float2(x[n][0], x[n][1]);
-        if (g + 8 < rem) *reinterpret_cast<float2*>(at + 8 * qns) = make_float2(x[n][2], x[n][3]);
-      }
-    }
-  }
+  if (lg != nullptr) store_scores<NT>(x, lg, qns, col0, qn, rem, lane);
   softmax_step<D, NT, true>(x, st, fast_log2(vs));
   uint32_t b[NT][NP][2];
   weight_parts<false, NT, NP>(x, b);
