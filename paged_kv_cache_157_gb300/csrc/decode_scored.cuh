@@ -33,10 +33,9 @@
 // Products on m16n8k16 MMAs, rows (or dims) x queries:
 //   S^T [16 rows x 8 queries] = K [16 x D] . Q^T,
 //   O^T [D x 8 queries] += V^T [D x 16 rows] . P^T
-// fp32 accumulation. The weights enter as a sum of 16-bit parts: two f16 parts
-// (22 bits; a weight is at most 2^8, the second part reaches 2^-25) or, for bf16
-// caches, three bf16 parts (24 bits), because fp32 outputs are to be as good
-// as an fp32 softmax; the extra products are hidden behind HBM. One-byte codes
+// fp32 accumulation. The weights enter as 16-bit parts: two f16 parts (22 bits,
+// see Margin) or, for bf16 caches, three bf16 parts (24 bits), because fp32 outputs
+// are to be as good as an fp32 softmax; the extra products are hidden behind HBM. One-byte codes
 // are exact f16 values and are converted in registers; queries become f16
 // after a scaling by a power of two that is exact, per query.
 #pragma once
@@ -82,6 +81,23 @@ __device__ __forceinline__ float fast_log2(float x) {
   return y;
 }
 
+// Where a query's reference m (log2 units) lies: kBelow under the largest score
+// when it moves, and it moves when a score exceeds it by kAbove.
+//
+// A weight 2^(x - m) enters the second product in 16-bit parts. Three bf16 parts
+// hold any fp32 weight in 24 bits: the reference is the maximum, and weights
+// reach 2^8. f16 ends at 2^-24, and rows beside an attention sink have weights
+// of that size. So f16 parts use the whole range (largest weight 2^11 to 2^15),
+// and the second part is the rest times 2^11 (kRestScale; at most 2^14), in a
+// product of its own that is scaled back: 22 bits down to 2^-25 of the largest
+// weight, and off by at most 2^-47 of the largest one below.
+template <bool BF>
+struct Margin {
+  static constexpr float kBelow = BF ? 0.f : 11.f;
+  static constexpr float kAbove = BF ? 8.f : 15.f;
+};
+constexpr float kRestScale = 2048.f;
+
 // State of a segment (one unit's tiles in one worker's range). Lane 4g + c
 // holds queries 2c and 2c + 1 of every group of 8 (index e & 1).
 template <int D, int NT, bool ONE>
@@ -111,8 +127,9 @@ __device__ __forceinline__ void mask_edge(float (&x)[NT][4], const State<D, NT, 
 
 // Moves the references up (all lanes of the warp together) and rescales sums
 // and outputs. lvs: log2 of the tile's V scale (one-byte caches).
-template <int D, int NT, bool ONE>
+template <int D, int NT, bool ONE, bool BF>
 __device__ __forceinline__ void raise_references(const float (&x)[NT][4], State<D, NT, ONE>& st, float lvs) {
+  constexpr float BELOW = Margin<BF>::kBelow;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     float t[2] = {fmaxf(x[n][0], x[n][2]), fmaxf(x[n][1], x[n][3])};
@@ -124,12 +141,12 @@ __device__ __forceinline__ void raise_references(const float (&x)[NT][4], State<
     float a[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float m = fmaxf(st.m[n][e], t[e]);
+      const float m = fmaxf(st.m[n][e], t[e] - BELOW);
       a[e] = fast_exp2(st.m[n][e] - m);
       st.l[n][e] *= a[e];
       st.m[n][e] = m;
       if constexpr (ONE) {
-        const float mo = fmaxf(st.mo[n][e], t[e] + lvs);
+        const float mo = fmaxf(st.mo[n][e], t[e] + lvs - BELOW);
         a[e] = fast_exp2(st.mo[n][e] - mo);
         st.mo[n][e] = mo;
       }
@@ -144,11 +161,13 @@ __device__ __forceinline__ void raise_references(const float (&x)[NT][4], State<
   }
 }
 
-// The weights' B fragments: parts of the 16-bit type whose sum is the fp32
-// weight, transposed from the C fragment [rows][queries] to [rows = k][queries = n].
+// The weights' B fragments: parts of the 16-bit type, transposed from the C
+// fragment [rows][queries] to [rows = k][queries = n]. bf16: their sum is the
+// weight; f16: the first plus the second / kRestScale.
 template <bool BF, int NT, int NP>
 __device__ __forceinline__ void weight_parts(const float (&w)[NT][4], uint32_t (&b)[NT][NP][2]) {
   using namespace wmma16;
+  constexpr float SCALE = BF ? 1.f : kRestScale;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     float r0 = w[n][0], r1 = w[n][1], r2 = w[n][2], r3 = w[n][3];
@@ -159,12 +178,29 @@ __device__ __forceinline__ void weight_parts(const float (&w)[NT][4], uint32_t (
       b[n][k][1] = movm_t(h23);
       if (k + 1 < NP) {
         const float2 f01 = unpack2<BF>(h01), f23 = unpack2<BF>(h23);
-        r0 -= f01.x;
-        r1 -= f01.y;
-        r2 -= f23.x;
-        r3 -= f23.y;
+        r0 = (r0 - f01.x) * SCALE;
+        r1 = (r1 - f01.y) * SCALE;
+        r2 = (r2 - f23.x) * SCALE;
+        r3 = (r3 - f23.y) * SCALE;
       }
     }
+  }
+}
+
+// o += a . (the weights' parts) for one output tile.
+template <bool BF, int NP>
+__device__ __forceinline__ void add_products(float (&o)[4], const uint32_t (&a)[4], const uint32_t (&b)[NP][2]) {
+  using namespace wmma16;
+  if constexpr (BF) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) mma<true>(o, a, b[j][0], b[j][1]);
+  } else {
+    static_assert(NP == 2, "a weight and its scaled rest");
+    float rest[4] = {0.f, 0.f, 0.f, 0.f};
+    mma<false>(rest, a, b[1][0], b[1][1]);
+    mma<false>(o, a, b[0][0], b[0][1]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = fmaf(rest[e], 1.f / kRestScale, o[e]);
   }
 }
 
@@ -239,19 +275,19 @@ __device__ __forceinline__ bool clean_rows(uint32_t v, int r0, int r1, int lane)
 
 // Running softmax over one tile: x becomes the weights relative to the
 // references (of the outputs), sums take the weights relative to m.
-template <int D, int NT, bool ONE>
+template <int D, int NT, bool ONE, bool BF>
 __device__ __forceinline__ void softmax_step(float (&x)[NT][4], State<D, NT, ONE>& st, float lvs) {
+  constexpr float ABOVE = Margin<BF>::kAbove;
   bool need = false;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      need |= x[n][e] > st.m[n][e & 1] + 8.0f;
-      if constexpr (ONE) need |= x[n][e] + lvs > st.mo[n][e & 1] + 8.0f;
+      need |= x[n][e] > st.m[n][e & 1] + ABOVE;
+      if constexpr (ONE) need |= x[n][e] + lvs > st.mo[n][e & 1] + ABOVE;
     }
   }
-  // lazy: a reference only moves when a score exceeds it by a factor 2^8
-  if (__any_sync(0xffffffffu, need)) raise_references<D, NT, ONE>(x, st, lvs);
+  if (__any_sync(0xffffffffu, need)) raise_references<D, NT, ONE, BF>(x, st, lvs);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -312,7 +348,7 @@ __device__ __forceinline__ void tile16(uint32_t k, uint32_t v, int rem, bool edg
     if (rem < kTileRows) clear_rows<128, D / 64>(v, rem, lane);
   }
   if (lg != nullptr) store_scores<NT>(x, lg, qns, col0, qn, rem, lane);
-  softmax_step<D, NT, false>(x, st, 0.f);
+  softmax_step<D, NT, false, BF>(x, st, 0.f);
   uint32_t b[NT][NP][2];
   weight_parts<BF, NT, NP>(x, b);
   // lane l addresses row (l & 7) + 8 (l >> 4), dims chunk 2 i + ((l >> 3) & 1)
@@ -323,9 +359,7 @@ __device__ __forceinline__ void tile16(uint32_t k, uint32_t v, int rem, bool edg
     uint32_t a[4];
     ldsm_x4_t(row + (i >> 2) * BOX + static_cast<uint32_t>(((i & 3) ^ s2) << 5), a);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < NP; ++j) mma<BF>(st.o[n][i], a, b[n][j][0], b[n][j][1]);
+    for (int n = 0; n < NT; ++n) add_products<BF, NP>(st.o[n][i], a, b[n]);
   }
 }
 
@@ -396,7 +430,7 @@ __device__ __forceinline__ void tile8(uint32_t k, uint32_t v, int rem, bool edge
     if (rem < kTileRows) clear_rows<BOXB, SPANS>(v, rem, lane);
   }
   if (lg != nullptr) store_scores<NT>(x, lg, qns, col0, qn, rem, lane);
-  softmax_step<D, NT, true>(x, st, fast_log2(vs));
+  softmax_step<D, NT, true, false>(x, st, fast_log2(vs));
   uint32_t b[NT][NP][2];
   weight_parts<false, NT, NP>(x, b);
 #pragma unroll
@@ -425,9 +459,7 @@ __device__ __forceinline__ void tile8(uint32_t k, uint32_t v, int rem, bool edge
       codes_to_f16x2<Q8>(__byte_perm(vw[0][i >> 1], vw[1][i >> 1], sel), a[0], a[1]);
       codes_to_f16x2<Q8>(__byte_perm(vw[2][i >> 1], vw[3][i >> 1], sel), a[2], a[3]);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < NP; ++j) mma<false>(st.o[n][sp * KS + i], a, b[n][j][0], b[n][j][1]);
+      for (int n = 0; n < NT; ++n) add_products<false, NP>(st.o[n][sp * KS + i], a, b[n]);
     }
   }
 }
