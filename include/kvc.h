@@ -416,7 +416,9 @@ kvc_status kvc_decode_scored_workspace_size(int batch, int n_tokens, int n_q_hea
  *   out    as kvc_decode_attention_multi: q, out [batch, n_tokens, n_q_heads,
  *          head_dim], token t of sequence i attends rows 0 .. n_i - n_tokens + t
  *          (n_i = context_lens[i] counts the new rows; append them first);
- *          what the other rows hold (infinities, NaN) does not reach it
+ *          what the other rows hold (infinities, NaN) does not reach it; an
+ *          infinity or NaN in V of a row that it attends is its output there,
+ *          whatever the row's weight (infinities of both signs make NaN)
  *   scores fp32 [batch, n_kv_heads, max_blocks_per_seq * block_size], in table
  *          order: entry (i, h, r) belongs to logical row r of sequence i. With
  *          w = the sum of row r's softmax weights over the n_tokens *

@@ -242,7 +242,7 @@ __device__ __forceinline__ void clear_rows(uint32_t v, int rem, int lane) {
 
 // Rows [r0, r1) of a tile's V, which some of the new tokens see and others do
 // not: an infinity or NaN there would reach the latter too (0 x NaN), so it
-// becomes 0 (close_odd_rows gives it to the others). True if there was one.
+// becomes 0 (give_odd_values gives it to the others). True if there was one.
 // FIELD: the elements' exponents (e4m3: all but the sign), LOW: their lowest
 // bits; a full field carries into its element's sign.
 template <int BOXB, int HALVES, uint32_t FIELD, uint32_t LOW>
@@ -574,54 +574,77 @@ __device__ __forceinline__ int out_dim(int i, int g) {
   return ONE ? (i / KS) * BOXB + (BOXB / 8) * g + 2 * (i % KS) : 16 * i + g;
 }
 
-// Gives the infinities and NaN of the segment's rows that clean_rows cleared to
-// the queries that see them (their weights are positive: the value itself). Rare.
-template <typename CT, int D, int NT>
-__device__ __forceinline__ void close_odd_rows(const ScoredParams& p, const Unit& u, int n_rows, int tile0, int tile1,
-                                               State<D, NT, sizeof(CT) == 1>& st, int lane) {
-  constexpr bool ONE = sizeof(CT) == 1;
-  const int g = lane >> 2;
-  const int r1 = min(n_rows, tile1 * kTileRows);
+// An infinity or NaN in V becomes the output of the queries that see its row,
+// as sum_r p_r v_r has it (p_r > 0), but the products cannot give that: a
+// weight's parts may be 0 or negative, and 0 x infinity is NaN. So where a
+// segment met one, its rows [r0, r1) are searched once more and what is found
+// (the sum of all: infinities of both signs make NaN) replaces the outputs of
+// the queries `cols` (bits), written before: part [8 NT, D], or p.out if NULL.
+// Rare, and out of the main loop's registers.
+template <typename CT, int D>
+__device__ __noinline__ void give_odd_values(const ScoredParams& p, int seq, int kvh, int col0, uint32_t cols,
+                                             int n_rows, int r0, int r1, float* part) {
+  constexpr int PER = D / 32;  // dims per lane: lane, lane + 32, ..
+  const int lane = threadIdx.x & 31;
+  auto search = [&](int from, int to, float (&z)[PER]) {
 #pragma unroll 1
-  for (int r = max(n_rows - p.n_tok + 1, tile0 * kTileRows); r < r1; ++r) {
-    const int b = r / p.block_size;
-    const int phys = __ldg(p.block_tables + static_cast<int64_t>(u.seq) * p.max_blocks + b);
-    if (phys < 0 || phys >= p.num_blocks) continue;
-    const int64_t at = (static_cast<int64_t>(phys) * p.n_kv_heads + u.kvh) * p.block_size + (r - b * p.block_size);
-    const CT* row = static_cast<const CT*>(p.v_cache) + at * D;
+    for (int r = from; r < to; ++r) {
+      const int b = r / p.block_size;
+      const int phys = __ldg(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks + b);
+      if (phys < 0 || phys >= p.num_blocks) continue;
+      const int64_t at = (static_cast<int64_t>(phys) * p.n_kv_heads + kvh) * p.block_size + (r - b * p.block_size);
+      const CT* row = static_cast<const CT*>(p.v_cache) + at * D + lane;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const CT* x = row + out_dim<D, ONE>(i, g) + (ONE ? k : 8 * k);
+      for (int i = 0; i < PER; ++i) {
         float y = 0.f;
-        if constexpr (ONE) {
-          if ((__ldg(reinterpret_cast<const unsigned char*>(x)) & 0x7f) == 0x7f) y = __int_as_float(0x7fffffff);
+        if constexpr (sizeof(CT) == 1) {  // e4m3 has a NaN and no infinity
+          if ((__ldg(reinterpret_cast<const unsigned char*>(row + 32 * i)) & 0x7f) == 0x7f)
+            y = __int_as_float(0x7fffffff);
         } else {
           y = wmma16::unpack2<std::is_same<CT, __nv_bfloat16>::value>(
-                  __ldg(reinterpret_cast<const unsigned short*>(x))).x;
+                  __ldg(reinterpret_cast<const unsigned short*>(row + 32 * i))).x;
         }
-        if (fabsf(y) < __builtin_huge_valf()) continue;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (r < n_rows - st.dt[n][e]) st.o[n][i][2 * k + e] += y;
-        }
+        if (!(fabsf(y) < __builtin_huge_valf())) z[i] += y;
       }
     }
+  };
+  const int shared_rows = n_rows - p.n_tok + 1;  // rows that all tokens see
+  float all[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) all[i] = 0.f;
+  search(r0, min(r1, shared_rows), all);
+#pragma unroll 1
+  for (; cols != 0; cols &= cols - 1) {
+    const int col = __ffs(cols) - 1, v = col0 + col, t = v / p.group;
+    float z[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) z[i] = all[i];
+    search(max(r0, shared_rows), min(r1, shared_rows + t), z);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (z[i] == 0.f) continue;
+      if (part != nullptr)
+        part[col * D + lane + 32 * i] = z[i];
+      else
+        store_out(p.out, query_row(p, seq, kvh, v) * D + lane + 32 * i, z[i], p.out_dtype);
+    }
   }
+}
+
+// The weight of a record relative to the largest one. Not below the smallest
+// normal number, which changes no finite sum and keeps an infinity.
+__device__ __forceinline__ float record_weight(float m, float largest) {
+  return fmaxf(fast_exp2(m - largest), 1.17549435e-38f);
 }
 
 }  // namespace scored
 
 // SHUT: rows of the last tokens are searched for infinities and NaN, which
-// earlier tokens do not see (several new tokens; the code costs the others 1 us
-// of 35 where it is merely present).
+// earlier tokens do not see (several new tokens; other calls are spared the code).
 template <typename CT, int D, int NT, bool SHUT>
 __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
     scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                         const ScoredParams p) {
+                         const __grid_constant__ ScoredParams p) {
   using namespace scored;
   constexpr bool ONE = sizeof(CT) == 1;
   constexpr bool BF = std::is_same<CT, __nv_bfloat16>::value;
@@ -781,7 +804,7 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
   Unit u{};
   int end = lo, n_rows = 0, col0 = 0, j = 0;
   int shared_rows = 0;  // rows that all tokens see
-  bool odd = false;     // clean_rows found an infinity or NaN in this segment
+  bool odd = false;     // this segment met an infinity or NaN in V
   float* lg0 = nullptr;
 #pragma unroll 1
   for (int pos = lo; pos < hi;) {
@@ -920,10 +943,6 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
     j += cnt;
     if (pos < end) continue;
 
-    if constexpr (SHUT) {
-      if (odd) close_odd_rows<CT, D, NT>(p, u, n_rows, max(u.u0, lo) - u.u0, pos - u.u0, st, lane);
-      odd = false;
-    }
     // ---- close the segment. A whole unit: its outputs. A part that ends
     // inside the range (the unit began in an earlier worker's): record 2 wk.
     // The part at the range's end: merged with its neighbours' below.
@@ -992,6 +1011,40 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
         if (p.scores != nullptr && lanes_g == 0) p.lse[row] = st.m[n][e] + fast_log2(l);
       }
     }
+    if constexpr (!ONE || SHUT) {
+      if constexpr (!ONE) {
+        float zero = 0.f;  // NaN if an output is not finite
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) zero = fmaf(st.o[n][i][e], 0.f, zero);
+        odd |= __any_sync(full, zero != 0.f);
+      }
+      if (odd) {
+        // queries without weight here, or whose weights are not finite, keep what the products gave
+        uint32_t cols = 0;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float l = st.l[n][e];
+#pragma unroll
+            for (int msk = 4; msk < 32; msk <<= 1) l += __shfl_xor_sync(full, l, msk);
+            const uint32_t has = __ballot_sync(full, l > 0.f && l < __builtin_huge_valf() &&
+                                                         col0 + 8 * n + 2 * c + e < p.qn);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) cols |= ((has >> k) & 1u) << (8 * n + 2 * k + e);
+          }
+        }
+        __syncwarp();  // the segment's outputs have been written
+        give_odd_values<CT, D>(p, u.seq, u.kvh, col0, cols, n_rows, (begin - u.u0) * kTileRows,
+                               min(n_rows, (pos - u.u0) * kTileRows),
+                               whole ? nullptr : keep ? so : p.rec_o + rec * NC * D);
+        odd = false;
+      }
+    }
     if (keep) held = static_cast<int>(unit);
   }
   if (!ok) {
@@ -1028,7 +1081,7 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
         float l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int x = a; x < b; ++x) {
-          const float f = fast_exp2(part(x)[NC * D + 2 * col] - m);
+          const float f = record_weight(part(x)[NC * D + 2 * col], m);
           const float4 y = *reinterpret_cast<const float4*>(part(x) + col * D + d);
           l += f * part(x)[NC * D + 2 * col + 1];
           o.x += f * y.x;
@@ -1234,7 +1287,7 @@ __global__ void __launch_bounds__(kFinishThreads, SCORED ? 4 : 2)
         l = ml.y;
       }
       const float M = warp_max(m);
-      const float f = lane < r.n ? fast_exp2(m - M) : 0.f;
+      const float f = lane < r.n ? record_weight(m, M) : 0.f;
       const float L = warp_sum(f * l);
       for (int i0 = 0; i0 < r.n; i0 += U) {
         float x[U][V];
@@ -1271,7 +1324,7 @@ __global__ void __launch_bounds__(kFinishThreads, SCORED ? 4 : 2)
       for (int i = 1; i < kFinishWarps; ++i) m = fmaxf(m, s_red[0][i]);
       float l = 0.f;
       for (int i = tid; i < r.n; i += kFinishThreads) {
-        const float f = fast_exp2(s_dyn[i] - m);
+        const float f = record_weight(s_dyn[i], m);
         l += f * __ldcg(p.rec_ml + (record_slot(r, i) * NC + col) * 2 + 1);
         s_dyn[i] = f;
       }
