@@ -78,7 +78,7 @@ typedef enum kvc_code { KVC_E4M3 = 0, KVC_INT8 = 1 } kvc_code;
 /* Bits of the device error word. */
 #define KVC_FLAG_BAD_BLOCK 0x1u   /* block table entry outside [0, num_blocks) */
 #define KVC_FLAG_BAD_LEN 0x2u     /* context_len < 1 (multi-token: < n_tokens) or > max_blocks_per_seq*block_size */
-#define KVC_FLAG_BAD_SLOT 0x4u    /* slot >= num_blocks*block_size */
+#define KVC_FLAG_BAD_SLOT 0x4u    /* slot >= num_blocks*block_size; kvc_append_block8: a block's tokens not adjacent */
 #define KVC_FLAG_TIMEOUT 0x8u     /* a bounded wait on an async copy gave up */
 #define KVC_FLAG_WORKSPACE 0x10u  /* decode workspace counters were not zero at entry */
 
@@ -235,8 +235,11 @@ kvc_status kvc_append_int8(const void* k, const void* v, const int64_t* slot_map
  * slot_mapping: as kvc_append (negative: skipped; >= num_blocks*block_size:
  * skipped and KVC_FLAG_BAD_SLOT). The tokens of one block must be adjacent in
  * it, as kvc_seq_reserve and kvc_seq_reserve_batch give them, with no skipped
- * one between them; two runs of one block in one call race (the block's codes
- * and scale are then a mixture of the two), as two tokens of one slot do.
+ * one between them. Two runs of one block race: the block's codes and scale are
+ * then a mixture of both (other blocks are not affected), and KVC_FLAG_BAD_SLOT
+ * is set if they begin within 1536 tokens of each other, or the call has at most
+ * 3072 (a token-major mapping of several sequences, say).
+ * Two tokens of one slot race as in kvc_append.
  * num_tokens == 0 is a no-op. head_dim 64, 128 or 256; block_size a multiple
  * of 16 up to 128; k, v and the caches 16-byte aligned. A block's scales move
  * with it: a copied block (kvc_copy_blocks) needs its scales copied too.

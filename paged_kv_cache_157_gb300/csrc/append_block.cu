@@ -62,6 +62,10 @@ struct AppendBlockParams {
   int n_heads, block_size;
   int stretch;     // tokens a CTA looks at at a time
   unsigned items;  // stretches x heads x 2
+  int checkers;    // CTAs behind the others that look for blocks with more than one run
+  unsigned parts;  // of a window's blocks, by hash: a table each
+  unsigned tasks;  // windows x parts
+  uint64_t block_inv;  // ceil(2^64 / block_size)
   unsigned int* err;
 };
 
@@ -78,6 +82,93 @@ constexpr int kAppendThreads = 32 * kAppendWarps;
 constexpr int kWindows = 8;
 constexpr int kInFlight = 8;      // 16-byte chunks a lane holds
 constexpr int kAppendCtasPerSm = 4;
+
+// Two runs of one block would race for its codes and scale, so a slot mapping
+// that has them is flagged. A few CTAs look for them beside the others: the
+// blocks that begin runs go into a hash table in shared memory, and one that is
+// there already has two. A table takes a part of the blocks of a window of
+// tokens (three quarters of its size if every token were a run), a CTA one or
+// more of them. Windows overlap by half. Their length, and with it the times a
+// token is looked at, grows with the heads, as the others' time does, so that the
+// check ends before they do (16384 tokens, 8 heads: 29.1 us with and without it).
+constexpr int kTableBits = 10;
+constexpr int kTokensPerPart = 3 << (kTableBits - 2);
+constexpr int kMinParts = 4;  // of a window, if the call has that many tokens
+constexpr int kLookAt = 8;  // tokens per lane in flight; a warp's are in one piece
+
+// (four CTAs stay within 32 KB: what they spill lives in the rest of the L1)
+union AppendShared {
+  struct {
+    int64_t slot[1 + 32 * kWindows];  // of the token before the stretch, and of the windows' tokens
+    int64_t block[kAppendThreads];
+    int first[kAppendThreads], end[kAppendThreads];  // the runs: first token, and the one behind
+    uint32_t ends[kWindows];                         // bit masks: a token that is not written, or begins a run
+    int count[kAppendWarps];                         // per window
+    uint32_t red[2 * kAppendWarps];
+  } runs;
+  struct {
+    uint4 table[(1 << kTableBits) / 4];
+    uint16_t queue[kAppendWarps][32 * kLookAt];
+  } check;
+};
+
+__device__ __noinline__ void find_split_blocks(const AppendBlockParams& p, unsigned checker, AppendShared& sh) {
+  constexpr uint32_t full = 0xffffffffu, size = 1u << kTableBits;
+  uint4* s_table4 = sh.check.table;
+  uint32_t* s_table = reinterpret_cast<uint32_t*>(s_table4);
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  uint16_t* queue = sh.check.queue[w];
+  bool found = false;
+  for (unsigned task = checker; task < p.tasks; task += p.checkers) {
+    const unsigned window = task / p.parts, part = task - window * p.parts;
+    const int64_t begin = window * (static_cast<int64_t>(p.parts) * (kTokensPerPart / 2));
+    const int64_t end = min(p.num_tokens, begin + static_cast<int64_t>(p.parts) * kTokensPerPart);
+    __syncthreads();  // the last table is done with
+#pragma unroll
+    for (uint32_t i = 0; i < size / 4; i += kAppendThreads) s_table4[i + tid] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+#pragma unroll 1
+    for (int64_t t0 = begin + w * (32 * kLookAt); t0 < end; t0 += kAppendThreads * kLookAt) {
+      const int64_t left = end - t0 - lane;
+      const int64_t* at = p.slots + t0 + lane;
+      int64_t slot[kLookAt];
+      int64_t last = lane == 31 && t0 > begin ? __ldg(p.slots + t0 - 1) : -1;  // of the token before lane 0's
+#pragma unroll
+      for (int i = 0; i < kLookAt; ++i) slot[i] = 32 * i < left ? __ldg(at + 32 * i) : -1;
+      // a token one row behind the one before begins a run only at a block's start, a multiple of 16
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < kLookAt; ++i) {
+        const int64_t prev = __shfl_sync(full, lane == 31 ? last : slot[i], (lane + 31) & 31);
+        last = slot[i];
+        const bool may = slot[i] >= 0 && slot[i] < p.num_slots && (slot[i] != prev + 1 || (slot[i] & 15) == 0);
+        const uint32_t m = __ballot_sync(full, may);
+        if (may) queue[n + __popc(m & ((1u << lane) - 1u))] = static_cast<uint16_t>(32 * i + lane);
+        n += __popc(m);
+      }
+      __syncwarp();
+      for (int q = lane; q < n; q += 32) {
+        const int64_t t = t0 + queue[q], sl = __ldg(p.slots + t), prev = t > begin ? __ldg(p.slots + t - 1) : -1;
+        // block (exact for slots below 2^57) and its first slot; multiplicative
+        // hashing: the top bits choose the part, others the place
+        const uint64_t blk = __umul64hi(static_cast<uint64_t>(sl), p.block_inv);
+        const int64_t first = static_cast<int64_t>(blk) * p.block_size;
+        if (prev >= first && prev - first < p.block_size) continue;
+        const uint64_t hash = blk * 0x9E3779B97F4A7C15ull;
+        if (__umulhi(static_cast<uint32_t>(hash >> 32), p.parts) != part) continue;
+        const uint32_t entry = static_cast<uint32_t>(blk) + 1;  // (no memory holds 2^32 blocks)
+        uint32_t place = static_cast<uint32_t>(hash >> 20) % size;
+        for (uint32_t k = 0; k < size; ++k, place = (place + 1) % size) {
+          const uint32_t there = atomicCAS(&s_table[place], 0u, entry);
+          found |= there == entry;
+          if (there == 0 || there == entry) break;
+        }
+      }
+      __syncwarp();
+    }
+  }
+  if (found) set_flag(p.err, KVC_FLAG_BAD_SLOT);
+}
 
 // A run: `rows` tokens from the one x and slots point at.
 struct Run {
@@ -206,24 +297,30 @@ __device__ __noinline__ void append_run(const Run run, uint32_t token_chunks, in
 // range of them, so that it finds a stretch's runs once for several heads (a
 // CTA per item spent 15 of 36 us of a 16384-token prompt on finding them).
 template <typename T, bool INT8, int D>
-__global__ void __launch_bounds__(kAppendThreads, kAppendCtasPerSm) append_block_kernel(const AppendBlockParams p) {
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtasPerSm)
+    append_block_kernel(const __grid_constant__ AppendBlockParams p) {
   constexpr int CPR = D * static_cast<int>(sizeof(T)) / 16;
   constexpr uint32_t full = 0xffffffffu;
-  __shared__ uint32_t s_red[2 * kAppendWarps];
-  __shared__ int64_t s_slot[1 + 32 * kWindows];  // of the token before the stretch, and of the windows' tokens
-  __shared__ uint32_t s_ends[kWindows];          // bit masks: a token that is not written, or begins a run
-  __shared__ int s_first[kAppendThreads], s_end[kAppendThreads];  // the runs: first token, and the one behind
-  __shared__ int64_t s_block[kAppendThreads];
-  __shared__ int s_runs[kAppendWarps];           // per window
+  __shared__ AppendShared sh;
+  uint32_t* s_red = sh.runs.red;
+  int64_t* s_slot = sh.runs.slot;
+  uint32_t* s_ends = sh.runs.ends;
+  int *s_first = sh.runs.first, *s_end = sh.runs.end, *s_runs = sh.runs.count;
+  int64_t* s_block = sh.runs.block;
   // a decode launched behind this kernel may set itself up meanwhile; it waits
   // for this grid to end before it reads any cached row
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const unsigned cta = blockIdx.x, ctas = gridDim.x - p.checkers;
+  if (cta >= ctas) {
+    find_split_blocks(p, cta - ctas, sh);
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int bs = p.block_size;
   const int per_stretch = 2 * p.n_heads;
   const uint32_t token_chunks = static_cast<uint32_t>(p.n_heads) * CPR;
-  unsigned item = static_cast<unsigned>(static_cast<uint64_t>(p.items) * blockIdx.x / gridDim.x);
-  const unsigned item_end = static_cast<unsigned>(static_cast<uint64_t>(p.items) * (blockIdx.x + 1) / gridDim.x);
+  unsigned item = static_cast<unsigned>(static_cast<uint64_t>(p.items) * cta / ctas);
+  const unsigned item_end = static_cast<unsigned>(static_cast<uint64_t>(p.items) * (cta + 1) / ctas);
 #pragma unroll 1
   while (item < item_end) {
     const unsigned st = item / per_stretch;
@@ -386,16 +483,31 @@ extern "C" kvc_status kvc_append_block8(const void* k, const void* v, const int6
   p.n_heads = n_kv_heads;
   p.block_size = block_size;
   p.err = dev->error_word;
-  // Stretches of a block for prompts, so that a stretch has one run. With few
-  // tokens, shorter ones: the CTAs are to fill the GPU, with a run for each of
-  // a CTA's warps if every token is one (a decode step).
   const int64_t resident = static_cast<int64_t>(kAppendCtasPerSm) * dev->num_sms;
-  const int64_t pairs = 2 * num_tokens * n_kv_heads;  // (token, head, K or V)
-  p.stretch = static_cast<int>(std::min<int64_t>(block_size, std::max<int64_t>(kAppendWarps, pairs / resident)));
-  const int64_t items = (num_tokens + p.stretch - 1) / p.stretch * n_kv_heads * 2;
+  const int64_t parts = std::min<int64_t>((num_tokens + kTokensPerPart - 1) / kTokensPerPart,
+                                          std::max(kMinParts, std::min(n_kv_heads, 64)));
+  const int64_t step = parts * (kTokensPerPart / 2), beyond = std::max<int64_t>(0, num_tokens - 2 * step);
+  const int64_t tasks = (1 + (beyond + step - 1) / step) * parts;
+  if (tasks >= (1ll << 31)) return fail(KVC_ERR_UNSUPPORTED, "num_tokens too large");
+  p.parts = static_cast<unsigned>(parts);
+  p.tasks = static_cast<unsigned>(tasks);
+  p.block_inv = ~0ull / static_cast<unsigned>(block_size) + 1;
+  // Stretches of a block for prompts, so that a stretch has one run. With few
+  // tokens, shorter ones: the CTAs are to fill the GPU, none with a second item
+  // (a chunk of 2232 tokens: 9 us, 12 where ten CTAs have one), with a run for
+  // each of a CTA's warps if every token is one (a decode step).
+  // (the check's share of a long call is 4 % of the work with one head, 2 % with eight)
+  const int64_t ctas = resident - std::min(tasks, std::max<int64_t>(1, resident / (16 + 2 * std::min(n_kv_heads, 8))));
+  const int64_t heads2 = 2ll * n_kv_heads, fit = std::max<int64_t>(1, ctas / heads2);  // stretches at a time
+  p.stretch = static_cast<int>(
+      std::min<int64_t>(block_size, std::max<int64_t>(kAppendWarps, (num_tokens + fit - 1) / fit)));
+  const int64_t items = (num_tokens + p.stretch - 1) / p.stretch * heads2;
   if (items >= (1ll << 31)) return fail(KVC_ERR_UNSUPPORTED, "num_tokens x n_kv_heads too large");
   p.items = static_cast<unsigned>(items);
-  const int64_t grid = std::min(items, resident);
+  // the check gets what the items leave free: as many CTAs as take no more items each
+  const int64_t each = (items + ctas - 1) / ctas, busy = (items + each - 1) / each;
+  p.checkers = static_cast<int>(std::min(tasks, resident - busy));
+  const int64_t grid = busy + p.checkers;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (dtype) {
     case KVC_F32: launch<float>(p, head_dim, code, grid, s); break;
