@@ -242,7 +242,7 @@ kvc_status kvc_append_int8(const void* k, const void* v, const int64_t* slot_map
  * Two tokens of one slot race as in kvc_append.
  * num_tokens == 0 is a no-op. head_dim 64, 128 or 256; block_size a multiple
  * of 16 up to 128; k, v and the caches 16-byte aligned. A block's scales move
- * with it: a copied block (kvc_copy_blocks) needs its scales copied too.
+ * with it: a copied block needs its scales copied too (kvc_copy_blocks on both).
  * Source: "KV-Cache——为什么AI回复越来越快" section 08 (KV-Cache quantisation);
  * the scale per block and head is this library's. */
 kvc_status kvc_append_block8(const void* k, const void* v, const int64_t* slot_mapping, int64_t num_tokens,
@@ -254,8 +254,10 @@ kvc_status kvc_append_block8(const void* k, const void* v, const int64_t* slot_m
  * pairs[2i + 1] becomes a byte copy of block pairs[2i]. cache: device pool of
  * num_blocks blocks of block_bytes bytes each (for a K or V pool,
  * n_kv_heads * block_size * head_dim * element size; for a latent pool,
- * block_size * (d_c + d_r) * element size), 16-byte aligned; block_bytes a
- * multiple of 16. pairs: int64 [n_pairs, 2] in device memory. Destination
+ * block_size * (d_c + d_r) * element size; for the scales of kvc_append_block8,
+ * n_kv_heads * 4, for those of kvc_append_fp8 and kvc_append_int8, n_kv_heads *
+ * block_size * 4), 16-byte aligned; block_bytes a multiple of 16, or of 4 with the
+ * cache 4-byte aligned. pairs: int64 [n_pairs, 2] in device memory. Destination
  * blocks must be distinct and must not be sources in the same call (copies
  * run concurrently). Pairs naming a block outside the pool are skipped and set
  * KVC_FLAG_BAD_BLOCK. Asynchronous on `stream`.

@@ -517,8 +517,8 @@ def decode_attention_window(q, k_cache, v_cache, block_tables, context_lens, sca
 
 
 def copy_blocks(cache, pairs, stream=None):
-    """kvc_copy_blocks: block pairs[i, 1] of ``cache`` (a pool tensor [num_blocks, ...]) becomes a copy of
-    block pairs[i, 0]. pairs: int64 device tensor [n, 2]."""
+    """kvc_copy_blocks: block pairs[i, 1] of ``cache`` (a pool tensor [num_blocks, ...], or the scales of a one-byte
+    one) becomes a copy of block pairs[i, 0]. pairs: int64 device tensor [n, 2]."""
     torch = _torch()
     _require(cache, "cache")
     _require(pairs, "pairs", torch.int64)

@@ -120,9 +120,11 @@ __global__ void __launch_bounds__(256) append_q8_kernel(const T* __restrict__ k,
 }
 
 // Copy-on-write: block pairs[2i] -> block pairs[2i + 1] inside one pool,
-// block_chunks 16-byte chunks per block. Pairs with a block id outside the
-// pool are skipped and flagged; src == dst is a no-op.
-__global__ void __launch_bounds__(256) copy_blocks_kernel(uint4* cache, const int64_t* __restrict__ pairs,
+// block_chunks chunks (16 bytes; 4 for the scales of one-byte caches, whose
+// blocks are that small) per block. Pairs with a block id outside the pool are
+// skipped and flagged; src == dst is a no-op.
+template <typename Chunk>
+__global__ void __launch_bounds__(256) copy_blocks_kernel(Chunk* cache, const int64_t* __restrict__ pairs,
                                                           int64_t n_pairs, int64_t num_blocks, int64_t block_chunks,
                                                           unsigned int* err) {
   const int64_t total = n_pairs * block_chunks;
@@ -240,20 +242,26 @@ kvc_status kvc_copy_blocks(void* cache, int64_t num_blocks, int64_t block_bytes,
                            kvc_stream stream) {
   using namespace kvc;
   clear_error();
-  if (num_blocks < 1 || block_bytes < 16 || block_bytes % 16 != 0 || n_pairs < 0)
-    return fail(KVC_ERR_INVALID_ARG, "num_blocks >= 1, block_bytes a positive multiple of 16, n_pairs >= 0");
+  if (num_blocks < 1 || block_bytes < 4 || block_bytes % 4 != 0 || n_pairs < 0)
+    return fail(KVC_ERR_INVALID_ARG, "num_blocks >= 1, block_bytes a positive multiple of 4, n_pairs >= 0");
   if (n_pairs == 0) return KVC_OK;
   if (cache == nullptr || pairs == nullptr) return fail(KVC_ERR_INVALID_ARG, "NULL pointer");
-  if (!aligned16(cache)) return fail(KVC_ERR_INVALID_ARG, "cache must be 16-byte aligned");
+  const int chunk = block_bytes % 16 == 0 ? 16 : 4;
+  if (reinterpret_cast<uintptr_t>(cache) % chunk != 0)
+    return fail(KVC_ERR_INVALID_ARG, "cache must be %d-byte aligned", chunk);
   DeviceInfo* dev = nullptr;
   kvc_status st = current_device(&dev);
   if (st != KVC_OK) return st;
-  const int64_t chunks = block_bytes / 16;
+  const int64_t chunks = block_bytes / chunk;
   const int64_t want = (n_pairs * chunks + 255) / 256;
   const int grid = static_cast<int>(want < dev->num_sms * 16LL ? want : dev->num_sms * 16LL);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  copy_blocks_kernel<<<grid, 256, 0, s>>>(static_cast<uint4*>(cache), pairs, n_pairs, num_blocks, chunks,
-                                          dev->error_word);
+  if (chunk == 16)
+    copy_blocks_kernel<<<grid, 256, 0, s>>>(static_cast<uint4*>(cache), pairs, n_pairs, num_blocks, chunks,
+                                            dev->error_word);
+  else
+    copy_blocks_kernel<<<grid, 256, 0, s>>>(static_cast<uint32_t*>(cache), pairs, n_pairs, num_blocks, chunks,
+                                            dev->error_word);
   return finish_call(s);
 }
 
