@@ -67,7 +67,8 @@ typedef enum kvc_status {
   KVC_ERR_NO_BLOCKS = 3,    /* block pool exhausted; nothing was allocated */
   KVC_ERR_CUDA = 4,         /* a CUDA runtime call failed */
   KVC_ERR_OUT_OF_RANGE = 5, /* checked mode: a kernel saw a bad device value */
-  KVC_ERR_WORKSPACE = 6     /* workspace smaller than the size query asked for */
+  KVC_ERR_WORKSPACE = 6,    /* workspace smaller than the size query asked for */
+  KVC_ERR_NO_MEMORY = 7     /* pool calls: host memory could not be had; nothing was changed */
 } kvc_status;
 
 typedef enum kvc_dtype { KVC_F32 = 0, KVC_F16 = 1, KVC_BF16 = 2 } kvc_dtype;

@@ -36,7 +36,7 @@ _LIB_PATH = os.path.join(_HERE, "libkvc.so")
 
 F32, F16, BF16 = 0, 1, 2
 E4M3, INT8 = 0, 1  # code formats of the block-scaled one-byte caches
-OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_NO_BLOCKS, ERR_CUDA, ERR_OUT_OF_RANGE, ERR_WORKSPACE = range(7)
+OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_NO_BLOCKS, ERR_CUDA, ERR_OUT_OF_RANGE, ERR_WORKSPACE, ERR_NO_MEMORY = range(8)
 FLAG_BAD_BLOCK, FLAG_BAD_LEN, FLAG_BAD_SLOT, FLAG_TIMEOUT, FLAG_WORKSPACE = 0x1, 0x2, 0x4, 0x8, 0x10
 OPT_CHECKED, OPT_BLOCKS_PER_CTA, OPT_MAX_CTAS, OPT_GQA_ENGINE, OPT_DYNAMIC_SHARE, OPT_DYNAMIC_CHUNK, OPT_WAIT_POLLS = \
     0, 1, 2, 3, 4, 5, 6

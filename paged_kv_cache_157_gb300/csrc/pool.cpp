@@ -11,9 +11,15 @@
 // a partly filled block that another sequence also holds needs copy-on-write:
 // kvc_seq_reserve refuses it, kvc_seq_reserve_cow first gives the writer a
 // fresh block and reports the (shared, fresh) pair for kvc_copy_blocks.
+//
+// Memory: a call gets all it needs before it changes anything, and what an
+// allocation throws becomes KVC_ERR_NO_MEMORY. The heap of free blocks is
+// allocated for all of them once, so taking and giving back blocks needs none.
+#include <algorithm>
 #include <cstdint>
+#include <exception>
 #include <functional>
-#include <new>
+#include <memory>
 #include <queue>
 #include <unordered_map>
 #include <utility>
@@ -44,6 +50,23 @@ kvc_status find_seq(kvc_pool* pool, int64_t id, kvc_pool::Seq** out) {
   return KVC_OK;
 }
 
+// The body of a call: exceptions end here.
+template <typename F>
+kvc_status guarded(const F& body) {
+  try {
+    return body();
+  } catch (const std::exception& e) {
+    return kvc::fail(KVC_ERR_NO_MEMORY, "host memory: %s", e.what());
+  }
+}
+
+// Room for `more` blocks (at least twice as many as before when it has to
+// grow, as push_back would make).
+void make_room(std::vector<int64_t>& blocks, int64_t more) {
+  const size_t n = blocks.size() + static_cast<size_t>(std::max<int64_t>(0, more));
+  if (n > blocks.capacity()) blocks.reserve(std::max(n, 2 * blocks.capacity()));
+}
+
 }  // namespace
 
 extern "C" {
@@ -54,16 +77,17 @@ kvc_status kvc_pool_create(int64_t num_blocks, int block_size, kvc_pool** pool) 
   *pool = nullptr;
   if (num_blocks < 1 || block_size < 1) return kvc::fail(KVC_ERR_INVALID_ARG, "num_blocks and block_size must be >= 1");
   if (num_blocks > (1ll << 31) - 1) return kvc::fail(KVC_ERR_UNSUPPORTED, "num_blocks must fit in int32");
-  kvc_pool* p = new (std::nothrow) kvc_pool();
-  if (p == nullptr) return kvc::fail(KVC_ERR_INVALID_ARG, "host allocation failed");
-  p->num_blocks = num_blocks;
-  p->block_size = block_size;
-  p->ref.assign(static_cast<size_t>(num_blocks), 0);
-  std::vector<int64_t> ids(static_cast<size_t>(num_blocks));
-  for (int64_t i = 0; i < num_blocks; ++i) ids[static_cast<size_t>(i)] = i;
-  p->free_heap = decltype(p->free_heap)(std::greater<int64_t>(), std::move(ids));
-  *pool = p;
-  return KVC_OK;
+  return guarded([&] {
+    std::unique_ptr<kvc_pool> p(new kvc_pool());
+    p->num_blocks = num_blocks;
+    p->block_size = block_size;
+    p->ref.assign(static_cast<size_t>(num_blocks), 0);
+    std::vector<int64_t> ids(static_cast<size_t>(num_blocks));
+    for (int64_t i = 0; i < num_blocks; ++i) ids[static_cast<size_t>(i)] = i;
+    p->free_heap = decltype(p->free_heap)(std::greater<int64_t>(), std::move(ids));
+    *pool = p.release();
+    return KVC_OK;
+  });
 }
 
 void kvc_pool_destroy(kvc_pool* pool) { delete pool; }
@@ -71,10 +95,11 @@ void kvc_pool_destroy(kvc_pool* pool) { delete pool; }
 kvc_status kvc_seq_add(kvc_pool* pool, int64_t* seq) {
   kvc::clear_error();
   if (pool == nullptr || seq == nullptr) return kvc::fail(KVC_ERR_INVALID_ARG, "NULL argument");
-  const int64_t id = pool->next_id++;
-  pool->seqs[id] = kvc_pool::Seq{};
-  *seq = id;
-  return KVC_OK;
+  return guarded([&] {
+    pool->seqs.emplace(pool->next_id, kvc_pool::Seq{});
+    *seq = pool->next_id++;
+    return KVC_OK;
+  });
 }
 
 kvc_status kvc_seq_fork(kvc_pool* pool, int64_t parent, int64_t* child) {
@@ -83,12 +108,12 @@ kvc_status kvc_seq_fork(kvc_pool* pool, int64_t parent, int64_t* child) {
   kvc_status s = find_seq(pool, parent, &ps);
   if (s != KVC_OK) return s;
   if (child == nullptr) return kvc::fail(KVC_ERR_INVALID_ARG, "child is NULL");
-  kvc_pool::Seq copy = *ps;
-  for (int64_t b : copy.blocks) pool->ref[static_cast<size_t>(b)] += 1;
-  const int64_t id = pool->next_id++;
-  pool->seqs[id] = std::move(copy);
-  *child = id;
-  return KVC_OK;
+  return guarded([&] {
+    const kvc_pool::Seq& made = pool->seqs.emplace(pool->next_id, *ps).first->second;
+    for (int64_t b : made.blocks) pool->ref[static_cast<size_t>(b)] += 1;
+    *child = pool->next_id++;
+    return KVC_OK;
+  });
 }
 
 kvc_status kvc_seq_reserve(kvc_pool* pool, int64_t seq, int64_t n_new, int64_t* slots_out) {
@@ -107,18 +132,21 @@ kvc_status kvc_seq_reserve(kvc_pool* pool, int64_t seq, int64_t n_new, int64_t* 
   if (need > static_cast<int64_t>(pool->free_heap.size()))
     return kvc::fail(KVC_ERR_NO_BLOCKS, "need %lld blocks, %zu free", static_cast<long long>(need),
                      pool->free_heap.size());
-  for (int64_t i = 0; i < n_new; ++i) {
-    const int64_t pos = n + i;
-    if (pos % bs == 0) {
-      const int64_t b = pool->free_heap.top();
-      pool->free_heap.pop();
-      pool->ref[static_cast<size_t>(b)] = 1;
-      sq->blocks.push_back(b);
+  return guarded([&] {
+    make_room(sq->blocks, need);
+    for (int64_t i = 0; i < n_new; ++i) {
+      const int64_t pos = n + i;
+      if (pos % bs == 0) {
+        const int64_t b = pool->free_heap.top();
+        pool->free_heap.pop();
+        pool->ref[static_cast<size_t>(b)] = 1;
+        sq->blocks.push_back(b);
+      }
+      slots_out[i] = sq->blocks[static_cast<size_t>(pos / bs)] * bs + pos % bs;
     }
-    slots_out[i] = sq->blocks[static_cast<size_t>(pos / bs)] * bs + pos % bs;
-  }
-  sq->length = n + n_new;
-  return KVC_OK;
+    sq->length = n + n_new;
+    return KVC_OK;
+  });
 }
 
 kvc_status kvc_seq_reserve_batch(kvc_pool* pool, const int64_t* seqs, int n, int64_t n_new, int64_t* slots_out) {
@@ -127,42 +155,46 @@ kvc_status kvc_seq_reserve_batch(kvc_pool* pool, const int64_t* seqs, int n, int
   if (n < 0 || n_new < 0) return kvc::fail(KVC_ERR_INVALID_ARG, "n and n_new must be >= 0");
   if (n == 0 || n_new == 0) return KVC_OK;
   if (seqs == nullptr || slots_out == nullptr) return kvc::fail(KVC_ERR_INVALID_ARG, "NULL argument");
-  // check everything first, so that a refused batch changes nothing
-  const int64_t bs = pool->block_size;
-  std::vector<kvc_pool::Seq*> ss(static_cast<size_t>(n));
-  std::unordered_map<int64_t, int> seen;
-  int64_t need = 0;
-  for (int i = 0; i < n; ++i) {
-    kvc_status s = find_seq(pool, seqs[i], &ss[static_cast<size_t>(i)]);
-    if (s != KVC_OK) return s;
-    if (!seen.emplace(seqs[i], i).second)
-      return kvc::fail(KVC_ERR_INVALID_ARG, "sequence %lld appears twice", static_cast<long long>(seqs[i]));
-    const kvc_pool::Seq* sq = ss[static_cast<size_t>(i)];
-    if (sq->length % bs != 0 && pool->ref[static_cast<size_t>(sq->blocks.back())] > 1)
-      return kvc::fail(KVC_ERR_UNSUPPORTED, "sequence %lld: append into a shared, partly filled block needs "
-                       "copy-on-write", static_cast<long long>(seqs[i]));
-    need += (sq->length + n_new + bs - 1) / bs - static_cast<int64_t>(sq->blocks.size());
-  }
-  if (need > static_cast<int64_t>(pool->free_heap.size()))
-    return kvc::fail(KVC_ERR_NO_BLOCKS, "need %lld blocks, %zu free", static_cast<long long>(need),
-                     pool->free_heap.size());
-  for (int i = 0; i < n; ++i) {
-    kvc_pool::Seq* sq = ss[static_cast<size_t>(i)];
-    int64_t* out = slots_out + static_cast<int64_t>(i) * n_new;
-    const int64_t len = sq->length;
-    for (int64_t t = 0; t < n_new; ++t) {
-      const int64_t pos = len + t;
-      if (pos % bs == 0) {
-        const int64_t b = pool->free_heap.top();
-        pool->free_heap.pop();
-        pool->ref[static_cast<size_t>(b)] = 1;
-        sq->blocks.push_back(b);
-      }
-      out[t] = sq->blocks[static_cast<size_t>(pos / bs)] * bs + pos % bs;
+  return guarded([&] {
+    // check everything first, so that a refused batch changes nothing
+    const int64_t bs = pool->block_size;
+    std::vector<kvc_pool::Seq*> ss(static_cast<size_t>(n));
+    std::unordered_map<int64_t, int> seen;
+    int64_t need = 0;
+    for (int i = 0; i < n; ++i) {
+      kvc_status s = find_seq(pool, seqs[i], &ss[static_cast<size_t>(i)]);
+      if (s != KVC_OK) return s;
+      if (!seen.emplace(seqs[i], i).second)
+        return kvc::fail(KVC_ERR_INVALID_ARG, "sequence %lld appears twice", static_cast<long long>(seqs[i]));
+      const kvc_pool::Seq* sq = ss[static_cast<size_t>(i)];
+      if (sq->length % bs != 0 && pool->ref[static_cast<size_t>(sq->blocks.back())] > 1)
+        return kvc::fail(KVC_ERR_UNSUPPORTED, "sequence %lld: append into a shared, partly filled block needs "
+                         "copy-on-write", static_cast<long long>(seqs[i]));
+      need += (sq->length + n_new + bs - 1) / bs - static_cast<int64_t>(sq->blocks.size());
     }
-    sq->length = len + n_new;
-  }
-  return KVC_OK;
+    if (need > static_cast<int64_t>(pool->free_heap.size()))
+      return kvc::fail(KVC_ERR_NO_BLOCKS, "need %lld blocks, %zu free", static_cast<long long>(need),
+                       pool->free_heap.size());
+    for (kvc_pool::Seq* sq : ss)
+      make_room(sq->blocks, (sq->length + n_new + bs - 1) / bs - static_cast<int64_t>(sq->blocks.size()));
+    for (int i = 0; i < n; ++i) {
+      kvc_pool::Seq* sq = ss[static_cast<size_t>(i)];
+      int64_t* out = slots_out + static_cast<int64_t>(i) * n_new;
+      const int64_t len = sq->length;
+      for (int64_t t = 0; t < n_new; ++t) {
+        const int64_t pos = len + t;
+        if (pos % bs == 0) {
+          const int64_t b = pool->free_heap.top();
+          pool->free_heap.pop();
+          pool->ref[static_cast<size_t>(b)] = 1;
+          sq->blocks.push_back(b);
+        }
+        out[t] = sq->blocks[static_cast<size_t>(pos / bs)] * bs + pos % bs;
+      }
+      sq->length = len + n_new;
+    }
+    return KVC_OK;
+  });
 }
 
 kvc_status kvc_seq_reserve_cow(kvc_pool* pool, int64_t seq, int64_t n_new, int64_t* slots_out, int64_t* copy_pair) {
@@ -182,6 +214,11 @@ kvc_status kvc_seq_reserve_cow(kvc_pool* pool, int64_t seq, int64_t n_new, int64
     if (need > static_cast<int64_t>(pool->free_heap.size()))
       return kvc::fail(KVC_ERR_NO_BLOCKS, "need %lld blocks, %zu free", static_cast<long long>(need),
                        pool->free_heap.size());
+    const kvc_status room = guarded([&] {
+      make_room(sq->blocks, need - 1);
+      return KVC_OK;
+    });
+    if (room != KVC_OK) return room;
     const int64_t old = sq->blocks.back();
     const int64_t fresh = pool->free_heap.top();
     pool->free_heap.pop();
@@ -200,49 +237,52 @@ kvc_status kvc_seq_evict_batch(kvc_pool* pool, const int64_t* seqs, int n, const
   if (n < 0) return kvc::fail(KVC_ERR_INVALID_ARG, "n must be >= 0");
   if (n == 0) return KVC_OK;
   if (seqs == nullptr || new_lengths == nullptr) return kvc::fail(KVC_ERR_INVALID_ARG, "NULL argument");
-  // check everything first, so that a refused batch changes nothing
-  const int64_t bs = pool->block_size;
-  std::vector<kvc_pool::Seq*> ss(static_cast<size_t>(n));
-  std::unordered_map<int64_t, int> seen;
-  int64_t need = 0;
-  for (int i = 0; i < n; ++i) {
-    kvc_status s = find_seq(pool, seqs[i], &ss[static_cast<size_t>(i)]);
-    if (s != KVC_OK) return s;
-    if (!seen.emplace(seqs[i], i).second)
-      return kvc::fail(KVC_ERR_INVALID_ARG, "sequence %lld appears twice", static_cast<long long>(seqs[i]));
-    const int64_t len = ss[static_cast<size_t>(i)]->length;
-    if (new_lengths[i] < 0 || new_lengths[i] > len)
-      return kvc::fail(KVC_ERR_INVALID_ARG, "sequence %lld: new length %lld outside 0 .. %lld",
-                       static_cast<long long>(seqs[i]), static_cast<long long>(new_lengths[i]),
-                       static_cast<long long>(len));
-    need += (new_lengths[i] + bs - 1) / bs;
-  }
-  if (need > static_cast<int64_t>(pool->free_heap.size()))
-    return kvc::fail(KVC_ERR_NO_BLOCKS, "need %lld blocks, %zu free", static_cast<long long>(need),
-                     pool->free_heap.size());
-  // the rows are copied out of the present blocks of all of them: every fresh
-  // block is taken before any of those is given back
-  std::vector<std::vector<int64_t>> old(static_cast<size_t>(n));
-  for (int i = 0; i < n; ++i) {
-    kvc_pool::Seq* sq = ss[static_cast<size_t>(i)];
-    std::vector<int64_t> fresh(static_cast<size_t>((new_lengths[i] + bs - 1) / bs));
-    for (int64_t& b : fresh) {
-      b = pool->free_heap.top();
-      pool->free_heap.pop();
-      pool->ref[static_cast<size_t>(b)] = 1;
+  return guarded([&] {
+    // check everything first, so that a refused batch changes nothing
+    const int64_t bs = pool->block_size;
+    std::vector<kvc_pool::Seq*> ss(static_cast<size_t>(n));
+    std::unordered_map<int64_t, int> seen;
+    int64_t need = 0;
+    for (int i = 0; i < n; ++i) {
+      kvc_status s = find_seq(pool, seqs[i], &ss[static_cast<size_t>(i)]);
+      if (s != KVC_OK) return s;
+      if (!seen.emplace(seqs[i], i).second)
+        return kvc::fail(KVC_ERR_INVALID_ARG, "sequence %lld appears twice", static_cast<long long>(seqs[i]));
+      const int64_t len = ss[static_cast<size_t>(i)]->length;
+      if (new_lengths[i] < 0 || new_lengths[i] > len)
+        return kvc::fail(KVC_ERR_INVALID_ARG, "sequence %lld: new length %lld outside 0 .. %lld",
+                         static_cast<long long>(seqs[i]), static_cast<long long>(new_lengths[i]),
+                         static_cast<long long>(len));
+      need += (new_lengths[i] + bs - 1) / bs;
     }
-    old[static_cast<size_t>(i)] = std::move(sq->blocks);
-    sq->blocks = std::move(fresh);
-    sq->length = new_lengths[i];
-  }
-  for (const std::vector<int64_t>& blocks : old) {
-    for (int64_t b : blocks) {
-      int32_t& r = pool->ref[static_cast<size_t>(b)];
-      r -= 1;
-      if (r == 0) pool->free_heap.push(b);
+    if (need > static_cast<int64_t>(pool->free_heap.size()))
+      return kvc::fail(KVC_ERR_NO_BLOCKS, "need %lld blocks, %zu free", static_cast<long long>(need),
+                       pool->free_heap.size());
+    std::vector<std::vector<int64_t>> fresh(static_cast<size_t>(n));
+    for (int i = 0; i < n; ++i) fresh[static_cast<size_t>(i)].resize(static_cast<size_t>((new_lengths[i] + bs - 1) / bs));
+    // the rows are copied out of the present blocks of all of them: every fresh
+    // block is taken before any of those is given back
+    for (std::vector<int64_t>& blocks : fresh) {
+      for (int64_t& b : blocks) {
+        b = pool->free_heap.top();
+        pool->free_heap.pop();
+        pool->ref[static_cast<size_t>(b)] = 1;
+      }
     }
-  }
-  return KVC_OK;
+    for (int i = 0; i < n; ++i) {
+      kvc_pool::Seq* sq = ss[static_cast<size_t>(i)];
+      sq->blocks.swap(fresh[static_cast<size_t>(i)]);  // now the old ones
+      sq->length = new_lengths[i];
+    }
+    for (const std::vector<int64_t>& blocks : fresh) {
+      for (int64_t b : blocks) {
+        int32_t& r = pool->ref[static_cast<size_t>(b)];
+        r -= 1;
+        if (r == 0) pool->free_heap.push(b);
+      }
+    }
+    return KVC_OK;
+  });
 }
 
 kvc_status kvc_seq_free(kvc_pool* pool, int64_t seq) {

@@ -12,19 +12,18 @@ static __device__ unsigned int g_kvc_error_word;
 
 namespace kvc {
 
-static thread_local std::string t_message;
+// (of fixed size: a failure for want of memory has a message too)
+static thread_local char t_message[512] = "";
 
 kvc_status fail(kvc_status s, const char* fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
+  vsnprintf(t_message, sizeof(t_message), fmt, ap);
   va_end(ap);
-  t_message = buf;
   return s;
 }
 
-void clear_error() { t_message.clear(); }
+void clear_error() { t_message[0] = '\0'; }
 
 kvc_status cuda_fail(cudaError_t e, const char* what) {
   return fail(KVC_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
@@ -111,11 +110,12 @@ const char* kvc_status_string(kvc_status s) {
     case KVC_ERR_CUDA: return "KVC_ERR_CUDA";
     case KVC_ERR_OUT_OF_RANGE: return "KVC_ERR_OUT_OF_RANGE";
     case KVC_ERR_WORKSPACE: return "KVC_ERR_WORKSPACE";
+    case KVC_ERR_NO_MEMORY: return "KVC_ERR_NO_MEMORY";
   }
   return "KVC_ERR_UNKNOWN";
 }
 
-const char* kvc_last_error_message(void) { return kvc::t_message.c_str(); }
+const char* kvc_last_error_message(void) { return kvc::t_message; }
 
 kvc_status kvc_set_option(kvc_option opt, int64_t value) {
   int o = static_cast<int>(opt);
