@@ -1445,6 +1445,8 @@ namespace scored {
 template <typename CT, int D, int NT, bool SHUT>
 kvc_status run_decode(const ScoredParams& p, int grid, const CUtensorMap& tk, const CUtensorMap& tv,
                       cudaLaunchAttribute* attr, cudaStream_t stream) {
+  static_assert(scored_warps(sizeof(CT), D, NT) == ScoredGeo<sizeof(CT), D, NT>::kWarps,
+                "the host counts a CTA's workers as the kernel does");
   auto* k = scored_decode_kernel<CT, D, NT, SHUT>;
   // The opt-in to large shared memory holds per device: made at the first call on each.
   static std::atomic<uint64_t> opted{0};

@@ -91,8 +91,10 @@ __host__ __device__ constexpr size_t scored_smem_bytes(int batch) {
 
 // Groups of 8 queries that a warp carries at once.
 inline int scored_nt(int D, int qn) { return D <= 128 && qn > 8 ? 2 : 1; }
-// Warps per CTA of the kernel for this element size, head size and nt.
-inline int scored_warps(int elt, int D, int nt) {
+// Warps per CTA of the kernel for this element size, head size and nt: what the
+// host sizes records and counts workers by (checked against ScoredGeo where the
+// kernel is launched).
+constexpr int scored_warps(int elt, int D, int nt) {
   return elt == 2 && D == 256 ? 4 : (elt == 1 && D <= 128 && nt == 1) ? 12 : 8;
 }
 
