@@ -445,6 +445,11 @@ kvc_status kvc_decode_scored_workspace_size(int batch, int n_tokens, int n_q_hea
  * kvc_decode_scored_workspace_size() bytes, 256-byte aligned; it need not be
  * cleared and holds nothing between calls; calls that may run concurrently
  * must not share one. Two kernels on `stream`; may be captured.
+ * The workspace holds a score per query and row (512 bytes per row and kv head
+ * for 128 queries, as much as a bf16 cache of D 128). Where that is too much, make
+ * the call in pieces with one workspace: some of the sequences at a time, or some
+ * of the tokens, tokens t0 .. t1 - 1 of T with context_lens[i] = n_i - T + t1.
+ * Outputs and scores are those of the one call, up to rounding.
  * Sources: "KV缓存原理与显存估算" knowledge point 2 (the decode) and closing
  * section (state that leaves the cache); the accumulated weights are this
  * library's. */
