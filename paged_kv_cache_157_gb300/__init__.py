@@ -681,9 +681,9 @@ def _check_block_scales(k_scale, v_scale, nb, hkv):
 
 
 def append_block8(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, stream=None):
-    """kvc_append_block8: k, v [T, Hkv, D] (f32/f16/bf16); slot_mapping int64 [T], the tokens of one block adjacent;
-    k_cache, v_cache codes [num_blocks, Hkv, bs, D], uint8 (e4m3) or int8; k_scale, v_scale fp32 [num_blocks, Hkv].
-    The blocks' scales grow with what is appended; a block's row 0 starts it afresh."""
+    """kvc_append_block8: k, v [T, Hkv, D] (f32/f16/bf16); slot_mapping int64 [T], the tokens of one block adjacent
+    (else FLAG_BAD_SLOT); k_cache, v_cache codes [num_blocks, Hkv, bs, D], uint8 (e4m3) or int8; k_scale, v_scale fp32
+    [num_blocks, Hkv]. The blocks' scales grow with what is appended; a block's row 0 starts it afresh."""
     torch = _torch()
     f32 = torch.float32
     _checked(k_cache, "k_cache", ((v_cache, "v_cache", getattr(k_cache, "dtype", None)), (k, "k", None),

@@ -17,8 +17,8 @@
 // are read again, out of L2). Bound, for prompts, by the load, barrier and store
 // phases of four CTAs per SM rather than by HBM; for a decode step, whose tokens
 // get a warp each, by the chain slots -> rows and scale -> codes of dependent
-// accesses. Measured (8 heads, D 128, bf16): a prompt of 16384 tokens 29.5 us
-// (3.4 TB/s of its 101 MB, 41 % issue), a step of 64 tokens 6.4 us.
+// accesses. Measured (8 heads, D 128, bf16): a prompt of 16384 tokens 29.4 us
+// (3.4 TB/s of its 101 MB, 36 % issue), a step of 64 tokens 6.3 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -90,7 +90,7 @@ constexpr int kAppendCtasPerSm = 4;
 // tokens (three quarters of its size if every token were a run), a CTA one or
 // more of them. Windows overlap by half. Their length, and with it the times a
 // token is looked at, grows with the heads, as the others' time does, so that the
-// check ends before they do (16384 tokens, 8 heads: 29.1 us with and without it).
+// check ends before they do (16384 tokens, 8 heads: 29.1 us without it, 29.4 with).
 constexpr int kTableBits = 10;
 constexpr int kTokensPerPart = 3 << (kTableBits - 2);
 constexpr int kMinParts = 4;  // of a window, if the call has that many tokens

@@ -9,17 +9,22 @@
 // with k_r = code * k_scale[block], v_r = code * v_scale[block] for one-byte
 // caches. One pass over the rows with the running maximum and sum of the
 // softmax; the weights of a row are only known once the denominator is, so the
-// pass leaves the scaled scores x (fp32, 4 bytes per query and row against 2 D
-// cache elements) in the workspace, and the finishing kernel, which merges the
-// partial outputs anyway, turns them into weights and adds them up. Reading K
-// a second time instead would cost D elements per row.
+// pass leaves the scaled scores x (fp32) in the workspace, and the finishing
+// kernel, which merges the partial outputs anyway, turns them into weights and
+// adds them up. That moves 8 bytes per query and row, mostly through L2; forming
+// the scores again from K would read D elements per row instead: more for up to
+// 31 queries (16-bit, D 128) or 15 (one byte), less beyond, but with the first
+// product done twice. exp2 and log2 are the hardware's (2^-22).
 //
-// What bounds it: HBM, for up to about 16 queries per kv head. Every cached
-// row is read once, by TMA, into a ring in shared memory. Measured (32 query, 8
-// kv heads, D 128), decode and finish: bf16, batch 32 x 4096 rows 97.7 us (90 us
-// of them the decode, 6.05 TB/s); e4m3 blocks, batch 32 x U[512, 4096] 34.7 us, at
-// 7.0 TB/s for what a larger batch adds. More queries (32 tokens, 128 queries per
-// kv head over 2 x 4000 rows: 38 us) are bound by the products' latency.
+// What bounds it, for up to about 16 queries per kv head: HBM in large 16-bit
+// batches; every cached row is read once, by TMA, into a ring in shared memory.
+// Measured (32 query, 8 kv heads, D 128), decode and finish: bf16, batch 32 x
+// 4096 rows 98.8 us (about 90 us of them the decode, 6 TB/s); e4m3 blocks, batch 32 x
+// U[512, 4096] 35.9 us, of which about 13 us are start, the SMs' different ends
+// and the finish, at 7.0 TB/s for what a larger batch adds (DRAM 53 % busy over
+// the whole decode); int8 likewise 40.8 us. More queries are bound by the
+// products: 32 tokens, 128 queries per kv head over 2 x 4000 rows 38 us (bf16),
+// 40 us (f16), 86 us (e4m3), 60 us (int8); 256 tokens over 4000 rows 209 us (f16).
 //
 // Work split. The 16-row tiles of all (sequence, kv head, column group) units
 // are laid end to end and cut into equal ranges, one per WARP. A warp is a
@@ -35,9 +40,9 @@
 //   O^T [D x 8 queries] += V^T [D x 16 rows] . P^T
 // fp32 accumulation. The weights enter as 16-bit parts: two f16 parts (22 bits,
 // see Margin) or, for bf16 caches, three bf16 parts (24 bits), because fp32 outputs
-// are to be as good as an fp32 softmax; the extra products are hidden behind HBM. One-byte codes
-// are exact f16 values and are converted in registers; queries become f16
-// after a scaling by a power of two that is exact, per query.
+// are to be as good as an fp32 softmax; in large batches the extra products are
+// mostly hidden behind HBM. One-byte codes are exact f16 values and are converted
+// in registers; queries become f16 after a scaling by a power of two, per query.
 #pragma once
 
 #include <algorithm>
@@ -838,8 +843,9 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
           }
         } else {
           // dims of lane c, k-step s of a span: 4 s .. 4 s + 3 of its part; scaled
-          // by 2^t so that the query's largest entry lies in [2^14, 2^15): exact
-          // in f16 but for entries below 2^-39 of the largest
+          // by 2^t so that the query's largest entry lies in [2^14, 2^15): entries
+          // down to 2^-31 (bf16; f16: 2^-28) of it are exact in f16, smaller ones are
+          // off by at most 2^-39 of it
           constexpr int BOXB = D < 128 ? D : 128;
           constexpr int KS = BOXB / 16;
           float y[D / 16][4];
@@ -1107,7 +1113,7 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
 // fixed order. Every step loads what it needs at once: bound by the scores' and
 // logits' bytes (which mostly sit in L2), for small calls by the chain unit ->
 // maxima -> outputs, or logits, of three loads: 5 us for a few short sequences,
-// 13 us for 32 x 4096 rows of 4 queries (25 MB), most of it under the end of the decode.
+// about 8 us behind the decode for 32 x 4096 rows of 4 queries (25 MB; 13 us alone).
 constexpr int kFinishThreads = 256;
 constexpr int kFinishWarps = kFinishThreads / 32;
 // cached rows a CTA takes at least: about 4 KB of scores, 16 KB of wide rows
