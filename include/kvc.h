@@ -238,8 +238,8 @@ kvc_status kvc_append_int8(const void* k, const void* v, const int64_t* slot_map
  * it, as kvc_seq_reserve and kvc_seq_reserve_batch give them, with no skipped
  * one between them. Two runs of one block race: the block's codes and scale are
  * then a mixture of both (other blocks are not affected), and KVC_FLAG_BAD_SLOT
- * is set if they begin within 1536 tokens of each other, or the call has at most
- * 3072 (a token-major mapping of several sequences, say).
+ * is set if they begin within 1280 tokens of each other, or the call has at most
+ * 2560 (a token-major mapping of several sequences, say).
  * Two tokens of one slot race as in kvc_append.
  * num_tokens == 0 is a no-op. head_dim 64, 128 or 256; block_size a multiple
  * of 16 up to 128; k, v and the caches 16-byte aligned. A block's scales move

@@ -62,7 +62,7 @@ struct AppendBlockParams {
   int n_heads, block_size;
   int stretch;     // tokens a CTA looks at at a time
   unsigned items;  // stretches x heads x 2
-  int checkers;    // CTAs behind the others that look for blocks with more than one run
+  int scouts;      // CTAs behind the others that look for blocks with more than one run
   unsigned parts;  // of a window's blocks, by hash: a table each
   unsigned tasks;  // windows x parts
   uint64_t block_inv;  // ceil(2^64 / block_size)
@@ -87,12 +87,12 @@ constexpr int kAppendCtasPerSm = 4;
 // that has them is flagged. A few CTAs look for them beside the others: the
 // blocks that begin runs go into a hash table in shared memory, and one that is
 // there already has two. A table takes a part of the blocks of a window of
-// tokens (three quarters of its size if every token were a run), a CTA one or
+// tokens (five eighths of its size if every token were a run), a CTA one or
 // more of them. Windows overlap by half. Their length, and with it the times a
 // token is looked at, grows with the heads, as the others' time does, so that the
 // check ends before they do (16384 tokens, 8 heads: 29.1 us without it, 29.4 with).
 constexpr int kTableBits = 10;
-constexpr int kTokensPerPart = 3 << (kTableBits - 2);
+constexpr int kTokensPerPart = 5 << (kTableBits - 3);
 constexpr int kMinParts = 4;  // of a window, if the call has that many tokens
 constexpr int kLookAt = 8;  // tokens per lane in flight; a warp's are in one piece
 
@@ -112,14 +112,14 @@ union AppendShared {
   } check;
 };
 
-__device__ __noinline__ void find_split_blocks(const AppendBlockParams& p, unsigned checker, AppendShared& sh) {
+__device__ __noinline__ void find_split_blocks(const AppendBlockParams& p, unsigned scout, AppendShared& sh) {
   constexpr uint32_t full = 0xffffffffu, size = 1u << kTableBits;
   uint4* s_table4 = sh.check.table;
   uint32_t* s_table = reinterpret_cast<uint32_t*>(s_table4);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   uint16_t* queue = sh.check.queue[w];
   bool found = false;
-  for (unsigned task = checker; task < p.tasks; task += p.checkers) {
+  for (unsigned task = scout; task < p.tasks; task += p.scouts) {
     const unsigned window = task / p.parts, part = task - window * p.parts;
     const int64_t begin = window * (static_cast<int64_t>(p.parts) * (kTokensPerPart / 2));
     const int64_t end = min(p.num_tokens, begin + static_cast<int64_t>(p.parts) * kTokensPerPart);
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtasPerSm)
   // a decode launched behind this kernel may set itself up meanwhile; it waits
   // for this grid to end before it reads any cached row
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const unsigned cta = blockIdx.x, ctas = gridDim.x - p.checkers;
+  const unsigned cta = blockIdx.x, ctas = gridDim.x - p.scouts;
   if (cta >= ctas) {
     find_split_blocks(p, cta - ctas, sh);
     return;
@@ -506,8 +506,8 @@ extern "C" kvc_status kvc_append_block8(const void* k, const void* v, const int6
   p.items = static_cast<unsigned>(items);
   // the check gets what the items leave free: as many CTAs as take no more items each
   const int64_t each = (items + ctas - 1) / ctas, busy = (items + each - 1) / each;
-  p.checkers = static_cast<int>(std::min(tasks, resident - busy));
-  const int64_t grid = busy + p.checkers;
+  p.scouts = static_cast<int>(std::min(tasks, resident - busy));
+  const int64_t grid = busy + p.scouts;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (dtype) {
     case KVC_F32: launch<float>(p, head_dim, code, grid, s); break;

@@ -63,8 +63,8 @@ def test_a_block_left_and_met_again(kvc, slots):
     p.same()
 
 
-@pytest.mark.parametrize("T,gap,H", [(769, 768, 1), (3072, 3071, 1), (2000, 2, 3), (3073, 1536, 1), (20000, 1536, 1),
-                                     (20000, 1, 2), (20000, 700, 5), (70000, 1500, 1), (2304, 2303, 40)])
+@pytest.mark.parametrize("T,gap,H", [(641, 640, 1), (2560, 2559, 1), (2000, 2, 3), (2561, 1280, 1), (20000, 1280, 1),
+                                     (20000, 1, 2), (20000, 700, 5), (70000, 1200, 1), (1920, 1919, 40)])
 def test_among_many_blocks(kvc, T, gap, H):
     # every token in a block of its own but for two, `gap` tokens apart, at the beginning, the end and in between
     D, bs = 64, 16
