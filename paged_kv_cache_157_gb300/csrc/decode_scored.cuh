@@ -1045,9 +1045,10 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
           }
         }
         __syncwarp();  // the segment's outputs have been written
-        give_odd_values<CT, D>(p, u.seq, u.kvh, col0, cols, n_rows, (begin - u.u0) * kTileRows,
-                               min(n_rows, (pos - u.u0) * kTileRows),
-                               whole ? nullptr : keep ? so : p.rec_o + rec * NC * D);
+        if (cols != 0)
+          give_odd_values<CT, D>(p, u.seq, u.kvh, col0, cols, n_rows, (begin - u.u0) * kTileRows,
+                                 min(n_rows, (pos - u.u0) * kTileRows),
+                                 whole ? nullptr : keep ? so : p.rec_o + rec * NC * D);
         odd = false;
       }
     }
