@@ -20,14 +20,19 @@ def setup(kind, case):
     return q, K, V, vs, tables, old, ref, ref_scores
 
 
+def faults(case):
+    """Those that show on a case: one new token has no mask; in peaked cases the weights of single rows vanish."""
+    yield from ("none", "query", "parts")
+    if case[6] < X.PEAKED:
+        yield from ("tile", "last", "scores")
+        if case[1] > 1:
+            yield "mask"
+
+
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("case", X.CASES, ids=lambda c: f"D{c[4]}-T{c[1]}-{len(c[0])}x{max(c[0])}-{c[6]:g}")
-@pytest.mark.parametrize("fault", ["none", "query", "tile", "parts", "mask", "last", "scores"])
+@pytest.mark.parametrize("case,fault", [
+    pytest.param(c, f, id=f"{f}-D{c[4]}-T{c[1]}-{len(c[0])}x{max(c[0])}-{c[6]:g}") for c in X.CASES for f in faults(c)])
 def test_a_planted_fault_exceeds_the_bounds(kind, case, fault):
-    if fault == "mask" and case[1] == 1:
-        pytest.skip("one new token has no mask")
-    if fault in ("tile", "mask", "last", "scores") and case[6] >= X.PEAKED:
-        pytest.skip("the rows' weights vanish")
     q, K, V, vs, tables, old, ref, ref_scores = setup(kind, case)
     tol, tol_scores = X.bounds(kind, q, K, V, vs, tables, case[0], case[6], torch.float32, ref, old)
     out, new = X.wrong(kind, q, K, V, tables, case[0], case[6], old, fault)
