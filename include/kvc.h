@@ -251,6 +251,40 @@ kvc_status kvc_append_block8(const void* k, const void* v, const int64_t* slot_m
                              int64_t num_blocks, int block_size, int n_kv_heads, int head_dim, kvc_dtype dtype,
                              kvc_stream stream);
 
+/* Append into a four-bit cache: a row is cut into groups of 16 elements, each
+ * with e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) and one
+ * e4m3 scale, and stands for code * scale: 4.5 bits per element, no calibration.
+ *   k_cache, v_cache  [num_blocks, n_kv_heads, block_size, head_dim / 2]: byte i
+ *                     of a row holds element 2i in its low half, 2i + 1 in its
+ *                     high half
+ *   k_scale, v_scale  e4m3 [num_blocks, n_kv_heads, block_size, head_dim / 16]
+ * With A the largest |x| of a group: scale = e4m3(A / 6), code = e2m1(x / scale),
+ * each rounded once, to nearest, ties to even, saturating at 448 and 6 (scale 0:
+ * zeros). Entries that are not finite do not count for A: infinities saturate, NaN
+ * becomes 0. A row's codes depend on that row alone, and no later append
+ * changes them. Scales below 2^-6 (A below 0.094) have fewer bits, those of
+ * A up to 6 * 2^-10 are 0: scale small keys (and the queries the other way) or
+ * values by a power of two. k, v: [num_tokens, n_kv_heads, head_dim] in `dtype`
+ * (F32, F16, BF16). slot_mapping: as kvc_append. num_tokens == 0 is a no-op.
+ * head_dim 64, 128 or 256; block_size a multiple of 16 up to 128; all pointers
+ * but slot_mapping 16-byte aligned. A copied block needs its scales copied too
+ * (kvc_copy_blocks on both pools). Source: "KV-Cache——为什么AI回复越来越快"
+ * section 08 (KV-Cache quantisation); the format is this library's. */
+kvc_status kvc_append_fp4(const void* k, const void* v, const int64_t* slot_mapping, int64_t num_tokens,
+                          void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale, int64_t num_blocks,
+                          int block_size, int n_kv_heads, int head_dim, kvc_dtype dtype, kvc_stream stream);
+
+/* Reads rows of such a cache back: k[t, h, :] and v[t, h, :] ([num_tokens,
+ * n_kv_heads, head_dim] in `dtype`) become the values of the row at
+ * slot_mapping[t], which every dtype holds exactly. Rows of k and v whose slot is
+ * negative, or outside the pool (KVC_FLAG_BAD_SLOT), are left as they are. What
+ * a chunk of a prompt attends to when its history is kept in four bits: with
+ * kvc_append it fills a 16-bit pool for kvc_prompt_attention. Otherwise as
+ * kvc_append_fp4. */
+kvc_status kvc_read_fp4(const int64_t* slot_mapping, int64_t num_tokens, const void* k_cache, const void* v_cache,
+                        const uint8_t* k_scale, const uint8_t* v_scale, int64_t num_blocks, int block_size,
+                        int n_kv_heads, int head_dim, void* k, void* v, kvc_dtype dtype, kvc_stream stream);
+
 /* Copy-on-write block copy inside one pool: for i < n_pairs, block
  * pairs[2i + 1] becomes a byte copy of block pairs[2i]. cache: device pool of
  * num_blocks blocks of block_bytes bytes each (for a K or V pool,
@@ -409,8 +443,9 @@ kvc_status kvc_decode_attention_int8(const void* q, const void* k_cache, const v
                                      kvc_dtype out_dtype, void* workspace, size_t workspace_bytes,
                                      kvc_stream stream);
 
-/* Scratch bytes for kvc_decode_attention_scored and kvc_decode_attention_block8
- * (either cache element size) on the current device; scored != 0: for calls
+/* Scratch bytes for kvc_decode_attention_scored, kvc_decode_attention_block8 and
+ * (scored = 0) kvc_decode_attention_sinks and kvc_decode_attention_fp4, for any of
+ * their caches, on the current device; scored != 0: for calls
  * with a scores buffer, which adds 4 bytes per query and row that the tables
  * can hold (batch x n_tokens x n_q_heads x max_blocks_per_seq x block_size).
  * Same shape errors as the calls. */
@@ -472,6 +507,78 @@ kvc_status kvc_decode_attention_block8(const void* q, const void* k_cache, const
                                        float scale, int n_q_heads, int n_kv_heads, int head_dim, int block_size,
                                        int64_t num_blocks, kvc_dtype q_dtype, void* out, kvc_dtype out_dtype,
                                        float* scores, void* workspace, size_t workspace_bytes, kvc_stream stream);
+
+/* --------------------------------------------- long streams: window and sinks */
+
+/* Decode attention that keeps the first rows of a stream in sight of its window:
+ *   out  as kvc_decode_attention_multi, q and out [batch, n_tokens, n_q_heads,
+ *        head_dim]; token t of sequence i, at position pos = n_i - n_tokens + t
+ *        (n_i = context_lens[i] counts the new rows; append them first), attends
+ *        row r if r <= pos and (r > pos - window or r < sinks)
+ * What the other rows hold (infinities, NaN) does not reach it; an infinity or
+ * NaN in V of a row that it attends is its output there, whatever the row's
+ * weight. window >= 1 (INT32_MAX: every row), sinks >= 0. Table entries of blocks
+ * that no token of the call sees are not used, so a caller may free the blocks
+ * between the sinks and the window. Types, shapes, flags and errors as
+ * kvc_decode_attention_scored; workspace: kvc_decode_scored_workspace_size with
+ * scored = 0 (it need not be cleared). May be captured.
+ * Source: "KV-Cache——为什么AI回复越来越快" section 08 (Window Attention); that the
+ * first rows stay is this library's. */
+kvc_status kvc_decode_attention_sinks(const void* q, const void* k_cache, const void* v_cache,
+                                      const int32_t* block_tables, int max_blocks_per_seq,
+                                      const int32_t* context_lens, int batch, int n_tokens, float scale,
+                                      int n_q_heads, int n_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                                      int window, int sinks, kvc_dtype dtype, void* out, kvc_dtype out_dtype,
+                                      void* workspace, size_t workspace_bytes, kvc_stream stream);
+
+/* The same decode over the caches written by kvc_append_fp4 (their scales, whose
+ * NaN code it never writes, 16-byte aligned). q F16 or BF16 in q_dtype. Otherwise
+ * as kvc_decode_attention_sinks; window INT32_MAX and sinks 0 is the plain decode. */
+kvc_status kvc_decode_attention_fp4(const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                                    const uint8_t* v_scale, const int32_t* block_tables, int max_blocks_per_seq,
+                                    const int32_t* context_lens, int batch, int n_tokens, float scale, int n_q_heads,
+                                    int n_kv_heads, int head_dim, int block_size, int64_t num_blocks, int window,
+                                    int sinks, kvc_dtype q_dtype, void* out, kvc_dtype out_dtype, void* workspace,
+                                    size_t workspace_bytes, kvc_stream stream);
+
+/* Scratch bytes for kvc_prompt_attention on the current device. Same shape
+ * errors as that call. */
+kvc_status kvc_prompt_workspace_size(int batch, int64_t num_tokens, int n_q_heads, int n_kv_heads, int head_dim,
+                                     int block_size, int max_blocks_per_seq, size_t* bytes);
+
+/* Attention of whole prompts, or of chunks of them, over the paged cache: a
+ * ragged batch of any number of new tokens per sequence.
+ *   q, out        [num_tokens, n_q_heads, head_dim] in `dtype` (F16 or BF16, the
+ *                 caches' type): the sequences' new tokens one behind the other
+ *   query_starts  int32 [batch + 1], ascending: sequence i's tokens are rows
+ *                 query_starts[i] .. query_starts[i + 1] - 1 of q (there may be
+ *                 none); rows of out that belong to no sequence are left as
+ *                 they are
+ *   context_lens  int32 [batch]: rows of sequence i, the m_i new ones included
+ *                 (append them first); not looked at where m_i is 0
+ * Token t of sequence i, at position pos = context_lens[i] - m_i + t, attends row
+ * r if r <= pos and (r > pos - window or r < sinks); window >= 1 (INT32_MAX: every
+ * row), sinks >= 0. Other rows' infinities and NaN do not reach it. Scores, sums
+ * and outputs accumulate in fp32; the softmax weights are rounded to `dtype` for
+ * the second product. Table entries of blocks that no token sees are not used.
+ * head_dim 64 or 128; block_size a multiple of 16 up to 128; batch <= 4096; at
+ * most 128 query heads per kv head; q, out and the caches 16-byte aligned.
+ * A sequence whose length is below m_i or above max_blocks_per_seq * block_size
+ * sets KVC_FLAG_BAD_LEN and gets zeros; one whose starts are out of order or range
+ * sets it and is left out. Rows in blocks outside the pool set
+ * KVC_FLAG_BAD_BLOCK and get no weight. num_tokens == 0 is a no-op.
+ * workspace: at least kvc_prompt_workspace_size() bytes, 256-byte aligned; it need
+ * not be cleared and holds nothing between calls; calls that may run concurrently
+ * must not share one. May be captured.
+ * Sources: the chunk mask of "单请求 KV Cache" (query row i of a chunk sees columns
+ * up to past_len + i) through the block table of "KV Cache（键值缓存）" section 2.3;
+ * Window Attention of "KV-Cache——为什么AI回复越来越快" section 08. */
+kvc_status kvc_prompt_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                                int max_blocks_per_seq, const int32_t* query_starts, const int32_t* context_lens,
+                                int batch, int64_t num_tokens, float scale, int n_q_heads, int n_kv_heads,
+                                int head_dim, int block_size, int64_t num_blocks, int window, int sinks,
+                                kvc_dtype dtype, void* out, void* workspace, size_t workspace_bytes,
+                                kvc_stream stream);
 
 /* --------------------------------------------------------------- eviction */
 

@@ -23,6 +23,8 @@ __all__ = [
     "append_int8", "decode_attention_int8",
     "append_block8", "decode_attention_block8", "decode_attention_scored", "scored_workspace_size",
     "new_scored_workspace", "evict_rows",
+    "append_fp4", "read_fp4", "decode_attention_fp4", "decode_attention_sinks",
+    "prompt_attention", "prompt_workspace_size", "new_prompt_workspace",
     "decode_mla_workspace_size", "decode_attention_mla", "set_option", "get_option",
     "get_error_flags", "BlockPool", "slots_from_tables",
     "F32", "F16", "BF16", "E4M3", "INT8", "FLAG_BAD_BLOCK", "FLAG_BAD_LEN", "FLAG_BAD_SLOT", "FLAG_TIMEOUT",
@@ -102,6 +104,15 @@ SIGNATURES = {
                               _i32, _vp, _vp, _vp, _vp]),
     "kvc_evict_rows_block8": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _i32, _i64,
                                      _i32, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "kvc_append_fp4": (_i32, [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp]),
+    "kvc_read_fp4": (_i32, [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _i32, _vp]),
+    "kvc_decode_attention_sinks": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _f32, _i32, _i32, _i32, _i32,
+                                          _i64, _i32, _i32, _i32, _vp, _i32, _vp, _sz, _vp]),
+    "kvc_decode_attention_fp4": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _f32, _i32, _i32, _i32,
+                                        _i32, _i64, _i32, _i32, _i32, _vp, _i32, _vp, _sz, _vp]),
+    "kvc_prompt_workspace_size": (_i32, [_i32, _i64, _i32, _i32, _i32, _i32, _i32, _szp]),
+    "kvc_prompt_attention": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i64, _f32, _i32, _i32, _i32, _i32,
+                                    _i64, _i32, _i32, _i32, _vp, _vp, _sz, _vp]),
     "kvc_seq_evict_batch": (_i32, [_vp, _vp, _i32, _vp]),
     "kvc_seq_free": (_i32, [_vp, _i64]),
     "kvc_seq_length": (_i32, [_vp, _i64, _i64p]),
@@ -817,3 +828,143 @@ def evict_rows(scores, k_cache, v_cache, block_tables, context_lens, budget, rec
                                        B, budget, recent, new_block_tables.data_ptr(), new_mb, nb, bs, hkv, d,
                                        kept.data_ptr(), new_lens.data_ptr(), new_scores.data_ptr(),
                                        _stream_of(stream, k_cache)), "kvc_evict_rows_block8")
+
+
+# ------------------------------- long streams: windows with sinks, four bits
+
+_ALL_ROWS = 2 ** 31 - 1  # a window that no sequence outgrows
+
+
+def _window(window, sinks):
+    window, sinks = _ALL_ROWS if window is None else int(window), int(sinks)
+    if not 1 <= window <= _ALL_ROWS or not 0 <= sinks <= _ALL_ROWS:
+        raise ValueError("window must be at least 1 and sinks at least 0, both below 2^31")
+    return window, sinks
+
+
+def _check_fp4(k_cache, v_cache, k_scale, v_scale):
+    """Shape (num_blocks, Hkv, bs, D) of a four-bit pool and its scales."""
+    nb, hkv, bs, half = _pool_shape(k_cache, v_cache)
+    if k_scale.shape != (nb, hkv, bs, half // 8) or v_scale.shape != k_scale.shape or half % 8 != 0:
+        raise ValueError("k_scale and v_scale must be [num_blocks, n_kv_heads, block_size, head_dim / 16]")
+    return nb, hkv, bs, 2 * half
+
+
+def append_fp4(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, stream=None):
+    """kvc_append_fp4: k, v [T, Hkv, D] (f32/f16/bf16); slot_mapping int64 [T]; k_cache, v_cache uint8
+    [num_blocks, Hkv, bs, D / 2] (two e2m1 codes per byte); k_scale, v_scale uint8 [num_blocks, Hkv, bs, D / 16] (e4m3,
+    one per 16 elements)."""
+    torch = _torch()
+    u8 = torch.uint8
+    _checked(k_cache, "k_cache", ((k_cache, "k_cache", u8), (v_cache, "v_cache", u8), (k, "k", None),
+                                  (v, "v", getattr(k, "dtype", None)), (slot_mapping, "slot_mapping", torch.int64),
+                                  (k_scale, "k_scale", u8), (v_scale, "v_scale", u8)))
+    nb, hkv, bs, d = _check_fp4(k_cache, v_cache, k_scale, v_scale)
+    T = slot_mapping.numel()
+    if k.shape != (T, hkv, d) or v.shape != k.shape:
+        raise ValueError("k and v must be [num_tokens, n_kv_heads, head_dim]")
+    _check(raw().kvc_append_fp4(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T, k_cache.data_ptr(),
+                                v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb, bs, hkv, d,
+                                _code_of(k), _stream_of(stream, k_cache)), "kvc_append_fp4")
+
+
+def read_fp4(slot_mapping, k_cache, v_cache, k_scale, v_scale, k, v, stream=None):
+    """kvc_read_fp4: writes the values of the rows at slot_mapping (int64 [T]) of a four-bit cache to k, v [T, Hkv, D]
+    (f32/f16/bf16, exact in each); rows of negative slots are left as they are."""
+    torch = _torch()
+    u8 = torch.uint8
+    _checked(k_cache, "k_cache", ((k_cache, "k_cache", u8), (v_cache, "v_cache", u8), (k, "k", None),
+                                  (v, "v", getattr(k, "dtype", None)), (slot_mapping, "slot_mapping", torch.int64),
+                                  (k_scale, "k_scale", u8), (v_scale, "v_scale", u8)))
+    nb, hkv, bs, d = _check_fp4(k_cache, v_cache, k_scale, v_scale)
+    T = slot_mapping.numel()
+    if k.shape != (T, hkv, d) or v.shape != k.shape:
+        raise ValueError("k and v must be [num_tokens, n_kv_heads, head_dim]")
+    _check(raw().kvc_read_fp4(slot_mapping.data_ptr(), T, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                              v_scale.data_ptr(), nb, bs, hkv, d, k.data_ptr(), v.data_ptr(), _code_of(k),
+                              _stream_of(stream, k_cache)), "kvc_read_fp4")
+
+
+def decode_attention_sinks(q, k_cache, v_cache, block_tables, context_lens, scale, window, sinks, out, workspace,
+                           stream=None):
+    """kvc_decode_attention_sinks: decode over a 16-bit cache in which every new token sees the newest ``window`` rows
+    (None: all) and the sequence's first ``sinks`` rows. q/out [B, Hq, D], or [B, T, Hq, D] for the T newest rows of
+    every sequence; workspace from new_scored_workspace(..., scored=False)."""
+    torch = _torch()
+    i32, dtype = torch.int32, getattr(k_cache, "dtype", None)
+    window, sinks = _window(window, sinks)
+    _checked(k_cache, "k_cache", ((v_cache, "v_cache", dtype), (q, "q", dtype), (block_tables, "block_tables", i32),
+                                  (context_lens, "context_lens", i32), (out, "out", None),
+                                  (workspace, "workspace", None)))
+    B, T, hq, d, nb, hkv, bs, mb = _decode_shape(q, out, k_cache, v_cache, block_tables, context_lens, None)
+    _check(raw().kvc_decode_attention_sinks(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                            block_tables.data_ptr(), mb, context_lens.data_ptr(), B, T, float(scale),
+                                            hq, hkv, d, bs, nb, window, sinks, _code_of(k_cache), out.data_ptr(),
+                                            _code_of(out), workspace.data_ptr(), workspace.nbytes,
+                                            _stream_of(stream, k_cache)), "kvc_decode_attention_sinks")
+
+
+def decode_attention_fp4(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale, out, workspace,
+                         window=None, sinks=0, stream=None):
+    """kvc_decode_attention_fp4: decode over the four-bit cache of append_fp4, over all rows or the newest ``window``
+    and the first ``sinks``. q (f16/bf16) and out [B, Hq, D], or [B, T, Hq, D] for the T newest rows of every sequence;
+    workspace from new_scored_workspace(..., scored=False)."""
+    torch = _torch()
+    i32, u8 = torch.int32, torch.uint8
+    window, sinks = _window(window, sinks)
+    _checked(k_cache, "k_cache", ((k_cache, "k_cache", u8), (v_cache, "v_cache", u8), (q, "q", None),
+                                  (k_scale, "k_scale", u8), (v_scale, "v_scale", u8),
+                                  (block_tables, "block_tables", i32), (context_lens, "context_lens", i32),
+                                  (out, "out", None), (workspace, "workspace", None)))
+    nb, hkv, bs, d = _check_fp4(k_cache, v_cache, k_scale, v_scale)
+    shape, table = q.shape, block_tables.shape
+    if len(shape) not in (3, 4) or shape[-1] != d or out.shape != shape:
+        raise ValueError("q and out must be [batch, n_q_heads, head_dim] or [batch, n_tokens, n_q_heads, head_dim]")
+    B, hq, T = shape[0], shape[-2], shape[1] if len(shape) == 4 else 1
+    if len(table) != 2 or table[0] != B or context_lens.numel() != B:
+        raise ValueError("block_tables must be [batch, max_blocks] and context_lens [batch]")
+    _check(raw().kvc_decode_attention_fp4(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                          v_scale.data_ptr(), block_tables.data_ptr(), table[1],
+                                          context_lens.data_ptr(), B, T, float(scale), hq, hkv, d, bs, nb, window,
+                                          sinks, _code_of(q), out.data_ptr(), _code_of(out), workspace.data_ptr(),
+                                          workspace.nbytes, _stream_of(stream, k_cache)), "kvc_decode_attention_fp4")
+
+
+def prompt_workspace_size(batch, num_tokens, n_q_heads, n_kv_heads, head_dim, block_size, max_blocks_per_seq) -> int:
+    n = ctypes.c_size_t()
+    _check(raw().kvc_prompt_workspace_size(batch, num_tokens, n_q_heads, n_kv_heads, head_dim, block_size,
+                                           max_blocks_per_seq, ctypes.byref(n)), "kvc_prompt_workspace_size")
+    return n.value
+
+
+def new_prompt_workspace(batch, num_tokens, n_q_heads, n_kv_heads, head_dim, block_size, max_blocks_per_seq,
+                         device="cuda"):
+    """uint8 workspace for prompt_attention. It need not be cleared; calls that may overlap need one each."""
+    torch = _torch()
+    n = prompt_workspace_size(batch, num_tokens, n_q_heads, n_kv_heads, head_dim, block_size, max_blocks_per_seq)
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+
+
+def prompt_attention(q, k_cache, v_cache, block_tables, query_starts, context_lens, scale, out, workspace, window=None,
+                     sinks=0, stream=None):
+    """kvc_prompt_attention: attention of a ragged batch of new tokens (whole prompts or chunks) over a 16-bit cache.
+    q/out [num_tokens, Hq, D] in the cache's type, the sequences one behind the other; query_starts int32 [B + 1];
+    context_lens int32 [B] counts every cached row, the new ones included; each token sees the rows up to its own, or of
+    those the newest ``window`` and the first ``sinks``; workspace from new_prompt_workspace."""
+    torch = _torch()
+    i32, dtype = torch.int32, getattr(k_cache, "dtype", None)
+    window, sinks = _window(window, sinks)
+    _checked(k_cache, "k_cache", ((v_cache, "v_cache", dtype), (q, "q", dtype), (block_tables, "block_tables", i32),
+                                  (query_starts, "query_starts", i32), (context_lens, "context_lens", i32),
+                                  (out, "out", dtype), (workspace, "workspace", None)))
+    nb, hkv, bs, d = _pool_shape(k_cache, v_cache)
+    if q.dim() != 3 or q.shape[2] != d or out.shape != q.shape:
+        raise ValueError("q and out must be [num_tokens, n_q_heads, head_dim]")
+    table, (T, hq, _) = block_tables.shape, q.shape
+    if len(table) != 2 or context_lens.numel() != table[0] or query_starts.numel() != table[0] + 1:
+        raise ValueError("block_tables must be [batch, max_blocks], query_starts [batch + 1] and context_lens [batch]")
+    _check(raw().kvc_prompt_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+                                      table[1], query_starts.data_ptr(), context_lens.data_ptr(), table[0], T,
+                                      float(scale), hq, hkv, d, bs, nb, window, sinks, _code_of(k_cache),
+                                      out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                                      _stream_of(stream, k_cache)), "kvc_prompt_attention")

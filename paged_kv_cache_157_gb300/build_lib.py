@@ -42,6 +42,8 @@ SOURCES = [
     "decode_scored_int8.cu",
     "decode_scored.cu",
     "append_block.cu",
+    "cache4.cu",
+    "prompt.cu",
     "evict.cu",
     "decode_wide.cu",
     "decode_mla.cu",

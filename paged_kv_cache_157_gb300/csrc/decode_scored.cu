@@ -1,5 +1,6 @@
-// Host side of kvc_decode_attention_scored and kvc_decode_attention_block8:
-// argument checks, workspace layout, tensor maps and launch.
+// Host side of kvc_decode_attention_scored, kvc_decode_attention_block8,
+// kvc_decode_attention_sinks and kvc_decode_attention_fp4: argument checks,
+// workspace layout, tensor maps and launch.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -7,6 +8,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "attend_row.cuh"
 #include "decode_scored.h"
 #include "kvc_device.cuh"
 
@@ -208,10 +210,131 @@ kvc_status decode(Cache cache, const ScoredShape& s, const void* q, kvc_dtype q_
   return finish_call(stream);
 }
 
+// One warp per query (sequence, token, head).
+struct RowsParams {
+  RowParams row;
+  const void* q;
+  void* out;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  unsigned int* err;
+  int batch, n_tok, n_q_heads, group, max_blocks, rows, out_dtype, q_f16;
+};
+
+template <typename CT, int D>
+__global__ void __launch_bounds__(256) decode_rows_kernel(const RowsParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
+  if (at >= static_cast<int64_t>(p.batch) * p.n_tok * p.n_q_heads) return;
+  const int h = static_cast<int>(at % p.n_q_heads);
+  const int64_t bt = at / p.n_q_heads;
+  const int t = static_cast<int>(bt % p.n_tok), b = static_cast<int>(bt / p.n_tok);
+  const int n = __ldg(p.context_lens + b);
+  constexpr int N = D / 32;
+  float q[N], o[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) o[j] = 0.f;
+  if (n < p.n_tok || n > p.rows) {
+    if (lane == 0) set_flag(p.err, KVC_FLAG_BAD_LEN);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      q[j] = p.q_f16 ? __half2float(static_cast<const __half*>(p.q)[at * D + lane * N + j])
+                     : __bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[at * D + lane * N + j]);
+    if (!attend_row<CT, D>(p.row, q, p.block_tables + static_cast<int64_t>(b) * p.max_blocks, h / p.group,
+                           n - p.n_tok + t, o) && lane == 0)
+      set_flag(p.err, KVC_FLAG_BAD_BLOCK);
+  }
+  store_out_vec<N>(p.out, at * D + lane * N, o, p.out_dtype);
+}
+
+template <typename CT>
+kvc_status decode_rows(const ScoredShape& s, const void* q, kvc_dtype q_dtype, const void* k_cache,
+                       const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
+                       const int32_t* block_tables, const int32_t* context_lens, float scale, int64_t num_blocks,
+                       int window, int sinks, void* out, kvc_dtype out_dtype, void* workspace,
+                       size_t workspace_bytes, cudaStream_t stream) {
+  kvc_status st = check_shape(s);
+  if (st != KVC_OK) return st;
+  if (window < 1 || sinks < 0) return fail(KVC_ERR_INVALID_ARG, "window must be >= 1 and sinks >= 0");
+  if (!dtype_ok(out_dtype)) return fail(KVC_ERR_INVALID_ARG, "unknown out_dtype %d", static_cast<int>(out_dtype));
+  if (num_blocks < 1) return fail(KVC_ERR_INVALID_ARG, "num_blocks must be >= 1");
+  if (num_blocks > ((1ll << 31) - 1) / s.block_size / s.n_kv_heads)
+    return fail(KVC_ERR_UNSUPPORTED, "num_blocks x n_kv_heads x block_size must be below 2^31");
+  if (q == nullptr || k_cache == nullptr || v_cache == nullptr || block_tables == nullptr ||
+      context_lens == nullptr || out == nullptr)
+    return fail(KVC_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+    return fail(KVC_ERR_INVALID_ARG, "q, k_cache and v_cache must be 16-byte aligned");
+  DeviceInfo* dev = nullptr;
+  if ((st = current_device(&dev)) != KVC_OK) return st;
+  const size_t needed = workspace_needed(s, false, dev->num_sms);
+  if (workspace == nullptr || workspace_bytes < needed)
+    return fail(KVC_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace == nullptr ? 0 : workspace_bytes,
+                needed);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(KVC_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  RowsParams p{};
+  p.row = {k_cache, v_cache, k_scale, v_scale, num_blocks, s.n_kv_heads, s.block_size, window, sinks,
+           scale * 1.4426950408889634f};
+  p.q = q;
+  p.out = out;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.err = dev->error_word;
+  p.batch = s.batch;
+  p.n_tok = s.n_tok;
+  p.n_q_heads = s.n_q_heads;
+  p.group = s.group();
+  p.max_blocks = s.max_blocks;
+  p.rows = static_cast<int>(s.rows());
+  p.out_dtype = out_dtype;
+  p.q_f16 = q_dtype == KVC_F16 ? 1 : 0;
+  const int64_t warps = static_cast<int64_t>(s.batch) * s.n_tok * s.n_q_heads;
+  auto* kernel = s.D == 64 ? decode_rows_kernel<CT, 64> : s.D == 128 ? decode_rows_kernel<CT, 128> : decode_rows_kernel<CT, 256>;
+  kernel<<<static_cast<unsigned>((warps + 7) / 8), 256, 0, stream>>>(p);
+  return finish_call(stream);
+}
+
 }  // namespace
 }  // namespace kvc
 
 extern "C" {
+
+kvc_status kvc_decode_attention_sinks(const void* q, const void* k_cache, const void* v_cache,
+                                      const int32_t* block_tables, int max_blocks_per_seq,
+                                      const int32_t* context_lens, int batch, int n_tokens, float scale,
+                                      int n_q_heads, int n_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                                      int window, int sinks, kvc_dtype dtype, void* out, kvc_dtype out_dtype,
+                                      void* workspace, size_t workspace_bytes, kvc_stream stream) {
+  using namespace kvc;
+  clear_error();
+  if (!dtype_ok(dtype)) return fail(KVC_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(dtype));
+  if (dtype == KVC_F32) return fail(KVC_ERR_UNSUPPORTED, "caches of 16-bit elements only (F16, BF16)");
+  const ScoredShape s{batch, n_tokens, n_q_heads, n_kv_heads, head_dim, block_size, max_blocks_per_seq};
+  auto* decode = dtype == KVC_F16 ? decode_rows<__half> : decode_rows<__nv_bfloat16>;
+  return decode(s, q, dtype, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens, scale, num_blocks,
+                window, sinks, out, out_dtype, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+kvc_status kvc_decode_attention_fp4(const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                                    const uint8_t* v_scale, const int32_t* block_tables, int max_blocks_per_seq,
+                                    const int32_t* context_lens, int batch, int n_tokens, float scale, int n_q_heads,
+                                    int n_kv_heads, int head_dim, int block_size, int64_t num_blocks, int window,
+                                    int sinks, kvc_dtype q_dtype, void* out, kvc_dtype out_dtype, void* workspace,
+                                    size_t workspace_bytes, kvc_stream stream) {
+  using namespace kvc;
+  clear_error();
+  if (!dtype_ok(q_dtype)) return fail(KVC_ERR_INVALID_ARG, "unknown q_dtype %d", static_cast<int>(q_dtype));
+  if (q_dtype == KVC_F32) return fail(KVC_ERR_UNSUPPORTED, "queries of 16-bit elements only (F16, BF16)");
+  if (k_scale == nullptr || v_scale == nullptr) return fail(KVC_ERR_INVALID_ARG, "k_scale / v_scale is NULL");
+  if (!aligned16(k_scale) || !aligned16(v_scale))
+    return fail(KVC_ERR_INVALID_ARG, "k_scale and v_scale must be 16-byte aligned");
+  const ScoredShape s{batch, n_tokens, n_q_heads, n_kv_heads, head_dim, block_size, max_blocks_per_seq};
+  return decode_rows<fp4e2m1>(s, q, q_dtype, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
+                              num_blocks, window, sinks, out, out_dtype, workspace, workspace_bytes,
+                              static_cast<cudaStream_t>(stream));
+}
 
 kvc_status kvc_decode_scored_workspace_size(int batch, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim,
                                             int block_size, int max_blocks_per_seq, int scored, size_t* bytes) {
