@@ -2,24 +2,80 @@
 // batch of new tokens, each attending its sequence's cached rows up to its own,
 // optionally only a window of them and the sequence's first rows.
 //
+// Mathematics. The token at position pos sees row r if r <= pos and (r > pos -
+// window or r < sinks): o = sum_r p_r v_r / sum_r p_r, p_r = 2^(x_r - m), x_r =
+// scale * log2(e) * q . k_r, in one pass over the rows with a running
+// reference m and sum. The reference lies kBelow under the largest score when
+// it moves, and moves only when a score exceeds it by kAbove: exact in exact
+// arithmetic for any m, and O is rarely rescaled.
+//
+// A work unit is 2 x 128 query rows of one kv head: the `group` query heads of
+// each token are rows of their own (row = token * group + head), so that a kv
+// head's rows are read once for its whole group and a tile's causal edge spans few
+// tokens. Both products run on tcgen05.mma, 128 x 128 x D each:
+//   S = Q K^T       Q and K from shared memory, S in TMEM
+//   O += P V        P from TMEM (where S was, 16 bits), V read MN-major
+// The two halves of a unit take turns: while one's softmax runs on its four
+// warps (one thread per row, no shuffles), the tensor core has the other's
+// products. Warp 0 copies pages by TMA (boxes of gcd(block_size, 128) rows) into a
+// ring of K and V tiles, one thread of warp 1 issues the products.
+//
+// P in 16 bits: its rounding (2^-8 of a weight in bf16, 2^-11 in f16) is of the
+// size of the output's own, and a second product for the rest would cost half
+// as much again. f16 weights use f16's whole range (see Margin).
+//
+// Work split. A planning kernel lists the units' (sequence, token range) tiles.
+// Many units: sorted by cost, dealt out in turn, the largest first. Few units:
+// the KV tiles of all units are laid end to end and cut into equal ranges, one
+// per CTA; the parts of a unit leave records that a merge kernel joins.
+//
+// Rows that nobody in a unit sees are neither looked up nor read (TMA fills
+// zeros), those beside visible ones are cleared in shared memory. A row
+// whose output is not finite is done again over its visible rows alone, so that
+// an infinity or NaN in V stays with those who see it.
+//
 // Sources: the chunk mask of "单请求 KV Cache" (query row i of a chunk sees
 // columns up to past_len + i) and the block table of "KV Cache（键值缓存）" section
 // 2.3; Window Attention of "KV-Cache——为什么AI回复越来越快" section 08.
+#include <cuda.h>
+
 #include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <mutex>
+#include <numeric>
 
 #include "attend_row.cuh"
 #include "kvc_internal.h"
+#include "umma.cuh"
+#include "umma_wide.cuh"
 
 namespace kvc {
 
 namespace {
 
+using namespace umma;
+
 constexpr int kPromptMaxBatch = 4096;
+constexpr int kM = 128;            // query rows of a half (M of the products)
+constexpr int kRows = 128;         // cached rows of a tile
+constexpr int kPromptThreads = 384;
+constexpr int kMinTiles = 4;       // KV tiles of a range at least, where units are split
+constexpr int kBadRing = 8;        // tiles whose bad blocks are remembered: more than the ring holds
 
 struct PromptShape {
   int batch;
   int64_t num_tokens;
   int n_q_heads, n_kv_heads, D, block_size, max_blocks;
+  int group() const { return n_q_heads / n_kv_heads; }
+  int tokens() const { return kM / group(); }  // of a half
+  int64_t tiles() const { return num_tokens / (2 * tokens()) + batch; }  // at most
+};
+
+// A token range of one sequence: at most 2 * tokens() new tokens.
+struct Tile {
+  int seq, first, count, cost;  // first: its first row of q; cost: KV tiles that it sees
+  int pos, before, pad0, pad1;  // position of its first token; KV tiles of the tiles before it
 };
 
 struct PromptParams {
@@ -29,9 +85,32 @@ struct PromptParams {
   const int32_t* block_tables;
   const int32_t* query_starts;  // [batch + 1]
   const int32_t* context_lens;
+  // workspace
+  int* head;     // number of tiles, their total cost
+  Tile* tiles;
+  float* rec_o;  // [2 * CTAs, 2 * kM, D] unnormalised partial outputs
+  float* rec_ml; // [2 * CTAs, 2 * kM, 2] (reference, sum of weights)
   unsigned int* err;
-  int batch, num_tokens, n_q_heads, group, max_blocks, rows;
+  int batch, num_tokens, n_q_heads, group, max_blocks, rows, tokens, max_tiles;
+  int split, grid;
+  int box, box_log2;  // rows of a TMA box: gcd(block_size, 128)
+  int pool_rows;  // rows of the pool: one past the last, TMA fills zeros
+  float qscale;   // |scale| * log2(e), not 0
+  int negative;   // scale < 0
 };
+
+// Where a query's reference m (log2 units) lies: kBelow under the largest score
+// when it moves, and it moves when a score exceeds it by kAbove. f16 ends at
+// 2^-24, and rows beside an attention sink have weights of that size: its
+// largest weights are 2^11 to 2^15, so that weights down to 2^-25 of the largest
+// keep their 11 bits.
+template <bool BF>
+struct PromptMargin {
+  static constexpr float kBelow = BF ? 0.f : 11.f;
+  static constexpr float kAbove = BF ? 8.f : 15.f;
+};
+
+// ------------------------------------------------------------------- plan
 
 // Sequence i's first new token, their number and its rows. Tokens of a
 // sequence whose starts are out of order or range are none; rows 0: the length
@@ -57,35 +136,735 @@ __device__ __forceinline__ Span span_of(const PromptParams& p, int i, bool flag)
   return s;
 }
 
-template <typename CT, int D>
-__global__ void __launch_bounds__(256) prompt_rows_kernel(const PromptParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t warp = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < p.batch; i += 256) (void)span_of(p, i, true);
-  if (warp >= static_cast<int64_t>(p.num_tokens) * p.n_q_heads) return;
-  const int t = static_cast<int>(warp / p.n_q_heads), h = static_cast<int>(warp - static_cast<int64_t>(t) * p.n_q_heads);
-  int a = 0, b = p.batch - 1;  // the last sequence that starts at or before t
-  while (a < b) {
-    const int mid = (a + b + 1) >> 1;
-    if (__ldg(p.query_starts + mid) <= t) a = mid; else b = mid - 1;
+// The KV tiles that tokens at positions [pos, pos + count) see: `front` ones of
+// the sinks, then those from `start` on; tile i of them is i < front ? i : i -
+// front + start.
+struct Seen {
+  int front, start, total;
+};
+__host__ __device__ __forceinline__ Seen seen_tiles(int pos, int count, int window, int sinks) {
+  const int low = pos >= window ? pos - window + 1 : 0;  // first row of the first token's window
+  Seen s;
+  s.start = low / kRows;
+  const int need = sinks < low ? sinks : low;  // sinks before the window
+  s.front = (need + kRows - 1) / kRows;
+  if (s.front > s.start) s.front = s.start;
+  s.total = s.front + (pos + count - 1) / kRows - s.start + 1;
+  return s;
+}
+
+constexpr int kPlanThreads = 1024;
+constexpr int kBuckets = 1024;
+
+// Exclusive prefix sum over the CTA; *total: the sum. Two barriers.
+__device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  const Span s = span_of(p, a, false);
-  if (t < s.first || t >= s.first + s.count) return;
+  if (lane == 31) s_warp[w] = x;
+  __syncthreads();
+  int before = 0, sum = 0;
+  for (int i = 0; i < kPlanThreads / 32; ++i) {
+    const int y = s_warp[i];
+    if (i < w) before += y;
+    sum += y;
+  }
+  *total = sum;
+  __syncthreads();
+  return before + x - v;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptParams p, int elem_bytes, int D) {
+  __shared__ int s_first[kPromptMaxBatch + 1];  // tiles of the sequences before
+  __shared__ int s_warp[kPlanThreads / 32], s_hist[kBuckets];
+  const int tid = threadIdx.x, B = p.batch, per_tile = 2 * p.tokens;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int per = (B + kPlanThreads - 1) / kPlanThreads;
+  const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  int local = 0, most = 0;
+  bool invalid = false;
+  for (int b = b0; b < b1; ++b) {
+    const Span s = span_of(p, b, true);
+    if (s.count > 0 && s.rows == 0) {
+      invalid = true;
+      continue;
+    }
+    local += (s.count + per_tile - 1) / per_tile;
+    if (s.count > 0) most = max(most, seen_tiles(s.rows - 1, 1, p.row.window, p.row.sinks).total + 1);
+  }
+  int n = 0;
+  int run = block_scan(local, s_warp, &n);
+  for (int b = b0; b < b1; ++b) {
+    s_first[b] = run;
+    const Span s = span_of(p, b, false);
+    if (s.count > 0 && s.rows > 0) run += (s.count + per_tile - 1) / per_tile;
+  }
+  // (the prefix sums are read behind the next barrier)
+  if (__syncthreads_or(invalid)) {
+    for (int b = 0; b < B; ++b) {
+      const Span s = span_of(p, b, false);
+      if (s.count == 0 || s.rows > 0) continue;
+      const int64_t row_words = static_cast<int64_t>(p.n_q_heads) * D * elem_bytes / 16;
+      uint4* to = static_cast<uint4*>(p.out) + s.first * row_words;
+      for (int64_t i = tid; i < s.count * row_words; i += kPlanThreads) to[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  if (n > p.max_tiles) {  // starts that overlap
+    if (tid == 0) set_flag(p.err, KVC_FLAG_BAD_LEN);
+    n = p.max_tiles;
+  }
+  auto tile_of = [&](int i) {
+    int a = 0, b = B - 1;  // the last sequence whose first tile is <= i
+    while (a < b) {
+      const int mid = (a + b + 1) >> 1;
+      if (s_first[mid] <= i) a = mid; else b = mid - 1;
+    }
+    const Span s = span_of(p, a, false);
+    Tile t;
+    const int t0 = (i - s_first[a]) * per_tile;
+    t.seq = a;
+    t.first = s.first + t0;
+    t.count = min(per_tile, s.count - t0);
+    t.pos = s.rows - s.count + t0;
+    t.cost = seen_tiles(t.pos, t.count, p.row.window, p.row.sinks).total;
+    t.before = t.pad0 = t.pad1 = 0;
+    return t;
+  };
+  int total = 0;
+  if (p.split) {  // few tiles: in order, with prefix sums
+    for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+      Tile t;
+      t.cost = 0;
+      if (i0 + tid < n) t = tile_of(i0 + tid);
+      int sum = 0;
+      const int before = block_scan(t.cost, s_warp, &sum);
+      if (i0 + tid < n) {
+        t.before = total + before;
+        p.tiles[i0 + tid] = t;
+      }
+      total += sum;
+    }
+  } else {  // sorted by cost, in up to 1024 classes
+    most = max(__reduce_max_sync(0xffffffffu, most), 1);
+    if ((tid & 31) == 0) s_warp[tid >> 5] = most;
+    for (int i = tid; i < kBuckets; i += kPlanThreads) s_hist[i] = 0;
+    __syncthreads();
+    for (int i = 0; i < kPlanThreads / 32; ++i) most = max(most, s_warp[i]);
+    int shift = 0;
+    while ((most >> shift) >= kBuckets) ++shift;
+    auto bucket = [&](int cost) { return max(0, (most >> shift) - (cost >> shift)); };
+    for (int i = tid; i < n; i += kPlanThreads) atomicAdd(&s_hist[min(kBuckets - 1, bucket(tile_of(i).cost))], 1);
+    __syncthreads();
+    const int mine = s_hist[tid];
+    int sum = 0;
+    const int before = block_scan(mine, s_warp, &sum);
+    s_hist[tid] = before;
+    __syncthreads();
+    for (int i = tid; i < n; i += kPlanThreads) {
+      const Tile t = tile_of(i);
+      p.tiles[atomicAdd(&s_hist[min(kBuckets - 1, bucket(t.cost))], 1)] = t;  // the order among equals is free
+    }
+  }
+  if (tid == 0) {
+    p.head[0] = n;
+    p.head[1] = total;
+  }
+}
+static_assert(kBuckets == kPlanThreads, "one class per thread");
+
+// The equal ranges of split units: range x is [start(x), start(x + 1)) of N positions.
+struct Ranges {
+  int64_t N;
+  int W;
+  __device__ __forceinline__ Ranges(int n_tiles, int total, int heads, int grid) {
+    N = static_cast<int64_t>(total) * heads;
+    const int64_t units = static_cast<int64_t>(n_tiles) * heads;
+    W = static_cast<int>(min(static_cast<int64_t>(grid), max(units, (N + kMinTiles - 1) / kMinTiles)));
+  }
+  __device__ __forceinline__ int64_t start(int64_t x) const { return x * N / W; }
+  __device__ __forceinline__ int holder(int64_t pos) const { return static_cast<int>(((pos + 1) * W - 1) / N); }
+};
+
+// A unit (tile, kv head) or the part of it in this CTA's range: KV tiles [i0, i1).
+struct Part {
+  Tile t;
+  int kvh, i0, i1;
+  int rec;  // -1: the whole unit
+};
+
+struct Walk {
+  int n, round;
+  int64_t lo, hi, pos;
+  __device__ __forceinline__ Walk(const PromptParams& p) {
+    n = __ldcg(p.head);  // (L2: the planning kernel may have run beside this one's start)
+    round = 0;
+    lo = hi = pos = 0;
+    if (p.split && n > 0) {
+      const Ranges r(n, __ldcg(p.head + 1), p.row.n_kv_heads, p.grid);
+      if (static_cast<int>(blockIdx.x) < r.W) {
+        lo = pos = r.start(blockIdx.x);
+        hi = r.start(blockIdx.x + 1);
+      }
+    }
+  }
+  __device__ __forceinline__ static Tile load(const PromptParams& p, int i) {
+    union {
+      int4 v[2];
+      Tile t;
+    } u;
+    u.v[0] = __ldcg(reinterpret_cast<const int4*>(p.tiles + i));
+    u.v[1] = __ldcg(reinterpret_cast<const int4*>(p.tiles + i) + 1);
+    return u.t;
+  }
+  __device__ __forceinline__ bool next(const PromptParams& p, Part& u) {
+    const int H = p.row.n_kv_heads;
+    if (!p.split) {
+      // dealt out there and back, so that nobody always gets the larger one
+      const int64_t i = static_cast<int64_t>(round) * p.grid +
+                        ((round & 1) ? p.grid - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
+      ++round;
+      if (i >= static_cast<int64_t>(n) * H) return false;
+      u.t = load(p, static_cast<int>(i / H));
+      u.kvh = static_cast<int>(i % H);
+      u.i0 = 0;
+      u.i1 = u.t.cost;
+      u.rec = -1;
+      return true;
+    }
+    if (pos >= hi) return false;
+    int a = 0, b = n - 1;  // the last tile that begins at or before pos
+    while (a < b) {
+      const int mid = (a + b + 1) >> 1;
+      if (static_cast<int64_t>(H) * __ldcg(&p.tiles[mid].before) <= pos) a = mid; else b = mid - 1;
+    }
+    u.t = load(p, a);
+    const int rest = static_cast<int>(pos - static_cast<int64_t>(H) * u.t.before);
+    u.kvh = rest / u.t.cost;
+    u.i0 = rest - u.kvh * u.t.cost;
+    u.i1 = static_cast<int>(min(static_cast<int64_t>(u.t.cost), u.i0 + (hi - pos)));
+    u.rec = u.i0 == 0 && u.i1 == u.t.cost ? -1 : 2 * static_cast<int>(blockIdx.x) + (pos == lo ? 0 : 1);
+    pos += u.i1 - u.i0;
+    return true;
+  }
+};
+
+// ------------------------------------------------------------ main kernel
+
+template <int D>
+struct PromptGeo {
+  static constexpr int kHalves = D / 64;                  // 128-byte wide parts of a row
+  static constexpr uint32_t kPart = kRows * 128;          // one part of a tile
+  static constexpr uint32_t kTile = kHalves * kPart;      // a K or V tile, or a half's queries
+  static constexpr int kSlots = D == 128 ? 5 : 8;         // K and V tiles in the ring
+  static constexpr uint32_t kOffRing = 2 * kTile;         // behind both halves' queries
+  static constexpr uint32_t kOffBar = kOffRing + kSlots * kTile;
+  enum {
+    QFULL = 0, QEMPTY, FULL0, EMPTY0 = FULL0 + kSlots, SFULL0 = EMPTY0 + kSlots, PFULL0 = SFULL0 + 2,
+    OFULL0 = PFULL0 + 2, OEMPTY0 = OFULL0 + 2, FINAL = OEMPTY0 + 2, COUNT
+  };
+  static constexpr uint32_t kOffMisc = kOffBar + COUNT * 8;  // TMEM address, abort flag, bad blocks
+  static constexpr uint32_t kBytes = kOffMisc + 8 + kBadRing * 4 + 1024;
+  // TMEM columns: S (P over it) of both halves, O of both
+  static constexpr uint32_t kColO = 256;
+  static constexpr uint32_t kTmemCols = 512;
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// D += A . B with A read from TMEM.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t r;
+  if constexpr (BF)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// One output row again, over its visible rows alone (attend_row.cuh). Rare.
+template <typename CT, int D>
+__device__ __noinline__ void redo_row(const PromptParams& p, int seq, int row, int head, int pos) {
   constexpr int N = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t at = (static_cast<int64_t>(row) * p.n_q_heads + head) * D + lane * N;
   float q[N], o[N];
 #pragma unroll
-  for (int j = 0; j < N; ++j) o[j] = 0.f;
-  if (s.rows > 0) {
-    const CT* qr = static_cast<const CT*>(p.q) + warp * D + lane * N;
-#pragma unroll
-    for (int j = 0; j < N; ++j) q[j] = Elem<CT>::to_float(qr[j]);
-    if (!attend_row<CT, D>(p.row, q, p.block_tables + static_cast<int64_t>(a) * p.max_blocks, h / p.group,
-                           s.rows - s.count + t - s.first, o) && lane == 0)
-      set_flag(p.err, KVC_FLAG_BAD_BLOCK);
-  }
-  store_out_vec<N>(p.out, warp * D + lane * N, o, std::is_same<CT, __half>::value ? KVC_F16 : KVC_BF16);
+  for (int j = 0; j < N; ++j) q[j] = Elem<CT>::to_float(static_cast<const CT*>(p.q)[at + j]);
+  (void)attend_row<CT, D>(p.row, q, p.block_tables + static_cast<int64_t>(seq) * p.max_blocks, head / p.group, pos, o);
+  store_out_vec<N>(p.out, at, o, std::is_same<CT, __half>::value ? KVC_F16 : KVC_BF16);
 }
+
+template <typename CT, int D>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PromptParams p) {
+  using G = PromptGeo<D>;
+  constexpr bool BF = std::is_same<CT, __nv_bfloat16>::value;
+  constexpr uint32_t full = 0xffffffffu;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char* sm = smem_raw + (base - raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + G::kOffBar);
+  volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(sm + G::kOffMisc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(sm + G::kOffMisc + 4);
+  volatile uint32_t* s_bad = reinterpret_cast<volatile uint32_t*>(sm + G::kOffMisc + 8);
+  auto bar = [&](int i) -> uint32_t { return base + G::kOffBar + 8u * static_cast<uint32_t>(i); };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    *s_abort = 0;
+    for (int i = 0; i < G::COUNT; ++i)
+      mbar_init(&bars[i], (i >= G::PFULL0 && i < G::OFULL0) || (i >= G::OEMPTY0 && i < G::FINAL) ? 4 : 1);
+    fence_barrier_init();
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
+  }
+  // Query rows that no token has (128 is no multiple of the group) stay zeros.
+  if (p.tokens * p.group < kM) {
+    for (uint32_t i = tid; i < 2 * G::kTile / 16; i += kPromptThreads)
+      *reinterpret_cast<uint4*>(sm + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + G::kOffMisc),
+                 "r"(G::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *s_tmem;
+  const int bs = p.row.block_size, window = p.row.window, sinks = p.row.sinks;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    // Lane i has box i of every tile: its table entry is read before the slot is
+    // free. One barrier per K or V tile.
+    uint32_t kk = 0, gt = 0, un = 0;  // tiles copied, KV tiles, units
+    uint32_t issued[G::kSlots] = {};
+    const int boxes = kRows / p.box;
+    bool ok = true;
+    Walk walk(p);
+    Part u;
+    while (ok && walk.next(p, u)) {
+      const int last = u.t.pos + u.t.count - 1;
+      const int low = u.t.pos >= window ? u.t.pos - window + 1 : 0;
+      const Seen seen = seen_tiles(u.t.pos, u.t.count, window, sinks);
+      const bool two = u.t.count > p.tokens;
+      const int32_t* table = p.block_tables + static_cast<int64_t>(u.t.seq) * p.max_blocks;
+      // ---- queries
+      bool got = true;
+      if (lane == 0 && un > 0) got = wait_phase(bar(G::QEMPTY), (un - 1) & 1u, s_abort, p.err);
+      if (!__shfl_sync(full, got ? 1 : 0, 0)) break;
+      if (lane == 0) {
+        const uint32_t bytes = static_cast<uint32_t>(p.tokens * p.group) * 128u * G::kHalves;
+        arrive_expect(bar(G::QFULL), two ? 2 * bytes : bytes);
+        for (int h = 0; h < (two ? 2 : 1); ++h)
+          for (int x = 0; x < G::kHalves; ++x)
+            tma_load_3d(base + h * G::kTile + x * G::kPart, &tm_q, 64 * x, u.kvh * p.group,
+                        u.t.first + h * p.tokens, bar(G::QFULL));
+      }
+      __syncwarp();
+      ++un;
+      // ---- rows
+      for (int i = u.i0; i < u.i1; ++i, ++gt) {
+        const int kt = i < seen.front ? i : i - seen.front + seen.start;
+        const int r0 = kt * kRows + lane * p.box;
+        const bool want = lane < boxes && r0 <= last && (r0 + p.box > low || r0 < sinks);
+        const int blk = r0 / bs;
+        const int phys = want ? __ldg(table + blk) : -1;
+        const bool there = phys >= 0 && phys < p.row.num_blocks;
+        const uint32_t bad = __ballot_sync(full, want && !there);
+        const int y = there ? (phys * p.row.n_kv_heads + u.kvh) * bs + (r0 - blk * bs) : p.pool_rows;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++kk) {
+          const uint32_t slot = kk % G::kSlots;
+          got = true;
+          if (lane == 0 && kk >= G::kSlots)
+            got = wait_phase(bar(G::EMPTY0 + slot), (kk / G::kSlots - 1) & 1u, s_abort, p.err);
+          if (!__shfl_sync(full, got ? 1 : 0, 0)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            if (kv == 0) {
+              s_bad[gt % kBadRing] = bad;
+              if (bad != 0) set_flag(p.err, KVC_FLAG_BAD_BLOCK);
+            }
+            arrive_expect(bar(G::FULL0 + slot), G::kTile);
+          }
+          __syncwarp();
+          if (lane < boxes) {
+            const uint32_t dst = base + G::kOffRing + slot * G::kTile + static_cast<uint32_t>(lane * p.box) * 128u;
+#pragma unroll
+            for (int x = 0; x < G::kHalves; ++x)
+              tma_load_2d(dst + x * G::kPart, kv == 0 ? &tm_k : &tm_v, 64 * x, y, bar(G::FULL0 + slot));
+          }
+          ++issued[slot];
+        }
+        if (!ok) break;
+      }
+    }
+    if (*s_abort && lane == 0) {
+      // Copies still in flight must land before this shared memory goes away.
+      for (int s = 0; s < G::kSlots; ++s) {
+        if (issued[s] == 0) continue;
+        const uint64_t t0 = globaltimer_ns();
+        while (!try_wait(bar(G::FULL0 + s), (issued[s] - 1) & 1u) && globaltimer_ns() - t0 < kWaitNs) {
+        }
+      }
+      if (un > 0) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!try_wait(bar(G::QFULL), (un - 1) & 1u) && globaltimer_ns() - t0 < kWaitNs) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    // Order per KV tile j: PV of half 0 (j), S of half 0 (j + 1), PV of half 1
+    // (j), S of half 1 (j + 1). P lies where S was: S (j + 1) follows PV (j).
+    if (lane == 0) {
+      const uint32_t id_s = instr_desc(kM, kRows, 0, 0, BF);
+      const uint32_t id_pv = instr_desc(kM, D, 0, 1, BF);
+      uint32_t gt = 0, un = 0;        // KV tiles begun, units begun
+      uint32_t np[2] = {0, 0}, nu[2] = {0, 0};  // per half: tiles whose P was used, units
+      bool ok = true;
+      Walk walk(p);
+      Part u;
+      // S of half h with KV tile g (of the CTA's count)
+      auto issue_s = [&](int h, uint32_t g) {
+        const uint32_t slot = (2 * g) % G::kSlots;
+        const uint64_t a = smem_desc(base + h * G::kTile, 16, 1024, 2);
+        const uint64_t b = smem_desc(base + G::kOffRing + slot * G::kTile, 16, 1024, 2);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint64_t off = ((ks >> 2) * G::kPart + (ks & 3) * 32) >> 4;
+          mma(tmem + h * kRows, a + off, b + off, id_s, ks == 0 ? 0u : 1u);
+        }
+        commit(bar(G::SFULL0 + h));
+      };
+      auto full_slot = [&](uint32_t k) {
+        return wait_phase(bar(G::FULL0 + k % G::kSlots), (k / G::kSlots) & 1u, s_abort, p.err);
+      };
+      while (ok && !*s_abort && walk.next(p, u)) {
+        const int halves = u.t.count > p.tokens ? 2 : 1;
+        const int J = u.i1 - u.i0;
+        if (!wait_phase(bar(G::QFULL), un & 1u, s_abort, p.err)) break;
+        if (!full_slot(2 * gt)) break;
+        fence_after();
+        for (int h = 0; h < halves; ++h) issue_s(h, gt);
+        commit(bar(G::EMPTY0 + (2 * gt) % G::kSlots));
+        if (J == 1) commit(bar(G::QEMPTY));
+        for (int j = 0; j < J && ok; ++j, ++gt) {
+          const bool more = j + 1 < J;
+          if (!full_slot(2 * gt + 1)) { ok = false; break; }
+          const uint32_t vslot = (2 * gt + 1) % G::kSlots;
+          const uint64_t v = smem_desc(base + G::kOffRing + vslot * G::kTile, G::kPart, 1024, 2);
+          for (int h = 0; h < halves; ++h) {
+            if (!wait_phase(bar(G::PFULL0 + h), np[h] & 1u, s_abort, p.err)) { ok = false; break; }
+            ++np[h];
+            // O of the unit before has been read
+            if (j == 0 && nu[h] > 0 && !wait_phase(bar(G::OEMPTY0 + h), (nu[h] - 1) & 1u, s_abort, p.err)) {
+              ok = false;
+              break;
+            }
+            fence_after();
+#pragma unroll
+            for (int ks = 0; ks < kRows / 16; ++ks)
+              mma_ts(tmem + G::kColO + h * D, tmem + h * kRows + ks * 8, v + ((ks * 2048) >> 4), id_pv,
+                     j == 0 && ks == 0 ? 0u : 1u);
+            if (!more) commit(bar(G::OFULL0 + h));
+            if (h == halves - 1) commit(bar(G::EMPTY0 + vslot));
+            if (more) {
+              if (h == 0) {
+                if (!full_slot(2 * gt + 2)) { ok = false; break; }
+                fence_after();
+              }
+              issue_s(h, gt + 1);
+              if (h == halves - 1) {
+                commit(bar(G::EMPTY0 + (2 * gt + 2) % G::kSlots));
+                if (j + 2 == J) commit(bar(G::QEMPTY));
+              }
+            }
+          }
+        }
+        for (int h = 0; h < halves; ++h) ++nu[h];
+        ++un;
+      }
+      // all products are done before TMEM is freed
+      commit(bar(G::FINAL));
+      const uint64_t t0 = globaltimer_ns();
+      while (!try_wait(bar(G::FINAL), 0) && globaltimer_ns() - t0 < kWaitNs) {
+      }
+    }
+  } else if (warp >= 4) {
+    // --------------------------------------------------- softmax, epilogue
+    // Thread = query row (TMEM lane) of half hf.
+    const int hf = (warp - 4) >> 2;
+    const int r = (tid - 128) & 127;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t col_s = lane_addr + hf * kRows, col_o = lane_addr + G::kColO + hf * D;
+    const int tk = r / p.group;  // token of the half
+    constexpr float BELOW = PromptMargin<BF>::kBelow, ABOVE = PromptMargin<BF>::kAbove;
+    const float qs = p.qscale;
+    // a warp goes on or gives up as one
+    auto wait_warp = [&](uint32_t b, uint32_t parity) {
+      return __all_sync(full, wait_phase_suspend(b, parity, s_abort, p.err));
+    };
+    uint32_t gt = 0, n = 0, nu = 0;  // the CTA's KV tiles; tiles and units of this half
+    bool ok = true;
+    Walk walk(p);
+    Part u;
+    while (ok && walk.next(p, u)) {
+      const int J = u.i1 - u.i0;
+      if (hf * p.tokens >= u.t.count) {  // the half has no token
+        gt += J;
+        continue;
+      }
+      const Seen seen = seen_tiles(u.t.pos, u.t.count, window, sinks);
+      const int end = u.t.pos + u.t.count - 1;  // last position of the unit
+      const int low = u.t.pos >= window ? u.t.pos - window + 1 : 0;
+      const int first = u.t.pos + hf * p.tokens;       // positions of the half
+      const int last = min(end, first + p.tokens - 1);
+      const bool valid = tk < p.tokens && first + tk <= last;
+      const int pos = min(first + tk, last);
+      float m = -1e30f, l = 0.f;  // finite: a row may meet only hidden columns
+      for (int j = 0; j < J; ++j, ++gt, ++n) {
+        const int i = u.i0 + j;
+        const int r0 = (i < seen.front ? i : i - seen.front + seen.start) * kRows;
+        if (!wait_warp(bar(G::SFULL0 + hf), n & 1u)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        float s[kRows];
+        tmem_ld128(col_s, s);
+        const uint32_t bad = s_bad[gt % kBadRing];
+        if (p.negative) {
+#pragma unroll
+          for (int c = 0; c < kRows; ++c) s[c] = -s[c];
+        }
+        if (r0 + kRows - 1 > first || (r0 <= last - window && r0 + kRows > sinks) || bad != 0) {
+          const int hi = pos - r0, lw = pos - window - r0, sk = sinks - r0;
+#pragma unroll
+          for (int c = 0; c < kRows; ++c)
+            if (c > hi || (c <= lw && c >= sk)) s[c] = -__builtin_huge_valf();
+          if (bad != 0) {
+#pragma unroll
+            for (int c = 0; c < kRows; ++c)
+              if ((bad >> (c >> p.box_log2)) & 1u) s[c] = -__builtin_huge_valf();
+          }
+          // V rows that nobody in the unit sees may hold anything, and 0 x NaN is
+          // NaN: half 0 clears them (its products come first).
+          if (hf == 0 && (r0 + kRows - 1 > end || (r0 < low && r0 + kRows > sinks))) {
+            const uint32_t k = 2 * gt + 1, slot = k % G::kSlots;
+            if (!wait_warp(bar(G::FULL0 + slot), (k / G::kSlots) & 1u)) {
+              ok = false;
+              break;
+            }
+            const int row = r0 + r;
+            if (row > end || (row < low && row >= sinks)) {
+              unsigned char* v = sm + G::kOffRing + slot * G::kTile + r * 128;
+#pragma unroll
+              for (int x = 0; x < G::kHalves; ++x)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                  *reinterpret_cast<uint4*>(v + x * G::kPart + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        float mx = max3(s[0], s[1], s[2]), mx2 = max3(s[3], s[4], s[5]);
+#pragma unroll
+        for (int c = 6; c < 126; c += 4) {
+          mx = max3(mx, s[c], s[c + 1]);
+          mx2 = max3(mx2, s[c + 2], s[c + 3]);
+        }
+        mx = max3(mx, s[126], s[127]);
+        mx = fmaxf(mx, mx2) * qs;
+        if (__any_sync(full, valid && mx > m + ABOVE)) {
+          const float to = fmaxf(m, mx - BELOW);
+          const float f = fast_exp2(m - to);
+          l *= f;
+          m = to;
+          if (j > 0) {  // PV of the tile before is done: S came behind it
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              tmem_ld32(col_o + c, o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] *= f;
+              tmem_st32_async(col_o + c, reinterpret_cast<const uint32_t*>(o));
+            }
+            tmem_wait_st();
+          }
+        }
+        const float2 q2 = make_float2(qs, qs), m2 = make_float2(-m, -m);
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kRows; c += 32) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float2 x = ffma2(make_float2(s[c + 2 * k], s[c + 2 * k + 1]), q2, m2);
+            const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            sum = fadd2(sum, e);
+            w[k] = pack16<BF>(e.x, e.y);
+          }
+          tmem_st16_async(col_s + c / 2, w);
+        }
+        l += sum.x + sum.y;
+        tmem_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(bar(G::PFULL0 + hf));
+      }
+      if (!ok) break;
+      // ---- epilogue
+      if (!wait_warp(bar(G::OFULL0 + hf), nu & 1u)) break;
+      ++nu;
+      fence_after();
+      const int head = u.kvh * p.group + r - tk * p.group;
+      const int row = u.t.first + hf * p.tokens + tk;
+      const int64_t at = (static_cast<int64_t>(row) * p.n_q_heads + head) * D;
+      float* rec = u.rec < 0 ? nullptr : p.rec_o + (static_cast<int64_t>(u.rec) * 2 * kM + hf * kM + r) * D;
+      const float inv = u.rec >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      float zero = 0.f;  // NaN if an output is not finite
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        tmem_ld32(col_o + c, o);
+        if (!valid) continue;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] *= inv;
+        if (rec != nullptr) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<float4*>(rec + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        } else {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            zero = fmaf(o[2 * k], 0.f, fmaf(o[2 * k + 1], 0.f, zero));
+            w[k] = pack16<BF>(o[2 * k], o[2 * k + 1]);
+          }
+          uint4* to = reinterpret_cast<uint4*>(static_cast<CT*>(p.out) + at + c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) to[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(bar(G::OEMPTY0 + hf));
+      if (rec != nullptr) {
+        if (valid)
+          *reinterpret_cast<float2*>(p.rec_ml + (static_cast<int64_t>(u.rec) * 2 * kM + hf * kM + r) * 2) =
+              make_float2(m, l);
+      } else {
+        for (uint32_t odd = __ballot_sync(full, valid && zero != 0.f); odd != 0; odd &= odd - 1) {
+          const int src = __ffs(odd) - 1;
+          redo_row<CT, D>(p, u.t.seq, __shfl_sync(full, row, src), __shfl_sync(full, head, src),
+                          __shfl_sync(full, pos, src));
+        }
+      }
+    }
+  }
+
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(G::kTmemCols) : "memory");
+}
+
+// ------------------------------------------------------------------ merge
+
+// Joins the records of units that several ranges share: o = sum_x 2^(m_x - M)
+// O_x / sum_x 2^(m_x - M) l_x. One warp per row, lanes over the dims.
+constexpr int kMergeRows = 32;  // rows of a unit per CTA
+
+template <typename CT, int D>
+__global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptParams p) {
+  constexpr int N = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int H = p.row.n_kv_heads, n = __ldcg(p.head);
+  const int i = static_cast<int>(blockIdx.x) / H, kvh = static_cast<int>(blockIdx.x) - i * H;
+  if (i >= n) return;
+  const Ranges r(n, __ldcg(p.head + 1), H, p.grid);
+  const Tile t = Walk::load(p, i);
+  const int64_t u0 = static_cast<int64_t>(H) * t.before + static_cast<int64_t>(kvh) * t.cost;
+  const int a = r.holder(u0), b = r.holder(u0 + t.cost - 1);
+  if (a == b) return;
+  const int lane = threadIdx.x & 31;
+  for (int k = threadIdx.x >> 5; k < kMergeRows; k += 8) {
+    const int at = blockIdx.y * kMergeRows + k;  // half and row
+    const int hf = at / kM, tk = (at % kM) / p.group, head = kvh * p.group + (at % kM) - tk * p.group;
+    const int tok = hf * p.tokens + tk;
+    if (tk >= p.tokens || tok >= t.count) continue;
+    auto rec = [&](int x) { return (2ll * x + (u0 > r.start(x) ? 1 : 0)) * 2 * kM + at; };
+    float M = -__builtin_huge_valf();
+    for (int x = a + lane; x <= b; x += 32) M = fmaxf(M, __ldcg(p.rec_ml + rec(x) * 2));
+    M = warp_max(M);
+    float L = 0.f, o[N];
+#pragma unroll
+    for (int c = 0; c < N; ++c) o[c] = 0.f;
+    for (int x = a; x <= b; ++x) {
+      const int64_t y = rec(x);
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.rec_ml + y * 2));
+      const float f = fast_exp2(ml.x - M);
+      L = fmaf(f, ml.y, L);
+#pragma unroll
+      for (int c = 0; c < N; ++c) o[c] = fmaf(f, __ldcg(p.rec_o + y * D + lane * N + c), o[c]);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    float zero = 0.f;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      o[c] *= inv;
+      zero = fmaf(o[c], 0.f, zero);
+    }
+    if (__any_sync(0xffffffffu, zero != 0.f))
+      redo_row<CT, D>(p, t.seq, t.first + tok, head, t.pos + tok);
+    else
+      store_out_vec<N>(p.out, (static_cast<int64_t>(t.first + tok) * p.n_q_heads + head) * D + lane * N, o,
+                       std::is_same<CT, __half>::value ? KVC_F16 : KVC_BF16);
+  }
+}
+
+// ------------------------------------------------------------------- host
 
 kvc_status check_shape(const PromptShape& s) {
   if (s.batch < 1 || s.num_tokens < 0 || s.n_q_heads < 1 || s.n_kv_heads < 1 || s.D < 1 || s.block_size < 1 ||
@@ -105,6 +884,108 @@ kvc_status check_shape(const PromptShape& s) {
     return fail(KVC_ERR_UNSUPPORTED, "max_blocks_per_seq x block_size too large");
   if (s.num_tokens >= (1ll << 31) / s.n_q_heads)
     return fail(KVC_ERR_UNSUPPORTED, "num_tokens x n_q_heads must be below 2^31");
+  // the kernels' sums of KV tiles are 32-bit
+  const int64_t rows = static_cast<int64_t>(s.max_blocks) * s.block_size;
+  if (s.tiles() * (rows / kRows + 2) >= (1ll << 31) || s.tiles() * s.n_kv_heads >= (1ll << 31))
+    return fail(KVC_ERR_UNSUPPORTED, "num_tokens x max_blocks_per_seq x block_size too large");
+  return KVC_OK;
+}
+
+// Workspace: [head][tiles][records' outputs][records' references and sums],
+// each 256-byte aligned. Records only where units are split: where there are too
+// few of them to keep all SMs busy to the end (measured below).
+struct PromptLayout {
+  size_t tiles, rec_o, rec_ml, total;
+  bool split;
+};
+
+constexpr int kWholeUnits = 4;  // units per SM from which none is split
+
+inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+PromptLayout layout(const PromptShape& s, int num_sms) {
+  PromptLayout l;
+  const int64_t units = (s.num_tokens + 2 * s.tokens() - 1) / (2 * s.tokens()) * s.n_kv_heads;
+  l.split = units < static_cast<int64_t>(kWholeUnits) * num_sms;
+  l.tiles = 256;
+  l.rec_o = l.tiles + up256(static_cast<size_t>(s.tiles()) * sizeof(Tile));
+  const size_t recs = l.split ? 2 * static_cast<size_t>(num_sms) * 2 * kM : 0;
+  l.rec_ml = l.rec_o + up256(recs * s.D * 4);
+  l.total = l.rec_ml + up256(recs * 8);
+  return l;
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled_fn() {
+  static std::once_flag once;
+  static EncodeTiledFn fn = nullptr;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  });
+  return fn;
+}
+
+// A map of 16-bit elements with 128-byte swizzled boxes, 64 elements wide. (The
+// elements are only moved: one type serves bf16 and f16.)
+kvc_status make_map(const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                    const cuuint32_t* box, CUtensorMap* map) {
+  EncodeTiledFn encode = encode_tiled_fn();
+  if (encode == nullptr) return fail(KVC_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint32_t es[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(base), dims, strides, box, es,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(KVC_ERR_CUDA, "tensor map: CUresult %d", static_cast<int>(r));
+  return KVC_OK;
+}
+
+template <typename CT, int D>
+kvc_status launch(const PromptParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                  cudaStream_t stream) {
+  auto* kernel = prompt_kernel<CT, D>;
+  // The opt-in to large shared memory holds per device: made at the first call on each.
+  static std::atomic<uint64_t> opted{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if ((opted.load() & bit) == 0) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(PromptGeo<D>::kBytes));
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(prompt)");
+    opted.fetch_or(bit);
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kPlanThreads);
+  e = cudaLaunchKernelEx(&cfg, prompt_plan_kernel, p, static_cast<int>(sizeof(CT)), D);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx(prompt plan)");
+  cfg.gridDim = dim3(static_cast<unsigned>(p.grid));
+  cfg.blockDim = dim3(kPromptThreads);
+  cfg.dynamicSmemBytes = PromptGeo<D>::kBytes;
+  e = cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, p);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx(prompt)");
+  if (p.split) {
+    cfg.gridDim = dim3(static_cast<unsigned>(p.max_tiles) * p.row.n_kv_heads, 2 * kM / kMergeRows);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, prompt_merge_kernel<CT, D>, p);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx(prompt merge)");
+  }
   return KVC_OK;
 }
 
@@ -124,7 +1005,8 @@ kvc_status kvc_prompt_workspace_size(int batch, int64_t num_tokens, int n_q_head
   DeviceInfo* dev = nullptr;
   const kvc_status sd = current_device(&dev);
   if (sd != KVC_OK) return sd;
-  *bytes = 256;
+  *bytes = layout({batch, num_tokens, n_q_heads, n_kv_heads, head_dim, block_size, max_blocks_per_seq},
+                  dev->num_sms).total;
   return KVC_OK;
 }
 
@@ -136,7 +1018,8 @@ kvc_status kvc_prompt_attention(const void* q, const void* k_cache, const void* 
                                 kvc_stream stream) {
   using namespace kvc;
   clear_error();
-  kvc_status st = check_shape({batch, num_tokens, n_q_heads, n_kv_heads, head_dim, block_size, max_blocks_per_seq});
+  const PromptShape shape{batch, num_tokens, n_q_heads, n_kv_heads, head_dim, block_size, max_blocks_per_seq};
+  kvc_status st = check_shape(shape);
   if (st != KVC_OK) return st;
   if (!dtype_ok(dtype)) return fail(KVC_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(dtype));
   if (dtype == KVC_F32) return fail(KVC_ERR_UNSUPPORTED, "16-bit elements only (F16, BF16)");
@@ -152,37 +1035,67 @@ kvc_status kvc_prompt_attention(const void* q, const void* k_cache, const void* 
     return fail(KVC_ERR_INVALID_ARG, "q, out, k_cache and v_cache must be 16-byte aligned");
   DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev)) != KVC_OK) return st;
-  size_t needed = 0;
-  if ((st = kvc_prompt_workspace_size(batch, num_tokens, n_q_heads, n_kv_heads, head_dim, block_size,
-                                      max_blocks_per_seq, &needed)) != KVC_OK)
-    return st;
+  const PromptLayout l = layout(shape, dev->num_sms);
+  const size_t needed = l.total;
   if (workspace == nullptr || workspace_bytes < needed)
     return fail(KVC_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace == nullptr ? 0 : workspace_bytes,
                 needed);
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(KVC_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  char* ws = static_cast<char*>(workspace);
   PromptParams p{};
-  p.row = {k_cache, v_cache, nullptr, nullptr, num_blocks, n_kv_heads, block_size, window, sinks,
-           scale * 1.4426950408889634f};
+  // positions are below 2^30: larger windows are all rows, and differences of them stay in 32 bits
+  p.row = {k_cache, v_cache, nullptr, nullptr, num_blocks, n_kv_heads, block_size, std::min(window, 1 << 30),
+           std::min(sinks, 1 << 30), scale * 1.4426950408889634f};
   p.q = q;
   p.out = out;
   p.block_tables = block_tables;
   p.query_starts = query_starts;
   p.context_lens = context_lens;
+  p.head = reinterpret_cast<int*>(ws);
+  p.tiles = reinterpret_cast<Tile*>(ws + l.tiles);
+  p.rec_o = reinterpret_cast<float*>(ws + l.rec_o);
+  p.rec_ml = reinterpret_cast<float*>(ws + l.rec_ml);
   p.err = dev->error_word;
   p.batch = batch;
   p.num_tokens = static_cast<int>(num_tokens);
   p.n_q_heads = n_q_heads;
-  p.group = n_q_heads / n_kv_heads;
+  p.group = shape.group();
   p.max_blocks = max_blocks_per_seq;
   p.rows = max_blocks_per_seq * block_size;
-  const unsigned grid = static_cast<unsigned>((num_tokens * n_q_heads + 7) / 8);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  auto* kernel = dtype == KVC_F16 ? (head_dim == 64 ? prompt_rows_kernel<__half, 64> : prompt_rows_kernel<__half, 128>)
-                                  : (head_dim == 64 ? prompt_rows_kernel<__nv_bfloat16, 64>
-                                                    : prompt_rows_kernel<__nv_bfloat16, 128>);
-  kernel<<<grid, 256, 0, s>>>(p);
-  return finish_call(s);
+  p.tokens = shape.tokens();
+  p.max_tiles = static_cast<int>(shape.tiles());
+  p.split = l.split ? 1 : 0;
+  const int64_t cap = option(KVC_OPT_MAX_CTAS);
+  p.grid = static_cast<int>(cap > 0 ? std::min<int64_t>(cap, dev->num_sms) : dev->num_sms);
+  p.box = std::gcd(block_size, kRows);
+  while ((1 << p.box_log2) < p.box) ++p.box_log2;
+  p.pool_rows = static_cast<int>(num_blocks * n_kv_heads * block_size);
+  // hidden scores are -infinity, which a factor of 0 would turn into NaN
+  p.qscale = std::max(std::fabs(p.row.qscale), 1e-35f);
+  p.negative = scale < 0.f ? 1 : 0;
+  CUtensorMap tq, tk, tv;
+  const cuuint64_t d = static_cast<cuuint64_t>(head_dim);
+  {
+    const cuuint64_t dims[3] = {d, static_cast<cuuint64_t>(n_q_heads), static_cast<cuuint64_t>(num_tokens)};
+    const cuuint64_t strides[2] = {d * 2, d * 2 * n_q_heads};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(p.tokens)};
+    if ((st = make_map(q, 3, dims, strides, box, &tq)) != KVC_OK) return st;
+  }
+  {
+    const cuuint64_t dims[2] = {d, static_cast<cuuint64_t>(p.pool_rows)};
+    const cuuint64_t strides[1] = {d * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(p.box)};
+    if ((st = make_map(k_cache, 2, dims, strides, box, &tk)) != KVC_OK) return st;
+    if ((st = make_map(v_cache, 2, dims, strides, box, &tv)) != KVC_OK) return st;
+  }
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (dtype == KVC_F16)
+    st = head_dim == 64 ? launch<__half, 64>(p, tq, tk, tv, cs) : launch<__half, 128>(p, tq, tk, tv, cs);
+  else
+    st = head_dim == 64 ? launch<__nv_bfloat16, 64>(p, tq, tk, tv, cs) : launch<__nv_bfloat16, 128>(p, tq, tk, tv, cs);
+  if (st != KVC_OK) return st;
+  return finish_call(cs);
 }
 
 }  // extern "C"

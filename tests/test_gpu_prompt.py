@@ -30,6 +30,9 @@ CASES = [
     ([130, 64], [1300, 500], 3, 1, 128, 32, 128, 256),
     ([520], [3000], 4, 1, 128, 96, 700, 21),
     ([260, 1], [260, 1000], 5, 1, 64, 112, 1000, 300),
+    # many units: dealt out whole, sorted by cost
+    ([200, 57, 0, 60], [200, 300, 7, 190], 512, 8, 64, 16, None, 0),
+    ([9] * 50 + [1] * 30, [9] * 50 + [40] * 30, 64, 8, 128, 32, 20, 3),
 ]
 
 
