@@ -15,10 +15,10 @@
 // tokens. Both products run on tcgen05.mma, 128 x 128 x D each:
 //   S = Q K^T       Q and K from shared memory, S in TMEM
 //   O += P V        P from TMEM (where S was, 16 bits), V read MN-major
-// The two halves of a unit take turns: while one's softmax runs on its four
-// warps (one thread per row, no shuffles), the tensor core has the other's
-// products. Warp 0 copies pages by TMA (boxes of gcd(block_size, 128) rows) into a
-// ring of K and V tiles, one thread of warp 1 issues the products.
+// The two halves of a unit take turns: while one's softmax runs on its eight
+// warps (two threads per row, no shuffles), the tensor core has the other's
+// products. One warp copies pages by TMA (boxes of gcd(block_size, 128) rows) into
+// a ring of K and V tiles, one thread of another issues the products.
 //
 // P in 16 bits: its rounding (2^-8 of a weight in bf16, 2^-11 in f16) is of the
 // size of the output's own, and a second product for the rest would cost half
@@ -59,7 +59,9 @@ using namespace umma;
 constexpr int kPromptMaxBatch = 4096;
 constexpr int kM = 128;            // query rows of a half (M of the products)
 constexpr int kRows = 128;         // cached rows of a tile
-constexpr int kPromptThreads = 384;
+constexpr int kSoftWarps = 16;      // softmax warps: [half][column group][TMEM quarter]
+constexpr int kCols = kRows / 2;    // columns of S that a softmax thread has
+constexpr int kPromptThreads = (kSoftWarps + 4) * 32;  // one warpgroup more: copies, products, two idle warps
 constexpr int kMinTiles = 4;       // KV tiles of a range at least, where units are split
 constexpr int kBadRing = 8;        // tiles whose bad blocks are remembered: more than the ring holds
 
@@ -279,15 +281,16 @@ static_assert(kBuckets == kPlanThreads, "one class per thread");
 
 // The equal ranges of split units: range x is [start(x), start(x + 1)) of N positions.
 struct Ranges {
-  int64_t N;
-  int W;
+  int N, W;  // N < 2^31: checked on the host
   __device__ __forceinline__ Ranges(int n_tiles, int total, int heads, int grid) {
-    N = static_cast<int64_t>(total) * heads;
-    const int64_t units = static_cast<int64_t>(n_tiles) * heads;
-    W = static_cast<int>(min(static_cast<int64_t>(grid), max(units, (N + kMinTiles - 1) / kMinTiles)));
+    N = total * heads;
+    W = min(grid, max(n_tiles * heads, N / kMinTiles + 1));
+    W = min(W, N);
   }
-  __device__ __forceinline__ int64_t start(int64_t x) const { return x * N / W; }
-  __device__ __forceinline__ int holder(int64_t pos) const { return static_cast<int>(((pos + 1) * W - 1) / N); }
+  __device__ __forceinline__ int start(int x) const { return static_cast<int>(static_cast<int64_t>(x) * N / W); }
+  __device__ __forceinline__ int holder(int pos) const {
+    return static_cast<int>((static_cast<int64_t>(pos + 1) * W - 1) / N);
+  }
 };
 
 // A unit (tile, kv head) or the part of it in this CTA's range: KV tiles [i0, i1).
@@ -298,8 +301,7 @@ struct Part {
 };
 
 struct Walk {
-  int n, round;
-  int64_t lo, hi, pos;
+  int n, round, lo, hi, pos;
   __device__ __forceinline__ Walk(const PromptParams& p) {
     n = __ldcg(p.head);  // (L2: the planning kernel may have run beside this one's start)
     round = 0;
@@ -325,12 +327,11 @@ struct Walk {
     const int H = p.row.n_kv_heads;
     if (!p.split) {
       // dealt out there and back, so that nobody always gets the larger one
-      const int64_t i = static_cast<int64_t>(round) * p.grid +
-                        ((round & 1) ? p.grid - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
+      const int i = round * p.grid + ((round & 1) ? p.grid - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
       ++round;
-      if (i >= static_cast<int64_t>(n) * H) return false;
-      u.t = load(p, static_cast<int>(i / H));
-      u.kvh = static_cast<int>(i % H);
+      if (i >= n * H) return false;
+      u.t = load(p, i / H);
+      u.kvh = i % H;
       u.i0 = 0;
       u.i1 = u.t.cost;
       u.rec = -1;
@@ -340,13 +341,13 @@ struct Walk {
     int a = 0, b = n - 1;  // the last tile that begins at or before pos
     while (a < b) {
       const int mid = (a + b + 1) >> 1;
-      if (static_cast<int64_t>(H) * __ldcg(&p.tiles[mid].before) <= pos) a = mid; else b = mid - 1;
+      if (H * __ldcg(&p.tiles[mid].before) <= pos) a = mid; else b = mid - 1;
     }
     u.t = load(p, a);
-    const int rest = static_cast<int>(pos - static_cast<int64_t>(H) * u.t.before);
+    const int rest = pos - H * u.t.before;
     u.kvh = rest / u.t.cost;
     u.i0 = rest - u.kvh * u.t.cost;
-    u.i1 = static_cast<int>(min(static_cast<int64_t>(u.t.cost), u.i0 + (hi - pos)));
+    u.i1 = min(u.t.cost, u.i0 + (hi - pos));
     u.rec = u.i0 == 0 && u.i1 == u.t.cost ? -1 : 2 * static_cast<int>(blockIdx.x) + (pos == lo ? 0 : 1);
     pos += u.i1 - u.i0;
     return true;
@@ -360,19 +361,34 @@ struct PromptGeo {
   static constexpr int kHalves = D / 64;                  // 128-byte wide parts of a row
   static constexpr uint32_t kPart = kRows * 128;          // one part of a tile
   static constexpr uint32_t kTile = kHalves * kPart;      // a K or V tile, or a half's queries
+  // Queries lie part by part; K and V tiles in groups of 8 rows, [group][part][8
+  // rows][128 bytes], so that one copy brings all parts of a page: of 16-row
+  // pages a tile needs 8 copies, and issuing twice as many cost 20 % (16384 rows).
+  static constexpr uint32_t kRowGroup = kHalves * 1024;
   static constexpr int kSlots = D == 128 ? 5 : 8;         // K and V tiles in the ring
   static constexpr uint32_t kOffRing = 2 * kTile;         // behind both halves' queries
   static constexpr uint32_t kOffBar = kOffRing + kSlots * kTile;
   enum {
     QFULL = 0, QEMPTY, FULL0, EMPTY0 = FULL0 + kSlots, SFULL0 = EMPTY0 + kSlots, PFULL0 = SFULL0 + 2,
-    OFULL0 = PFULL0 + 2, OEMPTY0 = OFULL0 + 2, FINAL = OEMPTY0 + 2, COUNT
+    OFULL0 = PFULL0 + 4, OEMPTY0 = OFULL0 + 2, FINAL = OEMPTY0 + 2, COUNT
   };
   static constexpr uint32_t kOffMisc = kOffBar + COUNT * 8;  // TMEM address, abort flag, bad blocks
-  static constexpr uint32_t kBytes = kOffMisc + 8 + kBadRing * 4 + 1024;
+  static constexpr uint32_t kOffPart = kOffMisc + 8 + kBadRing * 4;  // what the threads of a row tell each other
+  static constexpr uint32_t kOffFail = kOffPart + kSoftWarps * 32 * 4;
+  static constexpr uint32_t kBytes = kOffFail + kSoftWarps * 4;
+  static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
   // TMEM columns: S (P over it) of both halves, O of both
   static constexpr uint32_t kColO = 256;
   static constexpr uint32_t kTmemCols = 512;
 };
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], "
+      "[%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(w), "r"(bar)
+      : "memory");
+}
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
@@ -409,6 +425,35 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return r;
 }
 
+// True in one thread of the warp. The compiler knows that it is one, which
+// `lane == 0` does not tell it: operands of tcgen05.mma need no loop over the
+// threads then.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
+// Barrier of the two warps that share query rows; pair_or: the OR of a
+// predicate over their 64 threads.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool pair_or(int id, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "bar.red.or.pred q, %1, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(pred ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
 // One output row again, over its visible rows alone (attend_row.cuh). Rare.
 template <typename CT, int D>
 __device__ __noinline__ void redo_row(const PromptParams& p, int seq, int row, int head, int pos) {
@@ -429,10 +474,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   using G = PromptGeo<D>;
   constexpr bool BF = std::is_same<CT, __nv_bfloat16>::value;
   constexpr uint32_t full = 0xffffffffu;
-  extern __shared__ unsigned char smem_raw[];
-  const uint32_t raw = smem_addr(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  unsigned char* sm = smem_raw + (base - raw);
+  extern __shared__ __align__(1024) unsigned char sm[];  // the swizzle counts from multiples of 1024
+  const uint32_t base = smem_addr(sm);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + G::kOffBar);
   volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(sm + G::kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(sm + G::kOffMisc + 4);
@@ -440,10 +483,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   auto bar = [&](int i) -> uint32_t { return base + G::kOffBar + 8u * static_cast<uint32_t>(i); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  if ((base & 1023u) != 0) {  // the alignment above was not kept
+    set_flag(p.err, KVC_FLAG_TIMEOUT);
+    return;
+  }
   if (tid == 0) {
     *s_abort = 0;
     for (int i = 0; i < G::COUNT; ++i)
-      mbar_init(&bars[i], (i >= G::PFULL0 && i < G::OFULL0) || (i >= G::OEMPTY0 && i < G::FINAL) ? 4 : 1);
+      mbar_init(&bars[i], (i >= G::PFULL0 && i < G::OFULL0) || (i >= G::OEMPTY0 && i < G::FINAL) ? 8 : 1);
     fence_barrier_init();
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
@@ -455,7 +502,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       *reinterpret_cast<uint4*>(sm + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
   }
-  if (warp == 1) {
+  if (warp == kSoftWarps + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + G::kOffMisc),
                  "r"(G::kTmemCols)
                  : "memory");
@@ -469,7 +516,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const uint32_t tmem = *s_tmem;
   const int bs = p.row.block_size, window = p.row.window, sinks = p.row.sinks;
 
-  if (warp == 0) {
+#ifdef PR_DOWN
+  if (warp >= kSoftWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PR_DOWN));
+#endif
+  if (warp == kSoftWarps) {
     // ------------------------------------------------------------ producer
     // Lane i has box i of every tile: its table entry is read before the slot is
     // free. One barrier per K or V tile.
@@ -508,7 +558,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int phys = want ? __ldg(table + blk) : -1;
         const bool there = phys >= 0 && phys < p.row.num_blocks;
         const uint32_t bad = __ballot_sync(full, want && !there);
-        const int y = there ? (phys * p.row.n_kv_heads + u.kvh) * bs + (r0 - blk * bs) : p.pool_rows;
+        const int y = (there ? (phys * p.row.n_kv_heads + u.kvh) * bs + (r0 - blk * bs) : p.pool_rows) >> 3;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++kk) {
           const uint32_t slot = kk % G::kSlots;
@@ -528,10 +578,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
           __syncwarp();
           if (lane < boxes) {
-            const uint32_t dst = base + G::kOffRing + slot * G::kTile + static_cast<uint32_t>(lane * p.box) * 128u;
-#pragma unroll
-            for (int x = 0; x < G::kHalves; ++x)
-              tma_load_2d(dst + x * G::kPart, kv == 0 ? &tm_k : &tm_v, 64 * x, y, bar(G::FULL0 + slot));
+            const uint32_t dst = base + G::kOffRing + slot * G::kTile + static_cast<uint32_t>(lane * p.box) * (G::kRowGroup / 8);
+            tma_load_4d(dst, kv == 0 ? &tm_k : &tm_v, y, bar(G::FULL0 + slot));
           }
           ++issued[slot];
         }
@@ -552,11 +600,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
       }
     }
-  } else if (warp == 1) {
+  } else if (warp == kSoftWarps + 1) {
     // ---------------------------------------------------------- MMA issuer
     // Order per KV tile j: PV of half 0 (j), S of half 0 (j + 1), PV of half 1
     // (j), S of half 1 (j + 1). P lies where S was: S (j + 1) follows PV (j).
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t id_s = instr_desc(kM, kRows, 0, 0, BF);
       const uint32_t id_pv = instr_desc(kM, D, 0, 1, BF);
       uint32_t gt = 0, un = 0;        // KV tiles begun, units begun
@@ -568,12 +616,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       auto issue_s = [&](int h, uint32_t g) {
         const uint32_t slot = (2 * g) % G::kSlots;
         const uint64_t a = smem_desc(base + h * G::kTile, 16, 1024, 2);
-        const uint64_t b = smem_desc(base + G::kOffRing + slot * G::kTile, 16, 1024, 2);
+        const uint64_t b = smem_desc(base + G::kOffRing + slot * G::kTile, 16, G::kRowGroup, 2);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint64_t off = ((ks >> 2) * G::kPart + (ks & 3) * 32) >> 4;
-          mma(tmem + h * kRows, a + off, b + off, id_s, ks == 0 ? 0u : 1u);
-        }
+        for (int ks = 0; ks < D / 16; ++ks)
+          mma(tmem + h * kRows, a + (((ks >> 2) * G::kPart + (ks & 3) * 32) >> 4),
+              b + (((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), id_s, ks == 0 ? 0u : 1u);
         commit(bar(G::SFULL0 + h));
       };
       auto full_slot = [&](uint32_t k) {
@@ -592,20 +639,30 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const bool more = j + 1 < J;
           if (!full_slot(2 * gt + 1)) { ok = false; break; }
           const uint32_t vslot = (2 * gt + 1) % G::kSlots;
-          const uint64_t v = smem_desc(base + G::kOffRing + vslot * G::kTile, G::kPart, 1024, 2);
+          const uint64_t v = smem_desc(base + G::kOffRing + vslot * G::kTile, 1024, G::kRowGroup, 2);
           for (int h = 0; h < halves; ++h) {
-            if (!wait_phase(bar(G::PFULL0 + h), np[h] & 1u, s_abort, p.err)) { ok = false; break; }
-            ++np[h];
+            if (!wait_phase(bar(G::PFULL0 + 2 * h), np[h] & 1u, s_abort, p.err)) { ok = false; break; }
             // O of the unit before has been read
             if (j == 0 && nu[h] > 0 && !wait_phase(bar(G::OEMPTY0 + h), (nu[h] - 1) & 1u, s_abort, p.err)) {
               ok = false;
               break;
             }
-            fence_after();
+            // P comes in two parts, 32 columns of each column group at a time
 #pragma unroll
-            for (int ks = 0; ks < kRows / 16; ++ks)
-              mma_ts(tmem + G::kColO + h * D, tmem + h * kRows + ks * 8, v + ((ks * 2048) >> 4), id_pv,
-                     j == 0 && ks == 0 ? 0u : 1u);
+            for (int part = 0; part < 2; ++part) {
+              if (part == 1) {
+                if (!wait_phase(bar(G::PFULL0 + 2 * h + 1), np[h] & 1u, s_abort, p.err)) { ok = false; break; }
+              }
+              fence_after();
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int ks = (k >> 1) * 4 + part * 2 + (k & 1);
+                mma_ts(tmem + G::kColO + h * D, tmem + h * kRows + ks * 8, v + ((ks * 2 * G::kRowGroup) >> 4), id_pv,
+                       j == 0 && part == 0 && k == 0 ? 0u : 1u);
+              }
+            }
+            if (!ok) break;
+            ++np[h];
             if (!more) commit(bar(G::OFULL0 + h));
             if (h == halves - 1) commit(bar(G::EMPTY0 + vslot));
             if (more) {
@@ -630,19 +687,42 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       while (!try_wait(bar(G::FINAL), 0) && globaltimer_ns() - t0 < kWaitNs) {
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp < kSoftWarps) {
+#ifdef PR_UP
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PR_UP));
+#endif
     // --------------------------------------------------- softmax, epilogue
-    // Thread = query row (TMEM lane) of half hf.
-    const int hf = (warp - 4) >> 2;
-    const int r = (tid - 128) & 127;
+    // Two threads per query row (TMEM lane) of half hf: column group cg has
+    // columns 64 cg .. of S and half the columns of O. The two warps of a row
+    // meet at a barrier per tile, which also says whether the reference has to
+    // move (or one of them gave up).
+    const int hf = warp >> 3, cg = (warp >> 2) & 1;
+    const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t col_s = lane_addr + hf * kRows, col_o = lane_addr + G::kColO + hf * D;
+    const uint32_t col_s = lane_addr + hf * kRows + cg * kCols;       // S
+    const uint32_t col_p = lane_addr + hf * kRows + cg * (kCols / 2);  // P
+    constexpr int OC = D / 2;
+    const uint32_t col_o = lane_addr + G::kColO + hf * D + cg * OC;
+    float* s_part = reinterpret_cast<float*>(sm + G::kOffPart);
+    volatile int* s_fail = reinterpret_cast<volatile int*>(sm + G::kOffFail);
+    const int mine = warp * 32 + lane, other = mine ^ 128;  // the row's other thread
+    const int pair = 1 + hf * 4 + (warp & 3);                // barrier of the two warps
     const int tk = r / p.group;  // token of the half
     constexpr float BELOW = PromptMargin<BF>::kBelow, ABOVE = PromptMargin<BF>::kAbove;
     const float qs = p.qscale;
     // a warp goes on or gives up as one
     auto wait_warp = [&](uint32_t b, uint32_t parity) {
       return __all_sync(full, wait_phase_suspend(b, parity, s_abort, p.err));
+    };
+    // The row's other thread's x; ok: of both warps.
+    auto exchange = [&](float x, bool& ok) {
+      s_part[mine] = x;
+      if (lane == 0) s_fail[warp] = ok ? 0 : 1;
+      pair_sync(pair);
+      const float y = s_part[other];
+      ok = ok && s_fail[warp ^ 4] == 0;
+      pair_sync(pair);
+      return y;
     };
     uint32_t gt = 0, n = 0, nu = 0;  // the CTA's KV tiles; tiles and units of this half
     bool ok = true;
@@ -654,117 +734,140 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         gt += J;
         continue;
       }
-      const Seen seen = seen_tiles(u.t.pos, u.t.count, window, sinks);
-      const int end = u.t.pos + u.t.count - 1;  // last position of the unit
-      const int low = u.t.pos >= window ? u.t.pos - window + 1 : 0;
-      const int first = u.t.pos + hf * p.tokens;       // positions of the half
-      const int last = min(end, first + p.tokens - 1);
+      const int first = u.t.pos + hf * p.tokens;  // positions of the half
+      const int last = min(u.t.pos + u.t.count, first + p.tokens) - 1;
       const bool valid = tk < p.tokens && first + tk <= last;
       const int pos = min(first + tk, last);
+      // Tiles [f0, f1) lie in every row's window and behind no row: not masked
+      int f0, f1;
+      {
+        const Seen seen = seen_tiles(u.t.pos, u.t.count, window, sinks);
+        const int open = last >= window ? (last - window) / kRows + 1 : 0;
+        f0 = seen.front + max(0, open - seen.start);
+        f1 = seen.front + (first + 1) / kRows - seen.start;
+      }
       float m = -1e30f, l = 0.f;  // finite: a row may meet only hidden columns
-      for (int j = 0; j < J; ++j, ++gt, ++n) {
-        const int i = u.i0 + j;
-        const int r0 = (i < seen.front ? i : i - seen.front + seen.start) * kRows;
-        if (!wait_warp(bar(G::SFULL0 + hf), n & 1u)) {
-          ok = false;
-          break;
-        }
+      for (int i = u.i0; i < u.i1; ++i, ++gt, ++n) {
+        ok = wait_warp(bar(G::SFULL0 + hf), n & 1u);
         fence_after();
-        float s[kRows];
-        tmem_ld128(col_s, s);
         const uint32_t bad = s_bad[gt % kBadRing];
+        float s[kCols];
+        tmem_ld64(col_s, s);
         if (p.negative) {
 #pragma unroll
-          for (int c = 0; c < kRows; ++c) s[c] = -s[c];
+          for (int c = 0; c < kCols; ++c) s[c] = -s[c];
         }
-        if (r0 + kRows - 1 > first || (r0 <= last - window && r0 + kRows > sinks) || bad != 0) {
-          const int hi = pos - r0, lw = pos - window - r0, sk = sinks - r0;
+        if (i < f0 || i >= f1 || bad != 0) {
+          const Seen seen = seen_tiles(u.t.pos, u.t.count, window, sinks);
+          const int r0 = (i < seen.front ? i : i - seen.front + seen.start) * kRows;
+          const int c0 = r0 + cg * kCols;  // row of the first column
+          const int hi = pos - c0, lw = pos - window - c0, sk = sinks - c0;
 #pragma unroll
-          for (int c = 0; c < kRows; ++c)
+          for (int c = 0; c < kCols; ++c)
             if (c > hi || (c <= lw && c >= sk)) s[c] = -__builtin_huge_valf();
           if (bad != 0) {
 #pragma unroll
-            for (int c = 0; c < kRows; ++c)
-              if ((bad >> (c >> p.box_log2)) & 1u) s[c] = -__builtin_huge_valf();
+            for (int c = 0; c < kCols; ++c)
+              if ((bad >> ((cg * kCols + c) >> p.box_log2)) & 1u) s[c] = -__builtin_huge_valf();
           }
           // V rows that nobody in the unit sees may hold anything, and 0 x NaN is
           // NaN: half 0 clears them (its products come first).
+          const int end = u.t.pos + u.t.count - 1;
+          const int low = u.t.pos >= window ? u.t.pos - window + 1 : 0;
           if (hf == 0 && (r0 + kRows - 1 > end || (r0 < low && r0 + kRows > sinks))) {
             const uint32_t k = 2 * gt + 1, slot = k % G::kSlots;
-            if (!wait_warp(bar(G::FULL0 + slot), (k / G::kSlots) & 1u)) {
-              ok = false;
-              break;
-            }
+            ok = ok && wait_warp(bar(G::FULL0 + slot), (k / G::kSlots) & 1u);
             const int row = r0 + r;
-            if (row > end || (row < low && row >= sinks)) {
-              unsigned char* v = sm + G::kOffRing + slot * G::kTile + r * 128;
+            if (ok && (row > end || (row < low && row >= sinks))) {
+              unsigned char* v = sm + G::kOffRing + slot * G::kTile + (r >> 3) * G::kRowGroup + (r & 7) * 128;
+              constexpr int CH = G::kHalves * 4;  // 16-byte chunks of a thread
 #pragma unroll
-              for (int x = 0; x < G::kHalves; ++x)
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                  *reinterpret_cast<uint4*>(v + x * G::kPart + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+              for (int c = 0; c < CH; ++c) {
+                const int ch = cg * CH + c;
+                *reinterpret_cast<uint4*>(v + (ch >> 3) * 1024 + 16 * (ch & 7)) = make_uint4(0u, 0u, 0u, 0u);
+              }
             }
             fence_proxy_async_smem();
           }
         }
-        float mx = max3(s[0], s[1], s[2]), mx2 = max3(s[3], s[4], s[5]);
+        float mx[4];
 #pragma unroll
-        for (int c = 6; c < 126; c += 4) {
-          mx = max3(mx, s[c], s[c + 1]);
-          mx2 = max3(mx2, s[c + 2], s[c + 3]);
+        for (int c = 0; c < 4; ++c) mx[c] = max3(s[c], s[c + 4], s[c + 8]);
+#pragma unroll
+        for (int c = 12; c < 60; c += 8) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[c + k], s[c + 4 + k]);
         }
-        mx = max3(mx, s[126], s[127]);
-        mx = fmaxf(mx, mx2) * qs;
-        if (__any_sync(full, valid && mx > m + ABOVE)) {
-          const float to = fmaxf(m, mx - BELOW);
-          const float f = fast_exp2(m - to);
-          l *= f;
-          m = to;
-          if (j > 0) {  // PV of the tile before is done: S came behind it
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float o[32];
-              tmem_ld32(col_o + c, o);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] *= f;
-              tmem_st32_async(col_o + c, reinterpret_cast<const uint32_t*>(o));
-            }
-            tmem_wait_st();
-          }
-        }
-        const float2 q2 = make_float2(qs, qs), m2 = make_float2(-m, -m);
-        float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int c = 0; c < kRows; c += 32) {
-          uint32_t w[16];
+        mx[0] = max3(mx[0], s[60], s[61]);
+        mx[1] = max3(mx[1], s[62], s[63]);
+        float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * qs;
+        // The first half of the weights does not wait for the vote: it nearly
+        // always leaves the reference where it was.
+        uint32_t w[16];
+        float2 sum[2];
+        auto weigh = [&](int c) {
+          const float2 q2 = make_float2(qs, qs), m2 = make_float2(-m, -m);
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const float2 x = ffma2(make_float2(s[c + 2 * k], s[c + 2 * k + 1]), q2, m2);
             const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-            sum = fadd2(sum, e);
+            sum[k & 1] = fadd2(sum[k & 1], e);
             w[k] = pack16<BF>(e.x, e.y);
           }
-          tmem_st16_async(col_s + c / 2, w);
+        };
+        sum[0] = sum[1] = make_float2(0.f, 0.f);
+        weigh(0);
+        fence_before();  // both warps have read S before either writes P
+        if (pair_or(pair, !ok || (valid && top > m + ABOVE))) {
+          top = fmaxf(top, exchange(top, ok));
+          if (!ok) break;
+          const float to = fmaxf(m, top - BELOW);
+          const float f = fast_exp2(m - to);
+          l *= f;
+          m = to;
+          if (i > u.i0) {  // PV of the tile before is done: S came behind it
+#pragma unroll 1
+            for (int c = 0; c < OC; c += 16) {
+              float o[16];
+              tmem_ld16(col_o + c, o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] *= f;
+              tmem_st16_async(col_o + c, reinterpret_cast<const uint32_t*>(o));
+            }
+          }
+          sum[0] = sum[1] = make_float2(0.f, 0.f);
+          weigh(0);
         }
-        l += sum.x + sum.y;
+        fence_after();
+        tmem_st16_async(col_p, w);
         tmem_wait_st();
         fence_before();
         __syncwarp();
-        if (lane == 0) arrive(bar(G::PFULL0 + hf));
+        if (lane == 0) arrive(bar(G::PFULL0 + 2 * hf));
+        weigh(32);
+        tmem_st16_async(col_p + 16, w);
+        sum[0] = fadd2(sum[0], sum[1]);
+        l += sum[0].x + sum[0].y;
+        tmem_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(bar(G::PFULL0 + 2 * hf + 1));
       }
-      if (!ok) break;
       // ---- epilogue
-      if (!wait_warp(bar(G::OFULL0 + hf), nu & 1u)) break;
+      if (!ok) break;  // both warps of a row
+      ok = wait_warp(bar(G::OFULL0 + hf), nu & 1u);
+      l += exchange(l, ok);
+      if (!ok) break;
       ++nu;
       fence_after();
       const int head = u.kvh * p.group + r - tk * p.group;
       const int row = u.t.first + hf * p.tokens + tk;
-      const int64_t at = (static_cast<int64_t>(row) * p.n_q_heads + head) * D;
-      float* rec = u.rec < 0 ? nullptr : p.rec_o + (static_cast<int64_t>(u.rec) * 2 * kM + hf * kM + r) * D;
+      const int64_t at = (static_cast<int64_t>(row) * p.n_q_heads + head) * D + cg * OC;
+      float* rec = u.rec < 0 ? nullptr : p.rec_o + (static_cast<int64_t>(u.rec) * 2 * kM + hf * kM + r) * D + cg * OC;
       const float inv = u.rec >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
       float zero = 0.f;  // NaN if an output is not finite
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = 0; c < OC; c += 32) {
         float o[32];
         tmem_ld32(col_o + c, o);
         if (!valid) continue;
@@ -790,10 +893,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       __syncwarp();
       if (lane == 0) arrive(bar(G::OEMPTY0 + hf));
       if (rec != nullptr) {
-        if (valid)
+        if (valid && cg == 0)
           *reinterpret_cast<float2*>(p.rec_ml + (static_cast<int64_t>(u.rec) * 2 * kM + hf * kM + r) * 2) =
               make_float2(m, l);
       } else {
+        // rows done again whole, by either warp of the row or by both (the same values)
         for (uint32_t odd = __ballot_sync(full, valid && zero != 0.f); odd != 0; odd &= odd - 1) {
           const int src = __ffs(odd) - 1;
           redo_row<CT, D>(p, u.t.seq, __shfl_sync(full, row, src), __shfl_sync(full, head, src),
@@ -806,7 +910,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 1)
+  if (warp == kSoftWarps + 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(G::kTmemCols) : "memory");
 }
 
@@ -825,7 +929,7 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptParams p)
   if (i >= n) return;
   const Ranges r(n, __ldcg(p.head + 1), H, p.grid);
   const Tile t = Walk::load(p, i);
-  const int64_t u0 = static_cast<int64_t>(H) * t.before + static_cast<int64_t>(kvh) * t.cost;
+  const int u0 = H * t.before + kvh * t.cost;
   const int a = r.holder(u0), b = r.holder(u0 + t.cost - 1);
   if (a == b) return;
   const int lane = threadIdx.x & 31;
@@ -886,7 +990,7 @@ kvc_status check_shape(const PromptShape& s) {
     return fail(KVC_ERR_UNSUPPORTED, "num_tokens x n_q_heads must be below 2^31");
   // the kernels' sums of KV tiles are 32-bit
   const int64_t rows = static_cast<int64_t>(s.max_blocks) * s.block_size;
-  if (s.tiles() * (rows / kRows + 2) >= (1ll << 31) || s.tiles() * s.n_kv_heads >= (1ll << 31))
+  if (s.tiles() >= (1ll << 31) / s.n_kv_heads / (rows / kRows + 2))
     return fail(KVC_ERR_UNSUPPORTED, "num_tokens x max_blocks_per_seq x block_size too large");
   return KVC_OK;
 }
@@ -939,7 +1043,7 @@ kvc_status make_map(const void* base, int rank, const cuuint64_t* dims, const cu
                     const cuuint32_t* box, CUtensorMap* map) {
   EncodeTiledFn encode = encode_tiled_fn();
   if (encode == nullptr) return fail(KVC_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
-  const cuuint32_t es[3] = {1, 1, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
   const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(base), dims, strides, box, es,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1083,11 +1187,12 @@ kvc_status kvc_prompt_attention(const void* q, const void* k_cache, const void* 
     if ((st = make_map(q, 3, dims, strides, box, &tq)) != KVC_OK) return st;
   }
   {
-    const cuuint64_t dims[2] = {d, static_cast<cuuint64_t>(p.pool_rows)};
-    const cuuint64_t strides[1] = {d * 2};
-    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(p.box)};
-    if ((st = make_map(k_cache, 2, dims, strides, box, &tk)) != KVC_OK) return st;
-    if ((st = make_map(v_cache, 2, dims, strides, box, &tv)) != KVC_OK) return st;
+    // [8-row group][part][row of the group][64 elements]
+    const cuuint64_t dims[4] = {64, 8, d / 64, static_cast<cuuint64_t>(p.pool_rows / 8)};
+    const cuuint64_t strides[3] = {d * 2, 128, d * 16};
+    const cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(head_dim / 64), static_cast<cuuint32_t>(p.box / 8)};
+    if ((st = make_map(k_cache, 4, dims, strides, box, &tk)) != KVC_OK) return st;
+    if ((st = make_map(v_cache, 4, dims, strides, box, &tv)) != KVC_OK) return st;
   }
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (dtype == KVC_F16)
