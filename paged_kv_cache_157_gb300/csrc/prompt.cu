@@ -76,8 +76,9 @@ struct PromptShape {
 
 // A token range of one sequence: at most 2 * tokens() new tokens.
 struct Tile {
-  int seq, first, count, cost;  // first: its first row of q; cost: KV tiles that it sees
-  int pos, before, pad0, pad1;  // position of its first token; KV tiles of the tiles before it
+  int first, pos;            // its first row of q and that token's position
+  unsigned short seq, count;
+  int cost;                  // KV tiles that it sees
 };
 
 struct PromptParams {
@@ -90,6 +91,7 @@ struct PromptParams {
   // workspace
   int* head;     // number of tiles, their total cost
   Tile* tiles;
+  int* before;   // KV tiles of the tiles before each (where units are split)
   float* rec_o;  // [2 * CTAs, 2 * kM, D] unnormalised partial outputs
   float* rec_ml; // [2 * CTAs, 2 * kM, 2] (reference, sum of weights)
   unsigned int* err;
@@ -229,12 +231,11 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
     const Span s = span_of(p, a, false);
     Tile t;
     const int t0 = (i - s_first[a]) * per_tile;
-    t.seq = a;
+    t.seq = static_cast<unsigned short>(a);
     t.first = s.first + t0;
-    t.count = min(per_tile, s.count - t0);
+    t.count = static_cast<unsigned short>(min(per_tile, s.count - t0));
     t.pos = s.rows - s.count + t0;
     t.cost = seen_tiles(t.pos, t.count, p.row.window, p.row.sinks).total;
-    t.before = t.pad0 = t.pad1 = 0;
     return t;
   };
   int total = 0;
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
       int sum = 0;
       const int before = block_scan(t.cost, s_warp, &sum);
       if (i0 + tid < n) {
-        t.before = total + before;
+        p.before[i0 + tid] = total + before;
         p.tiles[i0 + tid] = t;
       }
       total += sum;
@@ -301,55 +302,65 @@ struct Part {
 };
 
 struct Walk {
-  int n, round, lo, hi, pos;
+  int n, at, hi, lo;  // whole units: `at` the next round; split ones: the next position of [lo, hi)
+  Tile ahead;         // of the next unit: loaded while this one is worked on
+  __device__ __forceinline__ static Tile load(const PromptParams& p, int i) {
+    union {
+      int4 v;
+      Tile t;
+    } u;
+    u.v = __ldcg(reinterpret_cast<const int4*>(p.tiles + i));
+    return u.t;
+  }
+  // Unit of round r, dealt out there and back, so that nobody always gets the larger one.
+  __device__ __forceinline__ static int unit(const PromptParams& p, int r) {
+    const int c = static_cast<int>(blockIdx.x);
+    return r * p.grid + ((r & 1) ? p.grid - 1 - c : c);
+  }
+  __device__ __forceinline__ void prefetch(const PromptParams& p) {
+    const int i = unit(p, at);
+    if (i < n * p.row.n_kv_heads) ahead = load(p, i / p.row.n_kv_heads);
+  }
   __device__ __forceinline__ Walk(const PromptParams& p) {
     n = __ldcg(p.head);  // (L2: the planning kernel may have run beside this one's start)
-    round = 0;
-    lo = hi = pos = 0;
-    if (p.split && n > 0) {
+    at = lo = hi = 0;
+    if (!p.split) {
+      prefetch(p);
+    } else if (n > 0) {
       const Ranges r(n, __ldcg(p.head + 1), p.row.n_kv_heads, p.grid);
       if (static_cast<int>(blockIdx.x) < r.W) {
-        lo = pos = r.start(blockIdx.x);
+        lo = at = r.start(blockIdx.x);
         hi = r.start(blockIdx.x + 1);
       }
     }
   }
-  __device__ __forceinline__ static Tile load(const PromptParams& p, int i) {
-    union {
-      int4 v[2];
-      Tile t;
-    } u;
-    u.v[0] = __ldcg(reinterpret_cast<const int4*>(p.tiles + i));
-    u.v[1] = __ldcg(reinterpret_cast<const int4*>(p.tiles + i) + 1);
-    return u.t;
-  }
   __device__ __forceinline__ bool next(const PromptParams& p, Part& u) {
     const int H = p.row.n_kv_heads;
     if (!p.split) {
-      // dealt out there and back, so that nobody always gets the larger one
-      const int i = round * p.grid + ((round & 1) ? p.grid - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
-      ++round;
+      const int i = unit(p, at);
       if (i >= n * H) return false;
-      u.t = load(p, i / H);
+      u.t = ahead;
       u.kvh = i % H;
       u.i0 = 0;
       u.i1 = u.t.cost;
       u.rec = -1;
+      ++at;
+      prefetch(p);
       return true;
     }
-    if (pos >= hi) return false;
-    int a = 0, b = n - 1;  // the last tile that begins at or before pos
+    if (at >= hi) return false;
+    int a = 0, b = n - 1;  // the last tile that begins at or before the position
     while (a < b) {
       const int mid = (a + b + 1) >> 1;
-      if (H * __ldcg(&p.tiles[mid].before) <= pos) a = mid; else b = mid - 1;
+      if (H * __ldcg(p.before + mid) <= at) a = mid; else b = mid - 1;
     }
     u.t = load(p, a);
-    const int rest = pos - H * u.t.before;
+    const int rest = at - H * __ldcg(p.before + a);
     u.kvh = rest / u.t.cost;
     u.i0 = rest - u.kvh * u.t.cost;
-    u.i1 = min(u.t.cost, u.i0 + (hi - pos));
-    u.rec = u.i0 == 0 && u.i1 == u.t.cost ? -1 : 2 * static_cast<int>(blockIdx.x) + (pos == lo ? 0 : 1);
-    pos += u.i1 - u.i0;
+    u.i1 = min(u.t.cost, u.i0 + (hi - at));
+    u.rec = u.i0 == 0 && u.i1 == u.t.cost ? -1 : 2 * static_cast<int>(blockIdx.x) + (at == lo ? 0 : 1);
+    at += u.i1 - u.i0;
     return true;
   }
 };
@@ -438,6 +449,9 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
+// The n lowest bits of 64.
+__device__ __forceinline__ uint64_t bits_below(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
+
 // Barrier of the two warps that share query rows; pair_or: the OR of a
 // predicate over their 64 threads.
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
@@ -516,9 +530,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const uint32_t tmem = *s_tmem;
   const int bs = p.row.block_size, window = p.row.window, sinks = p.row.sinks;
 
-#ifdef PR_DOWN
-  if (warp >= kSoftWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PR_DOWN));
-#endif
   if (warp == kSoftWarps) {
     // ------------------------------------------------------------ producer
     // Lane i has box i of every tile: its table entry is read before the slot is
@@ -550,15 +561,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       __syncwarp();
       ++un;
       // ---- rows
-      for (int i = u.i0; i < u.i1; ++i, ++gt) {
+      auto wanted = [&](int i) {
         const int kt = i < seen.front ? i : i - seen.front + seen.start;
         const int r0 = kt * kRows + lane * p.box;
-        const bool want = lane < boxes && r0 <= last && (r0 + p.box > low || r0 < sinks);
-        const int blk = r0 / bs;
-        const int phys = want ? __ldg(table + blk) : -1;
+        return lane < boxes && r0 <= last && (r0 + p.box > low || r0 < sinks) ? r0 : -1;
+      };
+      int r0 = wanted(u.i0);
+      int phys = r0 >= 0 ? __ldg(table + r0 / bs) : -1;
+      for (int i = u.i0; i < u.i1; ++i, ++gt) {
+        const bool want = r0 >= 0;
         const bool there = phys >= 0 && phys < p.row.num_blocks;
         const uint32_t bad = __ballot_sync(full, want && !there);
-        const int y = (there ? (phys * p.row.n_kv_heads + u.kvh) * bs + (r0 - blk * bs) : p.pool_rows) >> 3;
+        const int y = (there ? (phys * p.row.n_kv_heads + u.kvh) * bs + r0 % bs : p.pool_rows) >> 3;
+        if (i + 1 < u.i1) {  // the next tile's entry, while this one waits for its slots
+          r0 = wanted(i + 1);
+          phys = r0 >= 0 ? __ldg(table + r0 / bs) : -1;
+        }
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++kk) {
           const uint32_t slot = kk % G::kSlots;
@@ -688,9 +706,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     }
   } else if (warp < kSoftWarps) {
-#ifdef PR_UP
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PR_UP));
-#endif
     // --------------------------------------------------- softmax, epilogue
     // Two threads per query row (TMEM lane) of half hf: column group cg has
     // columns 64 cg .. of S and half the columns of O. The two warps of a row
@@ -751,25 +766,50 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         ok = wait_warp(bar(G::SFULL0 + hf), n & 1u);
         fence_after();
         const uint32_t bad = s_bad[gt % kBadRing];
-        float s[kCols];
-        tmem_ld64(col_s, s);
-        if (p.negative) {
+        float s[32];
+        uint32_t w[16], see[2] = {0xffffffffu, 0xffffffffu};  // see: which columns are visible
+        float2 sum[2];
+        auto load = [&](int part) {
+          tmem_ld32(col_s + 32 * part, s);
+          if (p.negative) {
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) s[c] = -s[c];
-        }
+            for (int c = 0; c < 32; ++c) s[c] = -s[c];
+          }
+          if (see[part] != 0xffffffffu) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if ((see[part] & (1u << c)) == 0) s[c] = -__builtin_huge_valf();
+          }
+        };
+        auto largest = [&]() {
+          float mx[2] = {max3(s[0], s[1], s[2]), max3(s[3], s[4], s[5])};
+#pragma unroll
+          for (int c = 6; c < 30; c += 4) {
+            mx[0] = max3(mx[0], s[c], s[c + 1]);
+            mx[1] = max3(mx[1], s[c + 2], s[c + 3]);
+          }
+          return max3(fmaxf(mx[0], mx[1]), s[30], s[31]);
+        };
+        auto weigh = [&]() {
+          const float2 q2 = make_float2(qs, qs), m2 = make_float2(-m, -m);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float2 x = ffma2(make_float2(s[2 * k], s[2 * k + 1]), q2, m2);
+            const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            sum[k & 1] = fadd2(sum[k & 1], e);
+            w[k] = pack16<BF>(e.x, e.y);
+          }
+        };
         if (i < f0 || i >= f1 || bad != 0) {
           const Seen seen = seen_tiles(u.t.pos, u.t.count, window, sinks);
           const int r0 = (i < seen.front ? i : i - seen.front + seen.start) * kRows;
           const int c0 = r0 + cg * kCols;  // row of the first column
-          const int hi = pos - c0, lw = pos - window - c0, sk = sinks - c0;
-#pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            if (c > hi || (c <= lw && c >= sk)) s[c] = -__builtin_huge_valf();
-          if (bad != 0) {
-#pragma unroll
-            for (int c = 0; c < kCols; ++c)
-              if ((bad >> ((cg * kCols + c) >> p.box_log2)) & 1u) s[c] = -__builtin_huge_valf();
-          }
+          uint64_t bits = bits_below(pos - c0 + 1) & (~bits_below(pos - window - c0 + 1) | bits_below(sinks - c0));
+          for (int b = 0; bad != 0 && b < kRows >> p.box_log2; ++b)
+            if ((bad >> b) & 1u)
+              bits &= ~(bits_below(((b + 1) << p.box_log2) - cg * kCols) & ~bits_below((b << p.box_log2) - cg * kCols));
+          see[0] = static_cast<uint32_t>(bits);
+          see[1] = static_cast<uint32_t>(bits >> 32);
           // V rows that nobody in the unit sees may hold anything, and 0 x NaN is
           // NaN: half 0 clears them (its products come first).
           const int end = u.t.pos + u.t.count - 1;
@@ -790,35 +830,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             fence_proxy_async_smem();
           }
         }
-        float mx[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) mx[c] = max3(s[c], s[c + 4], s[c + 8]);
-#pragma unroll
-        for (int c = 12; c < 60; c += 8) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[c + k], s[c + 4 + k]);
-        }
-        mx[0] = max3(mx[0], s[60], s[61]);
-        mx[1] = max3(mx[1], s[62], s[63]);
-        float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * qs;
-        // The first half of the weights does not wait for the vote: it nearly
-        // always leaves the reference where it was.
-        uint32_t w[16];
-        float2 sum[2];
-        auto weigh = [&](int c) {
-          const float2 q2 = make_float2(qs, qs), m2 = make_float2(-m, -m);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float2 x = ffma2(make_float2(s[c + 2 * k], s[c + 2 * k + 1]), q2, m2);
-            const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-            sum[k & 1] = fadd2(sum[k & 1], e);
-            w[k] = pack16<BF>(e.x, e.y);
-          }
-        };
-        sum[0] = sum[1] = make_float2(0.f, 0.f);
-        weigh(0);
-        fence_before();  // both warps have read S before either writes P
-        if (pair_or(pair, !ok || (valid && top > m + ABOVE))) {
+        // Once; again where the reference had to move. The first half of the
+        // weights does not wait for the second half's scores and the vote, and no
+        // scores need be kept: S is still in TMEM. (64 scores at once spill.)
+#pragma unroll 1
+        for (;;) {
+          load(0);
+          float top = largest();
+          sum[0] = sum[1] = make_float2(0.f, 0.f);
+          weigh();
+          load(1);
+          top = fmaxf(top, largest()) * qs;
+          fence_before();  // both warps have read S before either writes P
+          if (!pair_or(pair, !ok || (valid && top > m + ABOVE))) break;
           top = fmaxf(top, exchange(top, ok));
           if (!ok) break;
           const float to = fmaxf(m, top - BELOW);
@@ -835,16 +859,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               tmem_st16_async(col_o + c, reinterpret_cast<const uint32_t*>(o));
             }
           }
-          sum[0] = sum[1] = make_float2(0.f, 0.f);
-          weigh(0);
         }
+        if (!ok) break;
         fence_after();
         tmem_st16_async(col_p, w);
         tmem_wait_st();
         fence_before();
         __syncwarp();
         if (lane == 0) arrive(bar(G::PFULL0 + 2 * hf));
-        weigh(32);
+        weigh();
         tmem_st16_async(col_p + 16, w);
         sum[0] = fadd2(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
@@ -929,7 +952,7 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptParams p)
   if (i >= n) return;
   const Ranges r(n, __ldcg(p.head + 1), H, p.grid);
   const Tile t = Walk::load(p, i);
-  const int u0 = H * t.before + kvh * t.cost;
+  const int u0 = H * __ldcg(p.before + i) + kvh * t.cost;
   const int a = r.holder(u0), b = r.holder(u0 + t.cost - 1);
   if (a == b) return;
   const int lane = threadIdx.x & 31;
@@ -995,11 +1018,11 @@ kvc_status check_shape(const PromptShape& s) {
   return KVC_OK;
 }
 
-// Workspace: [head][tiles][records' outputs][records' references and sums],
+// Workspace: [head][tiles][their prefix sums][records' outputs][records' references and sums],
 // each 256-byte aligned. Records only where units are split: where there are too
 // few of them to keep all SMs busy to the end (measured below).
 struct PromptLayout {
-  size_t tiles, rec_o, rec_ml, total;
+  size_t tiles, before, rec_o, rec_ml, total;
   bool split;
 };
 
@@ -1012,7 +1035,8 @@ PromptLayout layout(const PromptShape& s, int num_sms) {
   const int64_t units = (s.num_tokens + 2 * s.tokens() - 1) / (2 * s.tokens()) * s.n_kv_heads;
   l.split = units < static_cast<int64_t>(kWholeUnits) * num_sms;
   l.tiles = 256;
-  l.rec_o = l.tiles + up256(static_cast<size_t>(s.tiles()) * sizeof(Tile));
+  l.before = l.tiles + up256(static_cast<size_t>(s.tiles()) * sizeof(Tile));
+  l.rec_o = l.before + up256(l.split ? static_cast<size_t>(s.tiles()) * 4 : 0);
   const size_t recs = l.split ? 2 * static_cast<size_t>(num_sms) * 2 * kM : 0;
   l.rec_ml = l.rec_o + up256(recs * s.D * 4);
   l.total = l.rec_ml + up256(recs * 8);
@@ -1158,6 +1182,7 @@ kvc_status kvc_prompt_attention(const void* q, const void* k_cache, const void* 
   p.context_lens = context_lens;
   p.head = reinterpret_cast<int*>(ws);
   p.tiles = reinterpret_cast<Tile*>(ws + l.tiles);
+  p.before = reinterpret_cast<int*>(ws + l.before);
   p.rec_o = reinterpret_cast<float*>(ws + l.rec_o);
   p.rec_ml = reinterpret_cast<float*>(ws + l.rec_ml);
   p.err = dev->error_word;
