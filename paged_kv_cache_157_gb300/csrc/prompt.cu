@@ -63,6 +63,9 @@ constexpr int kSoftWarps = 16;      // softmax warps: [half][column group][TMEM 
 constexpr int kCols = kRows / 2;    // columns of S that a softmax thread has
 constexpr int kPromptThreads = (kSoftWarps + 4) * 32;  // one warpgroup more: copies, products, two idle warps
 constexpr int kMinTiles = 4;       // KV tiles of a range at least, where units are split
+// Units are split where that makes the longest CTA's work shorter by more than
+// these KV tiles: what the records and their merge cost (about 15 us).
+constexpr int kSplitGain = 10;
 constexpr int kBadRing = 8;        // tiles whose bad blocks are remembered: more than the ring holds
 
 struct PromptShape {
@@ -81,6 +84,10 @@ struct Tile {
   int cost;                  // KV tiles that it sees
 };
 
+// How units are handed out: one per CTA without a plan; planned, whole; planned,
+// split where that pays.
+enum { kPlanNone = 0, kPlanWhole = 1, kPlanSplit = 2 };
+
 struct PromptParams {
   RowParams row;
   const void* q;  // [num_tokens, n_q_heads, D]
@@ -89,14 +96,14 @@ struct PromptParams {
   const int32_t* query_starts;  // [batch + 1]
   const int32_t* context_lens;
   // workspace
-  int* head;     // number of tiles, their total cost
+  int* head;     // number of tiles, their total cost, whether units are split
   Tile* tiles;
   int* before;   // KV tiles of the tiles before each (where units are split)
   float* rec_o;  // [2 * CTAs, 2 * kM, D] unnormalised partial outputs
   float* rec_ml; // [2 * CTAs, 2 * kM, 2] (reference, sum of weights)
   unsigned int* err;
   int batch, num_tokens, n_q_heads, group, max_blocks, rows, tokens, max_tiles;
-  int split, grid;
+  int mode, grid;  // mode: kPlan*
   int box, box_log2;  // rows of a TMA box: gcd(block_size, 128)
   int pool_rows;  // rows of the pool: one past the last, TMA fills zeros
   float qscale;   // |scale| * log2(e), not 0
@@ -110,7 +117,7 @@ struct PromptParams {
 // keep their 11 bits.
 template <bool BF>
 struct PromptMargin {
-  static constexpr float kBelow = BF ? 0.f : 11.f;
+  static constexpr float kBelow = BF ? 0.f : 7.f;
   static constexpr float kAbove = BF ? 8.f : 15.f;
 };
 
@@ -238,8 +245,15 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
     t.cost = seen_tiles(t.pos, t.count, p.row.window, p.row.sinks).total;
     return t;
   };
+  most = max(__reduce_max_sync(0xffffffffu, most), 1);
+  if ((tid & 31) == 0) s_warp[tid >> 5] = most;
+  s_hist[tid] = 0;
+  __syncthreads();
+  for (int i = 0; i < kPlanThreads / 32; ++i) most = max(most, s_warp[i]);
+  __syncthreads();
   int total = 0;
-  if (p.split) {  // few tiles: in order, with prefix sums
+  bool split = false;
+  if (p.mode == kPlanSplit) {  // few tiles: their prefix sums, and whether splitting pays
     for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
       Tile t;
       t.cost = 0;
@@ -252,16 +266,13 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
       }
       total += sum;
     }
-  } else {  // sorted by cost, in up to 1024 classes
-    most = max(__reduce_max_sync(0xffffffffu, most), 1);
-    if ((tid & 31) == 0) s_warp[tid >> 5] = most;
-    for (int i = tid; i < kBuckets; i += kPlanThreads) s_hist[i] = 0;
-    __syncthreads();
-    for (int i = 0; i < kPlanThreads / 32; ++i) most = max(most, s_warp[i]);
+    split = most - total * p.row.n_kv_heads / p.grid > kSplitGain;
+  }
+  if (!split) {  // sorted by cost, in up to 1024 classes
     int shift = 0;
     while ((most >> shift) >= kBuckets) ++shift;
-    auto bucket = [&](int cost) { return max(0, (most >> shift) - (cost >> shift)); };
-    for (int i = tid; i < n; i += kPlanThreads) atomicAdd(&s_hist[min(kBuckets - 1, bucket(tile_of(i).cost))], 1);
+    auto bucket = [&](int cost) { return min(kBuckets - 1, max(0, (most >> shift) - (cost >> shift))); };
+    for (int i = tid; i < n; i += kPlanThreads) atomicAdd(&s_hist[bucket(tile_of(i).cost)], 1);
     __syncthreads();
     const int mine = s_hist[tid];
     int sum = 0;
@@ -270,12 +281,13 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
     __syncthreads();
     for (int i = tid; i < n; i += kPlanThreads) {
       const Tile t = tile_of(i);
-      p.tiles[atomicAdd(&s_hist[min(kBuckets - 1, bucket(t.cost))], 1)] = t;  // the order among equals is free
+      p.tiles[atomicAdd(&s_hist[bucket(t.cost)], 1)] = t;  // the order among equals is free
     }
   }
   if (tid == 0) {
     p.head[0] = n;
     p.head[1] = total;
+    p.head[2] = split ? 1 : 0;
   }
 }
 static_assert(kBuckets == kPlanThreads, "one class per thread");
@@ -300,16 +312,19 @@ struct Part {
   int kvh, i0, i1;
   int rec;  // -1: the whole unit
 };
+static_assert(sizeof(Tile) == 16 && sizeof(Part) == 32, "copied as 16-byte words");
 
+// The CTA's units. One warp walks (all lanes with the same values) and tells the others.
 struct Walk {
   int n, at, hi, lo;  // whole units: `at` the next round; split ones: the next position of [lo, hi)
+  int i, kvh, split;  // split ones: the next unit
   Tile ahead;         // of the next unit: loaded while this one is worked on
   __device__ __forceinline__ static Tile load(const PromptParams& p, int i) {
     union {
       int4 v;
       Tile t;
     } u;
-    u.v = __ldcg(reinterpret_cast<const int4*>(p.tiles + i));
+    u.v = __ldcg(reinterpret_cast<const int4*>(p.tiles + i));  // (L2: the plan may have run beside this kernel's start)
     return u.t;
   }
   // Unit of round r, dealt out there and back, so that nobody always gets the larger one.
@@ -317,50 +332,86 @@ struct Walk {
     const int c = static_cast<int>(blockIdx.x);
     return r * p.grid + ((r & 1) ? p.grid - 1 - c : c);
   }
-  __device__ __forceinline__ void prefetch(const PromptParams& p) {
-    const int i = unit(p, at);
-    if (i < n * p.row.n_kv_heads) ahead = load(p, i / p.row.n_kv_heads);
-  }
   __device__ __forceinline__ Walk(const PromptParams& p) {
-    n = __ldcg(p.head);  // (L2: the planning kernel may have run beside this one's start)
-    at = lo = hi = 0;
-    if (!p.split) {
-      prefetch(p);
-    } else if (n > 0) {
-      const Ranges r(n, __ldcg(p.head + 1), p.row.n_kv_heads, p.grid);
-      if (static_cast<int>(blockIdx.x) < r.W) {
-        lo = at = r.start(blockIdx.x);
-        hi = r.start(blockIdx.x + 1);
+    at = lo = hi = i = kvh = split = 0;
+    const int H = p.row.n_kv_heads, lane = threadIdx.x & 31;
+    if (p.mode == kPlanNone) {
+      // the CTA's only unit: tiles of the sequences added up, 32 sequences at a time
+      n = 0;
+      const int want = static_cast<int>(blockIdx.x) / H, per = 2 * p.tokens;
+      for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        Span s{0, 0, 0};
+        if (b0 + lane < p.batch) s = span_of(p, b0 + lane, false);
+        const int mine = s.rows > 0 ? (s.count + per - 1) / per : 0;
+        int x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        const uint32_t has = __ballot_sync(0xffffffffu, n + x > want);
+        if (has != 0) {
+          const int src = __ffs(has) - 1;
+          const int t0 = (want - n - __shfl_sync(0xffffffffu, x - mine, src)) * per;
+          const int first = __shfl_sync(0xffffffffu, s.first, src), count = __shfl_sync(0xffffffffu, s.count, src);
+          const int rows = __shfl_sync(0xffffffffu, s.rows, src);
+          ahead.seq = static_cast<unsigned short>(b0 + src);
+          ahead.first = first + t0;
+          ahead.count = static_cast<unsigned short>(min(per, count - t0));
+          ahead.pos = rows - count + t0;
+          ahead.cost = seen_tiles(ahead.pos, ahead.count, p.row.window, p.row.sinks).total;
+          n = want + 1;
+          break;
+        }
+        n += __shfl_sync(0xffffffffu, x, 31);
       }
+      return;
     }
+    n = __ldcg(p.head);
+    split = __ldcg(p.head + 2);
+    if (n == 0) return;
+    if (!split) {
+      if (unit(p, 0) < n * H) ahead = load(p, unit(p, 0) / H);
+      return;
+    }
+    const Ranges r(n, __ldcg(p.head + 1), H, p.grid);
+    if (static_cast<int>(blockIdx.x) >= r.W) return;
+    lo = at = r.start(blockIdx.x);
+    hi = r.start(blockIdx.x + 1);
+    int b = n - 1;  // i: the last tile that begins at or before the position
+    while (i < b) {
+      const int mid = (i + b + 1) >> 1;
+      if (H * __ldcg(p.before + mid) <= at) i = mid; else b = mid - 1;
+    }
+    ahead = load(p, i);
+    kvh = (at - H * __ldcg(p.before + i)) / ahead.cost;
+    lo -= H * __ldcg(p.before + i) + kvh * ahead.cost;  // from the first unit's begin on
+    hi -= at - lo;
+    at = lo;
   }
   __device__ __forceinline__ bool next(const PromptParams& p, Part& u) {
     const int H = p.row.n_kv_heads;
-    if (!p.split) {
-      const int i = unit(p, at);
-      if (i >= n * H) return false;
-      u.t = ahead;
-      u.kvh = i % H;
-      u.i0 = 0;
-      u.i1 = u.t.cost;
-      u.rec = -1;
+    if (!split) {
+      const int j = unit(p, at);
+      if (j >= n * H) return false;
+      u = {ahead, j % H, 0, ahead.cost, -1};
       ++at;
-      prefetch(p);
+      const int k = unit(p, at);
+      if (p.mode != kPlanNone && k < n * H) ahead = load(p, k / H);
       return true;
     }
     if (at >= hi) return false;
-    int a = 0, b = n - 1;  // the last tile that begins at or before the position
-    while (a < b) {
-      const int mid = (a + b + 1) >> 1;
-      if (H * __ldcg(p.before + mid) <= at) a = mid; else b = mid - 1;
-    }
-    u.t = load(p, a);
-    const int rest = at - H * __ldcg(p.before + a);
-    u.kvh = rest / u.t.cost;
-    u.i0 = rest - u.kvh * u.t.cost;
+    const bool begins = at == lo;
+    u.t = ahead;
+    u.kvh = kvh;
+    u.i0 = begins ? lo : 0;
     u.i1 = min(u.t.cost, u.i0 + (hi - at));
-    u.rec = u.i0 == 0 && u.i1 == u.t.cost ? -1 : 2 * static_cast<int>(blockIdx.x) + (at == lo ? 0 : 1);
+    u.rec = u.i0 == 0 && u.i1 == u.t.cost ? -1 : 2 * static_cast<int>(blockIdx.x) + (begins ? 0 : 1);
     at += u.i1 - u.i0;
+    if (++kvh == H) {
+      kvh = 0;
+      if (++i < n) ahead = load(p, i);
+    }
     return true;
   }
 };
@@ -381,12 +432,13 @@ struct PromptGeo {
   static constexpr uint32_t kOffBar = kOffRing + kSlots * kTile;
   enum {
     QFULL = 0, QEMPTY, FULL0, EMPTY0 = FULL0 + kSlots, SFULL0 = EMPTY0 + kSlots, PFULL0 = SFULL0 + 2,
-    OFULL0 = PFULL0 + 4, OEMPTY0 = OFULL0 + 2, FINAL = OEMPTY0 + 2, COUNT
+    OFULL0 = PFULL0 + 4, OEMPTY0 = OFULL0 + 2, UFULL0 = OEMPTY0 + 2, UEMPTY0 = UFULL0 + 2, FINAL = UEMPTY0 + 2, COUNT
   };
   static constexpr uint32_t kOffMisc = kOffBar + COUNT * 8;  // TMEM address, abort flag, bad blocks
   static constexpr uint32_t kOffPart = kOffMisc + 8 + kBadRing * 4;  // what the threads of a row tell each other
   static constexpr uint32_t kOffFail = kOffPart + kSoftWarps * 32 * 4;
-  static constexpr uint32_t kBytes = kOffFail + kSoftWarps * 4;
+  static constexpr uint32_t kOffUnit = (kOffFail + kSoftWarps * 4 + 15) / 16 * 16;  // two units: this and the next
+  static constexpr uint32_t kBytes = kOffUnit + 2 * sizeof(Part);
   static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
   // TMEM columns: S (P over it) of both halves, O of both
   static constexpr uint32_t kColO = 256;
@@ -503,8 +555,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
   if (tid == 0) {
     *s_abort = 0;
-    for (int i = 0; i < G::COUNT; ++i)
-      mbar_init(&bars[i], (i >= G::PFULL0 && i < G::OFULL0) || (i >= G::OEMPTY0 && i < G::FINAL) ? 8 : 1);
+    for (int i = 0; i < G::COUNT; ++i) {
+      uint32_t from = 1;
+      if ((i >= G::PFULL0 && i < G::OFULL0) || (i >= G::OEMPTY0 && i < G::UFULL0)) from = kSoftWarps / 2;
+      if (i >= G::UEMPTY0 && i < G::FINAL) from = kSoftWarps + 1;
+      mbar_init(&bars[i], from);
+    }
     fence_barrier_init();
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
@@ -529,25 +585,36 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   fence_after();
   const uint32_t tmem = *s_tmem;
   const int bs = p.row.block_size, window = p.row.window, sinks = p.row.sinks;
+  Part* s_unit = reinterpret_cast<Part*>(sm + G::kOffUnit);
 
   if (warp == kSoftWarps) {
     // ------------------------------------------------------------ producer
     // Lane i has box i of every tile: its table entry is read before the slot is
     // free. One barrier per K or V tile.
-    uint32_t kk = 0, gt = 0, un = 0;  // tiles copied, KV tiles, units
+    uint32_t kk = 0, gt = 0, un = 0, nq = 0;  // tiles copied, KV tiles, units told, units' queries copied
     uint32_t issued[G::kSlots] = {};
     const int boxes = kRows / p.box;
     bool ok = true;
     Walk walk(p);
-    Part u;
-    while (ok && walk.next(p, u)) {
+    for (; ok; ++un) {
+      Part u;
+      const bool have = walk.next(p, u);
+      if (!have) u.t.count = 0;  // the end
+      bool got = true;
+      if (lane == 0 && un >= 2) got = wait_phase(bar(G::UEMPTY0 + (un & 1)), ((un >> 1) - 1) & 1u, s_abort, p.err);
+      if (!__shfl_sync(full, got ? 1 : 0, 0)) break;
+      if (lane == 0) {
+        s_unit[un & 1] = u;
+        arrive(bar(G::UFULL0 + (un & 1)));
+      }
+      __syncwarp();
+      if (!have) break;
       const int last = u.t.pos + u.t.count - 1;
       const int low = u.t.pos >= window ? u.t.pos - window + 1 : 0;
       const Seen seen = seen_tiles(u.t.pos, u.t.count, window, sinks);
       const bool two = u.t.count > p.tokens;
       const int32_t* table = p.block_tables + static_cast<int64_t>(u.t.seq) * p.max_blocks;
       // ---- queries
-      bool got = true;
       if (lane == 0 && un > 0) got = wait_phase(bar(G::QEMPTY), (un - 1) & 1u, s_abort, p.err);
       if (!__shfl_sync(full, got ? 1 : 0, 0)) break;
       if (lane == 0) {
@@ -559,7 +626,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         u.t.first + h * p.tokens, bar(G::QFULL));
       }
       __syncwarp();
-      ++un;
+      ++nq;
       // ---- rows
       auto wanted = [&](int i) {
         const int kt = i < seen.front ? i : i - seen.front + seen.start;
@@ -612,9 +679,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         while (!try_wait(bar(G::FULL0 + s), (issued[s] - 1) & 1u) && globaltimer_ns() - t0 < kWaitNs) {
         }
       }
-      if (un > 0) {
+      if (nq > 0) {
         const uint64_t t0 = globaltimer_ns();
-        while (!try_wait(bar(G::QFULL), (un - 1) & 1u) && globaltimer_ns() - t0 < kWaitNs) {
+        while (!try_wait(bar(G::QFULL), (nq - 1) & 1u) && globaltimer_ns() - t0 < kWaitNs) {
         }
       }
     }
@@ -628,8 +695,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       uint32_t gt = 0, un = 0;        // KV tiles begun, units begun
       uint32_t np[2] = {0, 0}, nu[2] = {0, 0};  // per half: tiles whose P was used, units
       bool ok = true;
-      Walk walk(p);
-      Part u;
       // S of half h with KV tile g (of the CTA's count)
       auto issue_s = [&](int h, uint32_t g) {
         const uint32_t slot = (2 * g) % G::kSlots;
@@ -644,7 +709,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       auto full_slot = [&](uint32_t k) {
         return wait_phase(bar(G::FULL0 + k % G::kSlots), (k / G::kSlots) & 1u, s_abort, p.err);
       };
-      while (ok && !*s_abort && walk.next(p, u)) {
+      for (; ok && !*s_abort; ++un) {
+        if (!wait_phase(bar(G::UFULL0 + (un & 1)), (un >> 1) & 1u, s_abort, p.err)) break;
+        const Part u = s_unit[un & 1];
+        arrive(bar(G::UEMPTY0 + (un & 1)));
+        if (u.t.count == 0) break;
         const int halves = u.t.count > p.tokens ? 2 : 1;
         const int J = u.i1 - u.i0;
         if (!wait_phase(bar(G::QFULL), un & 1u, s_abort, p.err)) break;
@@ -697,7 +766,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
         }
         for (int h = 0; h < halves; ++h) ++nu[h];
-        ++un;
       }
       // all products are done before TMEM is freed
       commit(bar(G::FINAL));
@@ -705,7 +773,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       while (!try_wait(bar(G::FINAL), 0) && globaltimer_ns() - t0 < kWaitNs) {
       }
     }
-  } else if (warp < kSoftWarps) {
+  } else if (warp >= kSoftWarps) {
+    // Without a plan: flags of invalid sequences, and their zeros.
+    if (p.mode == kPlanNone) {
+      for (int b = static_cast<int>(blockIdx.x) * 2 + warp - kSoftWarps - 2; b < p.batch; b += 2 * gridDim.x) {
+        const Span s = span_of(p, b, lane == 0);
+        if (s.count == 0 || s.rows > 0) continue;
+        const int64_t words = static_cast<int64_t>(p.n_q_heads) * D * 2 / 16;
+        uint4* to = static_cast<uint4*>(p.out) + s.first * words;
+        for (int64_t i = lane; i < s.count * words; i += 32) to[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  } else {
     // --------------------------------------------------- softmax, epilogue
     // Two threads per query row (TMEM lane) of half hf: column group cg has
     // columns 64 cg .. of S and half the columns of O. The two warps of a row
@@ -741,12 +820,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     };
     uint32_t gt = 0, n = 0, nu = 0;  // the CTA's KV tiles; tiles and units of this half
     bool ok = true;
-    Walk walk(p);
-    Part u;
-    while (ok && walk.next(p, u)) {
-      const int J = u.i1 - u.i0;
+    for (uint32_t un = 0;; ++un) {
+      if (!wait_warp(bar(G::UFULL0 + (un & 1)), (un >> 1) & 1u)) break;
+      const Part& u = s_unit[un & 1];
+      if (u.t.count == 0) break;
       if (hf * p.tokens >= u.t.count) {  // the half has no token
-        gt += J;
+        gt += u.i1 - u.i0;
+        __syncwarp();
+        if (lane == 0) arrive(bar(G::UEMPTY0 + (un & 1)));
         continue;
       }
       const int first = u.t.pos + hf * p.tokens;  // positions of the half
@@ -762,7 +843,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         f1 = seen.front + (first + 1) / kRows - seen.start;
       }
       float m = -1e30f, l = 0.f;  // finite: a row may meet only hidden columns
-      for (int i = u.i0; i < u.i1; ++i, ++gt, ++n) {
+      const int i0 = u.i0, i1 = u.i1;
+      for (int i = i0; i < i1; ++i, ++gt, ++n) {
         ok = wait_warp(bar(G::SFULL0 + hf), n & 1u);
         fence_after();
         const uint32_t bad = s_bad[gt % kBadRing];
@@ -849,7 +931,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const float f = fast_exp2(m - to);
           l *= f;
           m = to;
-          if (i > u.i0) {  // PV of the tile before is done: S came behind it
+          if (i > i0) {  // PV of the tile before is done: S came behind it
 #pragma unroll 1
             for (int c = 0; c < OC; c += 16) {
               float o[16];
@@ -886,8 +968,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int head = u.kvh * p.group + r - tk * p.group;
       const int row = u.t.first + hf * p.tokens + tk;
       const int64_t at = (static_cast<int64_t>(row) * p.n_q_heads + head) * D + cg * OC;
+      const int seq = u.t.seq;
+      float* ml = u.rec < 0 ? nullptr : p.rec_ml + (static_cast<int64_t>(u.rec) * 2 * kM + hf * kM + r) * 2;
       float* rec = u.rec < 0 ? nullptr : p.rec_o + (static_cast<int64_t>(u.rec) * 2 * kM + hf * kM + r) * D + cg * OC;
-      const float inv = u.rec >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      __syncwarp();
+      if (lane == 0) arrive(bar(G::UEMPTY0 + (un & 1)));  // u is not looked at any more
+      const float inv = rec != nullptr ? 1.f : l == 0.f ? 0.f : 1.f / l;
       float zero = 0.f;  // NaN if an output is not finite
 #pragma unroll 1
       for (int c = 0; c < OC; c += 32) {
@@ -916,14 +1002,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       __syncwarp();
       if (lane == 0) arrive(bar(G::OEMPTY0 + hf));
       if (rec != nullptr) {
-        if (valid && cg == 0)
-          *reinterpret_cast<float2*>(p.rec_ml + (static_cast<int64_t>(u.rec) * 2 * kM + hf * kM + r) * 2) =
-              make_float2(m, l);
+        if (valid && cg == 0) *reinterpret_cast<float2*>(ml) = make_float2(m, l);
       } else {
         // rows done again whole, by either warp of the row or by both (the same values)
         for (uint32_t odd = __ballot_sync(full, valid && zero != 0.f); odd != 0; odd &= odd - 1) {
           const int src = __ffs(odd) - 1;
-          redo_row<CT, D>(p, u.t.seq, __shfl_sync(full, row, src), __shfl_sync(full, head, src),
+          redo_row<CT, D>(p, seq, __shfl_sync(full, row, src), __shfl_sync(full, head, src),
                           __shfl_sync(full, pos, src));
         }
       }
@@ -949,7 +1033,7 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptParams p)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int H = p.row.n_kv_heads, n = __ldcg(p.head);
   const int i = static_cast<int>(blockIdx.x) / H, kvh = static_cast<int>(blockIdx.x) - i * H;
-  if (i >= n) return;
+  if (i >= n || __ldcg(p.head + 2) == 0) return;
   const Ranges r(n, __ldcg(p.head + 1), H, p.grid);
   const Tile t = Walk::load(p, i);
   const int u0 = H * __ldcg(p.before + i) + kvh * t.cost;
@@ -1018,26 +1102,34 @@ kvc_status check_shape(const PromptShape& s) {
   return KVC_OK;
 }
 
-// Workspace: [head][tiles][their prefix sums][records' outputs][records' references and sums],
-// each 256-byte aligned. Records only where units are split: where there are too
-// few of them to keep all SMs busy to the end (measured below).
+// Workspace: [head][tiles][their prefix sums][records' outputs][records'
+// references and sums], each 256-byte aligned; records and prefix sums only where
+// units may be split.
 struct PromptLayout {
   size_t tiles, before, rec_o, rec_ml, total;
-  bool split;
+  int mode;
 };
 
-constexpr int kWholeUnits = 4;  // units per SM from which none is split
+// Units per SM from which none is split: dealt out by size they end together.
+constexpr int kWholeUnits = 4;
+// Sequences that a call without a plan looks through.
+constexpr int kUnplannedBatch = 256;
 
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 PromptLayout layout(const PromptShape& s, int num_sms) {
   PromptLayout l;
-  const int64_t units = (s.num_tokens + 2 * s.tokens() - 1) / (2 * s.tokens()) * s.n_kv_heads;
-  l.split = units < static_cast<int64_t>(kWholeUnits) * num_sms;
+  const int64_t units = (s.num_tokens + 2 * s.tokens() - 1) / (2 * s.tokens()) * s.n_kv_heads;  // at least
+  const int64_t most = static_cast<int64_t>(s.max_blocks) * s.block_size / kRows + 2;           // KV tiles of a unit
+  l.mode = kPlanWhole;
+  if (units < static_cast<int64_t>(kWholeUnits) * num_sms && most > kSplitGain)
+    l.mode = kPlanSplit;
+  else if (s.tiles() * s.n_kv_heads <= num_sms && s.batch <= kUnplannedBatch)
+    l.mode = kPlanNone;
   l.tiles = 256;
   l.before = l.tiles + up256(static_cast<size_t>(s.tiles()) * sizeof(Tile));
-  l.rec_o = l.before + up256(l.split ? static_cast<size_t>(s.tiles()) * 4 : 0);
-  const size_t recs = l.split ? 2 * static_cast<size_t>(num_sms) * 2 * kM : 0;
+  l.rec_o = l.before + up256(l.mode == kPlanSplit ? static_cast<size_t>(s.tiles()) * 4 : 0);
+  const size_t recs = l.mode == kPlanSplit ? 2 * static_cast<size_t>(num_sms) * 2 * kM : 0;
   l.rec_ml = l.rec_o + up256(recs * s.D * 4);
   l.total = l.rec_ml + up256(recs * 8);
   return l;
@@ -1098,16 +1190,18 @@ kvc_status launch(const PromptParams& p, const CUtensorMap& tq, const CUtensorMa
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kPlanThreads);
-  e = cudaLaunchKernelEx(&cfg, prompt_plan_kernel, p, static_cast<int>(sizeof(CT)), D);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx(prompt plan)");
+  if (p.mode != kPlanNone) {
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kPlanThreads);
+    e = cudaLaunchKernelEx(&cfg, prompt_plan_kernel, p, static_cast<int>(sizeof(CT)), D);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx(prompt plan)");
+  }
   cfg.gridDim = dim3(static_cast<unsigned>(p.grid));
   cfg.blockDim = dim3(kPromptThreads);
   cfg.dynamicSmemBytes = PromptGeo<D>::kBytes;
   e = cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, p);
   if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx(prompt)");
-  if (p.split) {
+  if (p.mode == kPlanSplit) {
     cfg.gridDim = dim3(static_cast<unsigned>(p.max_tiles) * p.row.n_kv_heads, 2 * kM / kMergeRows);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
@@ -1194,9 +1288,15 @@ kvc_status kvc_prompt_attention(const void* q, const void* k_cache, const void* 
   p.rows = max_blocks_per_seq * block_size;
   p.tokens = shape.tokens();
   p.max_tiles = static_cast<int>(shape.tiles());
-  p.split = l.split ? 1 : 0;
+  p.mode = l.mode;
   const int64_t cap = option(KVC_OPT_MAX_CTAS);
   p.grid = static_cast<int>(cap > 0 ? std::min<int64_t>(cap, dev->num_sms) : dev->num_sms);
+  if (p.mode == kPlanNone) {
+    if (p.max_tiles * n_kv_heads <= p.grid)
+      p.grid = p.max_tiles * n_kv_heads;
+    else
+      p.mode = kPlanWhole;
+  }
   p.box = std::gcd(block_size, kRows);
   while ((1 << p.box_log2) < p.box) ++p.box_log2;
   p.pool_rows = static_cast<int>(num_blocks * n_kv_heads * block_size);
