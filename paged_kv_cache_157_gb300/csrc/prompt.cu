@@ -427,9 +427,10 @@ struct PromptGeo {
   // rows][128 bytes], so that one copy brings all parts of a page: of 16-row
   // pages a tile needs 8 copies, and issuing twice as many cost 20 % (16384 rows).
   static constexpr uint32_t kRowGroup = kHalves * 1024;
-  static constexpr int kSlots = D == 128 ? 5 : 8;         // K and V tiles in the ring
+  static constexpr int kSlots = D == 128 ? 4 : 8;         // K and V tiles in the ring (a fifth brings nothing)
   static constexpr uint32_t kOffRing = 2 * kTile;         // behind both halves' queries
-  static constexpr uint32_t kOffBar = kOffRing + kSlots * kTile;
+  static constexpr uint32_t kOffStage = kOffRing + kSlots * kTile;  // 2 KB per softmax warp: outputs on their way
+  static constexpr uint32_t kOffBar = kOffStage + kSoftWarps * 2048;
   enum {
     QFULL = 0, QEMPTY, FULL0, EMPTY0 = FULL0 + kSlots, SFULL0 = EMPTY0 + kSlots, PFULL0 = SFULL0 + 2,
     OFULL0 = PFULL0 + 4, OEMPTY0 = OFULL0 + 2, UFULL0 = OEMPTY0 + 2, UEMPTY0 = UFULL0 + 2, FINAL = UEMPTY0 + 2, COUNT
@@ -967,25 +968,46 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       fence_after();
       const int head = u.kvh * p.group + r - tk * p.group;
       const int row = u.t.first + hf * p.tokens + tk;
-      const int64_t at = (static_cast<int64_t>(row) * p.n_q_heads + head) * D + cg * OC;
-      const int seq = u.t.seq;
-      float* ml = u.rec < 0 ? nullptr : p.rec_ml + (static_cast<int64_t>(u.rec) * 2 * kM + hf * kM + r) * 2;
-      float* rec = u.rec < 0 ? nullptr : p.rec_o + (static_cast<int64_t>(u.rec) * 2 * kM + hf * kM + r) * D + cg * OC;
+      const int seq = u.t.seq, rec = u.rec;
       __syncwarp();
       if (lane == 0) arrive(bar(G::UEMPTY0 + (un & 1)));  // u is not looked at any more
-      const float inv = rec != nullptr ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      const float inv = rec >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      // Threads have rows, and a row's pieces lie far from the next row's: they go
+      // through shared memory, so that four lanes write 64 bytes of a row (one
+      // 16-byte piece per lane and row cost 8 times the cycles in the load-store unit).
+      unsigned char* to = nullptr;
+      if (valid)
+        to = rec < 0 ? static_cast<unsigned char*>(p.out) +
+                           ((static_cast<int64_t>(row) * p.n_q_heads + head) * D + cg * OC) * 2
+                     : reinterpret_cast<unsigned char*>(
+                           p.rec_o + ((static_cast<int64_t>(rec) * 2 + hf) * kM + r) * D + cg * OC);
+      unsigned char* stage = sm + G::kOffStage + warp * 2048;
+      auto put = [&](const uint32_t* x, int off) {  // 64 bytes of every row
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint4*>(stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int src = 8 * k + (lane >> 2);
+          unsigned char* at = reinterpret_cast<unsigned char*>(
+              __shfl_sync(full, reinterpret_cast<unsigned long long>(to), src));
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + src * 64 + (((lane & 3) ^ ((src >> 1) & 3)) << 4));
+          if (at != nullptr) *reinterpret_cast<uint4*>(at + off + 16 * (lane & 3)) = v;
+        }
+        __syncwarp();
+      };
       float zero = 0.f;  // NaN if an output is not finite
 #pragma unroll 1
       for (int c = 0; c < OC; c += 32) {
         float o[32];
         tmem_ld32(col_o + c, o);
-        if (!valid) continue;
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] *= inv;
-        if (rec != nullptr) {
-#pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<float4*>(rec + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        if (rec >= 0) {
+          put(reinterpret_cast<const uint32_t*>(o), 4 * c);
+          put(reinterpret_cast<const uint32_t*>(o) + 16, 4 * c + 64);
         } else {
           uint32_t w[16];
 #pragma unroll
@@ -993,16 +1015,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             zero = fmaf(o[2 * k], 0.f, fmaf(o[2 * k + 1], 0.f, zero));
             w[k] = pack16<BF>(o[2 * k], o[2 * k + 1]);
           }
-          uint4* to = reinterpret_cast<uint4*>(static_cast<CT*>(p.out) + at + c);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) to[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+          put(w, 2 * c);
         }
       }
       fence_before();
       __syncwarp();
       if (lane == 0) arrive(bar(G::OEMPTY0 + hf));
-      if (rec != nullptr) {
-        if (valid && cg == 0) *reinterpret_cast<float2*>(ml) = make_float2(m, l);
+      if (rec >= 0) {
+        if (valid && cg == 0)
+          *reinterpret_cast<float2*>(p.rec_ml + ((static_cast<int64_t>(rec) * 2 + hf) * kM + r) * 2) =
+              make_float2(m, l);
       } else {
         // rows done again whole, by either warp of the row or by both (the same values)
         for (uint32_t odd = __ballot_sync(full, valid && zero != 0.f); odd != 0; odd &= odd - 1) {
