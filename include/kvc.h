@@ -532,7 +532,7 @@ kvc_status kvc_decode_attention_sinks(const void* q, const void* k_cache, const 
                                       void* workspace, size_t workspace_bytes, kvc_stream stream);
 
 /* The same decode over the caches written by kvc_append_fp4 (their scales, whose
- * NaN code it never writes, 16-byte aligned). q F16 or BF16 in q_dtype. Otherwise
+ * NaN code it never writes, 16-byte aligned). q F16 or BF16 in q_dtype; batch <= 2048. Otherwise
  * as kvc_decode_attention_sinks; window INT32_MAX and sinks 0 is the plain decode. */
 kvc_status kvc_decode_attention_fp4(const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_scale,
                                     const uint8_t* v_scale, const int32_t* block_tables, int max_blocks_per_seq,

@@ -40,6 +40,9 @@ SOURCES = [
     "decode_scored_f16.cu",
     "decode_scored_fp8.cu",
     "decode_scored_int8.cu",
+    "decode_stream_bf16.cu",
+    "decode_stream_f16.cu",
+    "decode_stream_fp4.cu",
     "decode_scored.cu",
     "append_block.cu",
     "cache4.cu",

@@ -13,14 +13,10 @@
 #include <type_traits>
 
 #include "code4.cuh"
+#include "decode_scored.h"
 #include "kvc_internal.h"
 
 namespace kvc {
-
-// e2m1 codes, two to a byte.
-struct fp4e2m1 {
-  unsigned char bits;
-};
 
 struct RowParams {
   const void* k_cache;

@@ -8,7 +8,6 @@
 #include <algorithm>
 #include <mutex>
 
-#include "attend_row.cuh"
 #include "decode_scored.h"
 #include "kvc_device.cuh"
 
@@ -110,8 +109,9 @@ EncodeTiledFn encode_tiled_fn() {
   return fn;
 }
 
-// The pool as [num_blocks * n_kv_heads * block_size rows, D] in boxes of 16
-// rows by 128 bytes (64 bytes where a row is that short), swizzled by as much.
+// The pool as [num_blocks * n_kv_heads * block_size rows, row] in boxes of 16
+// rows by 128 bytes (64 or 32 bytes where a row is that short), swizzled by as
+// much. Rows of D elements of elt bytes.
 kvc_status pool_map(const void* cache, int64_t pool_rows, int D, int elt, CUtensorMap* map) {
   EncodeTiledFn encode = encode_tiled_fn();
   if (encode == nullptr) return fail(KVC_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
@@ -123,21 +123,32 @@ kvc_status pool_map(const void* cache, int64_t pool_rows, int D, int elt, CUtens
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes / elt), kTileRows};
   const cuuint32_t es[2] = {1, 1};
   CUresult r = encode(map, dt, 2, const_cast<void*>(cache), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                      box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                      box_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                      : box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                        : CU_TENSOR_MAP_SWIZZLE_32B,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(KVC_ERR_CUDA, "tensor map for the cache: CUresult %d", static_cast<int>(r));
   return KVC_OK;
 }
 
-// Cache element of a call: a 16-bit type, or one-byte codes.
-enum class Cache { kBf16, kF16, kE4m3, kInt8 };
+// Cache element of a call: a 16-bit type, one-byte codes, or four-bit ones.
+enum class Cache { kBf16, kF16, kE4m3, kInt8, kFp4 };
+
+// What calls with a window and sinks have besides.
+struct Stream {
+  int window, sinks;
+  const uint8_t *k_scale, *v_scale;  // four-bit caches
+};
 
 kvc_status decode(Cache cache, const ScoredShape& s, const void* q, kvc_dtype q_dtype, const void* k_cache,
                   const void* v_cache, const float* k_scale, const float* v_scale, const int32_t* block_tables,
                   const int32_t* context_lens, float scale, int64_t num_blocks, void* out, kvc_dtype out_dtype,
-                  float* scores, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+                  float* scores, void* workspace, size_t workspace_bytes, cudaStream_t stream,
+                  const Stream* win = nullptr) {
   kvc_status st = check_shape(s);
   if (st != KVC_OK) return st;
+  if (win != nullptr && (win->window < 1 || win->sinks < 0))
+    return fail(KVC_ERR_INVALID_ARG, "window must be >= 1 and sinks >= 0");
   if (!dtype_ok(out_dtype)) return fail(KVC_ERR_INVALID_ARG, "unknown out_dtype %d", static_cast<int>(out_dtype));
   if (num_blocks < 1) return fail(KVC_ERR_INVALID_ARG, "num_blocks must be >= 1");
   if (num_blocks > ((1ll << 31) - 1) / s.block_size / s.n_kv_heads)
@@ -159,8 +170,9 @@ kvc_status decode(Cache cache, const ScoredShape& s, const void* q, kvc_dtype q_
     return fail(KVC_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   CUtensorMap tk, tv;
   const int64_t pool_rows = num_blocks * s.n_kv_heads * s.block_size;
-  if ((st = pool_map(k_cache, pool_rows, s.D, elt, &tk)) != KVC_OK) return st;
-  if ((st = pool_map(v_cache, pool_rows, s.D, elt, &tv)) != KVC_OK) return st;
+  const int row = cache == Cache::kFp4 ? s.D / 2 : s.D;  // elements, or bytes of codes
+  if ((st = pool_map(k_cache, pool_rows, row, elt, &tk)) != KVC_OK) return st;
+  if ((st = pool_map(v_cache, pool_rows, row, elt, &tv)) != KVC_OK) return st;
 
   char* ws = static_cast<char*>(workspace);
   ScoredParams p{};
@@ -200,99 +212,26 @@ kvc_status decode(Cache cache, const ScoredShape& s, const void* q, kvc_dtype q_
   // the work split's option counts cache blocks per worker, here a warp
   p.min_tiles = forced > 0 ? static_cast<int>(std::min<int64_t>(forced, 1 << 20)) * (s.block_size / kTileRows)
                            : kMinTiles;
+  if (win != nullptr) {
+    // rows are below 2^30: larger windows are all rows, and differences stay in 32 bits
+    p.window = std::min(win->window, 1 << 30);
+    p.sinks = std::min(win->sinks, 1 << 30);
+    p.k_scale4 = win->k_scale;
+    p.v_scale4 = win->v_scale;
+    st = cache == Cache::kBf16  ? stream_launch<__nv_bfloat16>(p, s.D, l.nt, grid, tk, tv, stream)
+         : cache == Cache::kF16 ? stream_launch<__half>(p, s.D, l.nt, grid, tk, tv, stream)
+                                : stream_launch<fp4e2m1>(p, s.D, l.nt, grid, tk, tv, stream);
+    if (st != KVC_OK) return st;
+    return finish_call(stream);
+  }
   switch (cache) {
+    case Cache::kFp4: break;  // only with a window, above
     case Cache::kBf16: st = scored_launch<__nv_bfloat16>(p, s.D, l.nt, grid, tk, tv, stream); break;
     case Cache::kF16: st = scored_launch<__half>(p, s.D, l.nt, grid, tk, tv, stream); break;
     case Cache::kE4m3: st = scored_launch<fp8e4m3>(p, s.D, l.nt, grid, tk, tv, stream); break;
     case Cache::kInt8: st = scored_launch<s8q>(p, s.D, l.nt, grid, tk, tv, stream); break;
   }
   if (st != KVC_OK) return st;
-  return finish_call(stream);
-}
-
-// One warp per query (sequence, token, head).
-struct RowsParams {
-  RowParams row;
-  const void* q;
-  void* out;
-  const int32_t* block_tables;
-  const int32_t* context_lens;
-  unsigned int* err;
-  int batch, n_tok, n_q_heads, group, max_blocks, rows, out_dtype, q_f16;
-};
-
-template <typename CT, int D>
-__global__ void __launch_bounds__(256) decode_rows_kernel(const RowsParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
-  if (at >= static_cast<int64_t>(p.batch) * p.n_tok * p.n_q_heads) return;
-  const int h = static_cast<int>(at % p.n_q_heads);
-  const int64_t bt = at / p.n_q_heads;
-  const int t = static_cast<int>(bt % p.n_tok), b = static_cast<int>(bt / p.n_tok);
-  const int n = __ldg(p.context_lens + b);
-  constexpr int N = D / 32;
-  float q[N], o[N];
-#pragma unroll
-  for (int j = 0; j < N; ++j) o[j] = 0.f;
-  if (n < p.n_tok || n > p.rows) {
-    if (lane == 0) set_flag(p.err, KVC_FLAG_BAD_LEN);
-  } else {
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      q[j] = p.q_f16 ? __half2float(static_cast<const __half*>(p.q)[at * D + lane * N + j])
-                     : __bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[at * D + lane * N + j]);
-    if (!attend_row<CT, D>(p.row, q, p.block_tables + static_cast<int64_t>(b) * p.max_blocks, h / p.group,
-                           n - p.n_tok + t, o) && lane == 0)
-      set_flag(p.err, KVC_FLAG_BAD_BLOCK);
-  }
-  store_out_vec<N>(p.out, at * D + lane * N, o, p.out_dtype);
-}
-
-template <typename CT>
-kvc_status decode_rows(const ScoredShape& s, const void* q, kvc_dtype q_dtype, const void* k_cache,
-                       const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
-                       const int32_t* block_tables, const int32_t* context_lens, float scale, int64_t num_blocks,
-                       int window, int sinks, void* out, kvc_dtype out_dtype, void* workspace,
-                       size_t workspace_bytes, cudaStream_t stream) {
-  kvc_status st = check_shape(s);
-  if (st != KVC_OK) return st;
-  if (window < 1 || sinks < 0) return fail(KVC_ERR_INVALID_ARG, "window must be >= 1 and sinks >= 0");
-  if (!dtype_ok(out_dtype)) return fail(KVC_ERR_INVALID_ARG, "unknown out_dtype %d", static_cast<int>(out_dtype));
-  if (num_blocks < 1) return fail(KVC_ERR_INVALID_ARG, "num_blocks must be >= 1");
-  if (num_blocks > ((1ll << 31) - 1) / s.block_size / s.n_kv_heads)
-    return fail(KVC_ERR_UNSUPPORTED, "num_blocks x n_kv_heads x block_size must be below 2^31");
-  if (q == nullptr || k_cache == nullptr || v_cache == nullptr || block_tables == nullptr ||
-      context_lens == nullptr || out == nullptr)
-    return fail(KVC_ERR_INVALID_ARG, "NULL pointer");
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
-    return fail(KVC_ERR_INVALID_ARG, "q, k_cache and v_cache must be 16-byte aligned");
-  DeviceInfo* dev = nullptr;
-  if ((st = current_device(&dev)) != KVC_OK) return st;
-  const size_t needed = workspace_needed(s, false, dev->num_sms);
-  if (workspace == nullptr || workspace_bytes < needed)
-    return fail(KVC_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace == nullptr ? 0 : workspace_bytes,
-                needed);
-  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
-    return fail(KVC_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  RowsParams p{};
-  p.row = {k_cache, v_cache, k_scale, v_scale, num_blocks, s.n_kv_heads, s.block_size, window, sinks,
-           scale * 1.4426950408889634f};
-  p.q = q;
-  p.out = out;
-  p.block_tables = block_tables;
-  p.context_lens = context_lens;
-  p.err = dev->error_word;
-  p.batch = s.batch;
-  p.n_tok = s.n_tok;
-  p.n_q_heads = s.n_q_heads;
-  p.group = s.group();
-  p.max_blocks = s.max_blocks;
-  p.rows = static_cast<int>(s.rows());
-  p.out_dtype = out_dtype;
-  p.q_f16 = q_dtype == KVC_F16 ? 1 : 0;
-  const int64_t warps = static_cast<int64_t>(s.batch) * s.n_tok * s.n_q_heads;
-  auto* kernel = s.D == 64 ? decode_rows_kernel<CT, 64> : s.D == 128 ? decode_rows_kernel<CT, 128> : decode_rows_kernel<CT, 256>;
-  kernel<<<static_cast<unsigned>((warps + 7) / 8), 256, 0, stream>>>(p);
   return finish_call(stream);
 }
 
@@ -312,9 +251,10 @@ kvc_status kvc_decode_attention_sinks(const void* q, const void* k_cache, const 
   if (!dtype_ok(dtype)) return fail(KVC_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(dtype));
   if (dtype == KVC_F32) return fail(KVC_ERR_UNSUPPORTED, "caches of 16-bit elements only (F16, BF16)");
   const ScoredShape s{batch, n_tokens, n_q_heads, n_kv_heads, head_dim, block_size, max_blocks_per_seq};
-  auto* decode = dtype == KVC_F16 ? decode_rows<__half> : decode_rows<__nv_bfloat16>;
-  return decode(s, q, dtype, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens, scale, num_blocks,
-                window, sinks, out, out_dtype, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+  const Stream win{window, sinks, nullptr, nullptr};
+  return decode(dtype == KVC_BF16 ? Cache::kBf16 : Cache::kF16, s, q, dtype, k_cache, v_cache, nullptr, nullptr,
+                block_tables, context_lens, scale, num_blocks, out, out_dtype, nullptr, workspace, workspace_bytes,
+                static_cast<cudaStream_t>(stream), &win);
 }
 
 kvc_status kvc_decode_attention_fp4(const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_scale,
@@ -330,10 +270,12 @@ kvc_status kvc_decode_attention_fp4(const void* q, const void* k_cache, const vo
   if (k_scale == nullptr || v_scale == nullptr) return fail(KVC_ERR_INVALID_ARG, "k_scale / v_scale is NULL");
   if (!aligned16(k_scale) || !aligned16(v_scale))
     return fail(KVC_ERR_INVALID_ARG, "k_scale and v_scale must be 16-byte aligned");
+  if (batch > kScored4MaxBatch) return fail(KVC_ERR_UNSUPPORTED, "batch %d > %d", batch, kScored4MaxBatch);
   const ScoredShape s{batch, n_tokens, n_q_heads, n_kv_heads, head_dim, block_size, max_blocks_per_seq};
-  return decode_rows<fp4e2m1>(s, q, q_dtype, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
-                              num_blocks, window, sinks, out, out_dtype, workspace, workspace_bytes,
-                              static_cast<cudaStream_t>(stream));
+  const Stream win{window, sinks, k_scale, v_scale};
+  return decode(Cache::kFp4, s, q, q_dtype, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens, scale,
+                num_blocks, out, out_dtype, nullptr, workspace, workspace_bytes, static_cast<cudaStream_t>(stream),
+                &win);
 }
 
 kvc_status kvc_decode_scored_workspace_size(int batch, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim,

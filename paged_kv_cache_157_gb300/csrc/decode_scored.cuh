@@ -1,6 +1,7 @@
 // Paged decode attention that also adds up the attention weight each cached
 // row receives, over 16-bit caches and over one-byte caches with one scale per
-// (block, kv head).
+// (block, kv head); and, without those weights, with a window and sinks, over
+// 16-bit caches and four-bit ones (see the end of this comment).
 //
 // Mathematics. Query v of a kv head (v = t * group + j: new token t, query
 // head j of the group) attends rows r <= n - n_tok + t:
@@ -43,12 +44,22 @@
 // are to be as good as an fp32 softmax; in large batches the extra products are
 // mostly hidden behind HBM. One-byte codes are exact f16 values and are converted
 // in registers; queries become f16 after a scaling by a power of two, per query.
+//
+// Window and sinks (WIN): the token at position pos sees row r if r <= pos and
+// (r > pos - window or r < sinks). A sequence's tiles are those that hold sinks,
+// then those from its window's first row on; between them nothing is looked up
+// or read. The masks cost only the tiles at either border.
+//
+// Four-bit caches (fp4e2m1): code * scale (e2m1 * e4m3) has 6 significant bits and is
+// exact in f16, so the products are those of f16 caches; a register of codes takes
+// one conversion and one multiplication by its scale on the way to the fragment.
 #pragma once
 
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
 
+#include "code4.cuh"
 #include "decode_gqa_mma.cuh"
 #include "decode_scored.h"
 
@@ -57,11 +68,12 @@ namespace kvc {
 namespace scored {
 
 // Byte offset of 16-byte chunk q of row r in a box of kBoxBytes-wide rows as
-// TMA leaves it: 128-byte swizzle (q ^ (r & 7)), or 64-byte swizzle
-// (q ^ ((r >> 1) & 3)).
+// TMA leaves it: 128-byte swizzle (q ^ (r & 7)), 64-byte swizzle
+// (q ^ ((r >> 1) & 3)) or 32-byte swizzle (q ^ ((r >> 2) & 1)).
 template <int BOXB>
 __device__ __forceinline__ uint32_t chunk_at(int r, int q) {
   if constexpr (BOXB == 128) return static_cast<uint32_t>(r * 128 + ((q ^ (r & 7)) << 4));
+  if constexpr (BOXB == 32) return static_cast<uint32_t>(r * 32 + ((q ^ ((r >> 2) & 1)) << 4));
   return static_cast<uint32_t>(r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
 }
 
@@ -127,6 +139,21 @@ __device__ __forceinline__ void mask_edge(float (&x)[NT][4], const State<D, NT, 
     if (g >= v1) x[n][1] = kNegInf;
     if (g + 8 >= v0) x[n][2] = kNegInf;
     if (g + 8 >= v1) x[n][3] = kNegInf;
+  }
+}
+
+// The same with a window: row r0 + g is visible if it is not behind the query's
+// own and lies in its window or before the sinks' end. sk: sinks - r0.
+template <int D, int NT, bool ONE>
+__device__ __forceinline__ void mask_window(float (&x)[NT][4], const State<D, NT, ONE>& st, int rem, int sk, int window,
+                                            int g) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int v = rem - st.dt[n][e & 1], row = g + 8 * (e >> 1);
+      if (row >= v || (row < v - window && row >= sk)) x[n][e] = kNegInf;
+    }
   }
 }
 
@@ -228,14 +255,14 @@ __device__ __forceinline__ void store_scores(const float (&x)[NT][4], float* lg,
   }
 }
 
-// Clears the V rows at and behind rem (< 16) of a tile: they may hold anything,
+// Clears the V rows at and behind rem (< 16) of a tile (up to `end`): they may hold anything,
 // and 0 x NaN is NaN. The fence orders these writes before the copy that
 // next fills the stage.
 template <int BOXB, int HALVES>
-__device__ __forceinline__ void clear_rows(uint32_t v, int rem, int lane) {
+__device__ __forceinline__ void clear_rows(uint32_t v, int rem, int lane, int end = kTileRows) {
   constexpr int CH = BOXB / 16;
 #pragma unroll 1
-  for (int i = rem * CH + lane; i < kTileRows * CH; i += 32) {
+  for (int i = rem * CH + lane; i < end * CH; i += 32) {
 #pragma unroll
     for (int h = 0; h < HALVES; ++h)
       asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + h * (kTileRows * BOXB) + i * 16), "r"(0u)
@@ -308,11 +335,13 @@ __device__ __forceinline__ void softmax_step(float (&x)[NT][4], State<D, NT, ONE
 
 // One 16-row tile of a 16-bit cache. k, v: the tile's boxes; rem: the
 // sequence's rows from the tile's first on; edge: some query does not see all
-// 16. (One body for both: small calls run every line once, and what they wait
+// 16; sk, dead: the sinks and the rows before the first token's window, counted
+// from the tile's first row. (One body for both: small calls run every line once, and what they wait
 // for then is instructions.)
-template <bool BF, int D, int NT>
+template <bool BF, int D, int NT, bool WIN>
 __device__ __forceinline__ void tile16(uint32_t k, uint32_t v, int rem, bool edge, float qscale, float* lg, int qns,
-                                       int col0, int qn, State<D, NT, false>& st, int lane) {
+                                       int col0, int qn, State<D, NT, false>& st, int lane, int sk = 0, int dead = 0,
+                                       int window = 0) {
   using namespace wmma16;
   constexpr int NP = BF ? 3 : 2;
   constexpr int CH = NT == 1 ? 4 : 2;  // independent accumulator chains
@@ -349,7 +378,13 @@ __device__ __forceinline__ void tile16(uint32_t k, uint32_t v, int rem, bool edg
     }
   }
   if (edge) {
-    mask_edge<D, NT, false>(x, st, rem, g);
+    if constexpr (WIN) {
+      mask_window<D, NT, false>(x, st, rem, sk, window, g);
+      // rows that nobody sees: [sk, dead) before the window
+      if (sk < dead) clear_rows<128, D / 64>(v, max(sk, 0), lane, min(dead, kTileRows));
+    } else {
+      mask_edge<D, NT, false>(x, st, rem, g);
+    }
     if (rem < kTileRows) clear_rows<128, D / 64>(v, rem, lane);
   }
   if (lg != nullptr) store_scores<NT>(x, lg, qns, col0, qn, rem, lane);
@@ -469,6 +504,135 @@ __device__ __forceinline__ void tile8(uint32_t k, uint32_t v, int rem, bool edge
   }
 }
 
+// One 16-row tile of a four-bit cache; ks, vs: the tile's scales in shared memory,
+// [16 rows][D / 16] e4m3. A lane's dims are those of tile8; its codes of one row
+// are decoded two dims to a register (K) or, with two rows' nibbles interleaved,
+// one dim of both rows (V), and multiplied by their group's scale. fq: qscale / the
+// query's power of two.
+template <int D, int NT>
+__device__ __forceinline__ void tile4(uint32_t k, uint32_t v, const unsigned char* ks, const unsigned char* vs, int rem,
+                                      bool edge, const float (&fq)[NT][2], State<D, NT, false>& st, int lane, int sk,
+                                      int dead, int window) {
+  using namespace wmma16;
+  constexpr int NP = 2;
+  constexpr int CH = NT == 1 ? 4 : 2;
+  constexpr int RB = D / 2;    // bytes of a row
+  constexpr int GR = D / 16;   // groups of a row
+  constexpr int LW = D / 32;   // words of a lane's codes (K): D / 4 dims
+  const int g = lane >> 2, c = lane & 3;
+  auto mul2 = [](uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  };
+  auto scales = [](uint32_t two) {  // two e4m3 codes as an f16 pair
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(two)));
+    return h;
+  };
+  float x[NT][4];
+  {
+    float sc[NT][CH][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[n][j][e] = 0.f;
+    uint32_t kw[2][LW], sw[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = g + 8 * h;
+      if constexpr (D == 64) {
+        const uint2 u = lds64(k + chunk_at<RB>(r, c >> 1) + 8 * (c & 1));
+        kw[h][0] = u.x;
+        kw[h][1] = u.y;
+        sw[h] = ks[r * GR + c] * 0x0101u;
+      } else {
+#pragma unroll
+        for (int j = 0; j < LW / 4; ++j) {
+          const uint4 u = lds128(k + chunk_at<RB>(r, (LW / 4) * c + j));
+          kw[h][4 * j] = u.x;
+          kw[h][4 * j + 1] = u.y;
+          kw[h][4 * j + 2] = u.z;
+          kw[h][4 * j + 3] = u.w;
+        }
+        sw[h] = D == 128 ? *reinterpret_cast<const unsigned short*>(ks + r * GR + 2 * c)
+                         : *reinterpret_cast<const uint32_t*>(ks + r * GR + 4 * c);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < LW; ++i) {  // eight dims: two k-steps; a group has two words
+      uint32_t a[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t two = scales(sw[h] >> (i / 4 * 16));
+        const uint32_t s = __byte_perm(two, two, (i / 2) & 1 ? 0x3232u : 0x1010u);
+        uint32_t d[4];
+        decode8_e2m1(kw[h][i], d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j >> 1][(j & 1) * 2 + h] = mul2(d[j], s);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma<false>(sc[n][(2 * i) % CH], a[0], st.q[n][2 * i][0], st.q[n][2 * i][1]);
+        mma<false>(sc[n][(2 * i + 1) % CH], a[1], st.q[n][2 * i + 1][0], st.q[n][2 * i + 1][1]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float s = sc[n][0][e] + sc[n][1][e];
+        if constexpr (CH == 4) s += sc[n][2][e] + sc[n][3][e];
+        x[n][e] = s * fq[n][e & 1];
+      }
+    }
+  }
+  if (edge) mask_window<D, NT, false>(x, st, rem, sk, window, g);
+  softmax_step<D, NT, false, false>(x, st, 0.f);
+  uint32_t b[NT][NP][2];
+  weight_parts<false, NT, NP>(x, b);
+  constexpr int SPANS = D <= 128 ? 1 : D / 128;
+  constexpr int VW = D == 64 ? 1 : 2;  // words of a lane's codes of a row and span: one group, or half of one
+#pragma unroll
+  for (int sp = 0; sp < SPANS; ++sp) {
+    uint32_t vw[4][VW], sb[4];  // rows 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = 2 * c + (j & 1) + 8 * (j >> 1);
+      if constexpr (D == 64) {
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw[j][0]) : "r"(v + chunk_at<RB>(r, g >> 2) + 4 * (g & 3)));
+        sb[j] = vs[r * GR + (g >> 1)];
+      } else {
+        const uint2 u = lds64(v + chunk_at<RB>(r, 4 * sp + (g >> 1)) + 8 * (g & 1));
+        vw[j][0] = u.x;
+        vw[j][1] = u.y;
+        sb[j] = vs[r * GR + 8 * sp + g];
+      }
+      // what rows that nobody sees hold does not count: their scale may be NaN
+      if (edge && (r >= rem || (r >= sk && r < dead))) sb[j] = 0;
+    }
+    const uint32_t s0 = scales(sb[0] | sb[1] << 8), s1 = scales(sb[2] | sb[3] << 8);
+#pragma unroll
+    for (int w = 0; w < VW; ++w) {  // four output tiles
+      uint32_t e[2][2][4];          // [rows 2c, + 1 or + 8, + 9][even or odd dim][tile]
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w0 = vw[2 * h][w], w1 = vw[2 * h + 1][w];
+        decode8_e2m1((w0 & 0x0f0f0f0fu) | ((w1 & 0x0f0f0f0fu) << 4), e[h][0]);
+        decode8_e2m1(((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), e[h][1]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a[4] = {mul2(e[0][0][i], s0), mul2(e[0][1][i], s0), mul2(e[1][0][i], s1), mul2(e[1][1][i], s1)};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) add_products<false, NP>(st.o[n][sp * 4 * VW + 4 * w + i], a, b[n]);
+      }
+    }
+  }
+}
+
 // The MMA column (query) g of column group n: its row of q and whether it exists.
 __device__ __forceinline__ int64_t query_row(const ScoredParams& p, int seq, int kvh, int v) {
   const int t = v / p.group;
@@ -483,14 +647,34 @@ __device__ __forceinline__ int valid_rows(const ScoredParams& p, int b) {
 
 __device__ __forceinline__ int tiles_of(int rows) { return (rows + kTileRows - 1) / kTileRows; }
 
+// The tiles of a sequence of `rows` rows: all, or with a window `front` ones that hold
+// sinks and those from `front + skip` on, so that the j-th is tile j < front ? j : j +
+// skip. low: first row of the first token's window.
+struct Seen16 {
+  int low, front, skip, tiles;
+};
+template <bool WIN>
+__device__ __forceinline__ Seen16 seen_of(const ScoredParams& p, int rows) {
+  Seen16 s{0, 0, 0, tiles_of(rows)};
+  if constexpr (WIN) {
+    s.low = max(0, rows - p.n_tok + 1 - p.window);
+    const int start = s.low / kTileRows;
+    s.front = min(tiles_of(min(p.sinks, s.low)), start);
+    s.skip = start - s.front;
+    s.tiles = max(0, s.tiles - s.skip);
+  }
+  return s;
+}
+
 // Exclusive prefix sums of the sequences' tiles into s_scan[0 .. batch]; the
 // whole CTA takes part. s_scan has batch + 33 entries.
+template <bool WIN>
 __device__ inline void scan_tiles(const ScoredParams& p, int* s_scan) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wid = tid >> 5, B = p.batch;
   const int per = (B + nt - 1) / nt;
   const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
   int local = 0;
-  for (int b = b0; b < b1; ++b) local += tiles_of(valid_rows(p, b));
+  for (int b = b0; b < b1; ++b) local += seen_of<WIN>(p, valid_rows(p, b)).tiles;
   int v = local;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -504,7 +688,7 @@ __device__ inline void scan_tiles(const ScoredParams& p, int* s_scan) {
   for (int i = 0; i < wid; ++i) run += wsum[i];
   for (int b = b0; b < b1; ++b) {
     s_scan[b] = run;
-    run += tiles_of(valid_rows(p, b));
+    run += seen_of<WIN>(p, valid_rows(p, b)).tiles;
     if (b == B - 1) s_scan[B] = run;
   }
   __syncthreads();
@@ -586,14 +770,23 @@ __device__ __forceinline__ int out_dim(int i, int g) {
 // (the sum of all: infinities of both signs make NaN) replaces the outputs of
 // the queries `cols` (bits), written before: part [8 NT, D], or p.out if NULL.
 // Rare, and out of the main loop's registers.
-template <typename CT, int D>
+//
+// With a window [r0, r1) counts rows of the sequence's tiles one behind the other
+// (see seen_of), and each query looks at every row that it sees.
+template <typename CT, int D, bool WIN>
 __device__ __noinline__ void give_odd_values(const ScoredParams& p, int seq, int kvh, int col0, uint32_t cols,
                                              int n_rows, int r0, int r1, float* part) {
   constexpr int PER = D / 32;  // dims per lane: lane, lane + 32, ..
   const int lane = threadIdx.x & 31;
-  auto search = [&](int from, int to, float (&z)[PER]) {
+  auto search = [&](int from, int to, float (&z)[PER], int pos) {
+    const Seen16 seen = seen_of<WIN>(p, n_rows);
 #pragma unroll 1
-    for (int r = from; r < to; ++r) {
+    for (int x = from; x < to; ++x) {
+      int r = x;
+      if constexpr (WIN) {
+        if (x >= seen.front * kTileRows) r += seen.skip * kTileRows;
+        if (r > pos || (r <= pos - p.window && r >= p.sinks)) continue;
+      }
       const int b = r / p.block_size;
       const int phys = __ldg(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks + b);
       if (phys < 0 || phys >= p.num_blocks) continue;
@@ -613,18 +806,18 @@ __device__ __noinline__ void give_odd_values(const ScoredParams& p, int seq, int
       }
     }
   };
-  const int shared_rows = n_rows - p.n_tok + 1;  // rows that all tokens see
+  const int shared_rows = WIN ? 0 : n_rows - p.n_tok + 1;  // rows that all tokens see
   float all[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) all[i] = 0.f;
-  search(r0, min(r1, shared_rows), all);
+  search(r0, min(r1, shared_rows), all, 0);
 #pragma unroll 1
   for (; cols != 0; cols &= cols - 1) {
     const int col = __ffs(cols) - 1, v = col0 + col, t = v / p.group;
     float z[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) z[i] = all[i];
-    search(max(r0, shared_rows), min(r1, shared_rows + t), z);
+    search(max(r0, shared_rows), WIN ? r1 : min(r1, shared_rows + t), z, n_rows - p.n_tok + t);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       if (z[i] == 0.f) continue;
@@ -646,15 +839,19 @@ __device__ __forceinline__ float record_weight(float m, float largest) {
 
 // SHUT: rows of the last tokens are searched for infinities and NaN, which
 // earlier tokens do not see (several new tokens; other calls are spared the code).
-template <typename CT, int D, int NT, bool SHUT>
-__global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
+// WIN: window and sinks, no scores.
+template <typename CT, int D, int NT, bool SHUT, bool WIN>
+__global__ void __launch_bounds__(GeoOf<CT, D, NT>::Type::kThreads, 1)
     scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const __grid_constant__ ScoredParams p) {
   using namespace scored;
-  constexpr bool ONE = sizeof(CT) == 1;
+  constexpr bool FOUR = std::is_same<CT, fp4e2m1>::value;  // (its weights are those of a 16-bit cache)
+  constexpr bool ONE = sizeof(CT) == 1 && !FOUR;
+  constexpr bool PLAIN = !ONE && !FOUR;                     // queries and rows as they are
   constexpr bool BF = std::is_same<CT, __nv_bfloat16>::value;
   constexpr int Q8 = std::is_same<CT, fp8e4m3>::value ? 1 : 2;
-  using G = ScoredGeo<sizeof(CT), D, NT>;
+  using G = typename GeoOf<CT, D, NT>::Type;
+  constexpr int SB = GeoOf<CT, D, NT>::kScaleBytes;
   constexpr int TS = G::kStageTiles, S = G::kStages, W = G::kWarps, NC = 8 * NT;
   constexpr uint32_t full = 0xffffffffu;
   static_assert(static_cast<size_t>(S) * G::kStageBytes >= (D + 2) * NC * 4, "a warp's part fits its ring");
@@ -665,8 +862,9 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
   unsigned char* smem = smem_raw + (base - raw);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + G::kRingBytes) + w * S;
-  float* s_scale = reinterpret_cast<float*>(smem + G::kRingBytes + W * S * 8) + w * S * TS * 2;
-  int* s_scan = reinterpret_cast<int*>(smem + G::kRingBytes + W * S * 8 + W * S * TS * 2 * 4);
+  unsigned char* s_scale4 = smem + G::kRingBytes + W * S * 8 + w * S * SB;
+  float* s_scale = reinterpret_cast<float*>(s_scale4);
+  int* s_scan = reinterpret_cast<int*>(smem + G::kRingBytes + W * S * 8 + W * S * SB);
   const uint32_t ring = base + static_cast<uint32_t>(w * S * G::kStageBytes);
 
   if (lane < S) mbar_init(bars + lane, 1);
@@ -687,7 +885,7 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
   if (p.batch <= 32) {
     bt.s_scan = nullptr;
     bt.rows = lane < p.batch ? valid_rows(p, lane) : 0;
-    bt.tiles = tiles_of(bt.rows);
+    bt.tiles = seen_of<WIN>(p, bt.rows).tiles;
     int v = bt.tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -697,7 +895,7 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
     bt.before = v - bt.tiles;
     bt.total = __shfl_sync(full, v, 31);
   } else {
-    scan_tiles(p, s_scan);  // ends with a CTA barrier
+    scan_tiles<WIN>(p, s_scan);  // ends with a CTA barrier
     bt.s_scan = s_scan;
     bt.rows = bt.tiles = bt.before = 0;
     bt.total = s_scan[p.batch];
@@ -736,6 +934,7 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
   // ---- copies: the next tiles of the range into the next stage
   int ipos = lo, iend = lo;
   int ij = 0, iseq = 0, ikvh = 0, wb = 0, tw = -1;
+  int ifront = 0, iskip = 0;  // the unit's tiles: j < front ? j : j + skip
   uint32_t islot = 0, ivalid = 0;  // ivalid: bit slot * TS + t: the tile's block is inside the pool
   int issued = 0;
   auto issue = [&]() {
@@ -747,18 +946,27 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
         ij = ipos - u.u0;
         iend = min(u.u0 + u.tiles, hi);
         wb = -64;  // no entries yet
+        if constexpr (WIN) {
+          const Seen16 seen = seen_of<true>(p, bt.rows_of(iseq, p));
+          ifront = seen.front;
+          iskip = seen.skip;
+        }
       }
-      const int cnt = min(iend - ipos, TS);
-      const int b_last = divided(ij + cnt - 1, m_tpb);
+      int cnt = min(iend - ipos, TS), ik = ij;  // ik: the first tile
+      if constexpr (WIN) {
+        if (ij < ifront) cnt = min(cnt, ifront - ij);  // a stage's tiles lie one behind the other
+        else ik += iskip;
+      }
+      const int b_last = divided(ik + cnt - 1, m_tpb);
       if (b_last >= wb + 32) {  // lane i holds the table's entry wb + i
-        wb = divided(ij, m_tpb);
+        wb = divided(ik, m_tpb);
         tw = wb + lane < p.max_blocks ? __ldg(p.block_tables + static_cast<int64_t>(iseq) * p.max_blocks + wb + lane)
                                       : -1;
       }
       // lane i copies box i: [tile][K or V][half]
       constexpr int PER = 2 * G::kHalves;
       const int t = lane / PER < cnt ? lane / PER : 0;
-      const int jt = ij + t, blk = divided(jt, m_tpb);
+      const int jt = ik + t, blk = divided(jt, m_tpb);
       const int phys = __shfl_sync(full, tw, blk - wb);
       const bool ok = phys >= 0 && phys < p.num_blocks;
       uint32_t mask = 0;
@@ -771,7 +979,7 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
         if (mask == 0)
           mbar_arrive(bar);
         else
-          mbar_arrive_expect_tx(bar, __popc(mask) * 2 * G::kTileBytes);
+          mbar_arrive_expect_tx(bar, __popc(mask) * 2 * (G::kTileBytes + (FOUR ? D : 0)));
         if (__popc(mask) != cnt) set_flag(p.err, KVC_FLAG_BAD_BLOCK);
       }
       __syncwarp();
@@ -782,11 +990,14 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
                              half * (kTileRows * G::kBoxBytes);
         wmma16::tma2d(dst, kv == 0 ? &tm_k : &tm_v, half * (G::kBoxBytes / static_cast<int>(sizeof(CT))), y,
                       smem_addr(bar), pol);
+        if constexpr (FOUR)  // the tile's scales: 16 rows of D / 16 bytes
+          bulk_g2s(s_scale4 + islot * SB + (t * 2 + kv) * D,
+                   (kv == 0 ? p.k_scale4 : p.v_scale4) + static_cast<int64_t>(y) * (D / 16), D, bar, pol);
       }
       if constexpr (ONE) {
         // lane i copies scale i: [tile][K or V]
         const int t2 = (lane >> 1) < cnt ? lane >> 1 : 0;
-        const int phys2 = __shfl_sync(full, tw, divided(ij + t2, m_tpb) - wb);
+        const int phys2 = __shfl_sync(full, tw, divided(ik + t2, m_tpb) - wb);
         if (lane < 2 * cnt && phys2 >= 0 && phys2 < p.num_blocks)
           cp_async4(smem_addr(s_scale + (islot * TS + t2) * 2 + (lane & 1)),
                     ((lane & 1) ? p.v_scale : p.k_scale) + static_cast<int64_t>(phys2) * p.n_kv_heads + ikvh);
@@ -806,7 +1017,9 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
   int held = -1;  // the unit of the part at the range's end
   const int lanes_g = lane >> 2, c = lane & 3;
   State<D, NT, ONE> st;
+  float fq4[FOUR ? NT : 1][2];  // four-bit caches: qscale / the query's power of two
   Unit u{};
+  Seen16 seen{0, 0, 0, 0};      // with a window: the unit's tiles
   int end = lo, n_rows = 0, col0 = 0, j = 0;
   int shared_rows = 0;  // rows that all tokens see
   bool odd = false;     // this segment met an infinity or NaN in V
@@ -820,6 +1033,7 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
       end = min(u.u0 + u.tiles, hi);
       n_rows = bt.rows_of(u.seq, p);
       shared_rows = n_rows - p.n_tok + 1;
+      if constexpr (WIN) seen = seen_of<true>(p, n_rows);
       col0 = u.hsub * NC;
       j = pos - u.u0;
       lg0 = p.scores == nullptr
@@ -834,7 +1048,7 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
         const int64_t qrow =
             (static_cast<int64_t>(u.seq) * p.n_tok + tq) * p.n_q_heads + u.kvh * p.group + v - tq * p.group;
         const unsigned short* qr = static_cast<const unsigned short*>(p.q) + (have ? qrow * D : 0);
-        if constexpr (!ONE) {
+        if constexpr (PLAIN) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
 #pragma unroll
@@ -852,7 +1066,7 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
           float amax = 0.f;
 #pragma unroll
           for (int s = 0; s < D / 16; ++s) {
-            const int d = (s / KS) * BOXB + (BOXB / 4) * c + 4 * (s % KS);
+            const int d = FOUR ? (D / 4) * c + 4 * s : (s / KS) * BOXB + (BOXB / 4) * c + 4 * (s % KS);
             uint2 u2 = make_uint2(0u, 0u);
             if (have) u2 = __ldg(reinterpret_cast<const uint2*>(qr + d));
             float2 a, b;
@@ -880,8 +1094,9 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
             st.q[n][s][0] = wmma16::pack2<false>(y[s][0] * up, y[s][1] * up);
             st.q[n][s][1] = wmma16::pack2<false>(y[s][2] * up, y[s][3] * up);
           }
-          st.fq[n][0] = __shfl_sync(full, down, 8 * c);      // of query 2c, held by the lanes with g = 2c
-          st.fq[n][1] = __shfl_sync(full, down, 8 * c + 4);  // of query 2c + 1
+          float (&fq)[2] = FOUR ? fq4[FOUR ? n : 0] : st.fq[ONE ? n : 0];
+          fq[0] = __shfl_sync(full, down, 8 * c);      // of query 2c, held by the lanes with g = 2c
+          fq[1] = __shfl_sync(full, down, 8 * c + 4);  // of query 2c + 1
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -898,7 +1113,11 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
         }
       }
     }
-    const int cnt = min(end - pos, TS);
+    int cnt = min(end - pos, TS), k0 = j;  // k0: the first tile, as issue() counts
+    if constexpr (WIN) {
+      if (j < seen.front) cnt = min(cnt, seen.front - j);
+      else k0 += seen.skip;
+    }
     ok = mbar_wait_data(bars + slot, ph, p.wait_polls);
     ok = __all_sync(full, ok);
     if (!ok) break;
@@ -906,7 +1125,24 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
       cp_async_wait<S - 1>();
       __syncwarp();
     }
-    if constexpr (SHUT) {
+    if constexpr (SHUT && WIN) {
+      // rows that some of the tokens see: the newest, and those that leave the window
+      const int leave = n_rows - p.window;  // first row of the last token's window
+      if ((k0 + cnt) * kTileRows > shared_rows || (k0 * kTileRows < leave && (k0 + cnt) * kTileRows > p.sinks)) {
+        constexpr uint32_t FIELD = BF ? 0x7f807f80u : 0x7c007c00u, LOW = BF ? 0x00800080u : 0x04000400u;
+#pragma unroll 1
+        for (int t = 0; t < cnt; ++t) {
+          const int r0 = (k0 + t) * kTileRows;
+          if (((ivalid >> (slot * TS + t)) & 1u) == 0) continue;
+          const uint32_t vt = ring + slot * G::kStageBytes + (2 * t + 1) * G::kTileBytes;
+          const int a = max(max(shared_rows - r0, 0), 0), b = min(n_rows - r0, kTileRows);
+          if (a < b) odd |= clean_rows<G::kBoxBytes, G::kHalves, FIELD, LOW>(vt, a, b, lane);
+          const int d = max(max(seen.low, p.sinks) - r0, 0), e = min(min(leave, shared_rows) - r0, kTileRows);
+          if (d < e) odd |= clean_rows<G::kBoxBytes, G::kHalves, FIELD, LOW>(vt, d, e, lane);
+        }
+      }
+    }
+    if constexpr (SHUT && !WIN) {
       if ((j + cnt) * kTileRows > shared_rows) {
         constexpr uint32_t FIELD = ONE ? 0x7f7f7f7fu : BF ? 0x7f807f80u : 0x7c007c00u;
         constexpr uint32_t LOW = ONE ? 0x01010101u : BF ? 0x00800080u : 0x04000400u;
@@ -922,17 +1158,24 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
     }
 #pragma unroll 1
     for (int t = 0; t < cnt; ++t) {
-      const int r0 = (j + t) * kTileRows;
+      const int r0 = (k0 + t) * kTileRows;
       const int rem = n_rows - r0;
       float* lg = lg0 == nullptr ? nullptr : lg0 + static_cast<int64_t>(r0) * p.qns;
       const uint32_t kt = ring + slot * G::kStageBytes + t * 2 * G::kTileBytes, vt = kt + G::kTileBytes;
       if ((ivalid >> (slot * TS + t)) & 1u) {
-        const bool edge = rem < kTileRows + p.n_tok - 1;
-        if constexpr (ONE) {
+        const bool edge = rem < kTileRows + p.n_tok - 1 ||
+                          (WIN && rem > p.window && r0 + kTileRows > p.sinks);  // before the last token's window
+        if constexpr (FOUR) {
+          const unsigned char* sc = s_scale4 + slot * SB + t * 2 * D;
+          tile4<D, NT>(kt, vt, sc, sc + D, rem, edge, fq4, st, lane, p.sinks - r0, seen.low - r0, p.window);
+        } else if constexpr (ONE) {
           const float* sc = s_scale + (slot * TS + t) * 2;
           tile8<Q8, D, NT>(kt, vt, rem, edge, sc[0], sc[1], lg, p.qns, col0, p.qn, st, lane);
+        } else if constexpr (WIN) {
+          tile16<BF, D, NT, true>(kt, vt, rem, edge, p.qscale, nullptr, p.qns, col0, p.qn, st, lane, p.sinks - r0,
+                                  seen.low - r0, p.window);
         } else {
-          tile16<BF, D, NT>(kt, vt, rem, edge, p.qscale, lg, p.qns, col0, p.qn, st, lane);
+          tile16<BF, D, NT, false>(kt, vt, rem, edge, p.qscale, lg, p.qns, col0, p.qn, st, lane);
         }
       } else if (lg != nullptr) {  // a block outside the pool: its rows get no weight
         const int cols = min(NC, p.qns - col0);
@@ -970,8 +1213,8 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
     float* so = reinterpret_cast<float*>(smem + static_cast<size_t>(w) * S * G::kStageBytes);
     const int64_t rec = 2ll * wk + (last_part ? 1 : 0);
     if (keep) __syncwarp();
-    auto dim = [&](int i) { return out_dim<D, ONE>(i, lanes_g); };
-    constexpr int SECOND = ONE ? 1 : 8;
+    auto dim = [&](int i) { return out_dim<D, !PLAIN>(i, lanes_g); };
+    constexpr int SECOND = PLAIN ? 8 : 1;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -1017,8 +1260,8 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
         if (p.scores != nullptr && lanes_g == 0) p.lse[row] = st.m[n][e] + fast_log2(l);
       }
     }
-    if constexpr (!ONE || SHUT) {
-      if constexpr (!ONE) {
+    if constexpr (PLAIN || SHUT) {
+      if constexpr (PLAIN) {
         float zero = 0.f;  // NaN if an output is not finite
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -1046,8 +1289,8 @@ __global__ void __launch_bounds__(ScoredGeo<sizeof(CT), D, NT>::kThreads, 1)
         }
         __syncwarp();  // the segment's outputs have been written
         if (cols != 0)
-          give_odd_values<CT, D>(p, u.seq, u.kvh, col0, cols, n_rows, (begin - u.u0) * kTileRows,
-                                 min(n_rows, (pos - u.u0) * kTileRows),
+          give_odd_values<CT, D, WIN>(p, u.seq, u.kvh, col0, cols, n_rows, (begin - u.u0) * kTileRows,
+                                 WIN ? (pos - u.u0) * kTileRows : min(n_rows, (pos - u.u0) * kTileRows),
                                  whole ? nullptr : keep ? so : p.rec_o + rec * NC * D);
         odd = false;
       }
@@ -1449,12 +1692,13 @@ __global__ void __launch_bounds__(kFinishThreads, SCORED ? 4 : 2)
 
 namespace scored {
 
-template <typename CT, int D, int NT, bool SHUT>
+template <typename CT, int D, int NT, bool SHUT, bool WIN>
 kvc_status run_decode(const ScoredParams& p, int grid, const CUtensorMap& tk, const CUtensorMap& tv,
                       cudaLaunchAttribute* attr, cudaStream_t stream) {
-  static_assert(scored_warps(sizeof(CT), D, NT) == ScoredGeo<sizeof(CT), D, NT>::kWarps,
-                "the host counts a CTA's workers as the kernel does");
-  auto* k = scored_decode_kernel<CT, D, NT, SHUT>;
+  using G = typename GeoOf<CT, D, NT>::Type;
+  static_assert(scored_warps(sizeof(CT), D, NT) == G::kWarps, "the host counts a CTA's workers as the kernel does");
+  static_assert(scored_smem_bytes<CT, D, NT>(GeoOf<CT, D, NT>::kMaxBatch) <= 227 * 1024, "shared memory of a CTA");
+  auto* k = scored_decode_kernel<CT, D, NT, SHUT, WIN>;
   // The opt-in to large shared memory holds per device: made at the first call on each.
   static std::atomic<uint64_t> opted{0};
   int dev = 0;
@@ -1463,14 +1707,14 @@ kvc_status run_decode(const ScoredParams& p, int grid, const CUtensorMap& tk, co
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if ((opted.load() & bit) == 0) {
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(scored_smem_bytes<sizeof(CT), D, NT>(kScoredMaxBatch)));
+                             static_cast<int>(scored_smem_bytes<CT, D, NT>(GeoOf<CT, D, NT>::kMaxBatch)));
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(scored decode)");
     opted.fetch_or(bit);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(ScoredGeo<sizeof(CT), D, NT>::kThreads);
-  cfg.dynamicSmemBytes = scored_smem_bytes<sizeof(CT), D, NT>(p.batch);
+  cfg.blockDim = dim3(G::kThreads);
+  cfg.dynamicSmemBytes = scored_smem_bytes<CT, D, NT>(p.batch);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -1478,14 +1722,15 @@ kvc_status run_decode(const ScoredParams& p, int grid, const CUtensorMap& tk, co
   return e == cudaSuccess ? KVC_OK : cuda_fail(e, "cudaLaunchKernelEx(scored decode)");
 }
 
-template <typename CT, int D, int NT>
+template <typename CT, int D, int NT, bool WIN>
 kvc_status run(const ScoredParams& p, int grid, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  constexpr bool FINITE = std::is_same<CT, s8q>::value;  // every int8 code is
-  const kvc_status st = FINITE || p.n_tok == 1 ? run_decode<CT, D, NT, false>(p, grid, tk, tv, attr, stream)
-                                               : run_decode<CT, D, NT, !FINITE>(p, grid, tk, tv, attr, stream);
+  // every int8 and e2m1 code is
+  constexpr bool FINITE = std::is_same<CT, s8q>::value || std::is_same<CT, fp4e2m1>::value;
+  const kvc_status st = FINITE || p.n_tok == 1 ? run_decode<CT, D, NT, false, WIN>(p, grid, tk, tv, attr, stream)
+                                               : run_decode<CT, D, NT, !FINITE, WIN>(p, grid, tk, tv, attr, stream);
   if (st != KVC_OK) return st;
   // CTAs per (sequence, kv head): one wave of them on the GPU, no more than
   // there is work for. For the outputs a warp per query or a few of them in
@@ -1517,14 +1762,26 @@ kvc_status run(const ScoredParams& p, int grid, const CUtensorMap& tk, const CUt
 
 }  // namespace scored
 
+template <typename CT, bool WIN>
+kvc_status launch_decode(const ScoredParams& p, int D, int nt, int grid, const CUtensorMap& tk, const CUtensorMap& tv,
+                         cudaStream_t stream) {
+  if (D == 64 && nt == 1) return scored::run<CT, 64, 1, WIN>(p, grid, tk, tv, stream);
+  if (D == 64) return scored::run<CT, 64, 2, WIN>(p, grid, tk, tv, stream);
+  if (D == 128 && nt == 1) return scored::run<CT, 128, 1, WIN>(p, grid, tk, tv, stream);
+  if (D == 128) return scored::run<CT, 128, 2, WIN>(p, grid, tk, tv, stream);
+  return scored::run<CT, 256, 1, WIN>(p, grid, tk, tv, stream);
+}
+
 template <typename CT>
 kvc_status scored_launch(const ScoredParams& p, int D, int nt, int grid, const CUtensorMap& tk, const CUtensorMap& tv,
                          cudaStream_t stream) {
-  if (D == 64 && nt == 1) return scored::run<CT, 64, 1>(p, grid, tk, tv, stream);
-  if (D == 64) return scored::run<CT, 64, 2>(p, grid, tk, tv, stream);
-  if (D == 128 && nt == 1) return scored::run<CT, 128, 1>(p, grid, tk, tv, stream);
-  if (D == 128) return scored::run<CT, 128, 2>(p, grid, tk, tv, stream);
-  return scored::run<CT, 256, 1>(p, grid, tk, tv, stream);
+  return launch_decode<CT, false>(p, D, nt, grid, tk, tv, stream);
+}
+
+template <typename CT>
+kvc_status stream_launch(const ScoredParams& p, int D, int nt, int grid, const CUtensorMap& tk, const CUtensorMap& tv,
+                         cudaStream_t stream) {
+  return launch_decode<CT, true>(p, D, nt, grid, tk, tv, stream);
 }
 
 }  // namespace kvc

@@ -1,6 +1,7 @@
-// Parameters of the weight-accumulating decode (kvc_decode_attention_scored)
-// and of the decode over block-scaled one-byte caches
-// (kvc_decode_attention_block8), shared by the host planner and the kernels.
+// Parameters of the weight-accumulating decode (kvc_decode_attention_scored), of
+// the decode over block-scaled one-byte caches (kvc_decode_attention_block8) and
+// of the decodes with a window and sinks (kvc_decode_attention_sinks,
+// kvc_decode_attention_fp4), shared by the host planner and the kernels.
 #pragma once
 
 #include <cuda.h>
@@ -20,6 +21,8 @@ struct ScoredParams {
   const void* v_cache;
   const float* k_scale;         // one-byte caches: [num_blocks, n_kv_heads]
   const float* v_scale;
+  const unsigned char* k_scale4;  // four-bit caches: e4m3 [num_blocks, n_kv_heads, block_size, D / 16]
+  const unsigned char* v_scale4;
   void* out;      // [batch, n_tok, n_q_heads, D]
   float* scores;  // [batch, n_kv_heads, rows]; NULL: weights are not accumulated
   // workspace
@@ -44,6 +47,7 @@ struct ScoredParams {
   int min_tiles;  // tiles a worker takes at least
   float qscale;   // scale * log2(e)
   unsigned int wait_polls;
+  int window, sinks;  // calls with a window: both at most 2^30
 };
 
 // ScoredParams::units entries: x = the first worker that holds tiles of the
@@ -54,6 +58,7 @@ constexpr int kUnitEmpty = -2;  // the sequence's length is invalid: outputs are
 
 constexpr int kTileRows = 16;
 constexpr int kScoredMaxBatch = 4096;
+constexpr int kScored4MaxBatch = 2048;  // four-bit caches: their scales take the shared memory of longer prefix sums
 constexpr int kScoredMaxTokens = 256;
 constexpr int kScoredMaxQueries = 4096;  // n_tok * group: their denominators sit in shared memory
 
@@ -80,12 +85,46 @@ struct ScoredGeo {
   static constexpr size_t kRingBytes = static_cast<size_t>(kWarps) * kStages * kStageBytes;
 };
 
+// e2m1 codes, two to a byte.
+struct fp4e2m1 {
+  unsigned char bits;
+};
+
+// The same for four-bit caches: 8 KB of codes (2 to 8 tile pairs) and 1 KB of
+// scales per stage.
+template <int D, int NT>
+struct Scored4Geo {
+  static constexpr int kRowBytes = D / 2;
+  static constexpr int kBoxBytes = kRowBytes;  // 32, 64 or 128: the swizzled span
+  static constexpr int kHalves = 1;
+  static constexpr int kTileBytes = kTileRows * kRowBytes;
+  static constexpr int kStageTiles = 8192 / (2 * kTileBytes);
+  static constexpr int kStageBytes = 8192;
+  static constexpr int kWarps = D <= 128 && NT == 1 ? 12 : 8;
+  static constexpr int kStages = kWarps == 12 ? 2 : 3;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr size_t kRingBytes = static_cast<size_t>(kWarps) * kStages * kStageBytes;
+};
+
+template <typename CT, int D, int NT>
+struct GeoOf {
+  using Type = ScoredGeo<sizeof(CT), D, NT>;
+  static constexpr int kScaleBytes = Type::kStageTiles * 2 * 4;  // of a stage
+  static constexpr int kMaxBatch = kScoredMaxBatch;
+};
+template <int D, int NT>
+struct GeoOf<fp4e2m1, D, NT> {
+  using Type = Scored4Geo<D, NT>;
+  static constexpr int kScaleBytes = Type::kStageTiles * 2 * D;  // 16 rows of D / 16
+  static constexpr int kMaxBatch = kScored4MaxBatch;
+};
+
 // Shared memory: [ring, 1024-byte aligned][full barriers][scales of the
 // stages' tiles][prefix sums of the sequences' tiles].
-template <int ELT, int D, int NT>
+template <typename CT, int D, int NT>
 __host__ __device__ constexpr size_t scored_smem_bytes(int batch) {
-  using G = ScoredGeo<ELT, D, NT>;
-  return 1024 + G::kRingBytes + G::kWarps * G::kStages * 8 + G::kWarps * G::kStages * G::kStageTiles * 2 * 4 +
+  using G = typename GeoOf<CT, D, NT>::Type;
+  return 1024 + G::kRingBytes + G::kWarps * G::kStages * 8 + G::kWarps * G::kStages * GeoOf<CT, D, NT>::kScaleBytes +
          (static_cast<size_t>(batch) + 1 + 32) * 4;
 }
 
@@ -99,7 +138,10 @@ constexpr int scored_warps(int elt, int D, int nt) {
 }
 
 // Launches the decode and its finishing kernel. CT: __nv_bfloat16, __half,
-// fp8e4m3 or s8q.
+// fp8e4m3 or s8q; with a window and sinks __nv_bfloat16, __half or fp4e2m1.
+template <typename CT>
+kvc_status stream_launch(const ScoredParams& p, int D, int nt, int grid, const CUtensorMap& tk, const CUtensorMap& tv,
+                         cudaStream_t stream);
 template <typename CT>
 kvc_status scored_launch(const ScoredParams& p, int D, int nt, int grid, const CUtensorMap& tk, const CUtensorMap& tv,
                          cudaStream_t stream);

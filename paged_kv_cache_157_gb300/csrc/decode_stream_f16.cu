@@ -1,0 +1,9 @@
+// Decode with a window and sinks, f16 caches.
+#include "decode_scored.cuh"
+
+namespace kvc {
+
+template kvc_status stream_launch<__half>(const ScoredParams&, int, int, int, const CUtensorMap&, const CUtensorMap&,
+                                      cudaStream_t);
+
+}  // namespace kvc
