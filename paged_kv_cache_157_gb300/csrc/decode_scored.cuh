@@ -194,12 +194,12 @@ __device__ __forceinline__ void raise_references(const float (&x)[NT][4], State<
 }
 
 // The weights' B fragments: parts of the 16-bit type, transposed from the C
-// fragment [rows][queries] to [rows = k][queries = n]. bf16: their sum is the
-// weight; f16: the first plus the second / kRestScale.
-template <bool BF, int NT, int NP>
+// fragment [rows][queries] to [rows = k][queries = n]. bf16, or not SCALED: their
+// sum is the weight; f16: the first plus the second / kRestScale.
+template <bool BF, int NT, int NP, bool SCALED = true>
 __device__ __forceinline__ void weight_parts(const float (&w)[NT][4], uint32_t (&b)[NT][NP][2]) {
   using namespace wmma16;
-  constexpr float SCALE = BF ? 1.f : kRestScale;
+  constexpr float SCALE = BF || !SCALED ? 1.f : kRestScale;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     float r0 = w[n][0], r1 = w[n][1], r2 = w[n][2], r3 = w[n][3];
@@ -220,12 +220,12 @@ __device__ __forceinline__ void weight_parts(const float (&w)[NT][4], uint32_t (
 }
 
 // o += a . (the weights' parts) for one output tile.
-template <bool BF, int NP>
+template <bool BF, int NP, bool SCALED = true>
 __device__ __forceinline__ void add_products(float (&o)[4], const uint32_t (&a)[4], const uint32_t (&b)[NP][2]) {
   using namespace wmma16;
-  if constexpr (BF) {
+  if constexpr (BF || !SCALED) {
 #pragma unroll
-    for (int j = 0; j < NP; ++j) mma<true>(o, a, b[j][0], b[j][1]);
+    for (int j = 0; j < NP; ++j) mma<BF>(o, a, b[j][0], b[j][1]);
   } else {
     static_assert(NP == 2, "a weight and its scaled rest");
     float rest[4] = {0.f, 0.f, 0.f, 0.f};
@@ -504,18 +504,23 @@ __device__ __forceinline__ void tile8(uint32_t k, uint32_t v, int rem, bool edge
   }
 }
 
-// One 16-row tile of a four-bit cache; ks, vs: the tile's scales in shared memory,
-// [16 rows][D / 16] e4m3. A lane's dims are those of tile8; its codes of one row
-// are decoded two dims to a register (K) or, with two rows' nibbles interleaved,
-// one dim of both rows (V), and multiplied by their group's scale. fq: qscale / the
-// query's power of two.
-template <int D, int NT>
-__device__ __forceinline__ void tile4(uint32_t k, uint32_t v, const unsigned char* ks, const unsigned char* vs, int rem,
-                                      bool edge, const float (&fq)[NT][2], State<D, NT, false>& st, int lane, int sk,
-                                      int dead, int window) {
+// R neighbouring 16-row tiles of a four-bit cache (their boxes and scales `step` and
+// 2 D bytes apart); ks, vs: the first one's scales in shared memory, [16 rows][D / 16]
+// e4m3; rem: rows of the sequence from each tile's first on, 0 for a tile that is
+// not there or whose block lies outside the pool. Two tiles at once have two chains
+// of conversions and products to interleave and one vote: 40.0 -> %s us for 32 x
+// U[512, 4096].
+//
+// A lane's dims are those of tile8; its codes of one row are decoded two dims to a
+// register (K) or, with two rows' nibbles interleaved, one dim of both rows (V), and
+// multiplied by their group's scale. fq: qscale / the query's power of two.
+template <int D, int NT, int R>
+__device__ __forceinline__ void tile4(uint32_t k, uint32_t v, uint32_t step, const unsigned char* ks,
+                                      const unsigned char* vs, const int (&rem)[R], bool edge, const float (&fq)[NT][2],
+                                      State<D, NT, false>& st, int lane, int sk, int dead, int window) {
   using namespace wmma16;
   constexpr int NP = 2;
-  constexpr int CH = NT == 1 ? 4 : 2;
+  constexpr int CH = NT == 1 && R == 1 ? 4 : 2;
   constexpr int RB = D / 2;    // bytes of a row
   constexpr int GR = D / 16;   // groups of a row
   constexpr int LW = D / 32;   // words of a lane's codes (K): D / 4 dims
@@ -530,8 +535,11 @@ __device__ __forceinline__ void tile4(uint32_t k, uint32_t v, const unsigned cha
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(two)));
     return h;
   };
-  float x[NT][4];
-  {
+  float x[R][NT][4];
+#pragma unroll
+  for (int rt = 0; rt < R; ++rt) {
+    const uint32_t kt = k + rt * step;
+    const unsigned char* kst = ks + rt * 2 * D;
     float sc[NT][CH][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -544,21 +552,21 @@ __device__ __forceinline__ void tile4(uint32_t k, uint32_t v, const unsigned cha
     for (int h = 0; h < 2; ++h) {
       const int r = g + 8 * h;
       if constexpr (D == 64) {
-        const uint2 u = lds64(k + chunk_at<RB>(r, c >> 1) + 8 * (c & 1));
+        const uint2 u = lds64(kt + chunk_at<RB>(r, c >> 1) + 8 * (c & 1));
         kw[h][0] = u.x;
         kw[h][1] = u.y;
-        sw[h] = ks[r * GR + c] * 0x0101u;
+        sw[h] = kst[r * GR + c] * 0x0101u;
       } else {
 #pragma unroll
         for (int j = 0; j < LW / 4; ++j) {
-          const uint4 u = lds128(k + chunk_at<RB>(r, (LW / 4) * c + j));
+          const uint4 u = lds128(kt + chunk_at<RB>(r, (LW / 4) * c + j));
           kw[h][4 * j] = u.x;
           kw[h][4 * j + 1] = u.y;
           kw[h][4 * j + 2] = u.z;
           kw[h][4 * j + 3] = u.w;
         }
-        sw[h] = D == 128 ? *reinterpret_cast<const unsigned short*>(ks + r * GR + 2 * c)
-                         : *reinterpret_cast<const uint32_t*>(ks + r * GR + 4 * c);
+        sw[h] = D == 128 ? *reinterpret_cast<const unsigned short*>(kst + r * GR + 2 * c)
+                         : *reinterpret_cast<const uint32_t*>(kst + r * GR + 4 * c);
       }
     }
 #pragma unroll
@@ -585,49 +593,113 @@ __device__ __forceinline__ void tile4(uint32_t k, uint32_t v, const unsigned cha
       for (int e = 0; e < 4; ++e) {
         float s = sc[n][0][e] + sc[n][1][e];
         if constexpr (CH == 4) s += sc[n][2][e] + sc[n][3][e];
-        x[n][e] = s * fq[n][e & 1];
+        x[rt][n][e] = s * fq[n][e & 1];
       }
     }
   }
-  if (edge) mask_window<D, NT, false>(x, st, rem, sk, window, g);
-  softmax_step<D, NT, false, false>(x, st, 0.f);
-  uint32_t b[NT][NP][2];
-  weight_parts<false, NT, NP>(x, b);
+  if (edge) {
+#pragma unroll
+    for (int rt = 0; rt < R; ++rt) mask_window<D, NT, false>(x[rt], st, rem[rt], sk - 16 * rt, window, g);
+  }
+  // ---- running softmax: one vote for all tiles
+  constexpr float BELOW = Margin<false>::kBelow, ABOVE = Margin<false>::kAbove;
+  float top[NT][2];
+  bool need = false;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      top[n][e] = fmaxf(x[0][n][e], x[0][n][e + 2]);
+#pragma unroll
+      for (int rt = 1; rt < R; ++rt) top[n][e] = fmaxf(top[n][e], fmaxf(x[rt][n][e], x[rt][n][e + 2]));
+      need |= top[n][e] > st.m[n][e] + ABOVE;
+    }
+  }
+  if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float f[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float t = top[n][e];
+#pragma unroll
+        for (int msk = 4; msk < 32; msk <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, msk));
+        const float m = fmaxf(st.m[n][e], t - BELOW);
+        f[e] = fast_exp2(st.m[n][e] - m);
+        st.l[n][e] *= f[e];
+        st.m[n][e] = m;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.o[n][i][e] *= f[e & 1];
+      }
+    }
+  }
+  // The rest of a weight as it is, not scaled up: the parts give 22 bits down to
+  // 2^-14 of the largest weight and 11 at 2^-25, for values of 6 bits (a scaled rest
+  // took 64 of 530 instructions per tile).
+  uint32_t b[R][NT][NP][2];
+#pragma unroll
+  for (int rt = 0; rt < R; ++rt) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float p = fast_exp2(x[rt][n][e] - st.m[n][e & 1]);
+        st.l[n][e & 1] += p;
+        x[rt][n][e] = p;
+      }
+    }
+    weight_parts<false, NT, NP, false>(x[rt], b[rt]);
+  }
   constexpr int SPANS = D <= 128 ? 1 : D / 128;
   constexpr int VW = D == 64 ? 1 : 2;  // words of a lane's codes of a row and span: one group, or half of one
 #pragma unroll
-  for (int sp = 0; sp < SPANS; ++sp) {
-    uint32_t vw[4][VW], sb[4];  // rows 2c, 2c + 1, 2c + 8, 2c + 9
+  for (int rt = 0; rt < R; ++rt) {
+    const uint32_t vt = v + rt * step;
+    const unsigned char* vst = vs + rt * 2 * D;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = 2 * c + (j & 1) + 8 * (j >> 1);
-      if constexpr (D == 64) {
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw[j][0]) : "r"(v + chunk_at<RB>(r, g >> 2) + 4 * (g & 3)));
-        sb[j] = vs[r * GR + (g >> 1)];
-      } else {
-        const uint2 u = lds64(v + chunk_at<RB>(r, 4 * sp + (g >> 1)) + 8 * (g & 1));
-        vw[j][0] = u.x;
-        vw[j][1] = u.y;
-        sb[j] = vs[r * GR + 8 * sp + g];
+    for (int sp = 0; sp < SPANS; ++sp) {
+      uint32_t vw[4][VW], sb[4];  // rows 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = 2 * c + (j & 1) + 8 * (j >> 1);
+        if constexpr (D == 64) {
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw[j][0]) : "r"(vt + chunk_at<RB>(r, g >> 2) + 4 * (g & 3)));
+          sb[j] = vst[r * GR + (g >> 1)];
+        } else {
+          const uint2 u = lds64(vt + chunk_at<RB>(r, 4 * sp + (g >> 1)) + 8 * (g & 1));
+          vw[j][0] = u.x;
+          vw[j][1] = u.y;
+          sb[j] = vst[r * GR + 8 * sp + g];
+        }
       }
       // what rows that nobody sees hold does not count: their scale may be NaN
-      if (edge && (r >= rem || (r >= sk && r < dead))) sb[j] = 0;
-    }
-    const uint32_t s0 = scales(sb[0] | sb[1] << 8), s1 = scales(sb[2] | sb[3] << 8);
+      if (edge) {
 #pragma unroll
-    for (int w = 0; w < VW; ++w) {  // four output tiles
-      uint32_t e[2][2][4];          // [rows 2c, + 1 or + 8, + 9][even or odd dim][tile]
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t w0 = vw[2 * h][w], w1 = vw[2 * h + 1][w];
-        decode8_e2m1((w0 & 0x0f0f0f0fu) | ((w1 & 0x0f0f0f0fu) << 4), e[h][0]);
-        decode8_e2m1(((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), e[h][1]);
+        for (int j = 0; j < 4; ++j) {
+          const int r = 2 * c + (j & 1) + 8 * (j >> 1);
+          if (r >= rem[rt] || (r >= sk - 16 * rt && r < dead - 16 * rt)) sb[j] = 0;
+        }
       }
+      const uint32_t s0 = scales(sb[0] | sb[1] << 8), s1 = scales(sb[2] | sb[3] << 8);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t a[4] = {mul2(e[0][0][i], s0), mul2(e[0][1][i], s0), mul2(e[1][0][i], s1), mul2(e[1][1][i], s1)};
+      for (int w = 0; w < VW; ++w) {  // four output tiles
+        uint32_t e[2][2][4];          // [rows 2c, + 1 or + 8, + 9][even or odd dim][tile]
 #pragma unroll
-        for (int n = 0; n < NT; ++n) add_products<false, NP>(st.o[n][sp * 4 * VW + 4 * w + i], a, b[n]);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t w0 = vw[2 * h][w], w1 = vw[2 * h + 1][w];
+          decode8_e2m1((w0 & 0x0f0f0f0fu) | ((w1 & 0x0f0f0f0fu) << 4), e[h][0]);
+          decode8_e2m1(((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), e[h][1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a[4] = {mul2(e[0][0][i], s0), mul2(e[0][1][i], s0), mul2(e[1][0][i], s1),
+                                 mul2(e[1][1][i], s1)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) add_products<false, NP, false>(st.o[n][sp * 4 * VW + 4 * w + i], a, b[rt][n]);
+        }
       }
     }
   }
@@ -970,9 +1042,10 @@ __global__ void __launch_bounds__(GeoOf<CT, D, NT>::Type::kThreads, 1)
       const int phys = __shfl_sync(full, tw, blk - wb);
       const bool ok = phys >= 0 && phys < p.num_blocks;
       uint32_t mask = 0;
+      const uint32_t oks = __ballot_sync(full, ok);
 #pragma unroll
       for (int i = 0; i < TS; ++i)
-        if (i < cnt) mask |= (__shfl_sync(full, ok ? 1u : 0u, i * PER)) << i;
+        if (i < cnt) mask |= ((oks >> (i * PER)) & 1u) << i;
       ivalid = (ivalid & ~(((1u << TS) - 1u) << (islot * TS))) | (mask << (islot * TS));
       uint64_t* bar = bars + islot;
       if (lane == 0) {
@@ -1156,6 +1229,24 @@ __global__ void __launch_bounds__(GeoOf<CT, D, NT>::Type::kThreads, 1)
         }
       }
     }
+    if constexpr (FOUR) {
+      constexpr int R = NT == 1 && D <= 128 ? 2 : 1;  // (two tiles of more would spill)
+#pragma unroll 1
+      for (int t = 0; t < cnt; t += R) {
+        const int r0 = (k0 + t) * kTileRows;
+        int rem[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          rem[i] = t + i < cnt && ((ivalid >> (slot * TS + t + i)) & 1u) ? n_rows - r0 - 16 * i : 0;
+        bool edge = WIN && n_rows - r0 > p.window && r0 + R * kTileRows > p.sinks;  // before the last token's window
+#pragma unroll
+        for (int i = 0; i < R; ++i) edge |= rem[i] < kTileRows + p.n_tok - 1;
+        const unsigned char* sc = s_scale4 + slot * SB + t * 2 * D;
+        const uint32_t kt = ring + slot * G::kStageBytes + t * 2 * G::kTileBytes;
+        tile4<D, NT, R>(kt, kt + G::kTileBytes, 2 * G::kTileBytes, sc, sc + D, rem, edge, fq4, st, lane, p.sinks - r0,
+                        seen.low - r0, p.window);
+      }
+    } else
 #pragma unroll 1
     for (int t = 0; t < cnt; ++t) {
       const int r0 = (k0 + t) * kTileRows;
@@ -1165,10 +1256,7 @@ __global__ void __launch_bounds__(GeoOf<CT, D, NT>::Type::kThreads, 1)
       if ((ivalid >> (slot * TS + t)) & 1u) {
         const bool edge = rem < kTileRows + p.n_tok - 1 ||
                           (WIN && rem > p.window && r0 + kTileRows > p.sinks);  // before the last token's window
-        if constexpr (FOUR) {
-          const unsigned char* sc = s_scale4 + slot * SB + t * 2 * D;
-          tile4<D, NT>(kt, vt, sc, sc + D, rem, edge, fq4, st, lane, p.sinks - r0, seen.low - r0, p.window);
-        } else if constexpr (ONE) {
+        if constexpr (ONE) {
           const float* sc = s_scale + (slot * TS + t) * 2;
           tile8<Q8, D, NT>(kt, vt, rem, edge, sc[0], sc[1], lg, p.qns, col0, p.qn, st, lane);
         } else if constexpr (WIN) {
@@ -1696,7 +1784,7 @@ template <typename CT, int D, int NT, bool SHUT, bool WIN>
 kvc_status run_decode(const ScoredParams& p, int grid, const CUtensorMap& tk, const CUtensorMap& tv,
                       cudaLaunchAttribute* attr, cudaStream_t stream) {
   using G = typename GeoOf<CT, D, NT>::Type;
-  static_assert(scored_warps(sizeof(CT), D, NT) == G::kWarps, "the host counts a CTA's workers as the kernel does");
+  static_assert(scored_warps(std::is_same<CT, fp4e2m1>::value ? 0 : sizeof(CT), D, NT) == G::kWarps, "the host counts a CTA's workers as the kernel does");
   static_assert(scored_smem_bytes<CT, D, NT>(GeoOf<CT, D, NT>::kMaxBatch) <= 227 * 1024, "shared memory of a CTA");
   auto* k = scored_decode_kernel<CT, D, NT, SHUT, WIN>;
   // The opt-in to large shared memory holds per device: made at the first call on each.
