@@ -9,9 +9,15 @@
 // bf16. code * scale has at most 6 significant bits, so it is exact in f16,
 // bf16 and f32, and reading back does not round.
 //
-// Bound by HBM: one pass, every element read once and its code written once.
-// One thread has one group of K and the same one of V: 64 bytes of bf16 in
-// flight per thread. What the exact rounding costs: a 16-bit x
+// Bound by HBM: one pass, every element read once and its code written once. In the
+// append a thread has a group of K and the same one of V (64 bytes of bf16 in
+// flight; 17.8 us for 16384 tokens of 8 heads and 128 dims in 16 bits, 4.8 TB/s: half
+// a group per thread reads whole lines but finds every scale twice, 21.6 us; two
+// groups, 20.7 us). Reading back it has half a group, so that a warp's stores are
+// whole lines (15.6 us, 5.5 TB/s; whole groups 19.7 us). A CTA has the rows of one kv head and some neighbouring tokens, because a
+// prompt's rows lie one behind the other in its blocks: it writes their codes and
+// scales side by side (head by head within a token, each row's 8 bytes of scales
+// lay alone). What the exact rounding costs: a 16-bit x
 // times the rounded reciprocal of the scale is off by at most 2^-22, while it
 // keeps 2^-11 from every midpoint that it does not hit; so the product is
 // rounded to 17 bits (two integer instructions), which restores the hits, and
@@ -31,28 +37,58 @@ namespace kvc {
 namespace {
 
 constexpr int kThreads4 = 256;
+constexpr int kHalf4 = kGroup4 / 2;
 
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&x)[kGroup4]) {
-  constexpr int N = Elem<T>::kVec;
-  uint4 u[kGroup4 / N];
-#pragma unroll
-  for (int i = 0; i < kGroup4 / N; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-#pragma unroll
-  for (int i = 0; i < kGroup4 / N; ++i) Elem<T>::unpack(u[i], x + i * N);
+__device__ __forceinline__ T from_bits(unsigned short x) {
+  T r;
+  *reinterpret_cast<unsigned short*>(&r) = x;
+  return r;
 }
 
-// Codes (8 bytes) and the scale's code of one group.
-template <bool F32>
-__device__ __forceinline__ uint2 quantise(float (&x)[kGroup4], uint32_t& scale) {
-  float a = 0.f;
-  bool odd = false;
+// A group as it lies in memory.
+template <typename T>
+struct Group {
+  static constexpr int N = Elem<T>::kVec;
+  uint4 u[kGroup4 / N];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-  for (int i = 0; i < kGroup4; ++i) {
-    a = fmaxf(a, fabsf(x[i]));
-    odd |= x[i] != x[i];
+    for (int i = 0; i < kGroup4 / N; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
   }
-  if (odd || a == __builtin_huge_valf()) {
+  __device__ __forceinline__ void unpack(float (&x)[kGroup4]) const {
+#pragma unroll
+    for (int i = 0; i < kGroup4 / N; ++i) Elem<T>::unpack(u[i], x + i * N);
+  }
+  // The largest magnitude: the order of magnitudes is that of their bits, NaN above
+  // infinity, and 16-bit elements go two at a time.
+  __device__ __forceinline__ float largest() const {
+    if constexpr (sizeof(T) == 4) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kGroup4 / N; ++i)
+        m = max(max(max(u[i].x & 0x7fffffffu, u[i].y & 0x7fffffffu), max(u[i].z & 0x7fffffffu, u[i].w & 0x7fffffffu)), m);
+      return __uint_as_float(m);
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kGroup4 / N; ++i) {
+        m = __vmaxu2(m, __vmaxu2(u[i].x & 0x7fff7fffu, u[i].y & 0x7fff7fffu));
+        m = __vmaxu2(m, __vmaxu2(u[i].z & 0x7fff7fffu, u[i].w & 0x7fff7fffu));
+      }
+      m = max(m & 0xffffu, m >> 16);
+      return Elem<T>::to_float(from_bits<T>(static_cast<unsigned short>(m)));
+    }
+  }
+};
+
+// Codes (8 bytes) of a group and its scale's code.
+template <typename T>
+__device__ __forceinline__ uint2 quantise(const Group<T>& u, uint32_t& scale) {
+  constexpr bool F32 = sizeof(T) == 4;
+  float x[kGroup4];
+  u.unpack(x);
+  float a = u.largest();
+  if (!(a < __builtin_huge_valf())) {
     // NaN becomes 0; infinities take the largest finite number, which
     // saturates, and do not count for the scale
     a = 0.f;
@@ -88,100 +124,102 @@ __device__ __forceinline__ uint2 quantise(float (&x)[kGroup4], uint32_t& scale) 
   return make_uint2(encode8_e2m1(y), encode8_e2m1(y + 8));
 }
 
-// Where a token's group lives: (block, head, row) of its slot, then the group.
-struct Place4 {
-  int64_t row;  // row of the pool, [num_blocks, n_heads, block_size]
-  int g;        // group of the row
+// What a call's threads have: CTA (x, y) some tokens of kv head y, thread i token
+// i / lanes of them and piece i % lanes of its row: a group (append) or half of one
+// (reading back).
+struct Rows4 {
+  const int64_t* slots;
+  int64_t num_tokens, num_slots;
+  int n_heads, block_size;
+  int lanes_log2;
+  unsigned int* err;
 };
 
-// i: (token, head, group). False: the token is skipped.
-__device__ __forceinline__ bool place(int64_t i, const int64_t* slots, int64_t num_slots, int n_heads, int block_size,
-                                      int groups, unsigned int* err, Place4& at) {
-  const uint32_t per = static_cast<uint32_t>(n_heads) * groups;
-  const int64_t t = i / per;
-  const uint32_t r = static_cast<uint32_t>(i - t * per);
-  const uint32_t h = r / groups;
-  at.g = static_cast<int>(r - h * groups);
-  const int64_t slot = __ldg(slots + t);
+// in: piece of [num_tokens, n_heads, lanes]; pool: piece of the pool. False:
+// the token is skipped, or there is none.
+__device__ __forceinline__ bool place(const Rows4& p, int64_t& in, int64_t& pool) {
+  const int g = threadIdx.x & ((1 << p.lanes_log2) - 1);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads4 >> p.lanes_log2) + (threadIdx.x >> p.lanes_log2);
+  const int h = blockIdx.y;
+  in = pool = 0;
+  if (t >= p.num_tokens) return false;
+  const int64_t slot = __ldg(p.slots + t);
   if (slot < 0) return false;
-  if (slot >= num_slots) {
-    if (r == 0) set_flag(err, KVC_FLAG_BAD_SLOT);
+  if (slot >= p.num_slots) {
+    if (h == 0 && g == 0) set_flag(p.err, KVC_FLAG_BAD_SLOT);
     return false;
   }
-  const int64_t blk = slot / block_size;
-  at.row = (blk * n_heads + h) * block_size + (slot - blk * block_size);
+  int64_t blk;
+  int row;
+  if (p.num_slots < (1ll << 31)) {  // (the same in every thread; a 64-bit division takes four times as long)
+    const uint32_t b = static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.block_size);
+    row = static_cast<int>(static_cast<uint32_t>(slot) - b * p.block_size);
+    blk = b;
+  } else {
+    blk = slot / p.block_size;
+    row = static_cast<int>(slot - blk * p.block_size);
+  }
+  in = ((t * p.n_heads + h) << p.lanes_log2) + g;
+  pool = (((blk * p.n_heads + h) * p.block_size + row) << p.lanes_log2) + g;
   return true;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads4)
-    append4_kernel(const T* __restrict__ k, const T* __restrict__ v, const int64_t* __restrict__ slots, int64_t total,
-                   int64_t num_slots, int n_heads, int block_size, int groups, uint2* __restrict__ kc,
-                   uint2* __restrict__ vc, unsigned char* __restrict__ ks, unsigned char* __restrict__ vs,
-                   unsigned int* err) {
-  constexpr bool F32 = sizeof(T) == 4;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads4 + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kThreads4) {
-    Place4 at;
-    if (!place(i, slots, num_slots, n_heads, block_size, groups, err, at)) continue;
-    float x[kGroup4], y[kGroup4];
-    load16(k + i * kGroup4, x);
-    load16(v + i * kGroup4, y);
-    const int64_t to = at.row * groups + at.g;
-    uint32_t s;
-    kc[to] = quantise<F32>(x, s);
-    ks[to] = static_cast<unsigned char>(s);
-    vc[to] = quantise<F32>(y, s);
-    vs[to] = static_cast<unsigned char>(s);
-  }
+    append4_kernel(const T* __restrict__ k, const T* __restrict__ v, const Rows4 p, uint2* __restrict__ kc,
+                   uint2* __restrict__ vc, unsigned char* __restrict__ ks, unsigned char* __restrict__ vs) {
+  // a decode launched behind this kernel may start its prologue now; it waits for
+  // this grid to finish before it reads any cached row
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int64_t from, to;
+  if (!place(p, from, to)) return;
+  Group<T> x, y;
+  x.load(k + from * kGroup4);
+  y.load(v + from * kGroup4);
+  uint32_t s;
+  kc[to] = quantise<T>(x, s);
+  ks[to] = static_cast<unsigned char>(s);
+  vc[to] = quantise<T>(y, s);
+  vs[to] = static_cast<unsigned char>(s);
 }
 
 template <typename T>
-__device__ __forceinline__ void store16(T* p, const uint2 code, float s) {
-  uint32_t h[2][4];
-  decode8_e2m1(code.x, h[0]);
-  decode8_e2m1(code.y, h[1]);
+__device__ __forceinline__ void store8(T* p, uint32_t code, float s) {
+  uint32_t h[4];
+  decode8_e2m1(code, h);
+  float x[8];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h[i][j]));
-      x[2 * j] = f.x * s;
-      x[2 * j + 1] = f.y * s;
-    }
-    constexpr int kind = sizeof(T) == 4 ? KVC_F32 : std::is_same<T, __half>::value ? KVC_F16 : KVC_BF16;
-    if constexpr (kind == KVC_F32) {
-      store_out_vec<4>(p, 8 * i, x, kind);
-      store_out_vec<4>(p, 8 * i + 4, x + 4, kind);
-    } else {
-      store_out_vec<8>(p, 8 * i, x, kind);
-    }
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h[j]));
+    x[2 * j] = f.x * s;
+    x[2 * j + 1] = f.y * s;
+  }
+  constexpr int kind = sizeof(T) == 4 ? KVC_F32 : std::is_same<T, __half>::value ? KVC_F16 : KVC_BF16;
+  if constexpr (kind == KVC_F32) {
+    store_out_vec<4>(p, 0, x, kind);
+    store_out_vec<4>(p, 4, x + 4, kind);
+  } else {
+    store_out_vec<8>(p, 0, x, kind);
   }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads4)
-    read4_kernel(const int64_t* __restrict__ slots, int64_t total, int64_t num_slots, int n_heads, int block_size,
-                 int groups, const uint2* __restrict__ kc, const uint2* __restrict__ vc,
+    read4_kernel(const Rows4 p, const uint32_t* __restrict__ kc, const uint32_t* __restrict__ vc,
                  const unsigned char* __restrict__ ks, const unsigned char* __restrict__ vs, T* __restrict__ k,
-                 T* __restrict__ v, unsigned int* err) {
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads4 + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kThreads4) {
-    Place4 at;
-    if (!place(i, slots, num_slots, n_heads, block_size, groups, err, at)) continue;
-    const int64_t from = at.row * groups + at.g;
-    const uint2 a = __ldg(kc + from), b = __ldg(vc + from);
-    const uint32_t sa = __ldg(ks + from), sb = __ldg(vs + from);
-    store16(k + i * kGroup4, a, scale_value(sa));
-    store16(v + i * kGroup4, b, scale_value(sb));
-  }
+                 T* __restrict__ v) {
+  int64_t to, from;
+  if (!place(p, to, from)) return;
+  const uint32_t a = __ldg(kc + from), b = __ldg(vc + from);
+  const uint32_t sa = __ldg(ks + (from >> 1)), sb = __ldg(vs + (from >> 1));
+  store8(k + to * kHalf4, a, scale_value(sa));
+  store8(v + to * kHalf4, b, scale_value(sb));
 }
 
-// Checks shared by both calls. *total: groups of the call, 0 for no tokens.
+// Checks shared by both calls.
 kvc_status check4(const void* k, const void* v, const int64_t* slots, int64_t num_tokens, const void* kc,
                   const void* vc, const uint8_t* ks, const uint8_t* vs, int64_t num_blocks, int block_size,
-                  int n_kv_heads, int head_dim, kvc_dtype dtype, int64_t* total) {
+                  int n_kv_heads, int head_dim, kvc_dtype dtype) {
   if (!dtype_ok(dtype)) return fail(KVC_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(dtype));
   if (num_tokens < 0 || num_blocks < 1 || block_size < 1 || n_kv_heads < 1 || head_dim < 1)
     return fail(KVC_ERR_INVALID_ARG, "sizes must be positive (num_tokens >= 0)");
@@ -189,10 +227,9 @@ kvc_status check4(const void* k, const void* v, const int64_t* slots, int64_t nu
     return fail(KVC_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128, 256)", head_dim);
   if (block_size % 16 != 0 || block_size > 128)
     return fail(KVC_ERR_UNSUPPORTED, "block_size %d (supported: multiples of 16 up to 128)", block_size);
-  if (n_kv_heads > (1 << 24) || num_blocks > (1ll << 55) / block_size / n_kv_heads / head_dim ||
-      num_tokens > (1ll << 55) / n_kv_heads / head_dim)
+  if (n_kv_heads > 65535 || num_blocks > (1ll << 55) / block_size / n_kv_heads / head_dim ||
+      num_tokens > (1ll << 31) * (kThreads4 * kHalf4 / head_dim) - (1 << 20))
     return fail(KVC_ERR_UNSUPPORTED, "num_blocks, num_tokens or n_kv_heads too large");
-  *total = num_tokens * n_kv_heads * (head_dim / kGroup4);
   if (num_tokens == 0) return KVC_OK;
   if (k == nullptr || v == nullptr || slots == nullptr || kc == nullptr || vc == nullptr || ks == nullptr ||
       vs == nullptr)
@@ -202,9 +239,15 @@ kvc_status check4(const void* k, const void* v, const int64_t* slots, int64_t nu
   return KVC_OK;
 }
 
-int grid4(int64_t total, int num_sms) {
-  const int64_t want = (total + kThreads4 - 1) / kThreads4;
-  return static_cast<int>(want < num_sms * 64ll ? want : num_sms * 64ll);
+Rows4 rows4(const int64_t* slots, int64_t num_tokens, int64_t num_blocks, int block_size, int n_kv_heads,
+            int lanes, unsigned int* err) {
+  int log2 = 0;
+  while ((1 << log2) < lanes) ++log2;
+  return {slots, num_tokens, num_blocks * block_size, n_kv_heads, block_size, log2, err};
+}
+dim3 grid4(const Rows4& p) {
+  const int64_t per = kThreads4 >> p.lanes_log2;
+  return dim3(static_cast<unsigned>((p.num_tokens + per - 1) / per), static_cast<unsigned>(p.n_heads));
 }
 
 }  // namespace
@@ -217,19 +260,18 @@ kvc_status kvc_append_fp4(const void* k, const void* v, const int64_t* slot_mapp
                           int block_size, int n_kv_heads, int head_dim, kvc_dtype dtype, kvc_stream stream) {
   using namespace kvc;
   clear_error();
-  int64_t total = 0;
   kvc_status st = check4(k, v, slot_mapping, num_tokens, k_cache, v_cache, k_scale, v_scale, num_blocks, block_size,
-                         n_kv_heads, head_dim, dtype, &total);
-  if (st != KVC_OK || total == 0) return st;
+                         n_kv_heads, head_dim, dtype);
+  if (st != KVC_OK || num_tokens == 0) return st;
   DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev)) != KVC_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const Rows4 p = rows4(slot_mapping, num_tokens, num_blocks, block_size, n_kv_heads, head_dim / kGroup4, dev->error_word);
   auto launch = [&](auto* kernel, auto zero) {
     using T = decltype(zero);
-    kernel<<<grid4(total, dev->num_sms), kThreads4, 0, s>>>(
-        static_cast<const T*>(k), static_cast<const T*>(v), slot_mapping, total, num_blocks * block_size, n_kv_heads,
-        block_size, head_dim / kGroup4, static_cast<uint2*>(k_cache), static_cast<uint2*>(v_cache), k_scale, v_scale,
-        dev->error_word);
+    kernel<<<grid4(p), kThreads4, 0, s>>>(static_cast<const T*>(k), static_cast<const T*>(v), p,
+                                          static_cast<uint2*>(k_cache), static_cast<uint2*>(v_cache), k_scale,
+                                          v_scale);
   };
   if (dtype == KVC_F32) launch(append4_kernel<float>, float());
   else if (dtype == KVC_F16) launch(append4_kernel<__half>, __half());
@@ -242,19 +284,17 @@ kvc_status kvc_read_fp4(const int64_t* slot_mapping, int64_t num_tokens, const v
                         int n_kv_heads, int head_dim, void* k, void* v, kvc_dtype dtype, kvc_stream stream) {
   using namespace kvc;
   clear_error();
-  int64_t total = 0;
   kvc_status st = check4(k, v, slot_mapping, num_tokens, k_cache, v_cache, k_scale, v_scale, num_blocks, block_size,
-                         n_kv_heads, head_dim, dtype, &total);
-  if (st != KVC_OK || total == 0) return st;
+                         n_kv_heads, head_dim, dtype);
+  if (st != KVC_OK || num_tokens == 0) return st;
   DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev)) != KVC_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const Rows4 p = rows4(slot_mapping, num_tokens, num_blocks, block_size, n_kv_heads, head_dim / kHalf4, dev->error_word);
   auto launch = [&](auto* kernel, auto zero) {
     using T = decltype(zero);
-    kernel<<<grid4(total, dev->num_sms), kThreads4, 0, s>>>(
-        slot_mapping, total, num_blocks * block_size, n_kv_heads, block_size, head_dim / kGroup4,
-        static_cast<const uint2*>(k_cache), static_cast<const uint2*>(v_cache), k_scale, v_scale, static_cast<T*>(k),
-        static_cast<T*>(v), dev->error_word);
+    kernel<<<grid4(p), kThreads4, 0, s>>>(p, static_cast<const uint32_t*>(k_cache), static_cast<const uint32_t*>(v_cache),
+                                          k_scale, v_scale, static_cast<T*>(k), static_cast<T*>(v));
   };
   if (dtype == KVC_F32) launch(read4_kernel<float>, float());
   else if (dtype == KVC_F16) launch(read4_kernel<__half>, __half());
