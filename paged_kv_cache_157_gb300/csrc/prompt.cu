@@ -1046,54 +1046,99 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 // ------------------------------------------------------------------ merge
 
 // Joins the records of units that several ranges share: o = sum_x 2^(m_x - M)
-// O_x / sum_x 2^(m_x - M) l_x. One warp per row, lanes over the dims.
+// O_x / sum_x 2^(m_x - M) l_x, M the largest m so far. A warp has four rows at a time,
+// lanes over the dims, the loads of two records of each in flight: bound by a chain of
+// three loads (tile, its prefix sum, records) per unit.
 constexpr int kMergeRows = 32;  // rows of a unit per CTA
+constexpr int kMergeWarpRows = kMergeRows / 8;
 
 template <typename CT, int D>
 __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptParams p) {
-  constexpr int N = D / 32;
+  constexpr int N = D / 32, K = kMergeWarpRows;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int H = p.row.n_kv_heads, n = __ldcg(p.head);
-  const int i = static_cast<int>(blockIdx.x) / H, kvh = static_cast<int>(blockIdx.x) - i * H;
-  if (i >= n || __ldcg(p.head + 2) == 0) return;
+  if (__ldcg(p.head + 2) == 0) return;  // no unit was split
   const Ranges r(n, __ldcg(p.head + 1), H, p.grid);
-  const Tile t = Walk::load(p, i);
-  const int u0 = H * __ldcg(p.before + i) + kvh * t.cost;
-  const int a = r.holder(u0), b = r.holder(u0 + t.cost - 1);
-  if (a == b) return;
   const int lane = threadIdx.x & 31;
-  for (int k = threadIdx.x >> 5; k < kMergeRows; k += 8) {
-    const int at = blockIdx.y * kMergeRows + k;  // half and row
-    const int hf = at / kM, tk = (at % kM) / p.group, head = kvh * p.group + (at % kM) - tk * p.group;
-    const int tok = hf * p.tokens + tk;
-    if (tk >= p.tokens || tok >= t.count) continue;
-    auto rec = [&](int x) { return (2ll * x + (u0 > r.start(x) ? 1 : 0)) * 2 * kM + at; };
-    float M = -__builtin_huge_valf();
-    for (int x = a + lane; x <= b; x += 32) M = fmaxf(M, __ldcg(p.rec_ml + rec(x) * 2));
-    M = warp_max(M);
-    float L = 0.f, o[N];
+  constexpr int CH = 2 * kM / kMergeRows;  // CTAs' shares of a unit
+  for (int64_t w = blockIdx.x; w < static_cast<int64_t>(n) * H * CH; w += gridDim.x) {
+    const int unit = static_cast<int>(w / CH), i = unit / H, kvh = unit - i * H;
+    const Tile t = Walk::load(p, i);
+    const int u0 = H * __ldcg(p.before + i) + kvh * t.cost;
+    const int a = r.holder(u0), b = r.holder(u0 + t.cost - 1);
+    if (a == b) continue;
+    // a range's first part is its record 0: all parts of the unit but the first one's,
+    // unless that begins its range too
+    const int second = u0 > r.start(a) ? 1 : 0;
+    const int row0 = static_cast<int>(w % CH) * kMergeRows + (threadIdx.x >> 5) * K;  // half and row
+    int tok[K], head[K];
+    float M[K], L[K], o[K][N];
 #pragma unroll
-    for (int c = 0; c < N; ++c) o[c] = 0.f;
-    for (int x = a; x <= b; ++x) {
-      const int64_t y = rec(x);
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.rec_ml + y * 2));
-      const float f = fast_exp2(ml.x - M);
-      L = fmaf(f, ml.y, L);
+    for (int k = 0; k < K; ++k) {
+      const int hf = (row0 + k) / kM, at = (row0 + k) % kM, tk = at / p.group;
+      tok[k] = tk < p.tokens && hf * p.tokens + tk < t.count ? hf * p.tokens + tk : -1;
+      head[k] = kvh * p.group + at - tk * p.group;
+      M[k] = -1e30f;
+      L[k] = 0.f;
 #pragma unroll
-      for (int c = 0; c < N; ++c) o[c] = fmaf(f, __ldcg(p.rec_o + y * D + lane * N + c), o[c]);
+      for (int c = 0; c < N; ++c) o[k][c] = 0.f;
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    float zero = 0.f;
+    for (int x0 = a; x0 <= b; x0 += 2) {
+      float2 ml[2][K];
+      float y[2][K][N];
 #pragma unroll
-    for (int c = 0; c < N; ++c) {
-      o[c] *= inv;
-      zero = fmaf(o[c], 0.f, zero);
+      for (int d = 0; d < 2; ++d) {
+        const int x = min(x0 + d, b);
+        const int64_t rec = (2ll * x + (x == a ? second : 0)) * 2 * kM + row0;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (tok[k] < 0) continue;
+          ml[d][k] = __ldcg(reinterpret_cast<const float2*>(p.rec_ml + (rec + k) * 2));
+          const float* from = p.rec_o + (rec + k) * D + lane * N;
+          if constexpr (N == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(from));
+            y[d][k][0] = v.x;
+            y[d][k][1] = v.y;
+            y[d][k][2] = v.z;
+            y[d][k][3] = v.w;
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(from));
+            y[d][k][0] = v.x;
+            y[d][k][1] = v.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        if (x0 + d > b) break;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (tok[k] < 0) continue;
+          const float to = fmaxf(M[k], ml[d][k].x);
+          const float f = fast_exp2(M[k] - to), g = fast_exp2(ml[d][k].x - to);
+          M[k] = to;
+          L[k] = fmaf(g, ml[d][k].y, L[k] * f);
+#pragma unroll
+          for (int c = 0; c < N; ++c) o[k][c] = fmaf(g, y[d][k][c], o[k][c] * f);
+        }
+      }
     }
-    if (__any_sync(0xffffffffu, zero != 0.f))
-      redo_row<CT, D>(p, t.seq, t.first + tok, head, t.pos + tok);
-    else
-      store_out_vec<N>(p.out, (static_cast<int64_t>(t.first + tok) * p.n_q_heads + head) * D + lane * N, o,
-                       std::is_same<CT, __half>::value ? KVC_F16 : KVC_BF16);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (tok[k] < 0) continue;
+      const float inv = L[k] == 0.f ? 0.f : 1.f / L[k];
+      float zero = 0.f;
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        o[k][c] *= inv;
+        zero = fmaf(o[k][c], 0.f, zero);
+      }
+      if (__any_sync(0xffffffffu, zero != 0.f))
+        redo_row<CT, D>(p, t.seq, t.first + tok[k], head[k], t.pos + tok[k]);
+      else
+        store_out_vec<N>(p.out, (static_cast<int64_t>(t.first + tok[k]) * p.n_q_heads + head[k]) * D + lane * N, o[k],
+                         std::is_same<CT, __half>::value ? KVC_F16 : KVC_BF16);
+    }
   }
 }
 
@@ -1224,7 +1269,8 @@ kvc_status launch(const PromptParams& p, const CUtensorMap& tq, const CUtensorMa
   e = cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, p);
   if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx(prompt)");
   if (p.mode == kPlanSplit) {
-    cfg.gridDim = dim3(static_cast<unsigned>(p.max_tiles) * p.row.n_kv_heads, 2 * kM / kMergeRows);
+    const int64_t shares = static_cast<int64_t>(p.max_tiles) * p.row.n_kv_heads * (2 * kM / kMergeRows);
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(shares, 8 * p.grid)));  // what the GPU holds at once
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, prompt_merge_kernel<CT, D>, p);
