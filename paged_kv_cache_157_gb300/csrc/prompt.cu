@@ -84,6 +84,14 @@ struct Tile {
   int cost;                  // KV tiles that it sees
 };
 
+// Rows of a warp's 32 that are to be done again (bits of `rows`).
+struct Redo {
+  Tile t;
+  int kvh;
+  uint32_t rows;
+  int pad[2];
+};
+
 // How units are handed out: one per CTA without a plan; planned, whole; planned,
 // split where that pays.
 enum { kPlanNone = 0, kPlanWhole = 1, kPlanSplit = 2 };
@@ -101,6 +109,8 @@ struct PromptParams {
   int* before;   // KV tiles of the tiles before each (where units are split)
   float* rec_o;  // [2 * CTAs, 2 * kM, D] unnormalised partial outputs
   float* rec_ml; // [2 * CTAs, 2 * kM, 2] (reference, sum of weights)
+  Redo* redo;    // [CTAs, softmax warps, redo_max] rows to do again
+  int redo_max;
   unsigned int* err;
   int batch, num_tokens, n_q_heads, group, max_blocks, rows, tokens, max_tiles;
   int mode, grid;  // mode: kPlan*
@@ -522,7 +532,7 @@ __device__ __forceinline__ bool pair_or(int id, bool pred) {
 }
 
 // One output row again, over its visible rows alone (attend_row.cuh). Rare.
-template <typename CT, int D>
+template <typename CT, int D, int U>
 __device__ __noinline__ void redo_row(const PromptParams& p, int seq, int row, int head, int pos) {
   constexpr int N = D / 32;
   const int lane = threadIdx.x & 31;
@@ -530,7 +540,7 @@ __device__ __noinline__ void redo_row(const PromptParams& p, int seq, int row, i
   float q[N], o[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) q[j] = Elem<CT>::to_float(static_cast<const CT*>(p.q)[at + j]);
-  (void)attend_row<CT, D>(p.row, q, p.block_tables + static_cast<int64_t>(seq) * p.max_blocks, head / p.group, pos, o);
+  (void)attend_row<CT, D, U>(p.row, q, p.block_tables + static_cast<int64_t>(seq) * p.max_blocks, head / p.group, pos, o);
   store_out_vec<N>(p.out, at, o, std::is_same<CT, __half>::value ? KVC_F16 : KVC_BF16);
 }
 
@@ -820,6 +830,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       return y;
     };
     uint32_t gt = 0, n = 0, nu = 0;  // the CTA's KV tiles; tiles and units of this half
+    auto redo = [&](int i) { return p.redo + (static_cast<int64_t>(blockIdx.x) * kSoftWarps + warp) * p.redo_max + i; };
+    int n_redo = 0;
+    // Rows of the warp whose output was not finite, once more.
+    auto redo_rows = [&](const Tile& t, int kvh, uint32_t rows) {
+      for (; rows != 0; rows &= rows - 1) {
+        const int r1 = (warp & 3) * 32 + __ffs(rows) - 1, tk1 = r1 / p.group, tok = hf * p.tokens + tk1;
+        redo_row<CT, D, 4>(p, t.seq, t.first + tok, kvh * p.group + r1 - tk1 * p.group, t.pos + tok);
+      }
+    };
     bool ok = true;
     for (uint32_t un = 0;; ++un) {
       if (!wait_warp(bar(G::UFULL0 + (un & 1)), (un >> 1) & 1u)) break;
@@ -968,9 +987,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       fence_after();
       const int head = u.kvh * p.group + r - tk * p.group;
       const int row = u.t.first + hf * p.tokens + tk;
-      const int seq = u.t.seq, rec = u.rec;
-      __syncwarp();
-      if (lane == 0) arrive(bar(G::UEMPTY0 + (un & 1)));  // u is not looked at any more
+      const int rec = u.rec;
       const float inv = rec >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
       // Threads have rows, and a row's pieces lie far from the next row's: they go
       // through shared memory, so that four lanes write 64 bytes of a row (one
@@ -1026,13 +1043,26 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           *reinterpret_cast<float2*>(p.rec_ml + ((static_cast<int64_t>(rec) * 2 + hf) * kM + r) * 2) =
               make_float2(m, l);
       } else {
-        // rows done again whole, by either warp of the row or by both (the same values)
-        for (uint32_t odd = __ballot_sync(full, valid && zero != 0.f); odd != 0; odd &= odd - 1) {
-          const int src = __ffs(odd) - 1;
-          redo_row<CT, D>(p, seq, __shfl_sync(full, row, src), __shfl_sync(full, head, src),
-                          __shfl_sync(full, pos, src));
+        // Rows done again whole, by either warp of the row or by both (the same
+        // values): at the end, when nobody waits for this warp any more (a row of a
+        // long sequence takes milliseconds).
+        const uint32_t odd = __ballot_sync(full, valid && zero != 0.f);
+        if (odd != 0) {
+          if (n_redo < p.redo_max) {
+            if (lane == 0) *redo(n_redo) = {u.t, u.kvh, odd, {0, 0}};
+            ++n_redo;
+          } else {
+            redo_rows(u.t, u.kvh, odd);
+          }
         }
       }
+      __syncwarp();
+      if (lane == 0) arrive(bar(G::UEMPTY0 + (un & 1)));
+    }
+    __syncwarp();
+    for (int i = 0; i < n_redo; ++i) {
+      const Redo e = *redo(i);
+      redo_rows(e.t, e.kvh, e.rows);
     }
   }
 
@@ -1134,7 +1164,7 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptParams p)
         zero = fmaf(o[k][c], 0.f, zero);
       }
       if (__any_sync(0xffffffffu, zero != 0.f))
-        redo_row<CT, D>(p, t.seq, t.first + tok[k], head[k], t.pos + tok[k]);
+        redo_row<CT, D, 1>(p, t.seq, t.first + tok[k], head[k], t.pos + tok[k]);
       else
         store_out_vec<N>(p.out, (static_cast<int64_t>(t.first + tok[k]) * p.n_q_heads + head[k]) * D + lane * N, o[k],
                          std::is_same<CT, __half>::value ? KVC_F16 : KVC_BF16);
@@ -1170,11 +1200,11 @@ kvc_status check_shape(const PromptShape& s) {
 }
 
 // Workspace: [head][tiles][their prefix sums][records' outputs][records'
-// references and sums], each 256-byte aligned; records and prefix sums only where
+// references and sums][rows to do again], each 256-byte aligned; records and prefix sums only where
 // units may be split.
 struct PromptLayout {
-  size_t tiles, before, rec_o, rec_ml, total;
-  int mode;
+  size_t tiles, before, rec_o, rec_ml, redo, total;
+  int mode, redo_max;
 };
 
 // Units per SM from which none is split: dealt out by size they end together.
@@ -1198,7 +1228,9 @@ PromptLayout layout(const PromptShape& s, int num_sms) {
   l.rec_o = l.before + up256(l.mode == kPlanSplit ? static_cast<size_t>(s.tiles()) * 4 : 0);
   const size_t recs = l.mode == kPlanSplit ? 2 * static_cast<size_t>(num_sms) * 2 * kM : 0;
   l.rec_ml = l.rec_o + up256(recs * s.D * 4);
-  l.total = l.rec_ml + up256(recs * 8);
+  l.redo = l.rec_ml + up256(recs * 8);
+  l.redo_max = static_cast<int>((s.tiles() * s.n_kv_heads + num_sms - 1) / num_sms);
+  l.total = l.redo + up256(static_cast<size_t>(num_sms) * kSoftWarps * l.redo_max * sizeof(Redo));
   return l;
 }
 
@@ -1335,7 +1367,7 @@ kvc_status kvc_prompt_attention(const void* q, const void* k_cache, const void* 
   char* ws = static_cast<char*>(workspace);
   PromptParams p{};
   // positions are below 2^30: larger windows are all rows, and differences of them stay in 32 bits
-  p.row = {k_cache, v_cache, nullptr, nullptr, num_blocks, n_kv_heads, block_size, std::min(window, 1 << 30),
+  p.row = {k_cache, v_cache, num_blocks, n_kv_heads, block_size, std::min(window, 1 << 30),
            std::min(sinks, 1 << 30), scale * 1.4426950408889634f};
   p.q = q;
   p.out = out;
@@ -1347,6 +1379,8 @@ kvc_status kvc_prompt_attention(const void* q, const void* k_cache, const void* 
   p.before = reinterpret_cast<int*>(ws + l.before);
   p.rec_o = reinterpret_cast<float*>(ws + l.rec_o);
   p.rec_ml = reinterpret_cast<float*>(ws + l.rec_ml);
+  p.redo = reinterpret_cast<Redo*>(ws + l.redo);
+  p.redo_max = l.redo_max;
   p.err = dev->error_word;
   p.batch = batch;
   p.num_tokens = static_cast<int>(num_tokens);

@@ -95,6 +95,19 @@ def test_values_that_are_not_finite_stay_with_those_who_see_them(kvc, kind, wind
     p.check()
 
 
+@pytest.mark.parametrize("sizes", [([300, 40], [300, 40], 512, 8, 64, 16), ([70], [9000], 8, 1, 128, 16),
+                                   ([5, 9], [50, 90], 8, 2, 128, 16)])
+def test_a_sequence_that_is_not_finite_throughout(kvc, sizes):
+    """One value of a first row: every output of that dim, in whole units, split ones and a call without a plan."""
+    p = Prompt(*sizes, "bf16", seed=16)
+    b = int(p.tables[0, 0])
+    p.pools[1][0][b, :, 0, 3] = float("inf")
+    p.pools[1][1][b, :, 0, 3] = np.inf
+    p.run(kvc)
+    p.check()
+    assert np.isinf(f64(p.out)[:p.new[0], :, 3]).all() and kvc.get_error_flags() == 0
+
+
 def test_keys_that_are_not_finite_in_hidden_rows(kvc):
     p = Prompt([100], [100], 4, 1, 128, 16, "bf16", None, 0, seed=7)
     b, o = int(p.tables[0, 5]), 3  # row 83
