@@ -11,18 +11,19 @@
 //
 // Bound by HBM: one pass, every element read once and its code written once. In the
 // append a thread has a group of K and the same one of V (64 bytes of bf16 in
-// flight; 17.8 us for 16384 tokens of 8 heads and 128 dims in 16 bits, 4.8 TB/s: half
+// flight; 17.2 us for 16384 tokens of 8 heads and 128 dims in 16 bits, 5.0 TB/s: half
 // a group per thread reads whole lines but finds every scale twice, 21.6 us; two
 // groups, 20.7 us). Reading back it has half a group, so that a warp's stores are
-// whole lines (15.6 us, 5.5 TB/s; whole groups 19.7 us). A CTA has the rows of one kv head and some neighbouring tokens, because a
-// prompt's rows lie one behind the other in its blocks: it writes their codes and
-// scales side by side (head by head within a token, each row's 8 bytes of scales
-// lay alone). What the exact rounding costs: a 16-bit x
-// times the rounded reciprocal of the scale is off by at most 2^-22, while it
-// keeps 2^-11 from every midpoint that it does not hit; so the product is
-// rounded to 17 bits (two integer instructions), which restores the hits, and
-// goes to the hardware's conversion. f32 inputs can lie closer and take the
-// quotient with its remainder.
+// whole lines (15.2 us, 5.7 TB/s; whole groups 19.7 us). A CTA has the rows of one kv
+// head and some neighbouring tokens, because a prompt's rows lie one behind the other
+// in its blocks: it writes their codes and scales side by side (head by head within a
+// token, each row's 8 bytes of scales lay alone).
+//
+// What the exact rounding costs: a 16-bit x times the rounded reciprocal of the scale
+// is off by at most 2^-22, while it keeps 2^-11 from every midpoint that it does not
+// hit; so the product is rounded to 17 bits (two integer instructions), which restores
+// the hits, and goes to the hardware's conversion. f32 inputs can lie closer and take
+// the quotient with its remainder.
 //
 // Source: "KV-Cache——为什么AI回复越来越快" section 08 (KV-Cache quantisation);
 // the format is this library's choice for this GPU, which converts e2m1 and
@@ -66,7 +67,8 @@ struct Group {
       uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < kGroup4 / N; ++i)
-        m = max(max(max(u[i].x & 0x7fffffffu, u[i].y & 0x7fffffffu), max(u[i].z & 0x7fffffffu, u[i].w & 0x7fffffffu)), m);
+        m = max(max(max(u[i].x & 0x7fffffffu, u[i].y & 0x7fffffffu),
+                    max(u[i].z & 0x7fffffffu, u[i].w & 0x7fffffffu)), m);
       return __uint_as_float(m);
     } else {
       uint32_t m = 0;
@@ -266,7 +268,8 @@ kvc_status kvc_append_fp4(const void* k, const void* v, const int64_t* slot_mapp
   DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev)) != KVC_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const Rows4 p = rows4(slot_mapping, num_tokens, num_blocks, block_size, n_kv_heads, head_dim / kGroup4, dev->error_word);
+  const Rows4 p =
+      rows4(slot_mapping, num_tokens, num_blocks, block_size, n_kv_heads, head_dim / kGroup4, dev->error_word);
   auto launch = [&](auto* kernel, auto zero) {
     using T = decltype(zero);
     kernel<<<grid4(p), kThreads4, 0, s>>>(static_cast<const T*>(k), static_cast<const T*>(v), p,
@@ -290,7 +293,8 @@ kvc_status kvc_read_fp4(const int64_t* slot_mapping, int64_t num_tokens, const v
   DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev)) != KVC_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const Rows4 p = rows4(slot_mapping, num_tokens, num_blocks, block_size, n_kv_heads, head_dim / kHalf4, dev->error_word);
+  const Rows4 p =
+      rows4(slot_mapping, num_tokens, num_blocks, block_size, n_kv_heads, head_dim / kHalf4, dev->error_word);
   auto launch = [&](auto* kernel, auto zero) {
     using T = decltype(zero);
     kernel<<<grid4(p), kThreads4, 0, s>>>(p, static_cast<const uint32_t*>(k_cache), static_cast<const uint32_t*>(v_cache),

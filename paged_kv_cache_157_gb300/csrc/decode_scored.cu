@@ -88,8 +88,7 @@ ScoredLayout layout(const ScoredShape& s, int elt, bool scored, int num_sms) {
 
 // What the size query answers: one size for either kind of cache.
 size_t workspace_needed(const ScoredShape& s, bool scored, int num_sms) {
-  return std::max({layout(s, 0, scored, num_sms).total, layout(s, 1, scored, num_sms).total,
-                   layout(s, 2, scored, num_sms).total});
+  return std::max(layout(s, 1, scored, num_sms).total, layout(s, 2, scored, num_sms).total);
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -162,8 +161,7 @@ kvc_status decode(Cache cache, const ScoredShape& s, const void* q, kvc_dtype q_
   DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev)) != KVC_OK) return st;
   const int elt = cache == Cache::kBf16 || cache == Cache::kF16 ? 2 : 1;
-  const int kind = cache == Cache::kFp4 ? 0 : elt;  // as scored_warps counts
-  const ScoredLayout l = layout(s, kind, scores != nullptr, dev->num_sms);
+  const ScoredLayout l = layout(s, elt, scores != nullptr, dev->num_sms);
   const size_t needed = workspace_needed(s, scores != nullptr, dev->num_sms);
   if (workspace == nullptr || workspace_bytes < needed)
     return fail(KVC_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace == nullptr ? 0 : workspace_bytes,
@@ -210,7 +208,7 @@ kvc_status decode(Cache cache, const ScoredShape& s, const void* q, kvc_dtype q_
   p.wait_polls = static_cast<unsigned int>(option(KVC_OPT_WAIT_POLLS));
   const int64_t cap = option(KVC_OPT_MAX_CTAS), forced = option(KVC_OPT_BLOCKS_PER_CTA);
   const int grid = static_cast<int>(cap > 0 ? std::min<int64_t>(cap, l.grid) : l.grid);
-  p.workers = grid * scored_warps(kind, s.D, l.nt);
+  p.workers = grid * scored_warps(elt, s.D, l.nt);
   // the work split's option counts cache blocks per worker, here a warp
   p.min_tiles = forced > 0 ? static_cast<int>(std::min<int64_t>(forced, 1 << 20)) * (s.block_size / kTileRows)
                            : kMinTiles;

@@ -194,12 +194,12 @@ __device__ __forceinline__ void raise_references(const float (&x)[NT][4], State<
 }
 
 // The weights' B fragments: parts of the 16-bit type, transposed from the C
-// fragment [rows][queries] to [rows = k][queries = n]. bf16, or not SCALED: their
-// sum is the weight; f16: the first plus the second / kRestScale.
-template <bool BF, int NT, int NP, bool SCALED = true>
+// fragment [rows][queries] to [rows = k][queries = n]. bf16: their sum is the
+// weight; f16: the first plus the second / kRestScale.
+template <bool BF, int NT, int NP>
 __device__ __forceinline__ void weight_parts(const float (&w)[NT][4], uint32_t (&b)[NT][NP][2]) {
   using namespace wmma16;
-  constexpr float SCALE = BF || !SCALED ? 1.f : kRestScale;
+  constexpr float SCALE = BF ? 1.f : kRestScale;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     float r0 = w[n][0], r1 = w[n][1], r2 = w[n][2], r3 = w[n][3];
@@ -220,12 +220,12 @@ __device__ __forceinline__ void weight_parts(const float (&w)[NT][4], uint32_t (
 }
 
 // o += a . (the weights' parts) for one output tile.
-template <bool BF, int NP, bool SCALED = true>
+template <bool BF, int NP>
 __device__ __forceinline__ void add_products(float (&o)[4], const uint32_t (&a)[4], const uint32_t (&b)[NP][2]) {
   using namespace wmma16;
-  if constexpr (BF || !SCALED) {
+  if constexpr (BF) {
 #pragma unroll
-    for (int j = 0; j < NP; ++j) mma<BF>(o, a, b[j][0], b[j][1]);
+    for (int j = 0; j < NP; ++j) mma<true>(o, a, b[j][0], b[j][1]);
   } else {
     static_assert(NP == 2, "a weight and its scaled rest");
     float rest[4] = {0.f, 0.f, 0.f, 0.f};
@@ -403,7 +403,7 @@ __device__ __forceinline__ void tile16(uint32_t k, uint32_t v, int rem, bool edg
       if constexpr (BF && WIN) {
         // The tile's products on their own, the small parts first, then one rounded
         // addition: the tensor core cuts what it adds to, three times per tile, which
-        // left errors of 2.4e-6 in fp32 outputs (now %s).
+        // left errors of 2.4e-6 in fp32 outputs (3.3e-7 now, and no slower).
         float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = NP - 1; j >= 0; --j) mma<true>(t, a, b[n][j][0], b[n][j][1]);
@@ -521,12 +521,22 @@ __device__ __forceinline__ void tile8(uint32_t k, uint32_t v, int rem, bool edge
   }
 }
 
+// d = a . b for one m16n8k16 tile of f16.
+__device__ __forceinline__ void mma_fresh(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // R neighbouring 16-row tiles of a four-bit cache (their boxes and scales `step` and
 // 2 D bytes apart); ks, vs: the first one's scales in shared memory, [16 rows][D / 16]
 // e4m3; rem: rows of the sequence from each tile's first on, 0 for a tile that is
 // not there or whose block lies outside the pool. Two tiles at once have two chains
-// of conversions and products to interleave and one vote: 40.0 -> %s us for 32 x
-// U[512, 4096].
+// of conversions and products to interleave, one vote and one addition of the weights'
+// rests: 41.3 -> 38.0 us for 32 x U[512, 4096] (32 query, 8 kv heads, D 128). About 390
+// instructions per tile at 2.2 per cycle: bound by their latency with three warps per
+// scheduler, 3.5 TB/s in large batches.
 //
 // A lane's dims are those of tile8; its codes of one row are decoded two dims to a
 // register (K) or, with two rows' nibbles interleaved, one dim of both rows (V), and
@@ -653,9 +663,6 @@ __device__ __forceinline__ void tile4(uint32_t k, uint32_t v, uint32_t step, con
       }
     }
   }
-  // The rest of a weight as it is, not scaled up: the parts give 22 bits down to
-  // 2^-14 of the largest weight and 11 at 2^-25, for values of 6 bits (a scaled rest
-  // took 64 of 530 instructions per tile).
   uint32_t b[R][NT][NP][2];
 #pragma unroll
   for (int rt = 0; rt < R; ++rt) {
@@ -668,27 +675,30 @@ __device__ __forceinline__ void tile4(uint32_t k, uint32_t v, uint32_t step, con
         x[rt][n][e] = p;
       }
     }
-    weight_parts<false, NT, NP, false>(x[rt], b[rt]);
+    weight_parts<false, NT, NP>(x[rt], b[rt]);
   }
   constexpr int SPANS = D <= 128 ? 1 : D / 128;
   constexpr int VW = D == 64 ? 1 : 2;  // words of a lane's codes of a row and span: one group, or half of one
 #pragma unroll
-  for (int rt = 0; rt < R; ++rt) {
-    const uint32_t vt = v + rt * step;
-    const unsigned char* vst = vs + rt * 2 * D;
+  for (int sp = 0; sp < SPANS; ++sp) {
+    uint32_t vw[R][4][VW], s0[R], s1[R];  // of rows 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
-    for (int sp = 0; sp < SPANS; ++sp) {
-      uint32_t vw[4][VW], sb[4];  // rows 2c, 2c + 1, 2c + 8, 2c + 9
+    for (int rt = 0; rt < R; ++rt) {
+      const uint32_t vt = v + rt * step;
+      const unsigned char* vst = vs + rt * 2 * D;
+      uint32_t sb[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int r = 2 * c + (j & 1) + 8 * (j >> 1);
         if constexpr (D == 64) {
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw[j][0]) : "r"(vt + chunk_at<RB>(r, g >> 2) + 4 * (g & 3)));
+          asm volatile("ld.shared.u32 %0, [%1];"
+                       : "=r"(vw[rt][j][0])
+                       : "r"(vt + chunk_at<RB>(r, g >> 2) + 4 * (g & 3)));
           sb[j] = vst[r * GR + (g >> 1)];
         } else {
           const uint2 u = lds64(vt + chunk_at<RB>(r, 4 * sp + (g >> 1)) + 8 * (g & 1));
-          vw[j][0] = u.x;
-          vw[j][1] = u.y;
+          vw[rt][j][0] = u.x;
+          vw[rt][j][1] = u.y;
           sb[j] = vst[r * GR + 8 * sp + g];
         }
       }
@@ -700,22 +710,48 @@ __device__ __forceinline__ void tile4(uint32_t k, uint32_t v, uint32_t step, con
           if (r >= rem[rt] || (r >= sk - 16 * rt && r < dead - 16 * rt)) sb[j] = 0;
         }
       }
-      const uint32_t s0 = scales(sb[0] | sb[1] << 8), s1 = scales(sb[2] | sb[3] << 8);
+      s0[rt] = scales(sb[0] | sb[1] << 8);
+      s1[rt] = scales(sb[2] | sb[3] << 8);
+    }
 #pragma unroll
-      for (int w = 0; w < VW; ++w) {  // four output tiles
-        uint32_t e[2][2][4];          // [rows 2c, + 1 or + 8, + 9][even or odd dim][tile]
+    for (int w = 0; w < VW; ++w) {  // four output tiles
+      uint32_t e[R][2][2][4];       // [.][rows 2c, + 1 or + 8, + 9][even or odd dim][tile]
+#pragma unroll
+      for (int rt = 0; rt < R; ++rt) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t w0 = vw[2 * h][w], w1 = vw[2 * h + 1][w];
-          decode8_e2m1((w0 & 0x0f0f0f0fu) | ((w1 & 0x0f0f0f0fu) << 4), e[h][0]);
-          decode8_e2m1(((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), e[h][1]);
+          const uint32_t w0 = vw[rt][2 * h][w], w1 = vw[rt][2 * h + 1][w];
+          decode8_e2m1((w0 & 0x0f0f0f0fu) | ((w1 & 0x0f0f0f0fu) << 4), e[rt][h][0]);
+          decode8_e2m1(((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), e[rt][h][1]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t a[R][4];
+#pragma unroll
+        for (int rt = 0; rt < R; ++rt) {
+          a[rt][0] = mul2(e[rt][0][0][i], s0[rt]);
+          a[rt][1] = mul2(e[rt][0][1][i], s0[rt]);
+          a[rt][2] = mul2(e[rt][1][0][i], s1[rt]);
+          a[rt][3] = mul2(e[rt][1][1][i], s1[rt]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t a[4] = {mul2(e[0][0][i], s0), mul2(e[0][1][i], s0), mul2(e[1][0][i], s1),
-                                 mul2(e[1][1][i], s1)};
+        for (int n = 0; n < NT; ++n) {
+          // the weights' scaled rests (see Margin), of all tiles together
+          float (&o)[4] = st.o[n][sp * 4 * VW + 4 * w + i];
+          float rest[4];
+          mma_fresh(rest, a[0], b[0][n][1][0], b[0][n][1][1]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) add_products<false, NP, false>(st.o[n][sp * 4 * VW + 4 * w + i], a, b[rt][n]);
+          for (int rt = 1; rt < R; ++rt) mma<false>(rest, a[rt], b[rt][n][1][0], b[rt][n][1][1]);
+#pragma unroll
+          for (int rt = 0; rt < R; ++rt) mma<false>(o, a[rt], b[rt][n][0][0], b[rt][n][0][1]);
+          const float2 k2 = make_float2(1.f / kRestScale, 1.f / kRestScale);
+          const float2 lo = ffma2(make_float2(rest[0], rest[1]), k2, make_float2(o[0], o[1]));
+          const float2 hi = ffma2(make_float2(rest[2], rest[3]), k2, make_float2(o[2], o[3]));
+          o[0] = lo.x;
+          o[1] = lo.y;
+          o[2] = hi.x;
+          o[3] = hi.y;
         }
       }
     }
@@ -1395,8 +1431,8 @@ __global__ void __launch_bounds__(GeoOf<CT, D, NT>::Type::kThreads, 1)
         __syncwarp();  // the segment's outputs have been written
         if (cols != 0)
           give_odd_values<CT, D, WIN>(p, u.seq, u.kvh, col0, cols, n_rows, (begin - u.u0) * kTileRows,
-                                 WIN ? (pos - u.u0) * kTileRows : min(n_rows, (pos - u.u0) * kTileRows),
-                                 whole ? nullptr : keep ? so : p.rec_o + rec * NC * D);
+                                      WIN ? (pos - u.u0) * kTileRows : min(n_rows, (pos - u.u0) * kTileRows),
+                                      whole ? nullptr : keep ? so : p.rec_o + rec * NC * D);
         odd = false;
       }
     }
@@ -1801,7 +1837,7 @@ template <typename CT, int D, int NT, bool SHUT, bool WIN>
 kvc_status run_decode(const ScoredParams& p, int grid, const CUtensorMap& tk, const CUtensorMap& tv,
                       cudaLaunchAttribute* attr, cudaStream_t stream) {
   using G = typename GeoOf<CT, D, NT>::Type;
-  static_assert(scored_warps(std::is_same<CT, fp4e2m1>::value ? 0 : sizeof(CT), D, NT) == G::kWarps, "the host counts a CTA's workers as the kernel does");
+  static_assert(scored_warps(sizeof(CT), D, NT) == G::kWarps, "the host counts a CTA's workers as the kernel does");
   static_assert(scored_smem_bytes<CT, D, NT>(GeoOf<CT, D, NT>::kMaxBatch) <= 227 * 1024, "shared memory of a CTA");
   auto* k = scored_decode_kernel<CT, D, NT, SHUT, WIN>;
   // The opt-in to large shared memory holds per device: made at the first call on each.

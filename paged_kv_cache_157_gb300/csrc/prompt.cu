@@ -9,6 +9,12 @@
 // it moves, and moves only when a score exceeds it by kAbove: exact in exact
 // arithmetic for any m, and O is rarely rescaled.
 //
+// What bounds it: the tensor core. 128 x 128 x 128 takes it 512 cycles, so a KV tile of
+// both halves 2048; measured are about 2600 (8192 tokens of 32 query, 8 kv heads, D 128,
+// bf16: 364 us, 1.51 PFLOP/s; 16384 tokens 1.60): the softmax of one half, from S to the
+// first part of P, takes longer than the other half's products. Its exponentials alone
+// are 512 cycles (8 per cycle and scheduler).
+//
 // A work unit is 2 x 128 query rows of one kv head: the `group` query heads of
 // each token are rows of their own (row = token * group + head), so that a kv
 // head's rows are read once for its whole group and a tile's causal edge spans few
@@ -18,16 +24,22 @@
 // The two halves of a unit take turns: while one's softmax runs on its eight
 // warps (two threads per row, no shuffles), the tensor core has the other's
 // products. One warp copies pages by TMA (boxes of gcd(block_size, 128) rows) into
-// a ring of K and V tiles, one thread of another issues the products.
+// a ring of K and V tiles and hands out the units, one thread of another issues the
+// products. (Two threads per row with 32 scores at a time in registers: 1.46
+// PFLOP/s, one thread with all 128, which spills, 1.08. P is handed over in two
+// parts, so that its second half overlaps the first one's product.)
 //
 // P in 16 bits: its rounding (2^-8 of a weight in bf16, 2^-11 in f16) is of the
 // size of the output's own, and a second product for the rest would cost half
-// as much again. f16 weights use f16's whole range (see Margin).
+// as much again. f16 weights use f16's whole range (see PromptMargin).
 //
-// Work split. A planning kernel lists the units' (sequence, token range) tiles.
-// Many units: sorted by cost, dealt out in turn, the largest first. Few units:
-// the KV tiles of all units are laid end to end and cut into equal ranges, one
-// per CTA; the parts of a unit leave records that a merge kernel joins.
+// Work split. Calls with no more units than SMs, none of them long, have no plan: each
+// CTA finds its unit (a few short turns 18 -> 13.5 us). Else a planning kernel lists
+// the units' tiles (sequence, token range), sorted by cost, and they are dealt out in
+// turn, the largest first. Where that leaves the longest CTA more than kSplitGain KV
+// tiles behind the mean, the KV tiles of all units are laid end to end instead and cut
+// into equal ranges, one per CTA; the parts of a unit leave records that a merge
+// kernel joins (120 units of 70 to 235 KV tiles: 175 us, 16 of them the merge).
 //
 // Rows that nobody in a unit sees are neither looked up nor read (TMA fills
 // zeros), those beside visible ones are cleared in shared memory. A row
@@ -123,8 +135,9 @@ struct PromptParams {
 // Where a query's reference m (log2 units) lies: kBelow under the largest score
 // when it moves, and it moves when a score exceeds it by kAbove. f16 ends at
 // 2^-24, and rows beside an attention sink have weights of that size: its
-// largest weights are 2^11 to 2^15, so that weights down to 2^-25 of the largest
-// keep their 11 bits.
+// largest weights are 2^7 to 2^15, so that weights down to 2^-21 of the largest
+// keep their 11 bits. (Room for 8 binary places before O is rescaled: with 4, 432 us
+// for 8192 tokens against 382.)
 template <bool BF>
 struct PromptMargin {
   static constexpr float kBelow = BF ? 0.f : 7.f;
@@ -540,7 +553,8 @@ __device__ __noinline__ void redo_row(const PromptParams& p, int seq, int row, i
   float q[N], o[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) q[j] = Elem<CT>::to_float(static_cast<const CT*>(p.q)[at + j]);
-  (void)attend_row<CT, D, U>(p.row, q, p.block_tables + static_cast<int64_t>(seq) * p.max_blocks, head / p.group, pos, o);
+  (void)attend_row<CT, D, U>(p.row, q, p.block_tables + static_cast<int64_t>(seq) * p.max_blocks, head / p.group,
+                             pos, o);
   store_out_vec<N>(p.out, at, o, std::is_same<CT, __half>::value ? KVC_F16 : KVC_BF16);
 }
 
@@ -674,7 +688,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
           __syncwarp();
           if (lane < boxes) {
-            const uint32_t dst = base + G::kOffRing + slot * G::kTile + static_cast<uint32_t>(lane * p.box) * (G::kRowGroup / 8);
+            const uint32_t dst =
+                base + G::kOffRing + slot * G::kTile + static_cast<uint32_t>(lane * p.box) * (G::kRowGroup / 8);
             tma_load_4d(dst, kv == 0 ? &tm_k : &tm_v, y, bar(G::FULL0 + slot));
           }
           ++issued[slot];

@@ -46,16 +46,17 @@ def hide_unseen(pools, tables, lens, new, bs, window, sinks):
     return tables
 
 
-def tolerance(ref, mass, size, D, n, scale, weight_dtype, out_dtype):
+def tolerance(ref, mass, size, D, n, scale, weight_dtype, out_dtype, vmax=0.0):
     """Bound of |out - ref| for every output, with M = sum p |v| (`mass`) and S = the query's largest sum |q k|:
     a score is a sum of D products in fp32, each addition off by at most 2^-23 of what is summed (tensor cores cut), so
     off by (D + 4) 2^-23 |scale| S, and a weight and the denominator by twice that; the hardware's exp2 and the scaling to
-    log2 units add 2^-20; the weight's own rounding for the second product half a step of its type (none where it is
-    kept in parts: 2^-21); sums over n rows add 2^-23 for each 8 of them, and 64 for joins; the result's rounding half a
+    log2 units add 2^-20; the weight's own rounding for the second product half a step of its type (where it is kept in
+    two f16 parts, the second scaled by 2^11: 2^-21, and for weights below 2^-25 of the largest one 2^-47 of that, for each
+    of n values of at most vmax); sums over n rows add 2^-23 for each 8 of them, and 64 for joins; the result's rounding half a
     step of its type."""
     dx = (D + 4) * 2.0 ** -23 * abs(scale) * size[..., None]
     part = 2.0 ** -21 if weight_dtype is None else torch.finfo(weight_dtype).eps / 2
-    tol = (4 * dx + 2.0 ** -20 + part + (n / 8 + 64) * 2.0 ** -23) * mass
+    tol = (4 * dx + 2.0 ** -20 + part + (n / 8 + 64) * 2.0 ** -23) * mass + n * 2.0 ** -47 * vmax
     if out_dtype != torch.float32:
         tol = tol + torch.finfo(out_dtype).eps / 2 * np.abs(ref) * (1 + 2 ** -7) + float(torch.finfo(out_dtype).tiny)
     return tol + 1e-30
@@ -176,5 +177,6 @@ class Decode:
                 continue
             ref, mass, size = O.attend(f64(self.q[i]), self.pools[0][1], self.pools[1][1], self.tables[i], n,
                                        self.scale, self.window, self.sinks)
-            close(out[i], ref, tolerance(ref, mass, size, self.D, n, self.scale, None, self.out.dtype),
-                  f"sequence {i}")
+            V = self.pools[1][1]
+            close(out[i], ref, tolerance(ref, mass, size, self.D, n, self.scale, None, self.out.dtype,
+                                         float(np.abs(V[np.isfinite(V)]).max())), f"sequence {i}")

@@ -191,3 +191,23 @@ def test_a_stream_served_in_four_bits(kvc):
         for i in range(2):
             check(out[i:i + 1], q[i:i + 1], i, n[i])
     assert kvc.get_error_flags() == 0
+
+
+def test_rows_far_up_a_large_pool(kvc):
+    """Byte offsets beyond 32 bits, and rows on both sides of them."""
+    nb, H, bs, D = 700000, 8, 16, 128
+    dev = [torch.zeros((nb, H, bs, D // n), dtype=torch.uint8, device="cuda") for n in (2, 2, 16, 16)]
+    slots = [0, 5, nb * bs - 1, (nb - 3) * bs + 7, 524287 * bs + 15, 524288 * bs]
+    k, v = rows(len(slots), H, D, "bf16", 9)
+    t = torch.tensor(slots, dtype=torch.int64, device="cuda")
+    kvc.append_fp4(k, v, t, *dev)
+    a, b = torch.zeros_like(k), torch.zeros_like(v)
+    kvc.read_fp4(t, *dev, a, b)
+    for j, (x, back) in enumerate(((k, a), (v, b))):
+        codes, scales = O.encode_fp4(f64(x))
+        want = O.values_fp4(O.pack(codes), scales)
+        assert np.array_equal(f64(back), want)
+        for i, s in enumerate(slots):
+            assert np.array_equal(dev[j + 2][s // bs, :, s % bs].cpu().numpy(), scales[i])
+        assert int((dev[j + 2] != 0).sum()) == int((scales != 0).sum())  # nothing else was written
+    assert kvc.get_error_flags() == 0

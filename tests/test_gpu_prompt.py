@@ -230,3 +230,50 @@ def test_checked_mode_reports(kvc):
         assert e.value.status == kvc.ERR_OUT_OF_RANGE
     finally:
         kvc.set_option(kvc.OPT_CHECKED, 0)
+
+
+def test_blocks_far_up_a_large_pool(kvc):
+    """Byte offsets beyond 32 bits."""
+    p = Prompt([90, 20], [300, 20], 8, 8, 128, 16, "bf16", seed=17, garbage=False)
+    nb = 150000
+    small = [x[0] for x in p.pools]
+    for x in p.pools:
+        large = torch.empty((nb, *x[0].shape[1:]), dtype=x[0].dtype, device="cuda")
+        large[nb - len(x[0]):] = x[0].flip(0)
+        x[0] = large
+    tables = p.tables
+    p.tables = np.where(tables < (1 << 28), nb - 1 - tables, tables).astype(np.int32)
+    p.run(kvc)
+    p.tables = tables
+    for x, t in zip(p.pools, small):
+        x[0] = t
+    p.check()
+    assert kvc.get_error_flags() == 0
+
+
+def test_two_streams_at_once(kvc):
+    a = Prompt([300, 40], [900, 2500], 8, 2, 128, 16, "bf16", seed=18)
+    b = Prompt([60], [300], 8, 2, 128, 16, "f16", 90, 5, seed=19)
+    args = [(p, p.device(), p.workspace(kvc), torch.cuda.Stream()) for p in (a, b)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for p, (tables, starts, rows), ws, stream in args:
+            kvc.prompt_attention(p.q, p.pools[0][0], p.pools[1][0], tables, starts, rows, p.scale, p.out, ws,
+                                 window=p.window, sinks=p.sinks, stream=stream)
+    torch.cuda.synchronize()
+    a.check()
+    b.check()
+
+
+def test_fewer_ctas(kvc):
+    """Any number of CTAs gives the same outputs up to the order of the sums, in every way of handing out units."""
+    for sizes in (([300, 40], [300, 2500], 8, 2, 128, 16), ([200, 57], [200, 300], 512, 8, 64, 16),
+                  ([5, 9], [50, 90], 8, 2, 128, 16)):
+        p = Prompt(*sizes, "bf16", seed=20)
+        for ctas in (1, 2, 7, 100):
+            kvc.set_option(kvc.OPT_MAX_CTAS, ctas)
+            try:
+                p.run(kvc)
+            finally:
+                kvc.set_option(kvc.OPT_MAX_CTAS, 0)
+            p.check()

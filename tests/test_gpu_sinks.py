@@ -5,6 +5,9 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import streams as O
+
+from long_context_helpers import f64
 from stream_helpers import Decode, int32
 
 pytestmark = pytest.mark.gpu
@@ -166,3 +169,91 @@ def test_the_freed_middle_of_a_stream(kvc):
     d.run(kvc)
     assert kvc.get_error_flags() == 0
     d.check()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_blocks_far_up_a_large_pool(kvc, kind):
+    """Byte offsets beyond 32 bits, in the codes, the scales and the rows."""
+    d = Decode([200, 33], 1, 8, 8, 128, 16, kind, 60, 4, seed=13, garbage=False)
+    nb = 700000 if kind == "fp4" else 150000
+    move = torch.from_numpy(np.unique(d.tables[d.tables < len(d.pools[0][1])]).astype(np.int64)).cuda()
+    far = nb - 1 - move
+    before = [p[0] for p in d.pools]
+    for i, p in enumerate(d.pools):
+        parts = p[0] if kind == "fp4" else (p[0],)
+        large = [torch.empty((nb, *t.shape[1:]), dtype=t.dtype, device="cuda") for t in parts]
+        for t, x in zip(parts, large):
+            x[far] = t[move]
+        p[0] = tuple(large) if kind == "fp4" else large[0]
+    tables = torch.from_numpy(np.where(d.tables < (1 << 28), nb - 1 - d.tables, d.tables).astype(np.int32)).cuda()
+    d.call(kvc, tables, int32(d.lens), d.workspace(kvc))
+    torch.cuda.synchronize()
+    for p, t in zip(d.pools, before):
+        p[0] = t
+    d.check()
+    assert kvc.get_error_flags() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_two_streams_at_once(kvc, kind):
+    a = Decode([700, 300], 1, 8, 2, 128, 16, kind, 200, 4, seed=14)
+    b = Decode([90, 1500], 1, 8, 2, 128, 16, kind, None, 0, seed=15)
+    args = [(d, torch.from_numpy(d.tables).cuda(), int32(d.lens), d.workspace(kvc), torch.cuda.Stream()) for d in (a, b)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for d, tables, lens, ws, stream in args:
+            d.call(kvc, tables, lens, ws, stream)
+    torch.cuda.synchronize()
+    a.check()
+    b.check()
+
+
+def test_many_sequences(kvc):
+    """Prefix sums in shared memory, up to the largest batch of a four-bit cache."""
+    for kind, n in (("bf16", 4096), ("fp4", 2048)):
+        lens = [1 + (7 * i) % 37 for i in range(n)]
+        d = Decode(lens, 1, 1, 1, 64, 16, kind, 20, 2, seed=16, garbage=False)
+        d.run(kvc)
+        d.check(skip=set(range(n)) - set(range(0, n, 41)))
+        assert torch.isfinite(d.out).all() and (d.out != 7.0).any(-1).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("depth", [3, 6, 12, 16.5])  # e^-16.5: 2^-24 of the sink's weight
+@pytest.mark.parametrize("n,window,per", [(864, None, 0), (864, 300, 1000), (2100, 2000, 1000), (300, 17, 0)])
+def test_small_weights_beside_a_sink_keep_their_precision(kvc, kind, depth, n, window, per):
+    """The first row takes nearly all the weight and brings nothing; the outputs are made of the others' weights."""
+    H, G, D, bs = 2, 4, 128, 16
+    rng = np.random.default_rng(int(depth))
+    nb = -(-n // bs)
+    tables = rng.permutation(nb).astype(np.int32)[None]
+    k, v = np.zeros((nb, H, bs, D)), np.zeros((nb, H, bs, D))
+    at = tables[0, np.arange(n) // bs], np.arange(n) % bs
+    k[at[0], :, at[1], 0] = -depth
+    v[at[0], :, at[1]] = rng.choice([1.0, 2.0, 3.0, 4.0, 6.0], (n, H, D))
+    v[at[0], :, at[1], ::16] = 6.0  # a group's scale is then 1
+    k[tables[0, 0], :, 0] = v[tables[0, 0], :, 0] = 0
+    d = Decode([n], 1, H * G, H, D, bs, kind, window, 1, garbage=False)
+    if kind == "fp4":
+        caches = []
+        for x in (k, v):
+            c, s = O.encode_fp4(x)  # exact: -6 * (depth / 6), and codes of scale 1
+            assert np.array_equal(O.values_fp4(O.pack(c), s), x)
+            caches.append([(torch.from_numpy(O.pack(c)).cuda(), torch.from_numpy(s).cuda()), x])
+        d.pools = caches
+    else:
+        d.pools = [[torch.from_numpy(x).to(d.q.dtype).cuda(), x] for x in (k, v)]
+    d.tables, d.scale = tables, 1.0
+    d.q.zero_()
+    d.q[..., 0] = 1
+    kvc.set_option(kvc.OPT_BLOCKS_PER_CTA, per)
+    try:
+        d.run(kvc)
+    finally:
+        kvc.set_option(kvc.OPT_BLOCKS_PER_CTA, 0)
+    ref, _, _ = O.attend(f64(d.q[0]), k, v, tables[0], n, 1.0, window, 1)
+    # scores are whole numbers but for the factor log2(e) and its product, 2^-24 of at most 24 each, which moves a weight
+    # by 24 * 2^-23 * ln 2; exp2 2^-22; the parts 2^-21; all values are positive, so errors stay relative to the output:
+    # 3 products of 17 terms per 16 rows, each off by 2^-23 of the sum, and 64 joins
+    rel = 24 * 2.0 ** -23 * 0.7 * 2 + 2.0 ** -20 + (3 * 17 * (n / 16 + 1) + 64) * 2.0 ** -23
+    assert (np.abs(f64(d.out[0]) - ref) / ref).max() <= rel

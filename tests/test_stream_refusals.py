@@ -71,7 +71,7 @@ def test_decode_with_sinks_refuses(kvc, kw, status):
 
 
 @pytest.mark.parametrize("kw,status", DECODE + [(dict(ks=Z), "INVALID_ARG"), (dict(vs=Z), "INVALID_ARG"),
-                                                (dict(ks=ODD), "INVALID_ARG")])
+                                                (dict(ks=ODD), "INVALID_ARG"), (dict(B=2049), "UNSUPPORTED")])
 def test_decode_fp4_refuses(kvc, kw, status):
     assert fp4(kvc, **kw) == getattr(kvc, "ERR_" + status)
 
