@@ -62,6 +62,7 @@
 #include "code4.cuh"
 #include "decode_gqa_mma.cuh"
 #include "decode_scored.h"
+#include "packed.cuh"
 
 namespace kvc {
 

@@ -400,14 +400,6 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
   return R.f;
 }
 
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
-  F2U64 A, Bv, R;
-  A.f = a;
-  Bv.f = b;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(R.u) : "l"(A.u), "l"(Bv.u));
-  return R.f;
-}
-
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -59,6 +59,7 @@
 
 #include "attend_row.cuh"
 #include "kvc_internal.h"
+#include "packed.cuh"
 #include "umma.cuh"
 #include "umma_wide.cuh"
 
