@@ -291,7 +291,8 @@ kvc_status kvc_read_fp4(const int64_t* slot_mapping, int64_t num_tokens, const v
  * n_kv_heads * block_size * head_dim * element size; for a latent pool,
  * block_size * (d_c + d_r) * element size; for the scales of kvc_append_block8,
  * n_kv_heads * 4, for those of kvc_append_fp8 and kvc_append_int8, n_kv_heads *
- * block_size * 4), 16-byte aligned; block_bytes a multiple of 16, or of 4 with the
+ * block_size * 4, for the four-bit codes and scales of kvc_append_fp4,
+ * n_kv_heads * block_size * head_dim / 2 and / 16), 16-byte aligned; block_bytes a multiple of 16, or of 4 with the
  * cache 4-byte aligned. pairs: int64 [n_pairs, 2] in device memory. Destination
  * blocks must be distinct and must not be sources in the same call (copies
  * run concurrently). Pairs naming a block outside the pool are skipped and set

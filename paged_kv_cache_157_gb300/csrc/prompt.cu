@@ -857,7 +857,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     };
     bool ok = true;
     for (uint32_t un = 0;; ++un) {
-      if (!wait_warp(bar(G::UFULL0 + (un & 1)), (un >> 1) & 1u)) break;
+      // both warps of a row go on or give up: neither may wait at their barrier alone
+      if (pair_or(pair, !wait_warp(bar(G::UFULL0 + (un & 1)), (un >> 1) & 1u))) break;
       const Part& u = s_unit[un & 1];
       if (u.t.count == 0) break;
       if (hf * p.tokens >= u.t.count) {  // the half has no token
