@@ -1062,8 +1062,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       } else {
         // Rows done again whole, by either warp of the row or by both (the same
         // values): at the end, when nobody waits for this warp any more (a row of a
-        // long sequence takes milliseconds).
-        const uint32_t odd = __ballot_sync(full, valid && zero != 0.f);
+        // long sequence takes milliseconds). Where a visible score is NaN the sum is,
+        // and so are all outputs of the row: nothing to find out.
+        const uint32_t odd = __ballot_sync(full, valid && zero != 0.f && l == l);
         if (odd != 0) {
           if (n_redo < p.redo_max) {
             if (lane == 0) *redo(n_redo) = {u.t, u.kvh, odd, {0, 0}};
@@ -1180,7 +1181,7 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptParams p)
         o[k][c] *= inv;
         zero = fmaf(o[k][c], 0.f, zero);
       }
-      if (__any_sync(0xffffffffu, zero != 0.f))
+      if (L[k] == L[k] && __any_sync(0xffffffffu, zero != 0.f))  // (a sum that is NaN: see prompt_kernel)
         redo_row<CT, D, 1>(p, t.seq, t.first + tok[k], head[k], t.pos + tok[k]);
       else
         store_out_vec<N>(p.out, (static_cast<int64_t>(t.first + tok[k]) * p.n_q_heads + head[k]) * D + lane * N, o[k],

@@ -117,6 +117,18 @@ def test_keys_that_are_not_finite_in_hidden_rows(kvc):
     assert np.isfinite(out[:83]).all() and np.isnan(out[83:100]).all()
 
 
+@pytest.mark.parametrize("sizes", [([70], [9000], 8, 1, 128, 16), ([100], [100], 4, 1, 128, 16)])
+def test_queries_that_are_not_finite(kvc, sizes):
+    p = Prompt(*sizes, "bf16", seed=21)
+    p.q[5, 3, 7] = float("nan")
+    p.q[9, 1, 0] = float("inf")
+    p.run(kvc)
+    out = f64(p.out)
+    bad = np.zeros(out.shape[:2], bool)
+    bad[5, 3] = bad[9, 1] = True
+    assert np.isnan(out[bad]).all() and np.isfinite(out[~bad]).all() and kvc.get_error_flags() == 0
+
+
 def test_invalid_lengths_and_starts(kvc):
     p = Prompt([20, 30, 10, 5], [20, 60, 10, 5], 4, 1, 128, 16, "bf16", seed=8, garbage=False)
     tables, _, _ = p.device()
