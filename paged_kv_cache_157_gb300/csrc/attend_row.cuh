@@ -7,8 +7,9 @@
 // dims l * D / 32 on; every product and sum is fp32. Only visible rows are read.
 //
 // An infinity or NaN in V of a visible row is the output there, however small
-// the row's weight: weights and rescalings are kept at or above the smallest
-// normal number, which changes no finite output in fp32.
+// the row's weight: what is not finite is weighed and rescaled by the smallest normal
+// number at least. Finite values take weights as they are (bf16 ends at 3.4e38, where
+// a weight of 1.2e-38 in place of 0 would be seen).
 #pragma once
 
 #include <type_traits>
@@ -44,6 +45,7 @@ __device__ bool attend_row(const RowParams& p, const float (&q)[D / 32], const i
                            float (&o)[D / 32]) {
   constexpr int N = D / 32;
   constexpr float kTiny = 1.17549435e-38f;
+  auto finite = [](float a) { return fabsf(a) < __builtin_huge_valf(); };
   const int lane = threadIdx.x & 31;
   const int low = pos >= p.window ? pos - p.window + 1 : 0;  // first row of the window
   const int front = min(p.sinks, low);
@@ -88,10 +90,10 @@ __device__ bool attend_row(const RowParams& p, const float (&q)[D / 32], const i
     for (int u = 0; u < U; ++u)
       if (row[u] >= 0) load_dims<CT, D>(p.v_cache, row[u], lane, x[u]);
     if (top > m) {
-      const float f = fmaxf(fast_exp2(m - top), kTiny);
+      const float f = fast_exp2(m - top);
       l *= f;
 #pragma unroll
-      for (int j = 0; j < N; ++j) o[j] *= f;
+      for (int j = 0; j < N; ++j) o[j] *= finite(o[j]) ? f : fmaxf(f, kTiny);
       m = top;
     }
 #pragma unroll
@@ -100,7 +102,7 @@ __device__ bool attend_row(const RowParams& p, const float (&q)[D / 32], const i
       const float w = s[u] == -__builtin_huge_valf() ? 0.f : fast_exp2(s[u] - m);
       l += w;
 #pragma unroll
-      for (int j = 0; j < N; ++j) o[j] = fmaf(w >= 0.f ? fmaxf(w, kTiny) : w, x[u][j], o[j]);
+      for (int j = 0; j < N; ++j) o[j] = fmaf(finite(x[u][j]) || w != w ? w : fmaxf(w, kTiny), x[u][j], o[j]);
     }
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
