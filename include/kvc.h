@@ -559,7 +559,10 @@ kvc_status kvc_prompt_workspace_size(int batch, int64_t num_tokens, int n_q_head
  *                 (append them first); not looked at where m_i is 0
  * Token t of sequence i, at position pos = context_lens[i] - m_i + t, attends row
  * r if r <= pos and (r > pos - window or r < sinks); window >= 1 (INT32_MAX: every
- * row), sinks >= 0. Other rows' infinities and NaN do not reach it. Scores, sums
+ * row), sinks >= 0. Other rows' infinities and NaN do not reach it; an infinity or
+ * NaN in V of a row that it attends is its output there, whatever the row's weight.
+ * (Such values cost a second pass over the rows of the tokens around those that see
+ * them: at most about four times the time of finite values.) Scores, sums
  * and outputs accumulate in fp32; the softmax weights are rounded to `dtype` for
  * the second product. Table entries of blocks that no token sees are not used.
  * head_dim 64 or 128; block_size a multiple of 16 up to 128; batch <= 4096; at

@@ -42,9 +42,16 @@
 // kernel joins (120 units of 70 to 235 KV tiles: 175 us, 16 of them the merge).
 //
 // Rows that nobody in a unit sees are neither looked up nor read (TMA fills
-// zeros), those beside visible ones are cleared in shared memory. A row
-// whose output is not finite is done again over its visible rows alone, so that
-// an infinity or NaN in V stays with those who see it.
+// zeros), those beside visible ones are cleared in shared memory.
+//
+// Infinities and NaN in V: 0 x infinity is NaN, so they reach every row of a unit
+// through the second product, and a weight that is 0 loses them. A unit (or part of
+// one) with an output that is not finite is done again when the CTA's others are done: on the
+// way, what is not finite in its V tiles is replaced by 0 and written down, dim by dim, for
+// the rows that all tokens of the unit see together and row by row for the others;
+// each output then is the finite sum, or what its token sees of those. (One infinity in the
+// first of 2048 rows: 146 us against 46.) The code for it is apart: in the loops that every call
+// runs, it cost 3 to 8 % through the registers alone.
 //
 // Sources: the chunk mask of "单请求 KV Cache" (query row i of a chunk sees
 // columns up to past_len + i) and the block table of "KV Cache（键值缓存）" section
@@ -57,7 +64,6 @@
 #include <mutex>
 #include <numeric>
 
-#include "attend_row.cuh"
 #include "kvc_internal.h"
 #include "packed.cuh"
 #include "umma.cuh"
@@ -94,15 +100,7 @@ struct PromptShape {
 struct Tile {
   int first, pos;            // its first row of q and that token's position
   unsigned short seq, count;
-  int cost;                  // KV tiles that it sees
-};
-
-// Rows of a warp's 32 that are to be done again (bits of `rows`).
-struct Redo {
-  Tile t;
-  int kvh;
-  uint32_t rows;
-  int pad[2];
+  int cost;                  // KV tiles that it sees (in a Part: its place among PromptParams::odd)
 };
 
 // How units are handed out: one per CTA without a plan; planned, whole; planned,
@@ -110,7 +108,6 @@ struct Redo {
 enum { kPlanNone = 0, kPlanWhole = 1, kPlanSplit = 2 };
 
 struct PromptParams {
-  RowParams row;
   const void* q;  // [num_tokens, n_q_heads, D]
   void* out;
   const int32_t* block_tables;
@@ -122,9 +119,10 @@ struct PromptParams {
   int* before;   // KV tiles of the tiles before each (where units are split)
   float* rec_o;  // [2 * CTAs, 2 * kM, D] unnormalised partial outputs
   float* rec_ml; // [2 * CTAs, 2 * kM, 2] (reference, sum of weights)
-  Redo* redo;    // [CTAs, softmax warps, redo_max] rows to do again
-  int redo_max;
+  struct OddUnit* odd;  // [units, then records] those to be done again: lists, one per CTA
   unsigned int* err;
+  int64_t num_blocks;
+  int n_kv_heads, block_size, window, sinks;
   int batch, num_tokens, n_q_heads, group, max_blocks, rows, tokens, max_tiles;
   int mode, grid;  // mode: kPlan*
   int box, box_log2;  // rows of a TMA box: gcd(block_size, 128)
@@ -230,7 +228,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
       continue;
     }
     local += (s.count + per_tile - 1) / per_tile;
-    if (s.count > 0) most = max(most, seen_tiles(s.rows - 1, 1, p.row.window, p.row.sinks).total + 1);
+    if (s.count > 0) most = max(most, seen_tiles(s.rows - 1, 1, p.window, p.sinks).total + 1);
   }
   int n = 0;
   int run = block_scan(local, s_warp, &n);
@@ -266,7 +264,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
     t.first = s.first + t0;
     t.count = static_cast<unsigned short>(min(per_tile, s.count - t0));
     t.pos = s.rows - s.count + t0;
-    t.cost = seen_tiles(t.pos, t.count, p.row.window, p.row.sinks).total;
+    t.cost = seen_tiles(t.pos, t.count, p.window, p.sinks).total;
     return t;
   };
   most = max(__reduce_max_sync(0xffffffffu, most), 1);
@@ -290,7 +288,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
       }
       total += sum;
     }
-    split = most - total * p.row.n_kv_heads / p.grid > kSplitGain;
+    split = most - total * p.n_kv_heads / p.grid > kSplitGain;
   }
   if (!split) {  // sorted by cost, in up to 1024 classes
     int shift = 0;
@@ -336,7 +334,24 @@ struct Part {
   int kvh, i0, i1;
   int rec;  // -1: the whole unit
 };
-static_assert(sizeof(Tile) == 16 && sizeof(Part) == 32, "copied as 16-byte words");
+// One with an output that was not finite, and the place of the CTA's next one, -1: none.
+struct OddUnit {
+  Part u;
+  int next;
+  int pad[3];
+};
+static_assert(sizeof(Tile) == 16 && sizeof(Part) == 32 && sizeof(OddUnit) == 48, "copied as 16-byte words");
+
+struct OddList {
+  int at;
+  __device__ __forceinline__ bool next(const PromptParams& p, Part& u) {
+    if (at < 0) return false;
+    const OddUnit e = p.odd[at];  // (written by this CTA)
+    u = e.u;
+    at = e.next;
+    return true;
+  }
+};
 
 // The CTA's units. One warp walks (all lanes with the same values) and tells the others.
 struct Walk {
@@ -358,7 +373,7 @@ struct Walk {
   }
   __device__ __forceinline__ Walk(const PromptParams& p) {
     at = lo = hi = i = kvh = split = 0;
-    const int H = p.row.n_kv_heads, lane = threadIdx.x & 31;
+    const int H = p.n_kv_heads, lane = threadIdx.x & 31;
     if (p.mode == kPlanNone) {
       // the CTA's only unit: tiles of the sequences added up, 32 sequences at a time
       n = 0;
@@ -383,7 +398,7 @@ struct Walk {
           ahead.first = first + t0;
           ahead.count = static_cast<unsigned short>(min(per, count - t0));
           ahead.pos = rows - count + t0;
-          ahead.cost = seen_tiles(ahead.pos, ahead.count, p.row.window, p.row.sinks).total;
+          ahead.cost = seen_tiles(ahead.pos, ahead.count, p.window, p.sinks).total;
           n = want + 1;
           break;
         }
@@ -414,11 +429,12 @@ struct Walk {
     at = lo;
   }
   __device__ __forceinline__ bool next(const PromptParams& p, Part& u) {
-    const int H = p.row.n_kv_heads;
+    const int H = p.n_kv_heads;
     if (!split) {
       const int j = unit(p, at);
       if (j >= n * H) return false;
       u = {ahead, j % H, 0, ahead.cost, -1};
+      u.t.cost = j;
       ++at;
       const int k = unit(p, at);
       if (p.mode != kPlanNone && k < n * H) ahead = load(p, k / H);
@@ -431,6 +447,7 @@ struct Walk {
     u.i0 = begins ? lo : 0;
     u.i1 = min(u.t.cost, u.i0 + (hi - at));
     u.rec = u.i0 == 0 && u.i1 == u.t.cost ? -1 : 2 * static_cast<int>(blockIdx.x) + (begins ? 0 : 1);
+    u.t.cost = u.rec < 0 ? i * H + kvh : p.max_tiles * H + u.rec;
     at += u.i1 - u.i0;
     if (++kvh == H) {
       kvh = 0;
@@ -457,14 +474,21 @@ struct PromptGeo {
   static constexpr uint32_t kOffBar = kOffStage + kSoftWarps * 2048;
   enum {
     QFULL = 0, QEMPTY, FULL0, EMPTY0 = FULL0 + kSlots, SFULL0 = EMPTY0 + kSlots, PFULL0 = SFULL0 + 2,
-    OFULL0 = PFULL0 + 4, OEMPTY0 = OFULL0 + 2, UFULL0 = OEMPTY0 + 2, UEMPTY0 = UFULL0 + 2, FINAL = UEMPTY0 + 2, COUNT
+    OFULL0 = PFULL0 + 4, OEMPTY0 = OFULL0 + 2, UFULL0 = OEMPTY0 + 2, UEMPTY0 = UFULL0 + 2, FINAL = UEMPTY0 + 2,
+    ODDFULL, COUNT
   };
-  static constexpr uint32_t kOffMisc = kOffBar + COUNT * 8;  // TMEM address, abort flag, bad blocks
-  static constexpr uint32_t kOffPart = kOffMisc + 8 + kBadRing * 4;  // what the threads of a row tell each other
+  // a second set for the units done again: the first one's phases need not be known then
+  static constexpr uint32_t kOffMisc = kOffBar + 2 * COUNT * 8;  // TMEM address, abort flag, odd units, bad blocks
+  static constexpr uint32_t kOffPart = kOffMisc + 20 + kBadRing * 4;  // what the threads of a row tell each other
   static constexpr uint32_t kOffFail = kOffPart + kSoftWarps * 32 * 4;
   static constexpr uint32_t kOffUnit = (kOffFail + kSoftWarps * 4 + 15) / 16 * 16;  // two units: this and the next
   static constexpr uint32_t kBytes = kOffUnit + 2 * sizeof(Part);
   static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
+  // While a unit is done again, where outputs are staged: an OddDims of each (row of a tile,
+  // column group) for the rows that every token sees, then of each (row that some see,
+  // column group): at most 255 behind the first token's and 255 that leave the window.
+  static constexpr uint32_t kOffOddRows = kOffStage + kRows * 2 * 16;
+  static_assert(kOffOddRows + 2 * (2 * kM - 1) * 2 * 16 <= kOffBar, "records of what is not finite");
   // TMEM columns: S (P over it) of both halves, O of both
   static constexpr uint32_t kColO = 256;
   static constexpr uint32_t kTmemCols = 512;
@@ -545,72 +569,58 @@ __device__ __forceinline__ bool pair_or(int id, bool pred) {
   return r != 0;
 }
 
-// One output row again, over its visible rows alone (attend_row.cuh). Rare.
-template <typename CT, int D, int U>
-__device__ __noinline__ void redo_row(const PromptParams& p, int seq, int row, int head, int pos) {
-  constexpr int N = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t at = (static_cast<int64_t>(row) * p.n_q_heads + head) * D + lane * N;
-  float q[N], o[N];
+// What is not finite among values of a column group's dims (bits): x, y +infinity, z, w
+// -infinity, NaN both.
+using OddDims = uint4;
+
+// Replaces what is not finite in 16 bytes of V by 0 and notes it: dim0 the first element's.
+template <bool BF>
+__device__ __forceinline__ void take_odd(unsigned char* at, int dim0, OddDims& odd) {
+  constexpr uint32_t EXP = BF ? 0x7f80u : 0x7c00u;
+  uint32_t x[4];
+  *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(at);
+  uint32_t plus = 0, minus = 0;
 #pragma unroll
-  for (int j = 0; j < N; ++j) q[j] = Elem<CT>::to_float(static_cast<const CT*>(p.q)[at + j]);
-  (void)attend_row<CT, D, U>(p.row, q, p.block_tables + static_cast<int64_t>(seq) * p.max_blocks, head / p.group,
-                             pos, o);
-  store_out_vec<N>(p.out, at, o, std::is_same<CT, __half>::value ? KVC_F16 : KVC_BF16);
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t h = (x[k >> 1] >> (16 * (k & 1))) & 0xffffu;
+    if ((h & EXP) != EXP) continue;
+    const bool nan = (h & (0x7fffu & ~EXP)) != 0;
+    if (nan || h < 0x8000u) plus |= 1u << k;
+    if (nan || h >= 0x8000u) minus |= 1u << k;
+    x[k >> 1] &= k & 1 ? 0x0000ffffu : 0xffff0000u;
+  }
+  if ((plus | minus) == 0) return;
+  *reinterpret_cast<uint4*>(at) = *reinterpret_cast<const uint4*>(x);
+  (dim0 < 32 ? odd.x : odd.y) |= plus << (dim0 & 31);
+  (dim0 < 32 ? odd.z : odd.w) |= minus << (dim0 & 31);
 }
 
-template <typename CT, int D>
-__global__ void __launch_bounds__(kPromptThreads, 1)
-    prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PromptParams p) {
+// x, or what its dim has of infinities and NaN.
+__device__ __forceinline__ float odd_or(float x, uint32_t plus, uint32_t minus, int bit) {
+  const uint32_t b = 1u << bit;
+  if (((plus | minus) & b) == 0) return x;
+  const float inf = __builtin_huge_valf();
+  return (plus & b) == 0 ? -inf : (minus & b) == 0 ? inf : __int_as_float(0x7fffffff);
+}
+
+// The roles of a CTA's warps for all of its units (AGAIN: for those that are to be done
+// again). Ends with a CTA barrier.
+template <typename CT, int D, bool AGAIN>
+__device__ __forceinline__ void prompt_roles(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                             const PromptParams& p, unsigned char* sm, uint32_t tmem) {
   using G = PromptGeo<D>;
   constexpr bool BF = std::is_same<CT, __nv_bfloat16>::value;
   constexpr uint32_t full = 0xffffffffu;
-  extern __shared__ __align__(1024) unsigned char sm[];  // the swizzle counts from multiples of 1024
   const uint32_t base = smem_addr(sm);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + G::kOffBar);
-  volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(sm + G::kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(sm + G::kOffMisc + 4);
-  volatile uint32_t* s_bad = reinterpret_cast<volatile uint32_t*>(sm + G::kOffMisc + 8);
-  auto bar = [&](int i) -> uint32_t { return base + G::kOffBar + 8u * static_cast<uint32_t>(i); };
+  // the list of odd units' first; whether the units of s_unit are on it
+  volatile int* s_odd = reinterpret_cast<volatile int*>(sm + G::kOffMisc + 8);
+  volatile uint32_t* s_bad = reinterpret_cast<volatile uint32_t*>(sm + G::kOffMisc + 20);
+  auto bar = [&](int i) -> uint32_t {
+    return base + G::kOffBar + 8u * static_cast<uint32_t>(i + (AGAIN ? G::COUNT : 0));
+  };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
-  if ((base & 1023u) != 0) {  // the alignment above was not kept
-    set_flag(p.err, KVC_FLAG_TIMEOUT);
-    return;
-  }
-  if (tid == 0) {
-    *s_abort = 0;
-    for (int i = 0; i < G::COUNT; ++i) {
-      uint32_t from = 1;
-      if ((i >= G::PFULL0 && i < G::OFULL0) || (i >= G::OEMPTY0 && i < G::UFULL0)) from = kSoftWarps / 2;
-      if (i >= G::UEMPTY0 && i < G::FINAL) from = kSoftWarps + 1;
-      mbar_init(&bars[i], from);
-    }
-    fence_barrier_init();
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
-  }
-  // Query rows that no token has (128 is no multiple of the group) stay zeros.
-  if (p.tokens * p.group < kM) {
-    for (uint32_t i = tid; i < 2 * G::kTile / 16; i += kPromptThreads)
-      *reinterpret_cast<uint4*>(sm + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
-    fence_proxy_async_smem();
-  }
-  if (warp == kSoftWarps + 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + G::kOffMisc),
-                 "r"(G::kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  fence_before();
-  __syncthreads();
-  fence_after();
-  const uint32_t tmem = *s_tmem;
-  const int bs = p.row.block_size, window = p.row.window, sinks = p.row.sinks;
+  const int bs = p.block_size, window = p.window, sinks = p.sinks;
   Part* s_unit = reinterpret_cast<Part*>(sm + G::kOffUnit);
 
   if (warp == kSoftWarps) {
@@ -621,16 +631,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     uint32_t issued[G::kSlots] = {};
     const int boxes = kRows / p.box;
     bool ok = true;
-    Walk walk(p);
+    auto walk = [&] {
+      if constexpr (AGAIN) return OddList{*s_odd};
+      else return Walk(p);
+    }();
     for (; ok; ++un) {
       Part u;
       const bool have = walk.next(p, u);
       if (!have) u.t.count = 0;  // the end
       bool got = true;
-      if (lane == 0 && un >= 2) got = wait_phase(bar(G::UEMPTY0 + (un & 1)), ((un >> 1) - 1) & 1u, s_abort, p.err);
+      // A unit done again has the CTA to itself: its records lie where outputs are staged
+      constexpr uint32_t kBefore = AGAIN ? 1 : 2;
+      if (lane == 0 && un >= kBefore)
+        got = wait_phase(bar(G::UEMPTY0 + ((un - kBefore) & 1)), ((un - kBefore) >> 1) & 1u, s_abort, p.err);
       if (!__shfl_sync(full, got ? 1 : 0, 0)) break;
       if (lane == 0) {
         s_unit[un & 1] = u;
+        s_odd[1 + (un & 1)] = 0;
         arrive(bar(G::UFULL0 + (un & 1)));
       }
       __syncwarp();
@@ -663,9 +680,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       int phys = r0 >= 0 ? __ldg(table + r0 / bs) : -1;
       for (int i = u.i0; i < u.i1; ++i, ++gt) {
         const bool want = r0 >= 0;
-        const bool there = phys >= 0 && phys < p.row.num_blocks;
+        const bool there = phys >= 0 && phys < p.num_blocks;
         const uint32_t bad = __ballot_sync(full, want && !there);
-        const int y = (there ? (phys * p.row.n_kv_heads + u.kvh) * bs + r0 % bs : p.pool_rows) >> 3;
+        const int y = (there ? (phys * p.n_kv_heads + u.kvh) * bs + r0 % bs : p.pool_rows) >> 3;
         if (i + 1 < u.i1) {  // the next tile's entry, while this one waits for its slots
           r0 = wanted(i + 1);
           phys = r0 >= 0 ? __ldg(table + r0 / bs) : -1;
@@ -802,7 +819,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
   } else if (warp >= kSoftWarps) {
     // Without a plan: flags of invalid sequences, and their zeros.
-    if (p.mode == kPlanNone) {
+    if (!AGAIN && p.mode == kPlanNone) {
       for (int b = static_cast<int>(blockIdx.x) * 2 + warp - kSoftWarps - 2; b < p.batch; b += 2 * gridDim.x) {
         const Span s = span_of(p, b, lane == 0);
         if (s.count == 0 || s.rows > 0) continue;
@@ -829,7 +846,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int mine = warp * 32 + lane, other = mine ^ 128;  // the row's other thread
     const int pair = 1 + hf * 4 + (warp & 3);                // barrier of the two warps
     const int tk = r / p.group;  // token of the half
-    constexpr float BELOW = PromptMargin<BF>::kBelow, ABOVE = PromptMargin<BF>::kAbove;
+    // (done again, weights of bf16 stay at or below 1: its values end where fp32 does)
+    constexpr float BELOW = PromptMargin<BF>::kBelow, ABOVE = AGAIN && BF ? 0.f : PromptMargin<BF>::kAbove;
     const float qs = p.qscale;
     // a warp goes on or gives up as one
     auto wait_warp = [&](uint32_t b, uint32_t parity) {
@@ -846,15 +864,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       return y;
     };
     uint32_t gt = 0, n = 0, nu = 0;  // the CTA's KV tiles; tiles and units of this half
-    auto redo = [&](int i) { return p.redo + (static_cast<int64_t>(blockIdx.x) * kSoftWarps + warp) * p.redo_max + i; };
-    int n_redo = 0;
-    // Rows of the warp whose output was not finite, once more.
-    auto redo_rows = [&](const Tile& t, int kvh, uint32_t rows) {
-      for (; rows != 0; rows &= rows - 1) {
-        const int r1 = (warp & 3) * 32 + __ffs(rows) - 1, tk1 = r1 / p.group, tok = hf * p.tokens + tk1;
-        redo_row<CT, D, 4>(p, t.seq, t.first + tok, kvh * p.group + r1 - tk1 * p.group, t.pos + tok);
-      }
-    };
     bool ok = true;
     for (uint32_t un = 0;; ++un) {
       // both warps of a row go on or give up: neither may wait at their barrier alone
@@ -877,8 +886,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const Seen seen = seen_tiles(u.t.pos, u.t.count, window, sinks);
         const int open = last >= window ? (last - window) / kRows + 1 : 0;
         f0 = seen.front + max(0, open - seen.start);
-        f1 = seen.front + (first + 1) / kRows - seen.start;
+        f1 = AGAIN ? 0 : seen.front + (first + 1) / kRows - seen.start;
       }
+      // What is not finite in rows that every token of the unit sees, in tiles' row r, and
+      // in the others: row `behind` the first token's, or leaving the window.
+      OddDims* odd_all = reinterpret_cast<OddDims*>(sm + G::kOffStage) + cg;
+      OddDims* odd_row = reinterpret_cast<OddDims*>(sm + G::kOffOddRows) + cg;
+      if (AGAIN && hf == 0) odd_all[2 * r] = make_uint4(0u, 0u, 0u, 0u);
       float m = -1e30f, l = 0.f;  // finite: a row may meet only hidden columns
       const int i0 = u.i0, i1 = u.i1;
       for (int i = i0; i < i1; ++i, ++gt, ++n) {
@@ -933,20 +947,36 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           // NaN: half 0 clears them (its products come first).
           const int end = u.t.pos + u.t.count - 1;
           const int low = u.t.pos >= window ? u.t.pos - window + 1 : 0;
-          if (hf == 0 && (r0 + kRows - 1 > end || (r0 < low && r0 + kRows > sinks))) {
+          if (hf == 0 && (AGAIN || r0 + kRows - 1 > end || (r0 < low && r0 + kRows > sinks))) {
             const uint32_t k = 2 * gt + 1, slot = k % G::kSlots;
             ok = ok && wait_warp(bar(G::FULL0 + slot), (k / G::kSlots) & 1u);
             const int row = r0 + r;
+            unsigned char* v = sm + G::kOffRing + slot * G::kTile + (r >> 3) * G::kRowGroup + (r & 7) * 128;
+            constexpr int CH = G::kHalves * 4;  // 16-byte chunks of a thread
             if (ok && (row > end || (row < low && row >= sinks))) {
-              unsigned char* v = sm + G::kOffRing + slot * G::kTile + (r >> 3) * G::kRowGroup + (r & 7) * 128;
-              constexpr int CH = G::kHalves * 4;  // 16-byte chunks of a thread
 #pragma unroll
               for (int c = 0; c < CH; ++c) {
                 const int ch = cg * CH + c;
                 *reinterpret_cast<uint4*>(v + (ch >> 3) * 1024 + 16 * (ch & 7)) = make_uint4(0u, 0u, 0u, 0u);
               }
+            } else if (AGAIN && ok) {
+              OddDims odd = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+              for (int c = 0; c < CH; ++c) {  // (the swizzle: chunk c of row r lies at c ^ (r & 7))
+                const int ch = cg * CH + c;
+                take_odd<BF>(v + (ch >> 3) * 1024 + 16 * ((ch & 7) ^ (r & 7)), 8 * c, odd);
+              }
+              if (row > u.t.pos) {
+                odd_row[2 * (row - u.t.pos - 1)] = odd;
+              } else if (row <= end - window && row >= sinks) {
+                odd_row[2 * (2 * kM - 1 + row - low)] = odd;
+              } else {
+                OddDims& all = odd_all[2 * r];
+                all = make_uint4(all.x | odd.x, all.y | odd.y, all.z | odd.z, all.w | odd.w);
+              }
             }
             fence_proxy_async_smem();
+            if constexpr (AGAIN) __syncwarp();
           }
         }
         // Once; again where the reference had to move. The first half of the
@@ -997,7 +1027,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
       // ---- epilogue
       if (!ok) break;  // both warps of a row
-      ok = wait_warp(bar(G::OFULL0 + hf), nu & 1u);
+      if (AGAIN && hf == 0) {
+        __syncwarp();
+        if (lane == 0) arrive(bar(G::ODDFULL));
+      }
+      ok = wait_warp(bar(G::OFULL0 + hf), nu & 1u) && (!AGAIN || wait_warp(bar(G::ODDFULL), un & 1u));
       l += exchange(l, ok);
       if (!ok) break;
       ++nu;
@@ -1032,61 +1066,152 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         __syncwarp();
       };
-      float zero = 0.f;  // NaN if an output is not finite
+      if constexpr (!AGAIN) {
+        float zero = 0.f;  // NaN if an output is not finite
 #pragma unroll 1
-      for (int c = 0; c < OC; c += 32) {
-        float o[32];
-        tmem_ld32(col_o + c, o);
+        for (int c = 0; c < OC; c += 32) {
+          float o[32];
+          tmem_ld32(col_o + c, o);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] *= inv;
-        if (rec >= 0) {
-          put(reinterpret_cast<const uint32_t*>(o), 4 * c);
-          put(reinterpret_cast<const uint32_t*>(o) + 16, 4 * c + 64);
-        } else {
-          uint32_t w[16];
+          for (int k = 0; k < 32; ++k) o[k] *= inv;
+          if (rec >= 0) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            zero = fmaf(o[2 * k], 0.f, fmaf(o[2 * k + 1], 0.f, zero));
-            w[k] = pack16<BF>(o[2 * k], o[2 * k + 1]);
+            for (int k = 0; k < 32; ++k) zero = fmaf(o[k], 0.f, zero);
+            put(reinterpret_cast<const uint32_t*>(o), 4 * c);
+            put(reinterpret_cast<const uint32_t*>(o) + 16, 4 * c + 64);
+          } else {
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              zero = fmaf(o[2 * k], 0.f, fmaf(o[2 * k + 1], 0.f, zero));
+              w[k] = pack16<BF>(o[2 * k], o[2 * k + 1]);
+            }
+            put(w, 2 * c);
           }
-          put(w, 2 * c);
+        }
+        // Where a visible score is NaN the sum is, and so are all outputs of the row: nothing to find out.
+        // The unit's first warp that meets one puts it on the list.
+        if (__any_sync(full, valid && zero != 0.f && l == l) && lane == 0 &&
+            atomicExch(const_cast<int*>(s_odd) + 1 + (un & 1), 1) == 0) {
+          OddUnit& e = p.odd[u.t.cost];
+          e.u = u;
+          e.next = atomicExch(const_cast<int*>(s_odd), u.t.cost);
+        }
+      } else {
+        OddDims odd = make_uint4(0u, 0u, 0u, 0u);
+        auto add = [&](const OddDims& x) {
+          odd.x |= x.x;
+          odd.y |= x.y;
+          odd.z |= x.z;
+          odd.w |= x.w;
+        };
+        for (int i = 0; i < kRows; ++i) add(odd_all[2 * i]);
+        // of the others those that this token sees, in this part's tiles
+        const Seen seen = seen_tiles(u.t.pos, u.t.count, window, sinks);
+        const int low = u.t.pos >= window ? u.t.pos - window + 1 : 0, end = u.t.pos + u.t.count - 1;
+        const int r0 = (i0 - seen.front + seen.start) * kRows, r1 = (i1 - seen.front + seen.start) * kRows;
+        for (int x = max(u.t.pos + 1, r0); x <= min(pos, r1 - 1); ++x)
+          if (x > pos - window || x < sinks) add(odd_row[2 * (x - u.t.pos - 1)]);
+        for (int x = max(max(low, pos - window + 1), max(sinks, r0)); x <= min(min(end - window, u.t.pos), r1 - 1); ++x)
+          add(odd_row[2 * (2 * kM - 1 + x - low)]);
+        if (l != l) odd = make_uint4(0u, 0u, 0u, 0u);  // NaN throughout
+        __syncwarp();
+#pragma unroll 1
+        for (int c = 0; c < OC; c += 16) {
+          float o[16];
+          tmem_ld16(col_o + c, o);
+          const uint32_t plus = (c < 32 ? odd.x : odd.y) >> (c & 31), minus = (c < 32 ? odd.z : odd.w) >> (c & 31);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] = odd_or(o[k] * inv, plus, minus, k);
+          if (to != nullptr && rec >= 0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              reinterpret_cast<float4*>(to)[c / 4 + k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          } else if (to != nullptr) {
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = pack16<BF>(o[2 * k], o[2 * k + 1]);
+            reinterpret_cast<uint4*>(to)[c / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(to)[c / 8 + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+          __syncwarp();
         }
       }
       fence_before();
       __syncwarp();
       if (lane == 0) arrive(bar(G::OEMPTY0 + hf));
-      if (rec >= 0) {
-        if (valid && cg == 0)
-          *reinterpret_cast<float2*>(p.rec_ml + ((static_cast<int64_t>(rec) * 2 + hf) * kM + r) * 2) =
-              make_float2(m, l);
-      } else {
-        // Rows done again whole, by either warp of the row or by both (the same
-        // values): at the end, when nobody waits for this warp any more (a row of a
-        // long sequence takes milliseconds). Where a visible score is NaN the sum is,
-        // and so are all outputs of the row: nothing to find out.
-        const uint32_t odd = __ballot_sync(full, valid && zero != 0.f && l == l);
-        if (odd != 0) {
-          if (n_redo < p.redo_max) {
-            if (lane == 0) *redo(n_redo) = {u.t, u.kvh, odd, {0, 0}};
-            ++n_redo;
-          } else {
-            redo_rows(u.t, u.kvh, odd);
-          }
-        }
-      }
+      if (rec >= 0 && valid && cg == 0)
+        *reinterpret_cast<float2*>(p.rec_ml + ((static_cast<int64_t>(rec) * 2 + hf) * kM + r) * 2) = make_float2(m, l);
       __syncwarp();
       if (lane == 0) arrive(bar(G::UEMPTY0 + (un & 1)));
-    }
-    __syncwarp();
-    for (int i = 0; i < n_redo; ++i) {
-      const Redo e = *redo(i);
-      redo_rows(e.t, e.kvh, e.rows);
     }
   }
 
   fence_before();
   __syncthreads();
   fence_after();
+}
+
+// (out of line: its registers are its own)
+template <typename CT, int D>
+__device__ __noinline__ void prompt_roles_again(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                                                const CUtensorMap& tm_v, const PromptParams& p, unsigned char* sm,
+                                                uint32_t tmem) {
+  prompt_roles<CT, D, true>(tm_q, tm_k, tm_v, p, sm, tmem);
+}
+
+template <typename CT, int D>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PromptParams p) {
+  using G = PromptGeo<D>;
+  extern __shared__ __align__(1024) unsigned char sm[];  // the swizzle counts from multiples of 1024
+  const uint32_t base = smem_addr(sm);
+  volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(sm + G::kOffMisc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(sm + G::kOffMisc + 4);
+  volatile int* s_odd = reinterpret_cast<volatile int*>(sm + G::kOffMisc + 8);
+  const int tid = threadIdx.x, warp = tid >> 5;
+
+  if ((base & 1023u) != 0) {  // the alignment above was not kept
+    set_flag(p.err, KVC_FLAG_TIMEOUT);
+    return;
+  }
+  if (tid < 2 * G::COUNT) {
+    const int i = tid % G::COUNT;
+    uint32_t from = 1;
+    if ((i >= G::PFULL0 && i < G::OFULL0) || (i >= G::OEMPTY0 && i < G::UFULL0) || i == G::ODDFULL)
+      from = kSoftWarps / 2;
+    if (i >= G::UEMPTY0 && i < G::FINAL) from = kSoftWarps + 1;
+    mbar_init(reinterpret_cast<uint64_t*>(sm + G::kOffBar) + tid, from);
+    fence_barrier_init();
+  }
+  if (tid == 0) {
+    *s_abort = 0;
+    *s_odd = -1;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
+  }
+  // Query rows that no token has (128 is no multiple of the group) stay zeros.
+  if (p.tokens * p.group < kM) {
+    for (uint32_t i = tid; i < 2 * G::kTile / 16; i += kPromptThreads)
+      *reinterpret_cast<uint4*>(sm + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
+  if (warp == kSoftWarps + 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + G::kOffMisc),
+                 "r"(G::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *s_tmem;
+  prompt_roles<CT, D, false>(tm_q, tm_k, tm_v, p, sm, tmem);
+  if (*s_odd >= 0 && *s_abort == 0) prompt_roles_again<CT, D>(tm_q, tm_k, tm_v, p, sm, tmem);
   if (warp == kSoftWarps + 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(G::kTmemCols) : "memory");
 }
@@ -1094,7 +1219,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 // ------------------------------------------------------------------ merge
 
 // Joins the records of units that several ranges share: o = sum_x 2^(m_x - M)
-// O_x / sum_x 2^(m_x - M) l_x, M the largest m so far. A warp has four rows at a time,
+// O_x / sum_x 2^(m_x - M) l_x, M the largest m so far; an infinity or NaN of a record stays
+// as it is, whatever its factor. A warp has four rows at a time,
 // lanes over the dims, the loads of two records of each in flight: bound by a chain of
 // three loads (tile, its prefix sum, records) per unit.
 constexpr int kMergeRows = 32;  // rows of a unit per CTA
@@ -1104,10 +1230,11 @@ template <typename CT, int D>
 __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptParams p) {
   constexpr int N = D / 32, K = kMergeWarpRows;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int H = p.row.n_kv_heads, n = __ldcg(p.head);
+  const int H = p.n_kv_heads, n = __ldcg(p.head);
   if (__ldcg(p.head + 2) == 0) return;  // no unit was split
   const Ranges r(n, __ldcg(p.head + 1), H, p.grid);
   const int lane = threadIdx.x & 31;
+  auto finite = [](float x) { return fabsf(x) < __builtin_huge_valf(); };
   constexpr int CH = 2 * kM / kMergeRows;  // CTAs' shares of a unit
   for (int64_t w = blockIdx.x; w < static_cast<int64_t>(n) * H * CH; w += gridDim.x) {
     const int unit = static_cast<int>(w / CH), i = unit / H, kvh = unit - i * H;
@@ -1167,7 +1294,8 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptParams p)
           M[k] = to;
           L[k] = fmaf(g, ml[d][k].y, L[k] * f);
 #pragma unroll
-          for (int c = 0; c < N; ++c) o[k][c] = fmaf(g, y[d][k][c], o[k][c] * f);
+          for (int c = 0; c < N; ++c)
+            o[k][c] = fmaf(finite(y[d][k][c]) ? g : 1.f, y[d][k][c], finite(o[k][c]) ? o[k][c] * f : o[k][c]);
         }
       }
     }
@@ -1175,17 +1303,10 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptParams p)
     for (int k = 0; k < K; ++k) {
       if (tok[k] < 0) continue;
       const float inv = L[k] == 0.f ? 0.f : 1.f / L[k];
-      float zero = 0.f;
 #pragma unroll
-      for (int c = 0; c < N; ++c) {
-        o[k][c] *= inv;
-        zero = fmaf(o[k][c], 0.f, zero);
-      }
-      if (L[k] == L[k] && __any_sync(0xffffffffu, zero != 0.f))  // (a sum that is NaN: see prompt_kernel)
-        redo_row<CT, D, 1>(p, t.seq, t.first + tok[k], head[k], t.pos + tok[k]);
-      else
-        store_out_vec<N>(p.out, (static_cast<int64_t>(t.first + tok[k]) * p.n_q_heads + head[k]) * D + lane * N, o[k],
-                         std::is_same<CT, __half>::value ? KVC_F16 : KVC_BF16);
+      for (int c = 0; c < N; ++c) o[k][c] *= finite(o[k][c]) || inv != inv ? inv : 1.f;
+      store_out_vec<N>(p.out, (static_cast<int64_t>(t.first + tok[k]) * p.n_q_heads + head[k]) * D + lane * N, o[k],
+                       std::is_same<CT, __half>::value ? KVC_F16 : KVC_BF16);
     }
   }
 }
@@ -1218,11 +1339,11 @@ kvc_status check_shape(const PromptShape& s) {
 }
 
 // Workspace: [head][tiles][their prefix sums][records' outputs][records'
-// references and sums][rows to do again], each 256-byte aligned; records and prefix sums only where
+// references and sums][odd units], each 256-byte aligned; records and prefix sums only where
 // units may be split.
 struct PromptLayout {
-  size_t tiles, before, rec_o, rec_ml, redo, total;
-  int mode, redo_max;
+  size_t tiles, before, rec_o, rec_ml, odd, total;
+  int mode;
 };
 
 // Units per SM from which none is split: dealt out by size they end together.
@@ -1246,9 +1367,8 @@ PromptLayout layout(const PromptShape& s, int num_sms) {
   l.rec_o = l.before + up256(l.mode == kPlanSplit ? static_cast<size_t>(s.tiles()) * 4 : 0);
   const size_t recs = l.mode == kPlanSplit ? 2 * static_cast<size_t>(num_sms) * 2 * kM : 0;
   l.rec_ml = l.rec_o + up256(recs * s.D * 4);
-  l.redo = l.rec_ml + up256(recs * 8);
-  l.redo_max = static_cast<int>((s.tiles() * s.n_kv_heads + num_sms - 1) / num_sms);
-  l.total = l.redo + up256(static_cast<size_t>(num_sms) * kSoftWarps * l.redo_max * sizeof(Redo));
+  l.odd = l.rec_ml + up256(recs * 8);
+  l.total = l.odd + up256((static_cast<size_t>(s.tiles()) * s.n_kv_heads + 2 * num_sms) * sizeof(OddUnit));
   return l;
 }
 
@@ -1319,7 +1439,7 @@ kvc_status launch(const PromptParams& p, const CUtensorMap& tq, const CUtensorMa
   e = cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, p);
   if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx(prompt)");
   if (p.mode == kPlanSplit) {
-    const int64_t shares = static_cast<int64_t>(p.max_tiles) * p.row.n_kv_heads * (2 * kM / kMergeRows);
+    const int64_t shares = static_cast<int64_t>(p.max_tiles) * p.n_kv_heads * (2 * kM / kMergeRows);
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(shares, 8 * p.grid)));  // what the GPU holds at once
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
@@ -1385,8 +1505,11 @@ kvc_status kvc_prompt_attention(const void* q, const void* k_cache, const void* 
   char* ws = static_cast<char*>(workspace);
   PromptParams p{};
   // positions are below 2^30: larger windows are all rows, and differences of them stay in 32 bits
-  p.row = {k_cache, v_cache, num_blocks, n_kv_heads, block_size, std::min(window, 1 << 30),
-           std::min(sinks, 1 << 30), scale * 1.4426950408889634f};
+  p.window = std::min(window, 1 << 30);
+  p.sinks = std::min(sinks, 1 << 30);
+  p.num_blocks = num_blocks;
+  p.n_kv_heads = n_kv_heads;
+  p.block_size = block_size;
   p.q = q;
   p.out = out;
   p.block_tables = block_tables;
@@ -1397,8 +1520,7 @@ kvc_status kvc_prompt_attention(const void* q, const void* k_cache, const void* 
   p.before = reinterpret_cast<int*>(ws + l.before);
   p.rec_o = reinterpret_cast<float*>(ws + l.rec_o);
   p.rec_ml = reinterpret_cast<float*>(ws + l.rec_ml);
-  p.redo = reinterpret_cast<Redo*>(ws + l.redo);
-  p.redo_max = l.redo_max;
+  p.odd = reinterpret_cast<OddUnit*>(ws + l.odd);
   p.err = dev->error_word;
   p.batch = batch;
   p.num_tokens = static_cast<int>(num_tokens);
@@ -1421,7 +1543,7 @@ kvc_status kvc_prompt_attention(const void* q, const void* k_cache, const void* 
   while ((1 << p.box_log2) < p.box) ++p.box_log2;
   p.pool_rows = static_cast<int>(num_blocks * n_kv_heads * block_size);
   // hidden scores are -infinity, which a factor of 0 would turn into NaN
-  p.qscale = std::max(std::fabs(p.row.qscale), 1e-35f);
+  p.qscale = std::max(std::fabs(scale * 1.4426950408889634f), 1e-35f);
   p.negative = scale < 0.f ? 1 : 0;
   CUtensorMap tq, tk, tv;
   const cuuint64_t d = static_cast<cuuint64_t>(head_dim);
