@@ -955,10 +955,11 @@ __device__ __noinline__ void give_odd_values(const ScoredParams& p, int seq, int
   }
 }
 
-// The weight of a record relative to the largest one. Not below the smallest
-// normal number, which changes no finite sum and keeps an infinity.
-__device__ __forceinline__ float record_weight(float m, float largest) {
-  return fmaxf(fast_exp2(m - largest), 1.17549435e-38f);
+// A value of a record by the record's weight relative to the largest one. For an
+// infinity not below the smallest normal number, which keeps it; finite ones take the
+// weight as it is (bf16 ends at 3.4e38, where 2^-126 in place of 0 would be seen).
+__device__ __forceinline__ float weighed(float f, float x) {
+  return (fabsf(x) < __builtin_huge_valf() ? f : fmaxf(f, 1.17549435e-38f)) * x;
 }
 
 }  // namespace scored
@@ -1473,13 +1474,13 @@ __global__ void __launch_bounds__(GeoOf<CT, D, NT>::Type::kThreads, 1)
         float l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int x = a; x < b; ++x) {
-          const float f = record_weight(part(x)[NC * D + 2 * col], m);
+          const float f = fast_exp2(part(x)[NC * D + 2 * col] - m);
           const float4 y = *reinterpret_cast<const float4*>(part(x) + col * D + d);
           l += f * part(x)[NC * D + 2 * col + 1];
-          o.x += f * y.x;
-          o.y += f * y.y;
-          o.z += f * y.z;
-          o.w += f * y.w;
+          o.x += weighed(f, y.x);
+          o.y += weighed(f, y.y);
+          o.z += weighed(f, y.z);
+          o.w += weighed(f, y.w);
         }
         *reinterpret_cast<float4*>(p.rec_o + (rec * NC + col) * D + d) = o;
         if (d == 0) *reinterpret_cast<float2*>(p.rec_ml + (rec * NC + col) * 2) = make_float2(m, l);
@@ -1679,7 +1680,7 @@ __global__ void __launch_bounds__(kFinishThreads, SCORED ? 4 : 2)
         l = ml.y;
       }
       const float M = warp_max(m);
-      const float f = lane < r.n ? record_weight(m, M) : 0.f;
+      const float f = lane < r.n ? fast_exp2(m - M) : 0.f;
       const float L = warp_sum(f * l);
       for (int i0 = 0; i0 < r.n; i0 += U) {
         float x[U][V];
@@ -1691,7 +1692,7 @@ __global__ void __launch_bounds__(kFinishThreads, SCORED ? 4 : 2)
           const float fi = __shfl_sync(full, f, min(i0 + i, 31));
           if (i0 + i < r.n) {
 #pragma unroll
-            for (int k = 0; k < V; ++k) o[k] += fi * x[i][k];
+            for (int k = 0; k < V; ++k) o[k] += weighed(fi, x[i][k]);
           }
         }
       }
@@ -1716,7 +1717,7 @@ __global__ void __launch_bounds__(kFinishThreads, SCORED ? 4 : 2)
       for (int i = 1; i < kFinishWarps; ++i) m = fmaxf(m, s_red[0][i]);
       float l = 0.f;
       for (int i = tid; i < r.n; i += kFinishThreads) {
-        const float f = record_weight(s_dyn[i], m);
+        const float f = fast_exp2(s_dyn[i] - m);
         l += f * __ldcg(p.rec_ml + (record_slot(r, i) * NC + col) * 2 + 1);
         s_dyn[i] = f;
       }
@@ -1739,7 +1740,7 @@ __global__ void __launch_bounds__(kFinishThreads, SCORED ? 4 : 2)
           if (j < r.n) {
             const float f = s_dyn[j];
 #pragma unroll
-            for (int k = 0; k < V; ++k) o[k] += f * x[i][k];
+            for (int k = 0; k < V; ++k) o[k] += weighed(f, x[i][k]);
           }
         }
       }
