@@ -518,7 +518,8 @@ kvc_status kvc_decode_attention_block8(const void* q, const void* k_cache, const
  *        row r if r <= pos and (r > pos - window or r < sinks)
  * What the other rows hold (infinities, NaN) does not reach it; an infinity or
  * NaN in V of a row that it attends is its output there, whatever the row's
- * weight. window >= 1 (INT32_MAX: every row), sinks >= 0. Table entries of blocks
+ * weight. (Values beyond 2^100: their sums may leave fp32 before they are divided by
+ * the weights' sum.) window >= 1 (INT32_MAX: every row), sinks >= 0. Table entries of blocks
  * that no token of the call sees are not used, so a caller may free the blocks
  * between the sinks and the window. Types, shapes, flags and errors as
  * kvc_decode_attention_scored; workspace: kvc_decode_scored_workspace_size with

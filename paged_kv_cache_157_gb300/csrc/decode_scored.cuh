@@ -1228,7 +1228,8 @@ __global__ void __launch_bounds__(GeoOf<CT, D, NT>::Type::kThreads, 1)
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          st.m[n][e] = -1e30f;  // finite: a query that meets only masked rows keeps weight 0
+          // finite: a query that meets only masked rows keeps weight 0
+          st.m[n][e] = WIN ? -3.40282347e38f : -1e30f;
           st.l[n][e] = 0.f;
           if constexpr (ONE) st.mo[n][e] = -1e30f;
           const int t = divided(col0 + 8 * n + 2 * c + e, m_group);

@@ -85,6 +85,7 @@ constexpr int kMinTiles = 4;       // KV tiles of a range at least, where units 
 // Units are split where that makes the longest CTA's work shorter by more than
 // these KV tiles: what the records and their merge cost (about 15 us).
 constexpr int kSplitGain = 10;
+constexpr float kLowest = -3.40282347e38f;  // where a reference begins: no score that is a number lies below
 constexpr int kBadRing = 8;        // tiles whose bad blocks are remembered: more than the ring holds
 
 struct PromptShape {
@@ -893,7 +894,7 @@ __device__ __forceinline__ void prompt_roles(const CUtensorMap& tm_q, const CUte
       OddDims* odd_all = reinterpret_cast<OddDims*>(sm + G::kOffStage) + cg;
       OddDims* odd_row = reinterpret_cast<OddDims*>(sm + G::kOffOddRows) + cg;
       if (AGAIN && hf == 0) odd_all[2 * r] = make_uint4(0u, 0u, 0u, 0u);
-      float m = -1e30f, l = 0.f;  // finite: a row may meet only hidden columns
+      float m = kLowest, l = 0.f;  // finite: a row may meet only hidden columns
       const int i0 = u.i0, i1 = u.i1;
       for (int i = i0; i < i1; ++i, ++gt, ++n) {
         ok = wait_warp(bar(G::SFULL0 + hf), n & 1u);
@@ -927,7 +928,8 @@ __device__ __forceinline__ void prompt_roles(const CUtensorMap& tm_q, const CUte
           const float2 q2 = make_float2(qs, qs), m2 = make_float2(-m, -m);
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const float2 x = ffma2(make_float2(s[2 * k], s[2 * k + 1]), q2, m2);
+            const float2 a = make_float2(s[2 * k], s[2 * k + 1]);
+            const float2 x = AGAIN ? fadd2(make_float2(__fmul_rn(a.x, qs), __fmul_rn(a.y, qs)), m2) : ffma2(a, q2, m2);
             const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
             sum[k & 1] = fadd2(sum[k & 1], e);
             w[k] = pack16<BF>(e.x, e.y);
@@ -1089,9 +1091,12 @@ __device__ __forceinline__ void prompt_roles(const CUtensorMap& tm_q, const CUte
             put(w, 2 * c);
           }
         }
-        // Where a visible score is NaN the sum is, and so are all outputs of the row: nothing to find out.
+        // Where a visible score is NaN the sum is, and so are all outputs of the row: nothing to
+        // find out. A sum of 0 or infinity: the reference is the rounded product of a score, the
+        // weights' exponents are not, and for scores beyond 2^30 the difference alone leaves
+        // fp32's exponents. Done again, those are differences of rounded products.
         // The unit's first warp that meets one puts it on the list.
-        if (__any_sync(full, valid && zero != 0.f && l == l) && lane == 0 &&
+        if (__any_sync(full, valid && ((zero != 0.f && l == l) || (l == 0.f && m > kLowest))) && lane == 0 &&
             atomicExch(const_cast<int*>(s_odd) + 1 + (un & 1), 1) == 0) {
           OddUnit& e = p.odd[u.t.cost];
           e.u = u;
@@ -1253,7 +1258,7 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptParams p)
       const int hf = (row0 + k) / kM, at = (row0 + k) % kM, tk = at / p.group;
       tok[k] = tk < p.tokens && hf * p.tokens + tk < t.count ? hf * p.tokens + tk : -1;
       head[k] = kvh * p.group + at - tk * p.group;
-      M[k] = -1e30f;
+      M[k] = kLowest;
       L[k] = 0.f;
 #pragma unroll
       for (int c = 0; c < N; ++c) o[k][c] = 0.f;

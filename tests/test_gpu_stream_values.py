@@ -51,3 +51,34 @@ def test_a_large_value_without_weight_adds_nothing(kvc, op, odd, split):
         out[..., 9] = 1.0
     # 2360 equal weights over their sum: an fp32 division, products and sums of whole numbers
     assert (out - 1).abs().max() <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("score", [-1e10, 1e12, -1e29, -1e31, -3e38, 3e38])
+@pytest.mark.parametrize("op", ["sinks", "fp4", "prompt"])
+def test_scores_of_any_size(kvc, op, score, split):
+    """All scores alike and far from 0, none of them exact in fp32 once scaled: equal weights, also where a sequence is done
+    in parts."""
+    q, k, v, tables, lens = one_sequence(3000, 8, 2, 64)
+    q[..., 0] = abs(score) / 2 ** 10  # (the product of 3e38 is rounded to within bf16's range)
+    k[..., 0] = 1.0 if score > 0 else -1.0
+    v[...] = 2.0
+    v[:, :, ::2] = 1.0
+    out = torch.full((1, 8, 64), 7.0, device="cuda")
+    args = (tables, lens, 2.0 ** 10 / 1.4426950408889634 * 0.9837)  # scores in log2 units within fp32
+    if op == "prompt":
+        out = torch.full((1, 8, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        ws = kvc.new_prompt_workspace(1, 1, 8, 2, 64, 16, tables.shape[1])
+        kvc.prompt_attention(q, k, v, tables, int32([0, 1]), *args[1:], out, ws, window=2000, sinks=40)
+    else:
+        ws = kvc.new_scored_workspace(1, 1, 8, 2, 64, 16, tables.shape[1], scored=False)
+        if op == "sinks":
+            kvc.decode_attention_sinks(q, k, v, *args, 2000, 40, out, ws)
+        else:
+            codes = [torch.zeros((*k.shape[:3], 32), dtype=torch.uint8, device="cuda") for _ in range(2)]
+            scales = [torch.zeros((*k.shape[:3], 4), dtype=torch.uint8, device="cuda") for _ in range(2)]
+            slots = torch.arange(k.shape[0] * 16, device="cuda")
+            kvc.append_fp4(*(x.transpose(1, 2).reshape(-1, 2, 64).contiguous() for x in (k, v)), slots, *codes, *scales)
+            kvc.decode_attention_fp4(q, *codes, *scales, *args, out, ws, window=2000, sinks=40)
+    assert kvc.get_error_flags() == 0
+    # half of the 2040 rows hold 1 (a step of 0.125 in e4m3 x 6: 1.03), half 2: within 2^-4 of 1.5, the scales' rounding
+    assert (out.float() / 1.5 - 1).abs().max() <= (2.0 ** -4 if op == "fp4" else 2.0 ** -8)
