@@ -39,7 +39,9 @@
 // turn, the largest first. Where that leaves the longest CTA more than kSplitGain KV
 // tiles behind the mean, the KV tiles of all units are laid end to end instead and cut
 // into equal ranges, one per CTA; the parts of a unit leave records that a merge
-// kernel joins (120 units of 70 to 235 KV tiles: 175 us, 16 of them the merge).
+// kernel joins (120 units of 70 to 235 KV tiles: 175 us, 16 of them the merge). The plan
+// adds up what each CTA would get: with 160 units of 236 tiles, the longest has 471 and
+// the mean is 253 (1280 tokens over 30,000 rows: 689 us whole, 430 split).
 //
 // Rows that nobody in a unit sees are neither looked up nor read (TMA fills
 // zeros), those beside visible ones are cleared in shared memory.
@@ -189,6 +191,7 @@ __host__ __device__ __forceinline__ Seen seen_tiles(int pos, int count, int wind
 
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 1024;
+constexpr int kSplitTiles = kPromptMaxBatch + 1024;  // of calls whose units may be split, at most
 
 // Exclusive prefix sum over the CTA; *total: the sum. Two barriers.
 __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
@@ -212,9 +215,9 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
   return before + x - v;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptParams p, int elem_bytes, int D) {
+__global__ void __launch_bounds__(kPlanThreads, 1) prompt_plan_kernel(const PromptParams p, int elem_bytes, int D) {
   __shared__ int s_first[kPromptMaxBatch + 1];  // tiles of the sequences before
-  __shared__ int s_warp[kPlanThreads / 32], s_hist[kBuckets];
+  __shared__ int s_warp[kPlanThreads / 32], s_hist[kBuckets], s_load[kBuckets], s_cost[kSplitTiles];
   const int tid = threadIdx.x, B = p.batch, per_tile = 2 * p.tokens;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -270,42 +273,59 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
   };
   most = max(__reduce_max_sync(0xffffffffu, most), 1);
   if ((tid & 31) == 0) s_warp[tid >> 5] = most;
-  s_hist[tid] = 0;
+  s_hist[tid] = s_load[tid] = 0;
   __syncthreads();
   for (int i = 0; i < kPlanThreads / 32; ++i) most = max(most, s_warp[i]);
   __syncthreads();
   int total = 0;
   bool split = false;
-  if (p.mode == kPlanSplit) {  // few tiles: their prefix sums, and whether splitting pays
-    for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
-      Tile t;
-      t.cost = 0;
-      if (i0 + tid < n) t = tile_of(i0 + tid);
+  Tile mine{};  // (of most calls all that there are: found once)
+  if (tid < n) mine = tile_of(tid);
+  auto tile = [&](int i) { return i == tid ? mine : tile_of(i); };
+  // sorted by cost, in up to 1024 classes
+  int shift = 0;
+  while ((most >> shift) >= kBuckets) ++shift;
+  auto bucket = [&](int cost) { return min(kBuckets - 1, max(0, (most >> shift) - (cost >> shift))); };
+  for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+    const int cost = i0 + tid < n ? tile(i0 + tid).cost : 0;
+    if (i0 + tid < n) atomicAdd(&s_hist[bucket(cost)], 1);
+    if (p.mode == kPlanSplit) {  // few tiles: their prefix sums
       int sum = 0;
-      const int before = block_scan(t.cost, s_warp, &sum);
-      if (i0 + tid < n) {
-        p.before[i0 + tid] = total + before;
-        p.tiles[i0 + tid] = t;
-      }
+      const int before = block_scan(cost, s_warp, &sum);
+      if (i0 + tid < n) p.before[i0 + tid] = total + before;
       total += sum;
     }
-    split = most - total * p.n_kv_heads / p.grid > kSplitGain;
   }
-  if (!split) {  // sorted by cost, in up to 1024 classes
-    int shift = 0;
-    while ((most >> shift) >= kBuckets) ++shift;
-    auto bucket = [&](int cost) { return min(kBuckets - 1, max(0, (most >> shift) - (cost >> shift))); };
-    for (int i = tid; i < n; i += kPlanThreads) atomicAdd(&s_hist[bucket(tile_of(i).cost)], 1);
+  // Does splitting pay? What the longest CTA has of whole units against the mean
+  const int units = n * p.n_kv_heads, mean = total * p.n_kv_heads / p.grid;
+  const bool one_each = units <= p.grid;
+  if (p.mode == kPlanSplit && one_each) split = most - mean > kSplitGain;
+  if (!split) {
     __syncthreads();
-    const int mine = s_hist[tid];
     int sum = 0;
-    const int before = block_scan(mine, s_warp, &sum);
-    s_hist[tid] = before;
+    s_hist[tid] = block_scan(s_hist[tid], s_warp, &sum);
     __syncthreads();
     for (int i = tid; i < n; i += kPlanThreads) {
-      const Tile t = tile_of(i);
-      p.tiles[atomicAdd(&s_hist[bucket(t.cost)], 1)] = t;  // the order among equals is free
+      const Tile t = tile(i);
+      const int at = atomicAdd(&s_hist[bucket(t.cost)], 1);  // the order among equals is free
+      p.tiles[at] = t;
+      if (p.mode == kPlanSplit) s_cost[at] = t.cost >> shift << shift;  // (so that it is here, too)
     }
+    if (p.mode == kPlanSplit && !one_each) {
+      __syncthreads();
+      for (int j = tid; j < units; j += kPlanThreads) {
+        const int r = j / p.grid, c = j - r * p.grid;  // as Walk::unit deals them out
+        atomicAdd(&s_load[(r & 1) ? p.grid - 1 - c : c], s_cost[j / p.n_kv_heads]);
+      }
+      __syncthreads();
+      int longest = 0;
+      for (int c = tid & 31; c < p.grid; c += 32) longest = max(longest, s_load[c]);
+      split = __reduce_max_sync(0xffffffffu, longest) - mean > kSplitGain;
+    }
+  }
+  if (split) {  // in order
+    __syncthreads();
+    for (int i = tid; i < n; i += kPlanThreads) p.tiles[i] = tile(i);
   }
   if (tid == 0) {
     p.head[0] = n;
@@ -313,7 +333,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
     p.head[2] = split ? 1 : 0;
   }
 }
-static_assert(kBuckets == kPlanThreads, "one class per thread");
+static_assert(kBuckets == kPlanThreads, "one class per thread, and one counter per CTA");
 
 // The equal ranges of split units: range x is [start(x), start(x + 1)) of N positions.
 struct Ranges {
@@ -1363,7 +1383,8 @@ PromptLayout layout(const PromptShape& s, int num_sms) {
   const int64_t units = (s.num_tokens + 2 * s.tokens() - 1) / (2 * s.tokens()) * s.n_kv_heads;  // at least
   const int64_t most = static_cast<int64_t>(s.max_blocks) * s.block_size / kRows + 2;           // KV tiles of a unit
   l.mode = kPlanWhole;
-  if (units < static_cast<int64_t>(kWholeUnits) * num_sms && most > kSplitGain)
+  if (units < static_cast<int64_t>(kWholeUnits) * num_sms && most > kSplitGain && s.tiles() <= kSplitTiles &&
+      num_sms <= kBuckets)
     l.mode = kPlanSplit;
   else if (s.tiles() * s.n_kv_heads <= num_sms && s.batch <= kUnplannedBatch)
     l.mode = kPlanNone;

@@ -1,0 +1,45 @@
+"""GPU parity: how prompt attention hands out its work."""
+
+import pytest
+import torch
+
+from stream_helpers import Prompt
+
+pytestmark = pytest.mark.gpu
+
+
+def was_split(ws):
+    """The plan's third word: whether units were cut into parts."""
+    return int(ws[8:12].view(torch.int32).item())
+
+
+def ends_late(units, rows, ctas):
+    """Whether the CTA with the most work of units of two tokens, dealt out there and back by size, has more than ten
+    tiles of 128 rows above the mean."""
+    costs = sorted(((rows - 2 * u - 1) // 128 + 1 for u in range(units)), reverse=True)
+    load = [0] * ctas
+    for j, cost in enumerate(costs):
+        r, c = divmod(j, ctas)
+        load[ctas - 1 - c if r % 2 else c] += cost
+    return max(load) - sum(costs) // ctas > 10
+
+
+# units of 2 tokens per SM (and as many more), rows; for 152 SMs the longest CTA and the mean are
+@pytest.mark.parametrize("per_sm,more,rows", [
+    (0, 50, 2500),  # 20 tiles and 6
+    (1, 0, 2500),   # 20 and 18
+    (1, 8, 2500),   # 36 and 19
+    (2, 0, 2500),   # 36 and 35
+    (2, 40, 2500),  # 51 and 39
+    (1, 8, 1250),   # 16 and 9
+    (3, 20, 1700),  # 37 and 31
+    (3, 8, 3500),   # 92 and 71
+])
+def test_units_are_split_where_a_cta_would_end_late(kvc, per_sm, more, rows):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    units = per_sm * sms + more
+    p = Prompt([2 * units], [rows], 128, 1, 64, 16, "bf16", None, 0, seed=units, pad=0)
+    ws = p.workspace(kvc)
+    p.run(kvc, ws)
+    p.check()
+    assert was_split(ws) == ends_late(units, rows, sms) and kvc.get_error_flags() == 0
