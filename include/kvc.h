@@ -543,8 +543,12 @@ kvc_status kvc_decode_attention_fp4(const void* q, const void* k_cache, const vo
                                     int sinks, kvc_dtype q_dtype, void* out, kvc_dtype out_dtype, void* workspace,
                                     size_t workspace_bytes, kvc_stream stream);
 
-/* Scratch bytes for kvc_prompt_attention on the current device. Same shape
- * errors as that call. */
+/* Scratch bytes for kvc_prompt_attention on the current device. No argument but the
+ * heads' numbers makes it smaller by growing: the size for the largest batch, number of
+ * tokens and table serves every smaller call. Tables of more than 1151 rows add
+ * room for parts of units, 2 KB x head_dim + 4 KB per SM (41 MB for 152 SMs and head_dim
+ * 128); a call with smaller tables also starts faster where it has few tokens (one
+ * kernel instead of three). Same shape errors as that call. */
 kvc_status kvc_prompt_workspace_size(int batch, int64_t num_tokens, int n_q_heads, int n_kv_heads, int head_dim,
                                      int block_size, int max_blocks_per_seq, size_t* bytes);
 

@@ -1365,7 +1365,8 @@ kvc_status check_shape(const PromptShape& s) {
 
 // Workspace: [head][tiles][their prefix sums][records' outputs][records'
 // references and sums][odd units], each 256-byte aligned; records and prefix sums only where
-// units may be split.
+// units may be split, in this call or in one of fewer tokens: the size for the largest
+// call serves all smaller ones.
 struct PromptLayout {
   size_t tiles, before, rec_o, rec_ml, odd, total;
   int mode;
@@ -1390,8 +1391,8 @@ PromptLayout layout(const PromptShape& s, int num_sms) {
     l.mode = kPlanNone;
   l.tiles = 256;
   l.before = l.tiles + up256(static_cast<size_t>(s.tiles()) * sizeof(Tile));
-  l.rec_o = l.before + up256(l.mode == kPlanSplit ? static_cast<size_t>(s.tiles()) * 4 : 0);
-  const size_t recs = l.mode == kPlanSplit ? 2 * static_cast<size_t>(num_sms) * 2 * kM : 0;
+  l.rec_o = l.before + up256(most > kSplitGain ? static_cast<size_t>(s.tiles()) * 4 : 0);
+  const size_t recs = most > kSplitGain ? 2 * static_cast<size_t>(num_sms) * 2 * kM : 0;
   l.rec_ml = l.rec_o + up256(recs * s.D * 4);
   l.odd = l.rec_ml + up256(recs * 8);
   l.total = l.odd + up256((static_cast<size_t>(s.tiles()) * s.n_kv_heads + 2 * num_sms) * sizeof(OddUnit));

@@ -43,3 +43,27 @@ def test_units_are_split_where_a_cta_would_end_late(kvc, per_sm, more, rows):
     p.run(kvc, ws)
     p.check()
     assert was_split(ws) == ends_late(units, rows, sms) and kvc.get_error_flags() == 0
+
+
+def test_a_workspace_for_the_largest_call_serves_all(kvc):
+    """A serving loop makes its workspace once. Sizes never fall with the batch, the tokens or the table, and a call finds
+    what it needs in a workspace made for more."""
+    def size(batch, tokens, blocks):
+        return kvc.prompt_workspace_size(batch, tokens, 8, 2, 128, 16, blocks)
+
+    tokens = (0, 1, 40, 500, 2000, 9000, 16384, 70000, 300000)
+    batches, tables = (1, 3, 64, 300, 4096), (1, 70, 72, 73, 500, 9000)
+    for t in tables:
+        for b in batches:
+            assert [size(b, n, t) for n in tokens] == sorted(size(b, n, t) for n in tokens)
+        for n in tokens:
+            assert [size(b, n, t) for b in batches] == sorted(size(b, n, t) for b in batches)
+    for b in batches:
+        for n in tokens:
+            assert [size(b, n, t) for t in tables] == sorted(size(b, n, t) for t in tables)
+
+    p = Prompt([70, 3], [5000, 40], 8, 2, 128, 16, "bf16", None, 0, seed=33)
+    ws = torch.full((size(64, 300000, 500),), 255, dtype=torch.uint8, device="cuda")
+    p.run(kvc, ws)
+    p.check()
+    assert kvc.get_error_flags() == 0
