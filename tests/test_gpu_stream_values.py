@@ -4,7 +4,7 @@ relatives."""
 import pytest
 import torch
 
-from stream_helpers import int32
+from stream_helpers import Decode, int32
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +82,14 @@ def test_scores_of_any_size(kvc, op, score, split):
     assert kvc.get_error_flags() == 0
     # half of the 2040 rows hold 1 (a step of 0.125 in e4m3 x 6: 1.03), half 2: within 2^-4 of 1.5, the scales' rounding
     assert (out.float() / 1.5 - 1).abs().max() <= (2.0 ** -4 if op == "fp4" else 2.0 ** -8)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "fp4"])
+@pytest.mark.parametrize("out", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("T", [2, 3, 17])
+def test_types_and_splits_of_several_tokens(kvc, kind, out, T, split):
+    """A 16-bit output, several new tokens and a sequence that has no others, in every way of splitting the work."""
+    d = Decode([700, 90, T], T, 8, 2, 128, 16, kind, 300, 20, seed=50 + T, q_dtype="f16", out_dtype=out)
+    d.run(kvc)
+    d.check()
+    assert kvc.get_error_flags() == 0
