@@ -178,3 +178,52 @@ def test_an_infinity_costs_a_second_pass(kvc, new, rows, Hq, H):
     assert (out[..., 3].float() == float("inf")).all() and kvc.get_error_flags() == 0
     out[..., 3] = 0
     assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("sizes", [([300, 40], [300, 900], 4, 2, 128, 16), ([70, 9], [5000, 30], 8, 1, 64, 16),
+                                   ([5, 9], [50, 90], 8, 2, 128, 16)])
+@pytest.mark.parametrize("garbage", [0, 255])
+def test_infinities_that_come_and_go_between_replays(kvc, sizes, garbage):
+    """One captured call, its workspace full of anything: whether a row is done again is decided when the graph runs."""
+    p = Prompt(*sizes, "bf16", 90, 5, seed=34)
+    tables, starts, rows = p.device()
+    ws = torch.full_like(p.workspace(kvc), garbage)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kvc.prompt_attention(p.q, p.pools[0][0], p.pools[1][0], tables, starts, rows, p.scale, p.out, ws, window=90,
+                             sinks=5)
+    dev, host = p.pools[1][0].clone(), p.pools[1][1].copy()
+    for r in (None, 0, sizes[1][0] - 3, None, sizes[1][0] - 40):
+        p.pools[1][0].copy_(dev)
+        p.pools[1][1] = host.copy()
+        if r is not None:
+            plant(p, 0, r, 0, 17, np.inf)
+        p.out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        p.check()
+    assert kvc.get_error_flags() == 0
+
+
+def test_two_streams_with_infinities(kvc):
+    """Calls that are done again, side by side, give the same bits every time."""
+    a = Prompt([300, 40], [900, 2500], 8, 2, 128, 16, "bf16", seed=35)
+    b = Prompt([60], [300], 8, 2, 128, 16, "f16", 90, 5, seed=36)
+    for p in (a, b):
+        for r, x in ((1, np.inf), (p.rows[0] - 20, np.nan), (p.rows[0] - 70, -np.inf)):
+            plant(p, 0, r, 1, r % 128, x)
+    args = [(p, p.device(), p.workspace(kvc), torch.cuda.Stream()) for p in (a, b)]
+    torch.cuda.synchronize()
+    first = None
+    for _ in range(20):
+        for p, (tables, starts, rows), ws, stream in args:
+            kvc.prompt_attention(p.q, p.pools[0][0], p.pools[1][0], tables, starts, rows, p.scale, p.out, ws,
+                                 window=p.window, sinks=p.sinks, stream=stream)
+        torch.cuda.synchronize()
+        bits = [p.out.view(torch.int16).clone() for p in (a, b)]
+        first = first or bits
+        assert all(torch.equal(x, y) for x, y in zip(first, bits))
+    a.check()
+    b.check()
+    assert kvc.get_error_flags() == 0
