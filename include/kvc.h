@@ -102,7 +102,8 @@ typedef enum kvc_option {
    * decode kernels takes about N cache blocks (used by tests to force many
    * split-K partials). Process-wide. */
   KVC_OPT_BLOCKS_PER_CTA = 1,
-  /* Upper bound on decode CTAs (0 = automatic, SM count x resident CTAs). */
+  /* Upper bound on the CTAs of decodes and of prompt attention (0 = automatic, SM
+   * count x resident CTAs). */
   KVC_OPT_MAX_CTAS = 2,
   /* GQA decode engine. Three kernels compute the same decode:
    *  - the tcgen05 tensor-core kernel: bf16/f16 caches, head_dim 128, block
@@ -265,7 +266,8 @@ kvc_status kvc_append_block8(const void* k, const void* v, const int64_t* slot_m
  * changes them. Scales below 2^-6 (A below 0.094) have fewer bits, those of
  * A up to 6 * 2^-10 are 0: scale small keys (and the queries the other way) or
  * values by a power of two. k, v: [num_tokens, n_kv_heads, head_dim] in `dtype`
- * (F32, F16, BF16). slot_mapping: as kvc_append. num_tokens == 0 is a no-op.
+ * (F32, F16, BF16). slot_mapping: as kvc_append, but two tokens with the same slot may
+ * leave codes of one with scales of the other there. num_tokens == 0 is a no-op.
  * head_dim 64, 128 or 256; block_size a multiple of 16 up to 128; all pointers
  * but slot_mapping 16-byte aligned. A copied block needs its scales copied too
  * (kvc_copy_blocks on both pools). Source: "KV-Cache——为什么AI回复越来越快"
@@ -571,7 +573,8 @@ kvc_status kvc_prompt_workspace_size(int batch, int64_t num_tokens, int n_q_head
  * and outputs accumulate in fp32; the softmax weights are rounded to `dtype` for
  * the second product. Table entries of blocks that no token sees are not used.
  * head_dim 64 or 128; block_size a multiple of 16 up to 128; batch <= 4096; at
- * most 128 query heads per kv head; q, out and the caches 16-byte aligned.
+ * most 128 query heads per kv head; q, out and the caches 16-byte aligned; out must
+ * not overlap q.
  * A sequence whose length is below m_i or above max_blocks_per_seq * block_size
  * sets KVC_FLAG_BAD_LEN and gets zeros; one whose starts are out of order or range
  * sets it and is left out. Rows in blocks outside the pool set

@@ -9,11 +9,13 @@
 // it moves, and moves only when a score exceeds it by kAbove: exact in exact
 // arithmetic for any m, and O is rarely rescaled.
 //
-// What bounds it: the tensor core. 128 x 128 x 128 takes it 512 cycles, so a KV tile of
-// both halves 2048; measured are about 2600 (8192 tokens of 32 query, 8 kv heads, D 128,
-// bf16: 364 us, 1.51 PFLOP/s; 16384 tokens 1.60): the softmax of one half, from S to the
-// first part of P, takes longer than the other half's products. Its exponentials alone
-// are 512 cycles (8 per cycle and scheduler).
+// What bounds it: the tensor core, and the units' ends. 128 x 128 x 128 takes it 512
+// cycles, so a KV tile of both halves 2048; measured are about 2600, 1.44 us: the softmax of
+// one half, from S to the first part of P, takes longer than the other half's
+// products (its exponentials alone are 512 cycles, 8 per cycle and scheduler). A unit
+// takes 6 us besides: its queries' copy, the first tile's second run, the outputs of both
+// halves with nothing for the tensor core. (Fitted to 32 query, 8 kv heads, D 128, bf16:
+// 8192 tokens 359 us, 1.53 PFLOP/s; 16384 tokens 1335 us, 1.65.)
 //
 // A work unit is 2 x 128 query rows of one kv head: the `group` query heads of
 // each token are rows of their own (row = token * group + head), so that a kv
