@@ -569,7 +569,7 @@ kvc_status kvc_prompt_workspace_size(int batch, int64_t num_tokens, int n_q_head
  * row), sinks >= 0. Other rows' infinities and NaN do not reach it; an infinity or
  * NaN in V of a row that it attends is its output there, whatever the row's weight.
  * (Such values cost a second pass over the rows of the tokens around those that see
- * them: at most about four times the time of finite values.) Scores, sums
+ * them: three to five times the time of finite values if they concern all.) Scores, sums
  * and outputs accumulate in fp32; the softmax weights are rounded to `dtype` for
  * the second product. Table entries of blocks that no token sees are not used.
  * head_dim 64 or 128; block_size a multiple of 16 up to 128; batch <= 4096; at

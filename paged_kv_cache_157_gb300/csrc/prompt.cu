@@ -911,8 +911,8 @@ __device__ __forceinline__ void prompt_roles(const CUtensorMap& tm_q, const CUte
         f0 = seen.front + max(0, open - seen.start);
         f1 = AGAIN ? 0 : seen.front + (first + 1) / kRows - seen.start;
       }
-      // What is not finite in rows that every token of the unit sees, in tiles' row r, and
-      // in the others: row `behind` the first token's, or leaving the window.
+      // What is not finite: at [row of a tile] in the rows that every token of the unit sees;
+      // of the others at [row behind the first token's own], then [row leaving the window].
       OddDims* odd_all = reinterpret_cast<OddDims*>(sm + G::kOffStage) + cg;
       OddDims* odd_row = reinterpret_cast<OddDims*>(sm + G::kOffOddRows) + cg;
       if (AGAIN && hf == 0) odd_all[2 * r] = make_uint4(0u, 0u, 0u, 0u);
